@@ -6,22 +6,17 @@
 
 #include <cstdint>
 #include <cstring>
-#include <mutex>
-#include <string>
-#include <vector>
 
 #include "../../include/moe.h"
 #include "common.hpp"
 #include "gemm.hpp"
+#include "host.hpp"
 #include "routing.hpp"
 #include "rowwise.hpp"
 
 using namespace moe;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct Dims {
   int64_t T, H, I, E, K;
@@ -174,8 +169,6 @@ FwdLayout fwd_layout(const Dims& d) {
 size_t fwd_workspace(const Dims& d) { return fwd_layout(d).total; }
 
 // ---------------------------------------------------------------- validation
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 moe_status check_problem(const moe_problem* p) {
   if (!p) return MOE_ERR_NULL;
   if (p->tokens < 0 || p->hidden <= 0 || p->intermediate <= 0) return MOE_ERR_SHAPE;
@@ -203,8 +196,6 @@ moe_status check_mat(const moe_mat& m, int64_t cols, bool routed, int elem_bytes
   if (hb && routed && (m.expert_stride < 0 || (m.expert_stride * elem_bytes) % 16)) return MOE_ERR_LAYOUT;
   return MOE_OK;
 }
-
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // E8M0 scale matrices are read 4 bytes at a time: row stride and base 4-byte aligned.
 moe_status check_scale(const moe_mat& m, int64_t cols) {
@@ -331,51 +322,6 @@ GradRef gradref(const moe_grad& g) {
   r.row_offset = g.row_offset;
   return r;
 }
-
-// ---------------------------------------------------------------- kernel timer
-struct TimedLaunch {
-  const char* name;
-  hipEvent_t a, b;
-};
-struct Timer {
-  bool on = false;
-  std::vector<TimedLaunch> pending;
-  std::vector<hipEvent_t> pool;
-  std::vector<std::string> names;
-  std::vector<int> counts;
-  std::vector<double> ms;
-  std::mutex mu;
-  hipEvent_t get() {
-    if (!pool.empty()) { hipEvent_t e = pool.back(); pool.pop_back(); return e; }
-    hipEvent_t e = nullptr;
-    if (hipEventCreate(&e) != hipSuccess) return nullptr;
-    return e;
-  }
-};
-Timer g_timer;
-
-template <class F>
-moe_status launch(const char* name, hipStream_t st, F&& f) {
-  hipEvent_t a = nullptr, b = nullptr;
-  if (g_timer.on) {
-    a = g_timer.get();
-    b = g_timer.get();
-    if (a) (void)hipEventRecord(a, st);
-  }
-  f();
-  const hipError_t err = hipGetLastError();
-  if (g_timer.on && a && b) {
-    (void)hipEventRecord(b, st);
-    g_timer.pending.push_back({name, a, b});
-  }
-  return err == hipSuccess ? MOE_OK : MOE_ERR_HIP;
-}
-
-#define MOE_TRY(x)                        \
-  do {                                    \
-    const moe_status _s = (x);            \
-    if (_s != MOE_OK) return _s;          \
-  } while (0)
 
 // Token rows per M tile of the token-dimension GEMMs (one value per routed-weight type).
 int64_t tok_bm(const Dims& d) { return d.mx ? gemm::bm_of<true>() : gemm::bm_of<false>(); }
