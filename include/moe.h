@@ -300,6 +300,108 @@ moe_status moe_backward(const moe_problem* p, const void* grad_out, const void* 
                         float* grad_probs, const moe_main_grads* mg, void* workspace,
                         size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------- the router's decision
+ * From the router's logits to the [T][K] table that moe_forward_topk takes, and from
+ * the gradient of its weights (grad_probs of moe_backward with MOE_FLAG_TOPK_ROUTING) back
+ * to the logits.
+ *   s = softmax over the row's E logits (MOE_ROUTER_SOFTMAX) or sigmoid of each (MOE_ROUTER_SIGMOID)
+ *   chosen: the K largest s, or s + expert_bias when a bias is given (the bias takes part
+ *     in the choice only); descending, ties to the lowest expert index
+ *   w_k = scale * s_k / (sum of the chosen s + 1e-20) with MOE_ROUTER_NORMALIZE, else scale * s_k
+ * Scores and weights are FP32.  Without a bias the logits themselves are compared (the
+ * same order); s + expert_bias is compared in FP64.
+ * An expert whose logit is -inf is unavailable: it is never chosen and its score and
+ * gradient are 0.  A row with fewer than K available experts ends in -1 entries of weight 0
+ * (a row of only -inf has nothing else, and a zero gradient).  A NaN logit (or, with
+ * a bias, a NaN or -inf s + bias) is not chosen either, and any NaN in a row makes the
+ * weights of all its chosen experts NaN. */
+typedef enum { MOE_ROUTER_SOFTMAX = 1, MOE_ROUTER_SIGMOID = 2 } moe_router_score;
+#define MOE_ROUTER_NORMALIZE 1u
+typedef struct {
+  int64_t tokens;        /* T in [0, 2^30]                                                */
+  int32_t experts;       /* E in [1, 255]                                                 */
+  int32_t topk;          /* K in [1, min(8, E)]                                           */
+  int32_t score;         /* moe_router_score                                              */
+  int32_t logits_dtype;  /* MOE_FP32 or MOE_BF16, of logits and grad_logits               */
+  uint32_t flags;        /* MOE_ROUTER_NORMALIZE or 0                                     */
+  float scale;           /* finite                                                        */
+  int64_t ld_logits;     /* elements between rows of logits, >= E                         */
+} moe_router_problem;
+
+/*  logits          [T][E]
+ *  expert_bias     float [E], or NULL
+ *  top_experts     int32 [T][K], written
+ *  router_weights  float [T][K], written */
+moe_status moe_router_forward(const moe_router_problem* p, const void* logits, const float* expert_bias,
+                              int32_t* top_experts, float* router_weights, void* stream);
+
+/*  top_experts          the forward's table.  Entries outside [0, E) are skipped; an expert
+ *                       listed twice gets the sum of both gradients
+ *  grad_router_weights  float [T][K], not read at skipped entries' experts
+ *  grad_logits          [T][E], overwritten; rows ld_grad_logits >= E elements apart */
+moe_status moe_router_backward(const moe_router_problem* p, const void* logits, const int32_t* top_experts,
+                               const float* grad_router_weights, void* grad_logits, int64_t ld_grad_logits,
+                               void* stream);
+
+/* ------------------------------------------------------------------- norm
+ * Layer norm and RMS norm of rows, forward and backward: the norm in front of the layer,
+ * whose output is `hidden`.
+ *   v = x, or x + residual rounded to the storage type and written to `sum`
+ *   mean = sum v / cols (0 for MOE_NORM_RMS);  rstd = 1 / sqrt(sum (v - mean)^2 / cols + eps)
+ *   y = (v - mean) * rstd * weight (+ bias)
+ * Statistics and sums are FP32; y and grad_x are rounded once. */
+typedef enum { MOE_NORM_LAYER = 1, MOE_NORM_RMS = 2 } moe_norm_kind;
+/* Set: the backward overwrites grad_weight and grad_bias instead of accumulating. */
+#define MOE_NORM_OVERWRITE_GRADS 1u
+typedef struct {
+  int64_t rows;          /* in [0, 2^30]                                                  */
+  int64_t cols;          /* in [1, MOE_NORM_MAX_COLS]                                     */
+  int32_t kind;          /* moe_norm_kind                                                 */
+  int32_t dtype;         /* MOE_BF16 or MOE_FP32: x, residual, sum, y and their gradients */
+  int32_t param_dtype;   /* MOE_BF16 or MOE_FP32: weight and bias                         */
+  int32_t grad_dtype;    /* MOE_FP32 or MOE_BF16: grad_weight and grad_bias               */
+  uint32_t flags;        /* MOE_NORM_OVERWRITE_GRADS or 0                                 */
+  float eps;             /* finite, >= 0                                                  */
+} moe_norm_problem;
+#define MOE_NORM_MAX_COLS 16384
+
+/* A matrix [rows][cols] of the problem's dtype, rows `ld` >= cols elements apart.  Any
+ * element-aligned base and any ld are taken; rows that are all 16-byte aligned (and cols a
+ * multiple of 8) are read and written in 16-byte pieces. */
+typedef struct {
+  void* base;
+  int64_t ld;
+} moe_rows;
+
+/*  x, residual  residual may be NULL; with it `sum` is required, without it `sum` must be NULL
+ *  weight, bias [cols], bias may be NULL
+ *  sum          written: the row that was normalised.  May be x or residual itself (same
+ *               base and ld); no other output may overlap an input
+ *  y            written
+ *  stats        float [rows][2], written: mean and rstd, for the backward; NULL if not needed */
+moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const moe_rows* residual,
+                            const void* weight, const void* bias, const moe_rows* sum, const moe_rows* y,
+                            float* stats, void* stream);
+
+/* Workspace bytes of moe_norm_backward (0 on invalid input): the column sums of up to 256
+ * groups of rows.  The size does not depend on rows beyond that. */
+size_t moe_norm_workspace_bytes(const moe_norm_problem* p);
+
+/* Backward of sum(grad_y * y) + sum(grad_sum * sum).
+ *  x            what was normalised: the forward's x, or its sum if a residual was given
+ *  stats        the forward's
+ *  grad_sum     gradient that reaches `sum` (or x) past the norm; NULL if none
+ *  grad_x       overwritten: the gradient of x, and of residual, which share it
+ *  grad_weight, grad_bias  [cols], accumulated (or overwritten, see the flag): FP32, or BF16
+ *               with the rounding of a BF16 main_grad (the call's contribution is rounded
+ *               before it is added).  Either may be NULL and is then not computed
+ *  workspace    moe_norm_workspace_bytes(p); may be NULL when both gradients are
+ * Sums over rows run in a fixed order: the same call gives the same bits. */
+moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, const moe_rows* x,
+                             const void* weight, const float* stats, const moe_rows* grad_sum,
+                             const moe_rows* grad_x, void* grad_weight, void* grad_bias, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* A static description of a status code. */
 const char* moe_status_str(moe_status s);
 

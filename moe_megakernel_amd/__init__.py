@@ -24,10 +24,17 @@ MOE_FLAG_HAS_SHARED = 1
 MOE_FLAG_RECOMPUTE = 2
 MOE_FLAG_TOPK_ROUTING = 4
 MOE_FLAG_SHARED_GATE = 8
+MOE_ROUTER_SOFTMAX, MOE_ROUTER_SIGMOID = 1, 2
+MOE_ROUTER_NORMALIZE = 1
+MOE_NORM_LAYER, MOE_NORM_RMS = 1, 2
+MOE_NORM_OVERWRITE_GRADS = 1
+MOE_NORM_MAX_COLS = 16384
 
 EXPORTED = ("moe_saved_bytes", "moe_workspace_bytes", "moe_saved_view", "moe_forward",
             "moe_forward_topk", "moe_forward_noalloc", "moe_backward", "moe_status_str",
-            "moe_kernel_timer_enable", "moe_kernel_timer_read", "moe_mx_staging_view")
+            "moe_kernel_timer_enable", "moe_kernel_timer_read", "moe_mx_staging_view",
+            "moe_router_forward", "moe_router_backward", "moe_norm_forward", "moe_norm_backward",
+            "moe_norm_workspace_bytes")
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -73,6 +80,22 @@ class moe_mx_staging_layout(C.Structure):
                                           "dy_codes", "dy_scales", "dfc1_codes", "dfc1_scales")]
 
 
+class moe_router_problem(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("experts", C.c_int32), ("topk", C.c_int32), ("score", C.c_int32),
+                ("logits_dtype", C.c_int32), ("flags", C.c_uint32), ("scale", C.c_float),
+                ("ld_logits", C.c_int64)]
+
+
+class moe_norm_problem(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("kind", C.c_int32), ("dtype", C.c_int32),
+                ("param_dtype", C.c_int32), ("grad_dtype", C.c_int32), ("flags", C.c_uint32),
+                ("eps", C.c_float)]
+
+
+class moe_rows(C.Structure):
+    _fields_ = [("base", C.c_void_p), ("ld", C.c_int64)]
+
+
 _lib = None
 
 
@@ -112,6 +135,19 @@ def load(path: str | None = None):
     lib.moe_kernel_timer_read.restype = C.c_int
     lib.moe_mx_staging_view.argtypes = [P(moe_problem), P(moe_mx_staging_layout)]
     lib.moe_mx_staging_view.restype = C.c_int
+    lib.moe_router_forward.argtypes = [P(moe_router_problem)] + [C.c_void_p] * 5
+    lib.moe_router_forward.restype = C.c_int
+    lib.moe_router_backward.argtypes = [P(moe_router_problem)] + [C.c_void_p] * 4 + [C.c_int64, C.c_void_p]
+    lib.moe_router_backward.restype = C.c_int
+    lib.moe_norm_forward.argtypes = [P(moe_norm_problem), P(moe_rows), P(moe_rows), C.c_void_p, C.c_void_p,
+                                     P(moe_rows), P(moe_rows), C.c_void_p, C.c_void_p]
+    lib.moe_norm_forward.restype = C.c_int
+    lib.moe_norm_backward.argtypes = [P(moe_norm_problem), P(moe_rows), P(moe_rows), C.c_void_p, C.c_void_p,
+                                      P(moe_rows), P(moe_rows), C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
+                                      C.c_void_p]
+    lib.moe_norm_backward.restype = C.c_int
+    lib.moe_norm_workspace_bytes.argtypes = [P(moe_norm_problem)]
+    lib.moe_norm_workspace_bytes.restype = C.c_size_t
     if path is None:
         _lib = lib
     return lib
@@ -176,6 +212,40 @@ def moe_backward(p, grad_out, hidden, weights, saved, grad_hidden, grad_probs, m
                  workspace_bytes, stream) -> int:
     return load().moe_backward(C.byref(p), grad_out, hidden, C.byref(weights), saved, grad_hidden,
                                grad_probs, C.byref(main_grads), workspace, workspace_bytes, stream)
+
+
+def moe_router_forward(p, logits, expert_bias, top_experts, router_weights, stream) -> int:
+    """Raw call with integer device addresses; returns the status."""
+    return load().moe_router_forward(C.byref(p), logits, expert_bias, top_experts, router_weights, stream)
+
+
+def moe_router_backward(p, logits, top_experts, grad_router_weights, grad_logits, ld_grad_logits, stream) -> int:
+    """Raw call with integer device addresses; returns the status."""
+    return load().moe_router_backward(C.byref(p), logits, top_experts, grad_router_weights, grad_logits,
+                                      ld_grad_logits, stream)
+
+
+def _ref(rows):
+    return None if rows is None else C.byref(rows)
+
+
+def moe_norm_workspace_bytes(p: moe_norm_problem) -> int:
+    return int(load().moe_norm_workspace_bytes(C.byref(p)))
+
+
+def moe_norm_forward(p, x, residual, weight, bias, sum, y, stats, stream) -> int:
+    """Raw call: x, residual, sum and y are moe_rows (or None), the rest integer device
+    addresses; returns the status."""
+    return load().moe_norm_forward(C.byref(p), _ref(x), _ref(residual), weight, bias, _ref(sum), _ref(y), stats,
+                                   stream)
+
+
+def moe_norm_backward(p, grad_y, x, weight, stats, grad_sum, grad_x, grad_weight, grad_bias, workspace,
+                      workspace_bytes, stream) -> int:
+    """Raw call: grad_y, x, grad_sum and grad_x are moe_rows (or None), the rest integer
+    device addresses; returns the status."""
+    return load().moe_norm_backward(C.byref(p), _ref(grad_y), _ref(x), weight, stats, _ref(grad_sum), _ref(grad_x),
+                                    grad_weight, grad_bias, workspace, workspace_bytes, stream)
 
 
 def moe_kernel_timer_enable(on: bool) -> None:
@@ -294,3 +364,170 @@ class Layer:
             "slot_token": view(L.slot_token, T * K, torch.int32),
             "status_word": view(L.status_word, 1, torch.int32),
         }
+
+
+# ------------------------------------------------------------------ operators around the layer
+def _moe_dtype(dt, where: str) -> int:
+    import torch
+    code = {torch.bfloat16: MOE_BF16, torch.float32: MOE_FP32}.get(dt)
+    if code is None:
+        raise MoeError(MOE_ERR_DTYPE, where)
+    return code
+
+
+def _check(where, device, t, dtype, shape):
+    """t: a tensor of this dtype and shape on `device` (the first tensor's) whose last
+    dimension is dense.  A host tensor's address must never reach a kernel."""
+    if t is None:
+        raise MoeError(MOE_ERR_NULL, where)
+    if t.dtype != dtype:
+        raise MoeError(MOE_ERR_DTYPE, where)
+    if tuple(t.shape) != shape:
+        raise MoeError(MOE_ERR_SHAPE, where)
+    if not t.is_cuda or t.device != device or (t.stride(-1) != 1 and shape[-1] > 1):
+        raise MoeError(MOE_ERR_LAYOUT, where)
+
+
+def _check_dense(where, device, t, dtype, shape):
+    _check(where, device, t, dtype, shape)
+    if not t.is_contiguous():
+        raise MoeError(MOE_ERR_LAYOUT, where)
+
+
+def _ld(t) -> int:
+    """Elements between rows; a single row's stride means nothing."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _call(where, device, f):
+    """f(stream) on torch's current stream of `device`, with that device current."""
+    import torch
+    if device.index is None or device.index == torch.cuda.current_device():
+        st = f(current_stream())
+    else:
+        with torch.cuda.device(device):
+            st = f(current_stream())
+    if st != MOE_OK:
+        raise MoeError(st, where)
+
+
+class Router:
+    """The router's decision on logits [tokens, experts] (torch tensors, FP32 or BF16): the
+    table moe_forward_topk and DecodeLayer take, and the gradient back to the logits.
+    Holds options only; every buffer is the caller's."""
+
+    def __init__(self, experts, topk, score="softmax", normalize=False, scale=1.0, dtype=None):
+        import torch
+        self.dtype = dtype or torch.float32
+        kind = {"softmax": MOE_ROUTER_SOFTMAX, "sigmoid": MOE_ROUTER_SIGMOID}.get(score, 0)
+        self.p = moe_router_problem(0, experts, topk, kind, _moe_dtype(self.dtype, "Router"),
+                                    MOE_ROUTER_NORMALIZE if normalize else 0, scale, experts)
+        st = moe_router_forward(self.p, None, None, None, None, None)    # no tokens: checks the options
+        if st != MOE_OK:
+            raise MoeError(st, "Router")
+
+    def _problem(self, where, logits):
+        if logits is None:
+            raise MoeError(MOE_ERR_NULL, where)
+        if logits.dim() != 2:
+            raise MoeError(MOE_ERR_SHAPE, where)
+        T, q = logits.shape[0], self.p
+        _check(where, logits.device, logits, self.dtype, (T, q.experts))
+        p = moe_router_problem(T, q.experts, q.topk, q.score, q.logits_dtype, q.flags, q.scale, _ld(logits))
+        return T, p
+
+    def forward(self, logits, top_experts, router_weights, expert_bias=None):
+        """Writes top_experts (int32) and router_weights (float32), both [tokens, topk]."""
+        import torch
+        where, dev = "moe_router_forward", getattr(logits, "device", None)
+        T, p = self._problem(where, logits)
+        _check_dense(where, dev, top_experts, torch.int32, (T, p.topk))
+        _check_dense(where, dev, router_weights, torch.float32, (T, p.topk))
+        if expert_bias is not None:
+            _check_dense(where, dev, expert_bias, torch.float32, (p.experts,))
+        _call(where, dev, lambda s: moe_router_forward(p, _ptr(logits), _ptr(expert_bias), _ptr(top_experts),
+                                                       _ptr(router_weights), s))
+        return top_experts, router_weights
+
+    def backward(self, logits, top_experts, grad_router_weights, grad_logits):
+        """Writes grad_logits [tokens, experts] in the logits' dtype."""
+        import torch
+        where, dev = "moe_router_backward", getattr(logits, "device", None)
+        T, p = self._problem(where, logits)
+        _check_dense(where, dev, top_experts, torch.int32, (T, p.topk))
+        _check_dense(where, dev, grad_router_weights, torch.float32, (T, p.topk))
+        _check(where, dev, grad_logits, self.dtype, (T, p.experts))
+        _call(where, dev, lambda s: moe_router_backward(p, _ptr(logits), _ptr(top_experts),
+                                                        _ptr(grad_router_weights), _ptr(grad_logits),
+                                                        _ld(grad_logits), s))
+        return grad_logits
+
+
+class Norm:
+    """Layer norm (kind "layer") or RMS norm ("rms") of rows [rows, cols].  Holds the options
+    and the backward's workspace (its size covers any number of rows); two backward calls
+    of one Norm must not overlap on the GPU."""
+
+    def __init__(self, cols, kind="layer", eps=1e-5, dtype=None, param_dtype=None, grad_dtype=None, device="cuda"):
+        import torch
+        self.dtype = dtype or torch.bfloat16
+        self.param_dtype = param_dtype or self.dtype
+        self.grad_dtype = grad_dtype or torch.float32
+        code = {"layer": MOE_NORM_LAYER, "rms": MOE_NORM_RMS}.get(kind, 0)
+        self.p = moe_norm_problem(1 << 30, cols, code, _moe_dtype(self.dtype, "Norm"),
+                                  _moe_dtype(self.param_dtype, "Norm"), _moe_dtype(self.grad_dtype, "Norm"), 0, eps)
+        self.ws_bytes = moe_norm_workspace_bytes(self.p)
+        if self.ws_bytes == 0:
+            raise MoeError(MOE_ERR_SHAPE if kind in ("layer", "rms") else MOE_ERR_UNSUPPORTED, "Norm")
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+
+    def _problem(self, where, x, flags=0):
+        if x is None:
+            raise MoeError(MOE_ERR_NULL, where)
+        if x.dim() != 2:
+            raise MoeError(MOE_ERR_SHAPE, where)
+        q = self.p
+        p = moe_norm_problem(x.shape[0], q.cols, q.kind, q.dtype, q.param_dtype, q.grad_dtype, flags, q.eps)
+        return p, (x.shape[0], q.cols)
+
+    def _rows(self, where, device, t, shape):
+        _check(where, device, t, self.dtype, shape)
+        return moe_rows(_ptr(t), _ld(t))
+
+    def forward(self, x, weight, bias, y, stats=None, residual=None, sum=None):
+        """y = norm(x) or, with residual, sum = x + residual and y = norm(sum).  stats: float32
+        [rows, 2], what backward needs."""
+        import torch
+        where, dev = "moe_norm_forward", getattr(x, "device", None)
+        p, shape = self._problem(where, x)
+        rows = [None if t is None else self._rows(where, dev, t, shape) for t in (residual, sum)]
+        rx, ry = self._rows(where, dev, x, shape), self._rows(where, dev, y, shape)
+        _check_dense(where, dev, weight, self.param_dtype, (shape[1],))
+        if bias is not None:
+            _check_dense(where, dev, bias, self.param_dtype, (shape[1],))
+        if stats is not None:
+            _check_dense(where, dev, stats, torch.float32, (shape[0], 2))
+        _call(where, dev, lambda s: moe_norm_forward(p, rx, rows[0], _ptr(weight), _ptr(bias), rows[1], ry,
+                                                     _ptr(stats), s))
+        return y
+
+    def backward(self, grad_y, x, weight, stats, grad_x, grad_weight=None, grad_bias=None, grad_sum=None,
+                 overwrite=False):
+        """x: what was normalised (the forward's sum if it took a residual).  grad_weight and
+        grad_bias [cols] are accumulated, or overwritten."""
+        import torch
+        where, dev = "moe_norm_backward", getattr(x, "device", None)
+        p, shape = self._problem(where, x, MOE_NORM_OVERWRITE_GRADS if overwrite else 0)
+        rx, rdy, rdx = (self._rows(where, dev, t, shape) for t in (x, grad_y, grad_x))
+        rgs = None if grad_sum is None else self._rows(where, dev, grad_sum, shape)
+        _check_dense(where, dev, weight, self.param_dtype, (shape[1],))
+        _check_dense(where, dev, stats, torch.float32, (shape[0], 2))
+        for g in (grad_weight, grad_bias):
+            if g is not None:
+                _check_dense(where, dev, g, self.grad_dtype, (shape[1],))
+        if self.workspace.device != dev:
+            raise MoeError(MOE_ERR_WORKSPACE, where)
+        _call(where, dev, lambda s: moe_norm_backward(p, rdy, rx, _ptr(weight), _ptr(stats), rgs, rdx,
+                                                      _ptr(grad_weight), _ptr(grad_bias), _ptr(self.workspace),
+                                                      self.ws_bytes, s))
+        return grad_x

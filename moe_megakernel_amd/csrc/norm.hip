@@ -1,0 +1,495 @@
+// Layer norm and RMS norm of rows, forward and backward (C ABI: moe_norm_forward,
+// moe_norm_backward).
+//
+// Each row is held in the registers of `tpr` threads (a multiple of 64, 16 elements a
+// thread), so x is read once and every statistic is taken from registers:
+//   m = sum x / N;  d = x - m;  delta = sum d / N;  var = sum d^2 / N - delta^2
+// mean = m + delta.  The second pass over the registers removes what rounding m cost: with
+// m already close, delta is tiny and var has no cancellation.
+//
+// Backward, with xh = (x - mean) rstd and g = dy w:
+//   dx = rstd (g - sum(g) / N - xh sum(g xh) / N)    (RMS norm: without the sum(g) term)
+//   dw = sum over rows of dy xh,   db = sum over rows of dy
+// A workgroup walks rows and keeps its columns' dw and db in registers; the row groups
+// of a workgroup are joined in LDS, workgroups write one partial row each, and a second
+// kernel adds the partials in a fixed order.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/moe.h"
+#include "common.hpp"
+#include "host.hpp"
+#include "reduce.hpp"
+
+using namespace moe;
+
+namespace {
+
+constexpr int kEpt = 16;              // elements per thread
+constexpr int kNormThreads = 1024;    // largest workgroup
+constexpr int kNormGroups = 256;      // workgroups of the backward (partial rows): one per CU
+constexpr int kFinalCols = 32;        // columns per workgroup of the second kernel
+
+struct Rows {
+  uint8_t* base;
+  int64_t ld;      // elements
+};
+
+struct NormArgs {
+  Rows x, res, sum, y;      // forward
+  Rows dy, gsum, dx;        // backward (x: what was normalised)
+  const void *w, *b;
+  float* stats;
+  float* part;              // backward: [groups][nsum][cols]
+  int64_t rows;
+  int N;                    // cols
+  int tpr;                  // threads per row
+  int rms, wbf16;
+  int want_dw, want_db;
+  float eps;
+};
+
+// Columns of a thread: VEC (rows 16-byte aligned, N % 8 == 0) two pieces of 8 elements at
+// pieces j and j + tpr; otherwise single elements j + i tpr.  col < 0: past the end.
+template <bool VEC>
+__device__ __forceinline__ int col_of(int j, int i, int tpr) {
+  return VEC ? 8 * (j + (i >> 3) * tpr) + (i & 7) : j + i * tpr;
+}
+
+template <bool VEC, bool BF16>
+struct Raw;   // a thread's part of a row as loaded
+template <>
+struct Raw<true, true> { uint4 q[2]; };
+template <>
+struct Raw<true, false> { float4 q[4]; };
+template <>
+struct Raw<false, true> { uint16_t q[16]; };
+template <>
+struct Raw<false, false> { float q[16]; };
+
+template <bool VEC, bool BF16>
+__device__ __forceinline__ Raw<VEC, BF16> ld_row(const Rows& m, int64_t r, int j, int tpr, int N) {
+  Raw<VEC, BF16> v;
+  const uint8_t* p = m.base + r * m.ld * (BF16 ? 2 : 4);
+  if constexpr (VEC) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int c = 8 * (j + u * tpr);
+      if constexpr (BF16) {
+        v.q[u] = c < N ? *reinterpret_cast<const uint4*>(p + 2 * c) : make_uint4(0, 0, 0, 0);
+      } else {
+        const float4 z = make_float4(0, 0, 0, 0);
+        v.q[2 * u] = c < N ? *reinterpret_cast<const float4*>(p + 4 * c) : z;
+        v.q[2 * u + 1] = c < N ? *reinterpret_cast<const float4*>(p + 4 * c + 16) : z;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEpt; ++i) {
+      const int c = j + i * tpr;
+      if constexpr (BF16) v.q[i] = c < N ? reinterpret_cast<const uint16_t*>(p)[c] : (uint16_t)0;
+      else v.q[i] = c < N ? reinterpret_cast<const float*>(p)[c] : 0.0f;
+    }
+  }
+  return v;
+}
+
+template <bool VEC, bool BF16>
+__device__ __forceinline__ void unpack(const Raw<VEC, BF16>& v, float (&f)[kEpt]) {
+  if constexpr (VEC && BF16) {
+    unpack_bf16x8(v.q[0], f);
+    unpack_bf16x8(v.q[1], f + 8);
+  } else if constexpr (VEC) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      f[4 * u] = v.q[u].x; f[4 * u + 1] = v.q[u].y; f[4 * u + 2] = v.q[u].z; f[4 * u + 3] = v.q[u].w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEpt; ++i) {
+      if constexpr (BF16) f[i] = bf2f(v.q[i]);
+      else f[i] = v.q[i];
+    }
+  }
+}
+
+template <bool VEC, bool BF16>
+__device__ __forceinline__ void st_row(const Rows& m, int64_t r, int j, int tpr, int N, const float (&f)[kEpt]) {
+  uint8_t* p = m.base + r * m.ld * (BF16 ? 2 : 4);
+  if constexpr (VEC) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int c = 8 * (j + u * tpr);
+      if (c >= N) continue;
+      const float* s = f + 8 * u;
+      if constexpr (BF16) {
+        *reinterpret_cast<uint4*>(p + 2 * c) = make_uint4(pack_bf2(s[0], s[1]), pack_bf2(s[2], s[3]),
+                                                          pack_bf2(s[4], s[5]), pack_bf2(s[6], s[7]));
+      } else {
+        *reinterpret_cast<float4*>(p + 4 * c) = make_float4(s[0], s[1], s[2], s[3]);
+        *reinterpret_cast<float4*>(p + 4 * c + 16) = make_float4(s[4], s[5], s[6], s[7]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEpt; ++i) {
+      const int c = j + i * tpr;
+      if (c >= N) continue;
+      if constexpr (BF16) reinterpret_cast<uint16_t*>(p)[c] = (uint16_t)f2bf(f[i]);
+      else reinterpret_cast<float*>(p)[c] = f[i];
+    }
+  }
+}
+
+// weight or bias of a thread's columns (0 past the end)
+template <bool VEC>
+__device__ __forceinline__ void ld_param(const void* w, int bf16, int j, int tpr, int N, float (&f)[kEpt]) {
+#pragma unroll
+  for (int i = 0; i < kEpt; ++i) {
+    const int c = col_of<VEC>(j, i, tpr);
+    f[i] = c < N ? (bf16 ? bf2f(static_cast<const uint16_t*>(w)[c]) : static_cast<const float*>(w)[c]) : 0.0f;
+  }
+}
+
+// Sums of a and b over the `nw` waves of a row group, every thread of it gets both: the
+// waves in order.  `red` holds two floats per wave of the workgroup and call parity, so
+// one barrier a call is enough (a slot is rewritten two calls later, behind the next
+// call's barrier).
+__device__ __forceinline__ void group_sum2(float& a, float& b, int nw, float2* red, int parity) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if (nw == 1) return;
+  const int w = threadIdx.x >> 6;
+  float2* slot = red + parity * (kNormThreads / 64);
+  if ((threadIdx.x & 63) == 0) slot[w] = make_float2(a, b);
+  __syncthreads();
+  const int w0 = w - w % nw;
+  a = b = 0.0f;
+  for (int q = 0; q < nw; ++q) {
+    const float2 v = slot[w0 + q];
+    a += v.x;
+    b += v.y;
+  }
+}
+
+// Forward: blockDim.x = row groups * tpr, the groups walk rows with a common trip count
+// (the barriers are the workgroup's).
+template <bool VEC, bool BF16>
+__global__ __launch_bounds__(kNormThreads) void k_norm_fwd(NormArgs a) {
+  __shared__ float2 red[2 * (kNormThreads / 64)];
+  const int tpr = a.tpr, N = a.N, nw = tpr >> 6;
+  const int j = threadIdx.x % tpr;
+  const int rg = threadIdx.x / tpr, ng = blockDim.x / tpr;
+  float w[kEpt], b[kEpt];
+  ld_param<VEC>(a.w, a.wbf16, j, tpr, N, w);
+#pragma unroll
+  for (int i = 0; i < kEpt; ++i) b[i] = 0.0f;
+  if (a.b) ld_param<VEC>(a.b, a.wbf16, j, tpr, N, b);
+  const float inv_n = 1.0f / (float)N;
+  int parity = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * ng; r0 < a.rows; r0 += (int64_t)gridDim.x * ng) {
+    const int64_t r = r0 + rg;
+    const bool on = r < a.rows;
+    float v[kEpt];
+#pragma unroll
+    for (int i = 0; i < kEpt; ++i) v[i] = 0.0f;
+    if (on) {
+      unpack<VEC, BF16>(ld_row<VEC, BF16>(a.x, r, j, tpr, N), v);
+      if (a.res.base) {
+        float q[kEpt];
+        unpack<VEC, BF16>(ld_row<VEC, BF16>(a.res, r, j, tpr, N), q);
+#pragma unroll
+        for (int i = 0; i < kEpt; ++i) {
+          v[i] += q[i];
+          if constexpr (BF16) v[i] = bf2f(f2bf(v[i]));
+        }
+        st_row<VEC, BF16>(a.sum, r, j, tpr, N, v);
+      }
+    }
+    float mean = 0.0f, s = 0.0f, s2 = 0.0f;
+    if (!a.rms) {
+#pragma unroll
+      for (int i = 0; i < kEpt; ++i) s += v[i];
+      group_sum2(s, s2, nw, red, parity);
+      parity ^= 1;
+      mean = s / (float)N;
+    }
+    s = s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEpt; ++i) {
+      v[i] = col_of<VEC>(j, i, tpr) < N ? v[i] - mean : 0.0f;
+      s += v[i];
+      s2 += v[i] * v[i];
+    }
+    group_sum2(s, s2, nw, red, parity);
+    parity ^= 1;
+    const float delta = a.rms ? 0.0f : s * inv_n;
+    const float rstd = 1.0f / sqrtf(s2 / (float)N - delta * delta + a.eps);
+    if (on) {
+      if (a.stats && j == 0) reinterpret_cast<float2*>(a.stats)[r] = make_float2(mean + delta, rstd);
+#pragma unroll
+      for (int i = 0; i < kEpt; ++i) v[i] = (v[i] - delta) * rstd * w[i] + b[i];
+      st_row<VEC, BF16>(a.y, r, j, tpr, N, v);
+    }
+  }
+}
+
+template <bool VEC, bool BF16>
+__global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
+  extern __shared__ float join[];                        // [ng - 1][tpr * kEpt], reused
+  __shared__ float2 red[2 * (kNormThreads / 64)];
+  const int tpr = a.tpr, N = a.N, nw = tpr >> 6;
+  const int j = threadIdx.x % tpr;
+  const int rg = threadIdx.x / tpr, ng = blockDim.x / tpr;
+  float w[kEpt], dw[kEpt], db[kEpt];
+  ld_param<VEC>(a.w, a.wbf16, j, tpr, N, w);
+#pragma unroll
+  for (int i = 0; i < kEpt; ++i) dw[i] = db[i] = 0.0f;
+  const float inv_n = 1.0f / (float)N;
+  int parity = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * ng; r0 < a.rows; r0 += (int64_t)gridDim.x * ng) {
+    const int64_t r = r0 + rg;
+    const bool on = r < a.rows;
+    float xh[kEpt], g[kEpt], rstd = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEpt; ++i) xh[i] = g[i] = 0.0f;
+    if (on) {
+      unpack<VEC, BF16>(ld_row<VEC, BF16>(a.x, r, j, tpr, N), xh);
+      unpack<VEC, BF16>(ld_row<VEC, BF16>(a.dy, r, j, tpr, N), g);
+      const float2 st = reinterpret_cast<const float2*>(a.stats)[r];
+      rstd = st.y;
+#pragma unroll
+      for (int i = 0; i < kEpt; ++i) xh[i] = col_of<VEC>(j, i, tpr) < N ? (xh[i] - st.x) * rstd : 0.0f;
+    }
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEpt; ++i) {
+      dw[i] += g[i] * xh[i];
+      db[i] += g[i];
+      g[i] *= w[i];
+      s1 += g[i];
+      s2 += g[i] * xh[i];
+    }
+    group_sum2(s1, s2, nw, red, parity);
+    parity ^= 1;
+    if (on) {
+      const float m1 = a.rms ? 0.0f : s1 * inv_n, m2 = s2 * inv_n;
+#pragma unroll
+      for (int i = 0; i < kEpt; ++i) g[i] = rstd * (g[i] - m1 - xh[i] * m2);
+      if (a.gsum.base) {
+        unpack<VEC, BF16>(ld_row<VEC, BF16>(a.gsum, r, j, tpr, N), xh);
+#pragma unroll
+        for (int i = 0; i < kEpt; ++i) g[i] += xh[i];
+      }
+      st_row<VEC, BF16>(a.dx, r, j, tpr, N, g);
+    }
+  }
+  if (!a.part) return;
+  // join the row groups in order, then one partial row of this workgroup
+  const int nsum = a.want_dw + a.want_db;
+  float* out = a.part + (int64_t)blockIdx.x * nsum * N;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if (!(which ? a.want_db : a.want_dw)) continue;
+    if (ng > 1) {
+      __syncthreads();
+      if (rg > 0) {
+#pragma unroll
+        for (int i = 0; i < kEpt; ++i) join[((rg - 1) * kEpt + i) * tpr + j] = which ? db[i] : dw[i];
+      }
+      __syncthreads();
+    }
+    if (rg == 0) {
+#pragma unroll
+      for (int i = 0; i < kEpt; ++i) {
+        float v = which ? db[i] : dw[i];
+        for (int q = 0; q < ng - 1; ++q) v += join[(q * kEpt + i) * tpr + j];
+        const int c = col_of<VEC>(j, i, tpr);
+        if (c < N) out[(which && a.want_dw ? N : 0) + c] = v;
+      }
+    }
+  }
+}
+
+// grad[c] (+)= sum over the partial rows: kFinalCols columns a workgroup, 8 lanes of
+// rows per column joined in order.
+__global__ __launch_bounds__(256) void k_norm_bwd_final(const float* __restrict__ part, int groups, int width,
+                                                        int N, uint8_t* g0, uint8_t* g1, int bf16, int overwrite) {
+  __shared__ float red[8][kFinalCols];
+  const int cl = threadIdx.x % kFinalCols, q = threadIdx.x / kFinalCols;
+  const int c = blockIdx.x * kFinalCols + cl;
+  float v = 0.0f;
+  if (c < width)
+    for (int p = q; p < groups; p += 8) v += part[(int64_t)p * width + c];
+  red[q][cl] = v;
+  __syncthreads();
+  if (q != 0 || c >= width) return;
+  v = red[0][cl];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v += red[i][cl];
+  uint8_t* dst = c < N ? g0 : g1;
+  const int cc = c < N ? c : c - N;
+  if (bf16) {
+    uint16_t* o = reinterpret_cast<uint16_t*>(dst) + cc;
+    float r = bf2f(f2bf(v));
+    if (!overwrite) r = bf2f(*o) + r;
+    *o = (uint16_t)f2bf(r);
+  } else {
+    float* o = reinterpret_cast<float*>(dst) + cc;
+    *o = overwrite ? v : *o + v;
+  }
+}
+
+// ---------------------------------------------------------------- host side
+moe_status check_norm(const moe_norm_problem* p) {
+  if (!p) return MOE_ERR_NULL;
+  if (p->rows < 0 || p->rows > ((int64_t)1 << 30)) return MOE_ERR_SHAPE;
+  if (p->cols < 1 || p->cols > MOE_NORM_MAX_COLS) return MOE_ERR_SHAPE;
+  if (p->kind != MOE_NORM_LAYER && p->kind != MOE_NORM_RMS) return MOE_ERR_UNSUPPORTED;
+  for (int32_t d : {p->dtype, p->param_dtype, p->grad_dtype})
+    if (d != MOE_BF16 && d != MOE_FP32) return MOE_ERR_DTYPE;
+  if (p->flags & ~MOE_NORM_OVERWRITE_GRADS) return MOE_ERR_UNSUPPORTED;
+  if (!(p->eps >= 0.0f && p->eps < 3.0e38f)) return MOE_ERR_UNSUPPORTED;   // NaN, < 0, infinite
+  return MOE_OK;
+}
+
+bool elem_aligned(const void* q, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(q) & (dtype == MOE_BF16 ? 1u : 3u)) == 0;
+}
+
+moe_status check_rows(const moe_norm_problem* p, const moe_rows* m) {
+  if (!m || (p->rows > 0 && !m->base)) return MOE_ERR_NULL;
+  if (m->ld < p->cols || m->ld > ((int64_t)1 << 40) || !elem_aligned(m->base, p->dtype)) return MOE_ERR_LAYOUT;
+  return MOE_OK;
+}
+
+// every row 16-byte aligned (m: an optional matrix may be null)
+bool rows16(const moe_norm_problem* p, const moe_rows* m) {
+  return !m || (aligned16(m->base) && (m->ld * (p->dtype == MOE_BF16 ? 2 : 4)) % 16 == 0);
+}
+
+Rows rows_of(const moe_rows* m) { return m ? Rows{static_cast<uint8_t*>(m->base), m->ld} : Rows{nullptr, 0}; }
+
+int threads_per_row(int64_t cols) { return 64 * (int)((cols + 64 * kEpt - 1) / (64 * kEpt)); }
+
+NormArgs norm_args(const moe_norm_problem* p) {
+  NormArgs a{};
+  a.rows = p->rows;
+  a.N = (int)p->cols;
+  a.tpr = threads_per_row(p->cols);
+  a.rms = p->kind == MOE_NORM_RMS;
+  a.wbf16 = p->param_dtype == MOE_BF16;
+  a.eps = p->eps;
+  return a;
+}
+
+template <class F>
+void with_variant(bool vec, bool bf16, F&& f) {
+  if (vec && bf16) f(std::true_type{}, std::true_type{});
+  else if (vec) f(std::true_type{}, std::false_type{});
+  else if (bf16) f(std::false_type{}, std::true_type{});
+  else f(std::false_type{}, std::false_type{});
+}
+
+// Row groups per backward workgroup: as many as 1024 threads hold, no more than the rows.
+int bwd_row_groups(const NormArgs& a) {
+  const int64_t fit = kNormThreads / a.tpr;
+  return (int)(a.rows < fit ? (a.rows > 0 ? a.rows : 1) : fit);
+}
+int bwd_groups(const NormArgs& a) {
+  const int64_t ng = bwd_row_groups(a), need = (a.rows + ng - 1) / ng;
+  return (int)(need < kNormGroups ? need : kNormGroups);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const moe_rows* residual,
+                            const void* weight, const void* bias, const moe_rows* sum, const moe_rows* y,
+                            float* stats, void* stream) {
+  MOE_TRY(check_norm(p));
+  MOE_TRY(check_rows(p, x));
+  MOE_TRY(check_rows(p, y));
+  if ((residual != nullptr) != (sum != nullptr)) return residual ? MOE_ERR_NULL : MOE_ERR_LAYOUT;
+  if (residual) {
+    MOE_TRY(check_rows(p, residual));
+    MOE_TRY(check_rows(p, sum));
+  }
+  if (!weight) return MOE_ERR_NULL;
+  if (!elem_aligned(weight, p->param_dtype) || !elem_aligned(bias, p->param_dtype)) return MOE_ERR_LAYOUT;
+  if (reinterpret_cast<uintptr_t>(stats) & 7u) return MOE_ERR_LAYOUT;
+  if (p->rows == 0) return MOE_OK;
+  NormArgs a = norm_args(p);
+  a.x = rows_of(x); a.res = rows_of(residual); a.sum = rows_of(sum); a.y = rows_of(y);
+  a.w = weight; a.b = bias;
+  a.stats = stats;
+  const bool vec = p->cols % 8 == 0 && rows16(p, x) && rows16(p, residual) && rows16(p, sum) && rows16(p, y);
+  // about 256 threads a workgroup, and enough workgroups for 2048 threads per CU
+  int ng = 256 / a.tpr;
+  if (ng < 1) ng = 1;
+  if (ng > p->rows) ng = (int)p->rows;
+  const int64_t need = (p->rows + ng - 1) / ng, most = 256 * 2048 / (ng * a.tpr);
+  const dim3 grid((unsigned)(need < most ? need : most)), block(ng * a.tpr);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launch("norm_fwd", st, [&] {
+    with_variant(vec, p->dtype == MOE_BF16, [&](auto v, auto bf) {
+      hipLaunchKernelGGL((k_norm_fwd<v(), bf()>), grid, block, 0, st, a);
+    });
+  });
+}
+
+size_t moe_norm_workspace_bytes(const moe_norm_problem* p) {
+  if (check_norm(p) != MOE_OK) return 0;
+  return align_up((size_t)bwd_groups(norm_args(p)) * 2 * p->cols * sizeof(float) + 1);
+}
+
+moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, const moe_rows* x,
+                             const void* weight, const float* stats, const moe_rows* grad_sum,
+                             const moe_rows* grad_x, void* grad_weight, void* grad_bias, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  MOE_TRY(check_norm(p));
+  MOE_TRY(check_rows(p, grad_y));
+  MOE_TRY(check_rows(p, x));
+  MOE_TRY(check_rows(p, grad_x));
+  if (grad_sum) MOE_TRY(check_rows(p, grad_sum));
+  if (!weight || (p->rows > 0 && !stats)) return MOE_ERR_NULL;
+  if (!elem_aligned(weight, p->param_dtype) || (reinterpret_cast<uintptr_t>(stats) & 7u)) return MOE_ERR_LAYOUT;
+  if (!elem_aligned(grad_weight, p->grad_dtype) || !elem_aligned(grad_bias, p->grad_dtype)) return MOE_ERR_LAYOUT;
+  const bool sums = grad_weight || grad_bias;
+  if (sums) {
+    if (!workspace || workspace_bytes < moe_norm_workspace_bytes(p)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return MOE_ERR_LAYOUT;
+  }
+  NormArgs a = norm_args(p);
+  a.dy = rows_of(grad_y); a.x = rows_of(x); a.gsum = rows_of(grad_sum); a.dx = rows_of(grad_x);
+  a.w = weight;
+  a.stats = const_cast<float*>(stats);
+  a.part = sums ? static_cast<float*>(workspace) : nullptr;
+  a.want_dw = grad_weight != nullptr;
+  a.want_db = grad_bias != nullptr;
+  const bool vec = p->cols % 8 == 0 && rows16(p, grad_y) && rows16(p, x) && rows16(p, grad_sum) && rows16(p, grad_x);
+  const int ng = bwd_row_groups(a), groups = bwd_groups(a);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (p->rows > 0) {
+    MOE_TRY(launch("norm_bwd", st, [&] {
+      with_variant(vec, p->dtype == MOE_BF16, [&](auto v, auto bf) {
+        const size_t lds = sums ? (size_t)(ng - 1) * a.tpr * kEpt * sizeof(float) : 0;
+        hipLaunchKernelGGL((k_norm_bwd<v(), bf()>), dim3(groups), dim3(ng * a.tpr), lds, st, a);
+      });
+    }));
+  }
+  if (!sums) return MOE_OK;
+  // also with no rows: an overwriting call leaves zeros
+  const int width = a.N * (a.want_dw + a.want_db);
+  uint8_t* g0 = static_cast<uint8_t*>(grad_weight ? grad_weight : grad_bias);
+  return launch("norm_bwd_final", st, [&] {
+    hipLaunchKernelGGL(k_norm_bwd_final, dim3((width + kFinalCols - 1) / kFinalCols), dim3(256), 0, st,
+                       (const float*)workspace, groups, width, a.N, g0, static_cast<uint8_t*>(grad_bias),
+                       p->grad_dtype == MOE_BF16 ? 1 : 0, (p->flags & MOE_NORM_OVERWRITE_GRADS) ? 1 : 0);
+  });
+}
+
+}  // extern "C"

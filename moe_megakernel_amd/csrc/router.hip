@@ -1,0 +1,334 @@
+// The router's decision: scores from logits, the K best experts of every token, their
+// weights, and the gradient back to the logits (C ABI: moe_router_forward / _backward).
+//
+//   s = softmax(l) over the row, or sigmoid(l) per expert
+//   chosen: the K largest of s (+ bias), ties to the lowest expert index
+//   w_k = scale s_k / (sum of the chosen s + 1e-20)   or   scale s_k
+//
+// A row is held by 16 lanes (one DPP row), element e = lane + 16 j in register j, so that
+// the K rounds of "largest remaining" are a scan over a few registers and four DPP steps
+// each, with no LDS and no barrier, for four rows of a wave at once.
+//
+// Without a bias the order of the scores is the order of the logits, so the logits
+// themselves are compared: no rounding can make or break a tie.  With a bias s + bias is
+// compared in 64 bits: in 32 bits scores near 1 differ by rounding alone and two correct
+// programs would choose different experts.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "../../include/moe.h"
+#include "common.hpp"
+#include "host.hpp"
+#include "reduce.hpp"
+
+using namespace moe;
+
+namespace {
+
+constexpr int kRouterThreads = 256;
+constexpr int kRouterRows = kRouterThreads / 16;   // token rows per workgroup
+constexpr float kRouterEps = 1e-20f;
+
+struct RouterArgs {
+  const void* logits;
+  int64_t ld;
+  int64_t tokens;
+  int E, K, normalize;
+  float scale;
+  const float* bias;
+  int32_t* top;          // forward: written; backward: read
+  float* rw;             // forward: written
+  const float* gw;       // backward
+  void* dl;              // backward
+  int64_t ld_dl;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float ld_logit(const void* base, int64_t i) {
+  if constexpr (BF16) return bf2f(static_cast<const uint16_t*>(base)[i]);
+  else return static_cast<const float*>(base)[i];
+}
+
+__device__ __forceinline__ float ninf() { return -__builtin_huge_valf(); }
+
+// EPL registers of a row: logits (-inf past the last expert).
+template <int EPL, bool BF16>
+__device__ __forceinline__ void load_row(const RouterArgs& a, int64_t t, int lane, float (&l)[EPL]) {
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = lane + 16 * j;
+    l[j] = e < a.E ? ld_logit<BF16>(a.logits, t * a.ld + e) : ninf();
+  }
+}
+
+// Row scores in T (float or double).  -inf logits have score 0; a row with nothing else
+// keeps zeros (no 0/0).  A NaN logit leaves softmax's whole row NaN.
+template <int EPL, bool SOFTMAX, typename T>
+__device__ __forceinline__ void row_scores(const float (&l)[EPL], T (&s)[EPL]) {
+  if constexpr (SOFTMAX) {
+    float m = ninf();
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) m = fmaxf(m, l[j]);   // ignores NaN
+    m = row16_max(m);
+    T z = 0;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if constexpr (std::is_same<T, double>::value) s[j] = l[j] == ninf() ? 0.0 : exp((double)l[j] - (double)m);
+      else s[j] = l[j] == ninf() ? 0.0f : expf(l[j] - m);
+      z += s[j];
+    }
+    z = row16_sum(z);
+    const T inv = z == (T)0 ? (T)0 : (T)1 / z;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) s[j] *= inv;
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if constexpr (std::is_same<T, double>::value) s[j] = 1.0 / (1.0 + exp(-(double)l[j]));
+      else s[j] = 1.0f / (1.0f + expf(-l[j]));
+    }
+  }
+}
+
+// One round: the largest key left in the row and the lowest expert that has it (E's
+// successor and a -inf key when nothing is left), then that expert's key is struck out.
+template <int EPL, typename T>
+__device__ __forceinline__ int take_best(T (&key)[EPL], int lane, T lowest) {
+  T m = key[0];
+#pragma unroll
+  for (int j = 1; j < EPL; ++j) m = key[j] > m ? key[j] : m;
+  m = row16_max(m);
+  int e = 1 << 20;
+#pragma unroll
+  for (int j = EPL - 1; j >= 0; --j) e = key[j] == m ? lane + 16 * j : e;
+  e = row16_min(e);
+  const bool none = m == lowest;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) key[j] = (lane + 16 * j == e) ? lowest : key[j];
+  return none ? -1 : e;
+}
+
+template <int EPL, bool BF16, bool SOFTMAX, bool BIAS>
+__global__ __launch_bounds__(kRouterThreads) void k_router_fwd(RouterArgs a) {
+  const int lane = threadIdx.x & 15;
+  const int64_t t = (int64_t)blockIdx.x * kRouterRows + (threadIdx.x >> 4);
+  if (t >= a.tokens) return;   // whole 16-lane rows leave together
+  float l[EPL], s[EPL];
+  load_row<EPL, BF16>(a, t, lane, l);
+  float bad = 0.0f;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) bad = l[j] != l[j] ? 1.0f : bad;
+  bad = row16_max(bad);
+  row_scores<EPL, SOFTMAX, float>(l, s);
+
+  int pick[kMaxTopk];
+  if constexpr (!BIAS) {
+    float key[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = l[j] == l[j] ? l[j] : ninf();
+#pragma unroll
+    for (int k = 0; k < kMaxTopk; ++k) pick[k] = k < a.K ? take_best<EPL, float>(key, lane, ninf()) : -1;
+  } else {
+    double key[EPL];
+    const double lowest = -__builtin_huge_val();
+    row_scores<EPL, SOFTMAX, double>(l, key);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const int e = lane + 16 * j;
+      key[j] = e < a.E ? key[j] + (double)a.bias[e] : lowest;
+      // an expert whose logit is -inf or NaN, or whose key is NaN, is never chosen
+      if (!(l[j] > ninf()) || key[j] != key[j]) key[j] = lowest;
+    }
+#pragma unroll
+    for (int k = 0; k < kMaxTopk; ++k) pick[k] = k < a.K ? take_best<EPL, double>(key, lane, lowest) : -1;
+  }
+
+  // the chosen scores: each lane adds what it holds of pick k, then the row sums (one
+  // lane has the value, the others zero)
+  float w[kMaxTopk], sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kMaxTopk; ++k) {
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) v = (lane + 16 * j == pick[k]) ? s[j] : v;
+    w[k] = k < a.K ? row16_sum(v) : 0.0f;
+    sum += w[k];
+  }
+  const float f = a.normalize ? a.scale / (sum + kRouterEps) : a.scale;
+#pragma unroll
+  for (int k = 0; k < kMaxTopk; ++k) {
+    if (k < a.K && lane == k) {
+      a.top[t * a.K + k] = pick[k];
+      const float v = bad != 0.0f ? __builtin_nanf("") : w[k] * f;
+      a.rw[t * a.K + k] = pick[k] >= 0 ? v : 0.0f;
+    }
+  }
+}
+
+// Gradient of sum_k gw_k w_k.  With cnt_e the times e stands in the table's row (0 or 1
+// for a table of the forward), g_e the sum of its gw, S and G the row sums of cnt s, g s:
+//   ds_e = scale g_e                                    (raw scores)
+//   ds_e = scale (g_e - cnt_e G / (S + eps)) / (S + eps)  (normalised)
+//   softmax: dl_e = s_e (ds_e - sum_j ds_j s_j)     sigmoid: dl_e = ds_e s_e (1 - s_e)
+template <int EPL, bool BF16, bool SOFTMAX>
+__global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
+  const int lane = threadIdx.x & 15;
+  const int64_t t = (int64_t)blockIdx.x * kRouterRows + (threadIdx.x >> 4);
+  if (t >= a.tokens) return;
+  float l[EPL], s[EPL], g[EPL], cnt[EPL];
+  load_row<EPL, BF16>(a, t, lane, l);
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) g[j] = cnt[j] = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kMaxTopk; ++k) {
+    if (k < a.K) {
+      int e = a.top[t * a.K + k];
+      if (e >= a.E) e = -1;
+      const float v = a.gw[t * a.K + k];
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        const bool hit = lane + 16 * j == e;   // -1 and out-of-range entries hit nothing
+        g[j] += hit ? v : 0.0f;
+        cnt[j] += hit ? 1.0f : 0.0f;
+      }
+    }
+  }
+  row_scores<EPL, SOFTMAX, float>(l, s);
+  if (a.normalize) {
+    float S = 0.0f, G = 0.0f;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      S += cnt[j] * s[j];
+      G += g[j] * s[j];
+    }
+    S = row16_sum(S) + kRouterEps;
+    G = row16_sum(G) / S;
+    const float f = a.scale / S;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) g[j] = f * (g[j] - cnt[j] * G);
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) g[j] *= a.scale;
+  }
+  float dot = 0.0f;
+  if constexpr (SOFTMAX) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) dot += g[j] * s[j];
+    dot = row16_sum(dot);
+  }
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const int e = lane + 16 * j;
+    if (e < a.E) {
+      // 1 - sigmoid(l) as sigmoid(-l): the difference would cancel near 1
+      const float d = SOFTMAX ? s[j] * (g[j] - dot) : g[j] * s[j] / (1.0f + expf(l[j]));
+      if constexpr (BF16) static_cast<uint16_t*>(a.dl)[t * a.ld_dl + e] = (uint16_t)f2bf(d);
+      else static_cast<float*>(a.dl)[t * a.ld_dl + e] = d;
+    }
+  }
+}
+
+moe_status check_router(const moe_router_problem* p) {
+  if (!p) return MOE_ERR_NULL;
+  if (p->tokens < 0 || p->tokens > ((int64_t)1 << 30)) return MOE_ERR_SHAPE;
+  if (p->experts < 1 || p->experts > kMaxExperts) return MOE_ERR_SHAPE;
+  if (p->topk < 1 || p->topk > kMaxTopk || p->topk > p->experts) return MOE_ERR_SHAPE;
+  if (p->logits_dtype != MOE_BF16 && p->logits_dtype != MOE_FP32) return MOE_ERR_DTYPE;
+  if (p->score != MOE_ROUTER_SOFTMAX && p->score != MOE_ROUTER_SIGMOID) return MOE_ERR_UNSUPPORTED;
+  if (p->flags & ~MOE_ROUTER_NORMALIZE) return MOE_ERR_UNSUPPORTED;
+  if (!(p->scale > -3.0e38f && p->scale < 3.0e38f)) return MOE_ERR_UNSUPPORTED;   // NaN, infinite
+  if (p->ld_logits < p->experts) return MOE_ERR_LAYOUT;
+  return MOE_OK;
+}
+
+bool elem_aligned(const void* q, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(q) & (dtype == MOE_BF16 ? 1u : 3u)) == 0;
+}
+
+RouterArgs router_args(const moe_router_problem* p, const void* logits) {
+  RouterArgs a{};
+  a.logits = logits;
+  a.ld = p->ld_logits;
+  a.tokens = p->tokens;
+  a.E = p->experts; a.K = p->topk;
+  a.normalize = (p->flags & MOE_ROUTER_NORMALIZE) != 0;
+  a.scale = p->scale;
+  return a;
+}
+
+// Calls f with the number of registers a row takes per lane, for up to 255 experts.
+template <class F>
+void with_epl(int E, F&& f) {
+  if (E <= 32) f(std::integral_constant<int, 2>{});
+  else if (E <= 64) f(std::integral_constant<int, 4>{});
+  else if (E <= 128) f(std::integral_constant<int, 8>{});
+  else f(std::integral_constant<int, 16>{});
+}
+template <class F>
+void with_bool(bool b, F&& f) {
+  if (b) f(std::true_type{});
+  else f(std::false_type{});
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_router_forward(const moe_router_problem* p, const void* logits, const float* expert_bias,
+                              int32_t* top_experts, float* router_weights, void* stream) {
+  MOE_TRY(check_router(p));
+  if (p->tokens > 0 && (!logits || !top_experts || !router_weights)) return MOE_ERR_NULL;
+  if (!elem_aligned(logits, p->logits_dtype) || !aligned4(expert_bias) || !aligned4(top_experts) ||
+      !aligned4(router_weights))
+    return MOE_ERR_LAYOUT;
+  if (p->tokens == 0) return MOE_OK;
+  RouterArgs a = router_args(p, logits);
+  a.bias = expert_bias;
+  a.top = top_experts;
+  a.rw = router_weights;
+  const dim3 grid((unsigned)((p->tokens + kRouterRows - 1) / kRouterRows));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launch("router_fwd", st, [&] {
+    with_epl(a.E, [&](auto epl) {
+      with_bool(p->logits_dtype == MOE_BF16, [&](auto bf) {
+        with_bool(p->score == MOE_ROUTER_SOFTMAX, [&](auto sm) {
+          with_bool(a.bias != nullptr, [&](auto bi) {
+            hipLaunchKernelGGL((k_router_fwd<epl(), bf(), sm(), bi()>), grid, dim3(kRouterThreads), 0, st, a);
+          });
+        });
+      });
+    });
+  });
+}
+
+moe_status moe_router_backward(const moe_router_problem* p, const void* logits, const int32_t* top_experts,
+                               const float* grad_router_weights, void* grad_logits, int64_t ld_grad_logits,
+                               void* stream) {
+  MOE_TRY(check_router(p));
+  if (p->tokens > 0 && (!logits || !top_experts || !grad_router_weights || !grad_logits)) return MOE_ERR_NULL;
+  if (ld_grad_logits < p->experts) return MOE_ERR_LAYOUT;
+  if (!elem_aligned(logits, p->logits_dtype) || !elem_aligned(grad_logits, p->logits_dtype) ||
+      !aligned4(top_experts) || !aligned4(grad_router_weights))
+    return MOE_ERR_LAYOUT;
+  if (p->tokens == 0) return MOE_OK;
+  RouterArgs a = router_args(p, logits);
+  a.top = const_cast<int32_t*>(top_experts);
+  a.gw = grad_router_weights;
+  a.dl = grad_logits;
+  a.ld_dl = ld_grad_logits;
+  const dim3 grid((unsigned)((p->tokens + kRouterRows - 1) / kRouterRows));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launch("router_bwd", st, [&] {
+    with_epl(a.E, [&](auto epl) {
+      with_bool(p->logits_dtype == MOE_BF16, [&](auto bf) {
+        with_bool(p->score == MOE_ROUTER_SOFTMAX, [&](auto sm) {
+          hipLaunchKernelGGL((k_router_bwd<epl(), bf(), sm()>), grid, dim3(kRouterThreads), 0, st, a);
+        });
+      });
+    });
+  });
+}
+
+}  // extern "C"
