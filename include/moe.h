@@ -282,6 +282,23 @@ moe_status moe_forward_noalloc(const moe_problem* p, const void* hidden, const f
                                const uint8_t* routing_map, const moe_weights* w, void* out,
                                void* saved, void* stream);
 
+/* Forward of a few tokens (serving: one token of each of several streams), in two kernels
+ * that read the weights of each expert in use once.  Requires MOE_FLAG_TOPK_ROUTING; with
+ * MOE_FLAG_RECOMPUTE it returns MOE_ERR_UNSUPPORTED, and with more than
+ * MOE_DECODE_MAX_TOKENS tokens MOE_ERR_SHAPE.  Arguments as for moe_forward_topk, without
+ * `saved`: no backward can follow.  The result is moe_forward_topk's with BF16 weights, up to
+ * the order of the FP32 sums.  With MXFP8 weights it differs: the weights are decoded
+ * exactly and multiply the BF16 activations, which are not quantised.
+ *  workspace   moe_decode_workspace_bytes(p) bytes, 16-byte aligned, overwritten in every
+ *              call.  Its first int32 is the status word afterwards: 0 or
+ *              MOE_ERR_ROUTE_INVALID (invalid entries are dropped, as moe_forward_topk does)
+ * With no tokens nothing is enqueued and nothing is written. */
+#define MOE_DECODE_MAX_TOKENS 64
+size_t moe_decode_workspace_bytes(const moe_problem* p);
+moe_status moe_forward_decode(const moe_problem* p, const void* hidden, const int32_t* top_experts,
+                              const float* router_weights, const moe_weights* w, void* out,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Backward of sum(grad_out * out).
  *  grad_out     bf16  [T][H]
  *  hidden       the same bf16 [T][H] tensor given to moe_forward

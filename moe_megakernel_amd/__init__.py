@@ -33,9 +33,10 @@ MOE_NORM_MAX_COLS = 16384
 EXPORTED = ("moe_saved_bytes", "moe_workspace_bytes", "moe_saved_view", "moe_forward",
             "moe_forward_topk", "moe_forward_noalloc", "moe_backward", "moe_status_str",
             "moe_kernel_timer_enable", "moe_kernel_timer_read", "moe_mx_staging_view",
-            "moe_router_forward", "moe_router_backward", "moe_norm_forward", "moe_norm_backward",
+            "moe_decode_workspace_bytes", "moe_forward_decode", "moe_router_forward", "moe_router_backward", "moe_norm_forward", "moe_norm_backward",
             "moe_norm_workspace_bytes")
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
+MOE_DECODE_MAX_TOKENS = 64
 
 
 class moe_problem(C.Structure):
@@ -135,6 +136,11 @@ def load(path: str | None = None):
     lib.moe_kernel_timer_read.restype = C.c_int
     lib.moe_mx_staging_view.argtypes = [P(moe_problem), P(moe_mx_staging_layout)]
     lib.moe_mx_staging_view.restype = C.c_int
+    lib.moe_decode_workspace_bytes.argtypes = [P(moe_problem)]
+    lib.moe_decode_workspace_bytes.restype = C.c_size_t
+    lib.moe_forward_decode.argtypes = [P(moe_problem), C.c_void_p, C.c_void_p, C.c_void_p, P(moe_weights),
+                                       C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
+    lib.moe_forward_decode.restype = C.c_int
     lib.moe_router_forward.argtypes = [P(moe_router_problem)] + [C.c_void_p] * 5
     lib.moe_router_forward.restype = C.c_int
     lib.moe_router_backward.argtypes = [P(moe_router_problem)] + [C.c_void_p] * 4 + [C.c_int64, C.c_void_p]
@@ -212,6 +218,17 @@ def moe_backward(p, grad_out, hidden, weights, saved, grad_hidden, grad_probs, m
                  workspace_bytes, stream) -> int:
     return load().moe_backward(C.byref(p), grad_out, hidden, C.byref(weights), saved, grad_hidden,
                                grad_probs, C.byref(main_grads), workspace, workspace_bytes, stream)
+
+
+def moe_decode_workspace_bytes(p: moe_problem) -> int:
+    return int(load().moe_decode_workspace_bytes(C.byref(p)))
+
+
+def moe_forward_decode(p, hidden, top_experts, router_weights, weights, out, workspace, workspace_bytes,
+                       stream) -> int:
+    """Raw call of the few-token forward with integer device addresses; returns the status."""
+    return load().moe_forward_decode(C.byref(p), hidden, top_experts, router_weights, C.byref(weights), out,
+                                     workspace, workspace_bytes, stream)
 
 
 def moe_router_forward(p, logits, expert_bias, top_experts, router_weights, stream) -> int:
@@ -531,3 +548,43 @@ class Norm:
                                                       _ptr(grad_weight), _ptr(grad_bias), _ptr(self.workspace),
                                                       self.ws_bytes, s))
         return grad_x
+
+
+class DecodeLayer:
+    """The layer's forward for a few tokens.  Holds the problem (its `tokens` is the largest
+    batch; a call takes any number up to it) and the workspace; two calls of one DecodeLayer
+    must not overlap on the GPU."""
+
+    def __init__(self, p: moe_problem, device="cuda"):
+        import torch
+        self.p = moe_problem.from_buffer_copy(p)
+        self.ws_bytes = moe_decode_workspace_bytes(self.p)
+        if self.ws_bytes == 0:
+            raise MoeError(MOE_ERR_UNSUPPORTED if 0 <= p.tokens <= MOE_DECODE_MAX_TOKENS else MOE_ERR_SHAPE,
+                           "moe_decode_workspace_bytes")
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+
+    def forward(self, hidden, top_experts, router_weights, weights: moe_weights, out):
+        import torch
+        where, dev = "moe_forward_decode", getattr(hidden, "device", None)
+        if hidden is None:
+            raise MoeError(MOE_ERR_NULL, where)
+        T, H, K = hidden.shape[0], self.p.hidden, self.p.topk
+        if T > self.p.tokens:
+            raise MoeError(MOE_ERR_SHAPE, where)
+        p = moe_problem.from_buffer_copy(self.p)
+        p.tokens = T
+        _check_dense(where, dev, hidden, torch.bfloat16, (T, H))
+        _check_dense(where, dev, top_experts, torch.int32, (T, K))
+        _check_dense(where, dev, router_weights, torch.float32, (T, K))
+        _check_dense(where, dev, out, torch.bfloat16, (T, H))
+        if self.workspace.device != dev:
+            raise MoeError(MOE_ERR_WORKSPACE, where)
+        _call(where, dev, lambda s: moe_forward_decode(p, _ptr(hidden), _ptr(top_experts), _ptr(router_weights),
+                                                       weights, _ptr(out), _ptr(self.workspace), self.ws_bytes, s))
+        return out
+
+    def status_word(self):
+        """The last call's status word, a device int32 [1]: 0 or MOE_ERR_ROUTE_INVALID."""
+        import torch
+        return self.workspace[:4].view(torch.int32)

@@ -23,6 +23,7 @@ SOURCES = [
     ("moe_api.hip", []),                     # C ABI, routing and row kernels
     ("gemm_tok.hip", []),                    # token-dimension GEMMs
     ("gemm_wgrad.hip", _sched("max-ilp")),   # weight gradients
+    ("decode.hip", []),                      # the forward of a few tokens
     ("norm.hip", []),                        # layer norm and RMS norm
     ("router.hip", []),                      # the router's choice of experts
 ]

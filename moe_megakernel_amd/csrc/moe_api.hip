@@ -9,6 +9,7 @@
 
 #include "../../include/moe.h"
 #include "common.hpp"
+#include "decode.hpp"
 #include "gemm.hpp"
 #include "host.hpp"
 #include "routing.hpp"
@@ -168,6 +169,23 @@ FwdLayout fwd_layout(const Dims& d) {
 
 size_t fwd_workspace(const Dims& d) { return fwd_layout(d).total; }
 
+// Workspace of the few-token forward: the plan (its first word is the status), the gate
+// scores and h (routed rows by route, then the shared expert's).
+struct DecodeLayout {
+  size_t plan, gate_s, h, total;
+};
+
+DecodeLayout decode_layout(const Dims& d) {
+  DecodeLayout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t r = o; o = align_up(o + bytes); return r; };
+  L.plan = take(sizeof(decode::Plan));
+  L.gate_s = take(4 * d.T);
+  L.h = take(2 * d.R * d.I);
+  L.total = o;
+  return L;
+}
+
 // ---------------------------------------------------------------- validation
 moe_status check_problem(const moe_problem* p) {
   if (!p) return MOE_ERR_NULL;
@@ -182,6 +200,14 @@ moe_status check_problem(const moe_problem* p) {
   if ((p->flags & MOE_FLAG_SHARED_GATE) && !(p->flags & MOE_FLAG_HAS_SHARED)) return MOE_ERR_UNSUPPORTED;
   if (!(p->swiglu_limit >= 0.0f) || p->swiglu_limit > 3.0e38f) return MOE_ERR_UNSUPPORTED;   // NaN, < 0, inf
   if (p->routed_dtype != MOE_BF16 && p->routed_dtype != MOE_MXFP8_E4M3) return MOE_ERR_DTYPE;
+  return MOE_OK;
+}
+
+// The few-token forward: the router's table only, no saved context, few tokens.
+moe_status check_decode(const moe_problem* p) {
+  MOE_TRY(check_problem(p));
+  if (!(p->flags & MOE_FLAG_TOPK_ROUTING) || (p->flags & MOE_FLAG_RECOMPUTE)) return MOE_ERR_UNSUPPORTED;
+  if (p->tokens > MOE_DECODE_MAX_TOKENS) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 
@@ -658,6 +684,63 @@ moe_status moe_forward_topk(const moe_problem* p, const void* hidden, const int3
                             void* workspace, size_t workspace_bytes, void* stream) {
   return forward_impl(true, p, hidden, nullptr, nullptr, top_experts, router_weights, w, out, saved, workspace,
                       workspace_bytes, stream);
+}
+
+size_t moe_decode_workspace_bytes(const moe_problem* p) {
+  if (check_decode(p) != MOE_OK) return 0;
+  return decode_layout(dims_of(p)).total;
+}
+
+moe_status moe_forward_decode(const moe_problem* p, const void* hidden, const int32_t* top_experts,
+                              const float* router_weights, const moe_weights* w, void* out, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  static_assert(decode::kMaxTokens == MOE_DECODE_MAX_TOKENS, "token limit of the kernels and of the ABI");
+  MOE_TRY(check_decode(p));
+  MOE_TRY(check_weights(p, w));
+  const Dims d = dims_of(p);
+  if (d.T > 0 && (!hidden || !top_experts || !router_weights || !out)) return MOE_ERR_NULL;
+  const DecodeLayout L = decode_layout(d);
+  if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (!aligned16(hidden) || !aligned16(out) || !aligned16(workspace) || !aligned4(top_experts) ||
+      !aligned4(router_weights))
+    return MOE_ERR_LAYOUT;
+  if (d.T == 0) return MOE_OK;
+  uint8_t* W = static_cast<uint8_t*>(workspace);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  decode::Args a{};
+  a.x = static_cast<const uint16_t*>(hidden);
+  a.top = top_experts;
+  a.rw = router_weights;
+  a.T = (int)d.T; a.H = (int)d.H; a.I = (int)d.I; a.E = (int)d.E; a.K = (int)d.K;
+  a.shared = d.hs ? 1 : 0;
+  a.limit = d.L;
+  if (d.mx) {
+    a.gate = mxref(w->routed_gate, false);
+    a.up = mxref(w->routed_up, false);
+    a.down = mxref(w->routed_down, false);
+  } else {
+    a.gate.data = matref(w->routed_gate, w->routed_gate.data, 2);
+    a.up.data = matref(w->routed_up, w->routed_up.data, 2);
+    a.down.data = matref(w->routed_down, w->routed_down.data, 2);
+  }
+  if (d.hs) {
+    a.sgate = matref(w->shared_gate, w->shared_gate.data, 2);
+    a.sup = matref(w->shared_up, w->shared_up.data, 2);
+    a.sdown = matref(w->shared_down, w->shared_down.data, 2);
+  }
+  a.gw = d.sg ? static_cast<const uint16_t*>(w->shared_out_gate.data.base) : nullptr;
+  a.plan = reinterpret_cast<decode::Plan*>(W + L.plan);
+  a.gate_s = reinterpret_cast<float*>(W + L.gate_s);
+  a.h = reinterpret_cast<uint16_t*>(W + L.h);
+  a.out = static_cast<uint16_t*>(out);
+  MOE_TRY(launch("decode_fc1", st, [&] {
+    if (d.mx) decode::launch_fc1<true>(st, a);
+    else decode::launch_fc1<false>(st, a);
+  }));
+  return launch("decode_fc2", st, [&] {
+    if (d.mx) decode::launch_fc2<true>(st, a);
+    else decode::launch_fc2<false>(st, a);
+  });
 }
 
 moe_status moe_backward(const moe_problem* p, const void* grad_out, const void* hidden,

@@ -1,0 +1,358 @@
+"""The forward of a few tokens (moe_forward_decode) against the layer's formula in 64 bits on
+the stored weights (MXFP8 decoded, activations unquantised).
+
+Tolerances.  u = 2^-24.  A product of length n is accumulated in FP32 over at most 32 products
+inside a matrix instruction, n / 128 steps and 8 partial sums: (40 + n / 128) u of the sum
+of its magnitudes.  The SwiGLU passes errors of a and b on with factors of at most
+1.1 |b| and |silu(a)| and adds 32 u |h| (exp and reciprocal).  h is rounded to BF16: each term
+w W h of the output is off by at most 2^-8 of itself, independently, so by
+Hoeffding's inequality their sum stays within 6 sqrt(sum of squares) 2^-8 except once in 10^7
+elements at the largest possible spread (a rounding error's actual spread is 1/sqrt(3) of it).
+The output's own rounding is 2^-8 relative."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import moe_inputs as gen
+import moe_megakernel_amd as mk
+from oracle import moe_oracle as O
+
+U = 2.0 ** -24
+H8 = 2.0 ** -8
+TABLE = mk.MOE_FLAG_TOPK_ROUTING
+
+
+# ------------------------------------------------------------------ CPU: refusals
+PTR = 1 << 20
+
+
+def _weights(p):
+    def w(rows, cols, dt, **kw):
+        m = lambda c: mk.moe_mat(PTR, rows * c, 0, c)
+        if dt == mk.MOE_BF16:
+            return mk.weight(dt, rows, cols, m(cols))
+        return mk.weight(dt, rows, cols, m(cols), 0, m(cols // 32), m(cols), m(cols))
+    H, I, d = p.hidden, p.intermediate, p.routed_dtype
+    b = mk.MOE_BF16
+    return mk.moe_weights(w(I, H, b), w(I, H, b), w(H, I, b), w(I, H, d), w(I, H, d), w(H, I, d), w(1, H, b))
+
+
+def _call(p, w=None, x=PTR, top=PTR, rw=PTR, out=PTR, ws=PTR, nbytes=1 << 40):
+    return mk.moe_forward_decode(p, x, top, rw, w or _weights(p), out, ws, nbytes, None)
+
+
+def _p(tokens=4, hidden=256, inter=128, experts=8, topk=2, dt=mk.MOE_BF16, flags=TABLE | mk.MOE_FLAG_HAS_SHARED, L=0.0):
+    return mk.problem(tokens, hidden, inter, experts, topk, dt, flags, L)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(tokens=-1), mk.MOE_ERR_SHAPE), (dict(tokens=mk.MOE_DECODE_MAX_TOKENS + 1), mk.MOE_ERR_SHAPE),
+    (dict(hidden=130), mk.MOE_ERR_SHAPE), (dict(inter=64), mk.MOE_ERR_SHAPE), (dict(experts=256), mk.MOE_ERR_SHAPE),
+    (dict(topk=9, experts=16), mk.MOE_ERR_SHAPE), (dict(flags=mk.MOE_FLAG_HAS_SHARED), mk.MOE_ERR_UNSUPPORTED),
+    (dict(flags=TABLE | mk.MOE_FLAG_RECOMPUTE), mk.MOE_ERR_UNSUPPORTED),
+    (dict(flags=TABLE | mk.MOE_FLAG_SHARED_GATE), mk.MOE_ERR_UNSUPPORTED), (dict(flags=TABLE | 64), mk.MOE_ERR_UNSUPPORTED),
+    (dict(dt=mk.MOE_FP32), mk.MOE_ERR_DTYPE), (dict(L=float("nan")), mk.MOE_ERR_UNSUPPORTED),
+    (dict(L=-1.0), mk.MOE_ERR_UNSUPPORTED)])
+def test_bad_problems_are_refused(kw, status):
+    p = _p(**kw)
+    assert _call(p, _weights(_p())) == status
+    assert mk.moe_decode_workspace_bytes(p) == 0
+
+
+def test_bad_arguments_are_refused():
+    p = _p()
+    need = mk.moe_decode_workspace_bytes(p)
+    assert need > 0
+    assert mk.load().moe_forward_decode(None, PTR, PTR, PTR, C.byref(_weights(p)), PTR, PTR, 1 << 40, None) == mk.MOE_ERR_NULL
+    assert mk.load().moe_forward_decode(C.byref(p), PTR, PTR, PTR, None, PTR, PTR, 1 << 40, None) == mk.MOE_ERR_NULL
+    for k in ("x", "top", "rw", "out"):
+        assert _call(p, **{k: None}) == mk.MOE_ERR_NULL
+    assert _call(p, ws=None) == mk.MOE_ERR_WORKSPACE
+    assert _call(p, nbytes=need - 1) == mk.MOE_ERR_WORKSPACE
+    for k in ("x", "out", "ws"):
+        assert _call(p, **{k: PTR + 8}) == mk.MOE_ERR_LAYOUT
+    for k in ("top", "rw"):
+        assert _call(p, **{k: PTR + 2}) == mk.MOE_ERR_LAYOUT
+    w = _weights(p)
+    w.routed_up.rows = 64
+    assert _call(p, w) == mk.MOE_ERR_SHAPE
+    w = _weights(p)
+    w.shared_down.dtype = mk.MOE_MXFP8_E4M3
+    assert _call(p, w) == mk.MOE_ERR_DTYPE
+    assert _call(_p(tokens=0), x=None, top=None, rw=None, out=None) == mk.MOE_OK
+
+
+def test_binding_refuses_host_and_mismatched_tensors():
+    p = _p()
+    layer = mk.DecodeLayer(p, device="cpu")
+    x, top, rw = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    w = _weights(p)
+    for args, status in (((x, top, rw, w, x.clone()), mk.MOE_ERR_LAYOUT), ((x.float(), top, rw, w, x.clone()), mk.MOE_ERR_DTYPE),
+                         ((torch.zeros(5, 256, dtype=torch.bfloat16), top, rw, w, x.clone()), mk.MOE_ERR_SHAPE),
+                         ((x[:, :128], top, rw, w, x.clone()), mk.MOE_ERR_SHAPE),
+                         ((None, top, rw, w, x.clone()), mk.MOE_ERR_NULL)):
+        with pytest.raises(mk.MoeError) as ei:
+            layer.forward(*args)
+        assert ei.value.status == status
+    with pytest.raises(mk.MoeError) as ei:
+        mk.DecodeLayer(_p(tokens=65), device="cpu")
+    assert ei.value.status == mk.MOE_ERR_SHAPE
+    with pytest.raises(mk.MoeError) as ei:
+        mk.DecodeLayer(_p(flags=0), device="cpu")
+    assert ei.value.status == mk.MOE_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------ reference (64 bits)
+def clean_table(top, E):
+    """The table with invalid entries dropped (out of range, listed again in the row)."""
+    out = top.copy()
+    for t in range(top.shape[0]):
+        seen = set()
+        for k in range(top.shape[1]):
+            e = int(top[t, k])
+            if e < 0 or e >= E or e in seen:
+                out[t, k] = -1
+            else:
+                seen.add(e)
+    return out
+
+
+def reference(x_bits, top, rw, E, W):
+    """(out, tolerance without the output's rounding), float64."""
+    x = torch.from_numpy(O.bf16_decode(x_bits))
+    T, H = x.shape
+    top, rw = torch.from_numpy(top), torch.from_numpy(rw).double()
+    out, lin, sq = (torch.zeros(T, H, dtype=torch.float64) for _ in range(3))
+
+    def add(t, w, mats):
+        wg, wu, wd = (torch.from_numpy(np.ascontiguousarray(m)) for m in mats)
+        I = wg.shape[0]
+        a, b = x[t] @ wg.T, x[t] @ wu.T
+        ea, eb = (((40 + H / 128) * U) * (x[t].abs() @ m.abs().T) for m in (wg, wu))
+        L = W.swiglu_limit
+        if L > 0:
+            a, b = a.clamp(max=L), b.clamp(-L, L)
+        s = a * torch.sigmoid(a)
+        h = s * b
+        eh = 1.1 * b.abs() * ea + s.abs() * eb + 32 * U * h.abs()
+        w = w[:, None]
+        out.index_add_(0, t, w * (h @ wd.T))
+        mag = h.abs() @ wd.abs().T
+        lin.index_add_(0, t, w.abs() * (eh @ wd.abs().T + (48 + I / 128 + E) * U * mag))
+        sq.index_add_(0, t, w ** 2 * (h ** 2 @ (wd ** 2).T))
+
+    for e in range(E):
+        t, k = (top == e).nonzero(as_tuple=True)
+        if t.numel():
+            add(t, rw[t, k], W.routed(e))
+    if W.shared is not None:
+        s = torch.ones(T, dtype=torch.float64)
+        if W.shared_gate is not None:
+            s = torch.sigmoid(x @ torch.from_numpy(W.shared_gate))
+        add(torch.arange(T), s, W.shared)
+    return out, lin + 6 * H8 * sq.sqrt()
+
+
+def test_reference_is_the_layer():
+    cfg = gen.custom(5, 256, 6, 3, 128, idx=3)
+    s1, s2 = gen.shared_weights(cfg)
+    routed = gen.routed_all(cfg)
+    W = O.Weights.from_bits(128, s1, s2, lambda e: routed[e], "bf16", swiglu_limit=0.5)
+    top, rw = table("short", 5, 6, 3, 0)
+    out, _ = reference(gen.hidden(cfg), clean_table(top, 6), rw, 6, W)
+    want = O.moe_forward_table(gen.hidden(cfg), clean_table(top, 6), rw, 6, W)
+    assert np.allclose(out.numpy(), want, rtol=1e-10, atol=1e-12)
+
+
+# ------------------------------------------------------------------ GPU
+def table(kind, T, E, K, seed):
+    rng = np.random.default_rng(seed)
+    top = np.stack([rng.permutation(E)[:K] for _ in range(T)]).astype(np.int32)
+    rw = rng.random((T, K), dtype=np.float32) - 0.25
+    if kind == "short":
+        top[rng.random((T, K)) < 0.4] = -1
+    elif kind == "none":
+        top[:] = -1
+    elif kind == "one":                       # every token to expert E - 1, the rest to none
+        top[:] = -1
+        top[:, rng.integers(K)] = E - 1
+    elif kind == "invalid":
+        top[::3, 0] = E
+        top[1::3, 0] = -5
+        if K > 1:
+            top[2::3, K - 1] = top[2::3, 0]
+    rw[top < 0] = np.nan                      # weights at missing routes are not looked at
+    return top, rw
+
+
+def problem(T, H, I, E, K, routed="bf16", layout="single", kind="random", seed=0, **kw):
+    from moe_inputs.device import DeviceProblem
+    cfg = gen.custom(T, H, E, K, I, routed=routed, layout=layout, backward=False, idx=200 + seed)
+    top, rw = table(kind, T, E, K, seed)
+    dp = DeviceProblem(cfg, routing_table=(top, rw), **kw)
+    dp.decode = mk.DecodeLayer(dp.p)
+    dp.decode.workspace.fill_(0xFF)
+    W = O.Weights.from_bits(I, dp.np_s1 if dp.shared else None, dp.np_s2 if dp.shared else None,
+                            lambda e: dp.np_routed[e], routed, shared_gate=dp.np_gate, swiglu_limit=dp.swiglu_limit)
+    return dp, W
+
+
+def run(dp):
+    return dp.decode.forward(dp.x, dp.top, dp.rw, dp.weights, dp.out)
+
+
+def check(dp, W, out=None):
+    top = clean_table(dp.np_top, dp.cfg.experts)
+    ref, tol = reference(dp.np_x, top, np.nan_to_num(dp.np_rw), dp.cfg.experts, W)
+    got = (dp.out if out is None else out).cpu().double()
+    tol = tol + H8 * (ref.abs() + tol)
+    bad = (got - ref).abs() > tol
+    assert not bool(bad.any()), (int(bad.sum()), float(((got - ref).abs() / tol.clamp(min=1e-30)).max()))
+    invalid = bool(((dp.np_top < -1) | (dp.np_top >= dp.cfg.experts)).any()) or bool(
+        ((dp.np_top >= 0) & (dp.np_top < dp.cfg.experts) & (top < 0)).any())
+    assert int(dp.decode.status_word().cpu()[0]) == (mk.MOE_ERR_ROUTE_INVALID if invalid else 0)
+
+
+CASES = [
+    # T, H, I, E, K, extra
+    dict(T=1, H=128, I=128, E=1, K=1),
+    dict(T=1, H=256, I=128, E=8, K=2, layout="table"),
+    dict(T=2, H=384, I=256, E=5, K=5, gate=True),
+    dict(T=3, H=640, I=384, E=9, K=4, kind="short", shared=False),
+    dict(T=7, H=1152, I=128, E=255, K=8, layout="table", pad=32),
+    dict(T=16, H=256, I=640, E=6, K=3, kind="one"),
+    dict(T=17, H=512, I=256, E=4, K=1, limit=0.4, kind="one"),
+    dict(T=16, H=128, I=128, E=3, K=2, kind="none", shared=False),
+    dict(T=33, H=256, I=128, E=12, K=4, kind="invalid", gate=True),
+    dict(T=48, H=384, I=256, E=4, K=4, kind="random", pad=16),
+    dict(T=64, H=256, I=128, E=2, K=1, kind="one"),
+    dict(T=64, H=512, I=256, E=40, K=8, kind="short", limit=0.4),
+    dict(T=31, H=256, I=1024, E=64, K=6, sep=True),
+    dict(T=64, H=128, I=128, E=255, K=8, kind="invalid", shared=False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("routed", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_matches_formula(gpu_lib, i, routed):
+    c = dict(CASES[i])
+    kw = dict(shared=c.pop("shared", True), shared_gate=c.pop("gate", False), swiglu_limit=c.pop("limit", 0.0),
+              pad_bytes=c.pop("pad", 0), separate_gate_up=c.pop("sep", False))
+    dp, W = problem(routed=routed, seed=i, **c, **kw)
+    run(dp)
+    torch.cuda.synchronize()
+    check(dp, W)
+    first = dp.out.clone()
+    dp.decode.workspace.fill_(0x5A)
+    run(dp)
+    torch.cuda.synchronize()
+    assert torch.equal(dp.out, first)
+    if c.get("kind") == "none" and not dp.shared:
+        assert bool((dp.out == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("routed", ["bf16", "mxfp8"])
+def test_full_width(gpu_lib, routed):
+    dp, W = problem(5, 4096, 1024, 10, 4, routed=routed, seed=40)
+    run(dp)
+    torch.cuda.synchronize()
+    check(dp, W)
+
+
+@pytest.mark.gpu
+def test_agrees_with_the_training_forward(gpu_lib):
+    """BF16: the same roundings as moe_forward_topk, so the outputs differ by at most FP32
+    summation order and the BF16 steps it tips: h may move by a step (2^-7 of itself), as may out."""
+    dp, W = problem(40, 512, 256, 12, 3, seed=41, kind="short", shared_gate=True)
+    run(dp)
+    got = dp.out.double().cpu()
+    dp.forward()
+    want = dp.out.double().cpu()
+    _, tol = reference(dp.np_x, clean_table(dp.np_top, 12), np.nan_to_num(dp.np_rw), 12, W)
+    assert bool(((got - want).abs() <= 2 * (tol + H8 * (want.abs() + tol))).all())
+
+
+@pytest.mark.gpu
+def test_smaller_batches_of_one_layer(gpu_lib):
+    dp, W = problem(24, 256, 128, 8, 2, seed=42)
+    run(dp)
+    full = dp.out.clone()
+    for T in (1, 2, 15, 16, 17, 24):
+        out = torch.full_like(dp.out, float("nan"))
+        dp.decode.forward(dp.x[:T], dp.top[:T], dp.rw[:T], dp.weights, out[:T])
+        torch.cuda.synchronize()
+        assert bool(torch.isnan(out[T:]).all())         # rows behind the last token stay
+        top = clean_table(dp.np_top[:T], 8)
+        ref, tol = reference(dp.np_x[:T], top, dp.np_rw[:T], 8, W)
+        assert bool(((out[:T].cpu().double() - ref).abs() <= tol + H8 * (ref.abs() + tol)).all())
+    e = dp.x[:0]
+    dp.decode.forward(e, dp.top[:0], dp.rw[:0], dp.weights, dp.out[:0])
+    torch.cuda.synchronize()
+    assert torch.equal(dp.out, full)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("routed", ["bf16", "mxfp8"])
+def test_nonfinite_tokens_stay_in_their_row(gpu_lib, routed):
+    dp, W = problem(20, 256, 128, 4, 2, routed=routed, seed=43)
+    run(dp)
+    want = dp.out.clone()
+    dp.x[3, 5] = float("nan")
+    dp.x[11] = float("inf")
+    dp.rw[7, 0] = float("nan")
+    run(dp)
+    torch.cuda.synchronize()
+    keep = [t for t in range(20) if t not in (3, 7, 11)]
+    assert torch.equal(dp.out[keep], want[keep])
+    assert bool(torch.isnan(dp.out[[3, 7]]).all()) and not bool(torch.isfinite(dp.out[11].float()).any())
+
+
+@pytest.mark.gpu
+def test_graph_replay_and_side_stream(gpu_lib):
+    dp, W = problem(19, 384, 256, 16, 4, seed=44, shared_gate=True)
+    run(dp)
+    torch.cuda.synchronize()
+    want = dp.out.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(dp)
+    torch.cuda.synchronize()
+    assert torch.equal(dp.out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(dp)
+    for i in range(3):                                   # new tokens and a new table each time
+        top, rw = table("short", 19, 16, 4, 60 + i)
+        dp.top.copy_(torch.from_numpy(top))
+        dp.rw.copy_(torch.from_numpy(rw))
+        dp.x.copy_(torch.randn(19, 384, device="cuda"))
+        run(dp)
+        torch.cuda.synchronize()
+        want = dp.out.clone()
+        dp.out.zero_()
+        dp.decode.workspace.fill_(0xA5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dp.out, want), i
+
+
+@pytest.mark.gpu
+def test_two_layers_on_two_streams(gpu_lib):
+    """Calls with distinct workspaces may overlap."""
+    a, Wa = problem(9, 256, 128, 8, 2, seed=45)
+    b, Wb = problem(21, 256, 256, 8, 2, seed=46, routed="mxfp8")
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            run(a)
+        with torch.cuda.stream(s2):
+            run(b)
+    torch.cuda.synchronize()
+    check(a, Wa)
+    check(b, Wb)
