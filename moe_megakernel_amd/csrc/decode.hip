@@ -26,7 +26,22 @@ namespace decode {
 namespace {
 
 constexpr int kStep = 128;          // elements of the contraction per step (the ABI's multiple)
-constexpr int kFc1Waves = 4, kFc2Waves = 8;
+#ifndef DEC_W1
+#define DEC_W1 4
+#endif
+constexpr int kFc1Waves = DEC_W1, kFc2Waves = 8;
+
+// Loads through global (not flat) addresses: the pointers may come out of a table in
+// memory, which hides their address space, and a flat load is waited for with every other
+// load in flight.
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+  const u32x4_t v = *(const __attribute__((address_space(1))) u32x4_t*)(uintptr_t)p;
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ uint32_t ld4(const uint8_t* p) {
+  return *(const __attribute__((address_space(1))) uint32_t*)(uintptr_t)p;
+}
 
 // One step of 16 weight rows: lane (r = lane & 15, q = lane >> 4) has elements
 // 64 s + 16 q .. + 15 of row r, s = 0, 1.
@@ -36,10 +51,10 @@ template <>
 struct WStep<false> {
   uint4 v[4];
   __device__ __forceinline__ void load(const uint8_t* p, const uint8_t*) {
-    v[0] = *reinterpret_cast<const uint4*>(p);
-    v[1] = *reinterpret_cast<const uint4*>(p + 16);
-    v[2] = *reinterpret_cast<const uint4*>(p + 128);
-    v[3] = *reinterpret_cast<const uint4*>(p + 144);
+    v[0] = ld16(p);
+    v[1] = ld16(p + 16);
+    v[2] = ld16(p + 128);
+    v[3] = ld16(p + 144);
   }
   // the 8 elements 64 s + 16 q + 8 u ..
   __device__ __forceinline__ bf16x8_t frag(int s, int u, int) const {
@@ -52,14 +67,13 @@ struct WStep<true> {
   uint4 v[2];
   uint32_t sc;   // E8M0 of the row's four blocks of 32
   __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* s) {
-    v[0] = *reinterpret_cast<const uint4*>(p);
-    v[1] = *reinterpret_cast<const uint4*>(p + 64);
-    sc = *reinterpret_cast<const uint32_t*>(s);
+    v[0] = ld16(p);
+    v[1] = ld16(p + 64);
+    sc = ld4(s);
   }
   __device__ __forceinline__ bf16x8_t frag(int s, int u, int q) const {
     const float scale = __uint_as_float(((sc >> (16 * s + 8 * (q >> 1))) & 0xffu) << 23);
     const uint32_t lo = u ? v[s].z : v[s].x, hi = u ? v[s].w : v[s].y;
-    typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
     const u32x4_t r = {
         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false)),
         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true)),
@@ -70,17 +84,18 @@ struct WStep<true> {
   static constexpr int kBytes = kStep, kLane = 16;
 };
 
-// acc[f] += W (16 rows) X_f^T (16 columns) over n steps.  w, ws: the lane's row at its first
-// element (scales: the row's first block); x[f]: the lane's column at its first element.
-// D steps are in flight; the steady loop has no conditions.
-template <bool MX, int NF, int D>
-__device__ __forceinline__ void dot_steps(const uint8_t* w, const uint8_t* ws, const uint8_t* const (&x)[NF], int n,
-                                          f32x4_t (&acc)[NF]) {
+// acc[g][f] += W_g (16 rows) X_f^T (16 columns) over n steps.  w, ws: the lane's rows at
+// their first element (scales: the rows' first block); x: the lane's columns at their first
+// element.  D steps are in flight; the steady loop has no conditions.
+template <bool MX, int R, int NF, int D>
+__device__ __forceinline__ void dot_steps(const uint8_t* const (&w)[R], const uint8_t* const (&ws)[R],
+                                          const uint8_t* const (&x)[NF], int n, f32x4_t (&acc)[R][NF]) {
   const int q = (threadIdx.x & 63) >> 4;
-  WStep<MX> wr[D];
+  WStep<MX> wr[D][R];
   WStep<false> xr[D][NF];
   auto load = [&](int d, int i) __attribute__((always_inline)) {
-    wr[d].load(w + (int64_t)i * WStep<MX>::kBytes, ws + i * 4);
+#pragma unroll
+    for (int g = 0; g < R; ++g) wr[d][g].load(w[g] + (int64_t)i * WStep<MX>::kBytes, ws[g] + i * 4);
 #pragma unroll
     for (int f = 0; f < NF; ++f) xr[d][f].load(x[f] + i * WStep<false>::kBytes, nullptr);
   };
@@ -88,12 +103,14 @@ __device__ __forceinline__ void dot_steps(const uint8_t* w, const uint8_t* ws, c
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const bf16x8_t a = wr[d].frag(s, u, q);
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int f = 0; f < NF; ++f)
-          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, xr[d][f].frag(s, u, q), acc[f], 0, 0, 0);
-      }
+        for (int g = 0; g < R; ++g) {
+          const bf16x8_t a = wr[d][g].frag(s, u, q);
+#pragma unroll
+          for (int f = 0; f < NF; ++f)
+            acc[g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, xr[d][f].frag(s, u, q), acc[g][f], 0, 0, 0);
+        }
   };
 #pragma unroll
   for (int d = 0; d < D; ++d)
@@ -104,6 +121,7 @@ __device__ __forceinline__ void dot_steps(const uint8_t* w, const uint8_t* ws, c
     for (int d = 0; d < D; ++d) {
       mul(d);
       load(d, i + D + d);
+      __builtin_amdgcn_sched_barrier(0);   // the next stage's products stay behind these loads
     }
   }
 #pragma unroll
@@ -117,9 +135,27 @@ __device__ __forceinline__ void dot_steps(const uint8_t* w, const uint8_t* ws, c
     if (i + D + d < n) mul(d);
 }
 
-// Steps in flight by the number of 16-token column groups: about 100 registers each.
-template <int NF>
-constexpr int depth() { return NF == 1 ? 2 : 1; }
+#ifndef DEC_D_BF
+#define DEC_D_BF 2
+#endif
+#ifndef DEC_D_MX
+#define DEC_D_MX 2
+#endif
+#ifndef DEC_R_BF
+#define DEC_R_BF 1
+#endif
+#ifndef DEC_R_MX
+#define DEC_R_MX 2
+#endif
+#ifndef DEC_D2_MX
+#define DEC_D2_MX 3
+#endif
+// Steps in flight: what fits 128 registers beside the accumulators and addresses.
+template <bool MX, int R, int NF>
+constexpr int depth() {
+  if (NF == 2) return 1;
+  return MX ? (R == 1 ? DEC_D2_MX : DEC_D_MX) : (R == 1 ? DEC_D_BF : 2);
+}
 
 __device__ __forceinline__ float swiglu(float a, float b, float L) {
   if (L > 0.0f) {   // comparisons that keep a NaN
@@ -135,40 +171,27 @@ __device__ __forceinline__ float swiglu(float a, float b, float L) {
 // Grid: [plan] [shared expert's tiles] [min(E, T K) experts' tiles] [gate scores, 4 tokens each].
 struct Fc1Shared {
   uint32_t mask[8];
-  int16_t id[kMaxRoutes];          // expert of each route, -1: none
+  int16_t id[kMaxRoutes];          // expert of each route, -1: none, -2: outside [-1, E)
   int16_t list[kMaxTokens];        // the group's routes
-  int count, invalid;
 };
 
-// Marks the experts in use; every thread returns behind a barrier.
+// Reads the table and marks the experts in use.
+template <int NT>
 __device__ __forceinline__ void read_table(const Args& a, Fc1Shared& s) {
   const int tid = threadIdx.x, n = a.T * a.K;
+  int e[(kMaxRoutes + NT - 1) / NT];
+#pragma unroll
+  for (int u = 0; u < (kMaxRoutes + NT - 1) / NT; ++u) {
+    const int i = tid + u * NT;
+    e[u] = i < n ? a.top[i] : -1;
+    if (e[u] < -1 || e[u] >= a.E) e[u] = -2;
+    if (i < n) s.id[i] = (int16_t)e[u];
+  }
   if (tid < 8) s.mask[tid] = 0;
-  if (tid == 0) s.invalid = 0;
-  for (int i = tid; i < n; i += 64 * kFc1Waves) {
-    const int e = a.top[i];
-    s.id[i] = (int16_t)(e >= 0 && e < a.E ? e : (e == -1 ? -1 : -2));
-  }
-  __syncthreads();
-  int keep[(kMaxRoutes + 64 * kFc1Waves - 1) / (64 * kFc1Waves)];
-#pragma unroll
-  for (int u = 0; u < kMaxRoutes / (64 * kFc1Waves); ++u) {
-    const int i = tid + u * 64 * kFc1Waves;
-    int e = i < n ? s.id[i] : -1;
-    for (int j = i - i % a.K; j < i && i < n; ++j)   // an expert listed again in its row is dropped
-      if (e >= 0 && s.id[j] == e) e = -2;
-    keep[u] = e;
-  }
   __syncthreads();
 #pragma unroll
-  for (int u = 0; u < kMaxRoutes / (64 * kFc1Waves); ++u) {
-    const int i = tid + u * 64 * kFc1Waves;
-    if (i < n) {
-      if (keep[u] == -2) s.invalid = 1;
-      s.id[i] = (int16_t)(keep[u] < 0 ? -1 : keep[u]);
-      if (keep[u] >= 0) atomicOr(&s.mask[keep[u] >> 5], 1u << (keep[u] & 31));
-    }
-  }
+  for (int u = 0; u < (kMaxRoutes + NT - 1) / NT; ++u)
+    if (e[u] >= 0) atomicOr(&s.mask[e[u] >> 5], 1u << (e[u] & 31));
   __syncthreads();
 }
 
@@ -186,124 +209,154 @@ __device__ __forceinline__ int group_expert(const Fc1Shared& s, int g) {
   return -1;
 }
 
-// The routes of expert e in order (wave 0; visible behind the next barrier).
-__device__ __forceinline__ void list_routes(const Args& a, Fc1Shared& s, int e) {
-  if (threadIdx.x >= 64) return;
-  const int lane = threadIdx.x, n = a.T * a.K;
+// Route i goes to expert e, and no earlier entry of its row does (an expert listed again
+// in a row is dropped).
+__device__ __forceinline__ bool takes(const Args& a, const Fc1Shared& s, int i, int e) {
+  if (i >= a.T * a.K || s.id[i] != e) return false;
+  for (int j = i - i % a.K; j < i; ++j)
+    if (s.id[j] == e) return false;
+  return true;
+}
+
+// Calls f(position, route) for the routes of expert e in order, one lane each; returns their
+// number.  One wave.
+template <class F>
+__device__ __forceinline__ int each_route(const Args& a, const Fc1Shared& s, int e, F&& f) {
+  const int lane = threadIdx.x & 63, n = a.T * a.K;
   int pos = 0;
   for (int i0 = 0; i0 < n; i0 += 64) {
-    const int i = i0 + lane;
-    const bool hit = i < n && s.id[i] == e;
+    const bool hit = takes(a, s, i0 + lane, e);
     const uint64_t m = __ballot(hit);
-    if (hit) s.list[pos + __popcll(m & ((1ull << lane) - 1))] = (int16_t)i;
+    if (hit) f(pos + __popcll(m & ((1ull << lane) - 1)), i0 + lane);
     pos += __popcll(m);
   }
-  if (lane == 0) s.count = pos;
+  return pos;
 }
 
-// The first workgroup leaves the plan for the second kernel: one wave a group lists its
-// routes by ballot, at the sum of the counts of the groups before it.
-__device__ __forceinline__ void write_plan(const Args& a, Fc1Shared& s, int* cnt /* LDS [kMaxExperts + 1] */) {
-  const int tid = threadIdx.x, n = a.T * a.K, lane = tid & 63;
-  if (tid == 0) a.plan->status = s.invalid ? 9 /* MOE_ERR_ROUTE_INVALID */ : 0;
-  for (int e = tid; e <= kMaxExperts; e += 64 * kFc1Waves) cnt[e] = 0;
-  __syncthreads();
-  for (int i = tid; i < n; i += 64 * kFc1Waves)
-    if (s.id[i] >= 0) atomicAdd(&cnt[s.id[i]], 1);
-  __syncthreads();
+// The first workgroup leaves the plan for the second kernel: one wave a group counts and
+// then lists its routes, at the sum of the counts of the groups before it.
+template <int NT>
+__device__ __forceinline__ void write_plan(const Args& a, const Fc1Shared& s, int* cnt /* LDS [kMaxExperts + 2] */) {
+  const int tid = threadIdx.x, n = a.T * a.K, lane = tid & 63, wave = tid >> 6;
   int groups = 0;
   for (int w = 0; w < 8; ++w) groups += __popc(s.mask[w]);
-  for (int g = tid >> 6; g <= groups; g += kFc1Waves) {
-    const int e = group_expert(s, g);       // -1 for the end mark
+  int* invalid = cnt + kMaxExperts + 1;
+  if (tid == 0) *invalid = 0;
+  __syncthreads();
+  for (int g = wave; g < groups; g += NT / 64) {
+    const int c = each_route(a, s, group_expert(s, g), [](int, int) {});
+    if (lane == 0) cnt[g] = c;
+  }
+  for (int i = tid; i < n; i += NT)
+    if (s.id[i] == -2 || (s.id[i] >= 0 && !takes(a, s, i, s.id[i]))) *invalid = 1;
+  __syncthreads();
+  if (tid == 0) {
+    a.plan->status = *invalid ? 9 /* MOE_ERR_ROUTE_INVALID */ : 0;
+    a.plan->groups = groups;
+  }
+  for (int g = wave; g <= groups; g += NT / 64) {
     int before = 0;
-    for (int f = lane; f < (e < 0 ? kMaxExperts : e); f += 64) before += cnt[f];
+    for (int f = lane; f < g; f += 64) before += cnt[f];
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) before += __shfl_xor(before, o);
-    if (lane == 0) {
-      a.plan->first[g] = before;
-      if (e >= 0) a.plan->expert[g] = e;
-      else a.plan->groups = groups;
-    }
-    if (e < 0) break;
-    for (int i0 = 0; i0 < n; i0 += 64) {
-      const bool hit = i0 + lane < n && s.id[i0 + lane] == e;
-      const uint64_t m = __ballot(hit);
-      if (hit) a.plan->route[before + __popcll(m & ((1ull << lane) - 1))] = i0 + lane;
-      before += __popcll(m);
-    }
+    if (lane == 0) a.plan->first[g] = before;
+    if (g == groups) break;
+    const int e = group_expert(s, g);
+    if (lane == 0) a.plan->expert[g] = e;
+    each_route(a, s, e, [&](int p, int i) {
+      a.plan->route[before + p] = i;
+      a.plan->weight[before + p] = a.rw[i];
+    });
   }
 }
 
-template <bool MX, int NF>
-__device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, float* red, int e, int i0, int count) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Columns c0 .. c0 + 16 NF - 1 (of `count`) of one tile.
+template <bool MX, int R, int W, int NF>
+__device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, float* red, int e, int i0, int c0,
+                                         int count) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int row = i0 + (r >> 1);
-  const uint8_t *w, *ws = nullptr;
-  if (e < 0) {
-    w = (r & 1 ? a.sup : a.sgate).row(0, row);
-  } else {
-    const MxRef& m = r & 1 ? a.up : a.gate;
-    w = m.data.row(e, row);
-    if constexpr (MX) ws = m.scale.row(e, row);
-  }
   const int steps = a.H / kStep;
-  const int s0 = wave * steps / kFc1Waves, s1 = (wave + 1) * steps / kFc1Waves;
-  w += (int64_t)s0 * WStep<MX>::kBytes + q * WStep<MX>::kLane;
-  ws += s0 * 4;
+  const int s0 = wave * steps / W, s1 = (wave + 1) * steps / W;
+  const uint8_t *w[R], *ws[R];
+#pragma unroll
+  for (int g = 0; g < R; ++g) {
+    const int row = i0 + 8 * g + (r >> 1);
+    ws[g] = nullptr;
+    if (e < 0) {
+      w[g] = (r & 1 ? a.sup : a.sgate).row(0, row);
+    } else {
+      const MxRef& m = r & 1 ? a.up : a.gate;
+      w[g] = m.data.row(e, row);
+      if constexpr (MX) ws[g] = m.scale.row(e, row) + s0 * 4;
+    }
+    w[g] += (int64_t)s0 * WStep<MX>::kBytes + q * WStep<MX>::kLane;
+  }
   const uint8_t* x[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
-    const int c = 16 * f + r < count ? 16 * f + r : 0;     // columns past the last repeat the first
+    const int c = c0 + 16 * f + r < count ? c0 + 16 * f + r : c0;   // columns past the last repeat one
     const int t = e < 0 ? c : s.list[c] / a.K;
     x[f] = reinterpret_cast<const uint8_t*>(a.x + (int64_t)t * a.H) + (int64_t)s0 * WStep<false>::kBytes +
            q * WStep<false>::kLane;
   }
-  f32x4_t acc[NF];
+  f32x4_t acc[R][NF];
 #pragma unroll
-  for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  dot_steps<MX, NF, depth<NF>()>(w, ws, x, s1 - s0, acc);
+  for (int g = 0; g < R; ++g)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) acc[g][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  dot_steps<MX, R, NF, depth<MX, R, NF>()>(w, ws, x, s1 - s0, acc);
   // [wave][column][row]: a lane has rows 4 q .. 4 q + 3 of column r
 #pragma unroll
-  for (int f = 0; f < NF; ++f)
-    *reinterpret_cast<f32x4_t*>(red + ((wave * NF + f) * 16 + r) * 16 + 4 * q) = acc[f];
+  for (int g = 0; g < R; ++g)
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+      *reinterpret_cast<f32x4_t*>(red + ((wave * NF + f) * 16 + r) * (16 * R) + 16 * g + 4 * q) = acc[g][f];
   __syncthreads();
-  for (int o = threadIdx.x; o < 8 * count; o += 64 * kFc1Waves) {
-    const int c = o >> 3, p = o & 7;
+  const int cols = min(16 * NF, count - c0);
+  for (int o = threadIdx.x; o < 8 * R * cols; o += 64 * W) {
+    const int c = o / (8 * R), p = o % (8 * R);
     float g = 0.0f, u = 0.0f;
 #pragma unroll
-    for (int v = 0; v < kFc1Waves; ++v) {
-      const float2 z = *reinterpret_cast<const float2*>(red + (v * NF * 16 + c) * 16 + 2 * p);
+    for (int v = 0; v < W; ++v) {
+      const float2 z = *reinterpret_cast<const float2*>(red + (v * NF * 16 + c) * (16 * R) + 2 * p);
       g += z.x;
       u += z.y;
     }
-    const int64_t hrow = e < 0 ? (int64_t)a.T * a.K + c : s.list[c];
+    const int64_t hrow = e < 0 ? (int64_t)a.T * a.K + c0 + c : s.list[c0 + c];
     a.h[hrow * a.I + i0 + p] = (uint16_t)f2bf(swiglu(g, u, a.limit));
   }
 }
 
-template <bool MX>
+// More than 32 tokens go in passes over the tile's weights, which the caches then hold.
+template <bool MX, int R, int W>
 __device__ __forceinline__ void fc1_group(const Args& a, const Fc1Shared& s, float* red, int e, int i0, int count) {
-  if (count <= 16) fc1_tile<MX, 1>(a, s, red, e, i0, count);
-  else if (count <= 32) fc1_tile<MX, 2>(a, s, red, e, i0, count);
-  else fc1_tile<MX, 4>(a, s, red, e, i0, count);
+  if (count <= 16) {
+    fc1_tile<MX, R, W, 1>(a, s, red, e, i0, 0, count);
+    return;
+  }
+  for (int c0 = 0; c0 < count; c0 += 32) {
+    if (c0) __syncthreads();
+    fc1_tile<MX, R, W, 2>(a, s, red, e, i0, c0, count);
+  }
 }
 
-template <bool MX>
-__global__ __launch_bounds__(64 * kFc1Waves, 4) void k_decode_fc1(Args a) {
+template <bool MX, int R, int W>
+__global__ __launch_bounds__(64 * W, 4) void k_decode_fc1(Args a) {
   __shared__ Fc1Shared s;
-  __shared__ __align__(16) float red[kFc1Waves * 4 * 256];
-  const int tiles = a.I / 8;
-  const int shared_blocks = a.shared ? tiles : 0;
+  __shared__ __align__(16) float red[W * 2 * 256 * R];
+  const int tiles = a.I / (8 * R);
+  constexpr int RS = MX ? 1 : R;                      // BF16 fragments take twice the registers
+  const int shared_blocks = a.shared ? a.I / (8 * RS) : 0;
   const int routed_blocks = min(a.E, a.T * a.K) * tiles;
   if (blockIdx.x == 0) {
-    read_table(a, s);
-    write_plan(a, s, reinterpret_cast<int*>(red));
+    read_table<64 * W>(a, s);
+    write_plan<64 * W>(a, s, reinterpret_cast<int*>(red));
     return;
   }
   int b = blockIdx.x - 1;
   if (b >= shared_blocks + routed_blocks) {   // shared output gate: one wave a token
-    const int t = (b - shared_blocks - routed_blocks) * kFc1Waves + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int t = (b - shared_blocks - routed_blocks) * W + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (t >= a.T) return;
     float v = 0.0f;
     for (int c = lane; c < a.H / 8; c += 64) {
@@ -319,16 +372,17 @@ __global__ __launch_bounds__(64 * kFc1Waves, 4) void k_decode_fc1(Args a) {
     return;
   }
   if (b < shared_blocks) {
-    fc1_group<false>(a, s, red, -1, b * 8, a.T);
+    fc1_group<false, RS, W>(a, s, red, -1, b * 8 * RS, a.T);
     return;
   }
   b -= shared_blocks;
-  read_table(a, s);
-  const int e = group_expert(s, b / tiles);
+  read_table<64 * W>(a, s);
+  const int e = __builtin_amdgcn_readfirstlane(group_expert(s, b / tiles));
   if (e < 0) return;
-  list_routes(a, s, e);
-  __syncthreads();
-  fc1_group<MX>(a, s, red, e, b % tiles * 8, s.count);
+  // every wave lists the routes for itself, to the same place with the same values
+  const int count = each_route(a, s, e, [&](int p, int i) { s.list[p] = (int16_t)i; });
+  __builtin_amdgcn_wave_barrier();
+  fc1_group<MX, R, W>(a, s, red, e, b % tiles * 8 * R, count);
 }
 
 // ---------------------------------------------------------------- FC2 + combine
@@ -338,48 +392,45 @@ __global__ __launch_bounds__(64 * kFc1Waves, 4) void k_decode_fc1(Args a) {
 // order at the end.
 struct Fc2Shared {
   int32_t expert[kMaxExperts + 1], first[kMaxExperts + 2];
-  int16_t route[kMaxRoutes], token[kMaxRoutes];
+  int16_t route[kMaxRoutes];
   float weight[kMaxRoutes], gate[kMaxTokens];
 };
 
+// Columns c0 .. of one expert, steps s0 .. s0 + n - 1.
 template <bool MX, int NF>
 __device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, float* acc_lds, int n0, int e, int first,
-                                         int count, int s0, int n) {
+                                         int c0, int count, int s0, int n) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const uint8_t *w, *ws = nullptr;
+  const uint8_t *w[1], *ws[1] = {nullptr};
   if (e < 0) {
-    w = a.sdown.row(0, n0 + r);
+    w[0] = a.sdown.row(0, n0 + r);
   } else {
-    w = a.down.data.row(e, n0 + r);
-    if constexpr (MX) ws = a.down.scale.row(e, n0 + r);
+    w[0] = a.down.data.row(e, n0 + r);
+    if constexpr (MX) ws[0] = a.down.scale.row(e, n0 + r) + s0 * 4;
   }
-  w += (int64_t)s0 * WStep<MX>::kBytes + q * WStep<MX>::kLane;
-  ws += s0 * 4;
+  w[0] += (int64_t)s0 * WStep<MX>::kBytes + q * WStep<MX>::kLane;
   const uint8_t* x[NF];
-  int tok[NF];
-  float wt[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
-    const int c = 16 * f + r;
-    const bool on = c < count;
-    const int cc = on ? c : 0;
-    tok[f] = !on ? -1 : (e < 0 ? cc : s.token[first + cc]);
-    wt[f] = e < 0 ? s.gate[cc] : s.weight[first + cc];
-    const int64_t hrow = e < 0 ? (int64_t)a.T * a.K + cc : s.route[first + cc];
+    const int c = c0 + 16 * f + r < count ? c0 + 16 * f + r : c0;
+    const int64_t hrow = e < 0 ? (int64_t)a.T * a.K + c : s.route[first + c];
     x[f] = reinterpret_cast<const uint8_t*>(a.h + hrow * a.I) + (int64_t)s0 * WStep<false>::kBytes +
            q * WStep<false>::kLane;
   }
-  f32x4_t acc[NF];
+  f32x4_t acc[1][NF];
 #pragma unroll
-  for (int f = 0; f < NF; ++f) acc[f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  dot_steps<MX, NF, depth<NF>()>(w, ws, x, n, acc);
+  for (int f = 0; f < NF; ++f) acc[0][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  dot_steps<MX, 1, NF, depth<MX, 1, NF>()>(w, ws, x, n, acc);
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
-    if (tok[f] < 0) continue;
-    f32x4_t* o = reinterpret_cast<f32x4_t*>(acc_lds + tok[f] * 16 + 4 * q);   // the wave's own
+    const int c = c0 + 16 * f + r;
+    if (c >= count) continue;
+    const int tok = e < 0 ? c : s.route[first + c] / a.K;
+    const float wt = e < 0 ? s.gate[c] : s.weight[first + c];
+    f32x4_t* o = reinterpret_cast<f32x4_t*>(acc_lds + tok * 16 + 4 * q);   // the wave's own
     f32x4_t v = *o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += wt[f] * acc[f][i];
+    for (int i = 0; i < 4; ++i) v[i] += wt * acc[0][f][i];
     *o = v;
   }
 }
@@ -387,25 +438,25 @@ __device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, floa
 template <bool MX>
 __device__ __forceinline__ void fc2_group(const Args& a, const Fc2Shared& s, float* acc_lds, int n0, int e, int first,
                                           int count, int s0, int n) {
-  if (count <= 16) fc2_part<MX, 1>(a, s, acc_lds, n0, e, first, count, s0, n);
-  else if (count <= 32) fc2_part<MX, 2>(a, s, acc_lds, n0, e, first, count, s0, n);
-  else fc2_part<MX, 4>(a, s, acc_lds, n0, e, first, count, s0, n);
+  if (count <= 16) {
+    fc2_part<MX, 1>(a, s, acc_lds, n0, e, first, 0, count, s0, n);
+    return;
+  }
+  for (int c0 = 0; c0 < count; c0 += 32) fc2_part<MX, 2>(a, s, acc_lds, n0, e, first, c0, count, s0, n);
 }
 
 template <bool MX>
-__global__ __launch_bounds__(64 * kFc2Waves, 2) void k_decode_fc2(Args a) {
+__global__ __launch_bounds__(64 * kFc2Waves, 4) void k_decode_fc2(Args a) {
   extern __shared__ __align__(16) float acc_all[];   // [kFc2Waves][T][16]
   __shared__ Fc2Shared s;
-  const int tid = threadIdx.x, wave = tid >> 6;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // whole arrays, past the plan's ends too: no load waits for another
   const int routed = a.plan->groups;
-  for (int g = tid; g < routed; g += 64 * kFc2Waves) s.expert[g] = a.plan->expert[g];
-  for (int g = tid; g <= routed; g += 64 * kFc2Waves) s.first[g] = a.plan->first[g];
-  const int routes = a.plan->first[routed];
-  for (int i = tid; i < routes; i += 64 * kFc2Waves) {
-    const int rt = a.plan->route[i];
-    s.route[i] = (int16_t)rt;
-    s.token[i] = (int16_t)(rt / a.K);
-    s.weight[i] = a.rw[rt];
+  if (tid <= kMaxExperts) s.expert[tid] = a.plan->expert[tid];
+  if (tid < kMaxExperts + 2) s.first[tid] = a.plan->first[tid];
+  if (tid < a.T * a.K) {
+    s.route[tid] = (int16_t)a.plan->route[tid];
+    s.weight[tid] = a.plan->weight[tid];
   }
   if (tid < a.T) s.gate[tid] = a.gw ? a.gate_s[tid] : 1.0f;
   for (int i = tid; i < kFc2Waves * a.T * 16; i += 64 * kFc2Waves) acc_all[i] = 0.0f;
@@ -418,13 +469,15 @@ __global__ __launch_bounds__(64 * kFc2Waves, 2) void k_decode_fc2(Args a) {
   int64_t p = wave * total / kFc2Waves;
   const int64_t end = (wave + 1) * total / kFc2Waves;
   while (p < end) {
-    const int g = (int)(p / steps), s0 = (int)(p % steps);
+    const int g = (int)(p / steps), s0 = (int)(p % steps);   // uniform in the wave
     const int n = (int)min((int64_t)(steps - s0), end - p);
     if (a.shared && g == 0) {
       fc2_group<false>(a, s, mine, n0, -1, 0, a.T, s0, n);
     } else {
       const int u = g - (a.shared ? 1 : 0);
-      fc2_group<MX>(a, s, mine, n0, s.expert[u], s.first[u], s.first[u + 1] - s.first[u], s0, n);
+      const int e = __builtin_amdgcn_readfirstlane(s.expert[u]), first = __builtin_amdgcn_readfirstlane(s.first[u]);
+      const int count = __builtin_amdgcn_readfirstlane(s.first[u + 1]) - first;
+      fc2_group<MX>(a, s, mine, n0, e, first, count, s0, n);
     }
     p += n;
   }
@@ -441,13 +494,16 @@ __global__ __launch_bounds__(64 * kFc2Waves, 2) void k_decode_fc2(Args a) {
 
 template <bool MX>
 void launch_fc1(hipStream_t st, const Args& a) {
-  const int tiles = a.I / 8, used = a.E < a.T * a.K ? a.E : a.T * a.K;
-  const int gate = a.gw ? (a.T + kFc1Waves - 1) / kFc1Waves : 0;
-  hipLaunchKernelGGL((k_decode_fc1<MX>), dim3((unsigned)(1 + (used + (a.shared ? 1 : 0)) * tiles + gate)),
-                     dim3(64 * kFc1Waves), 0, st, a);
+  constexpr int R = MX ? DEC_R_MX : DEC_R_BF, W = kFc1Waves;
+  const int tiles = a.I / (8 * R), used = a.E < a.T * a.K ? a.E : a.T * a.K;
+  const int gate = a.gw ? (a.T + W - 1) / W : 0;
+  const int shared = a.shared ? a.I / (8 * (MX ? 1 : R)) : 0;
+  hipLaunchKernelGGL((k_decode_fc1<MX, R, W>), dim3((unsigned)(1 + shared + used * tiles + gate)), dim3(64 * W), 0,
+                     st, a);
 }
 template <bool MX>
 void launch_fc2(hipStream_t st, const Args& a) {
+  static_assert(64 * kFc2Waves >= kMaxRoutes && 64 * kFc2Waves >= kMaxExperts + 2, "the plan in one load a thread");
   hipLaunchKernelGGL((k_decode_fc2<MX>), dim3(a.H / 16), dim3(64 * kFc2Waves),
                      (size_t)kFc2Waves * a.T * 16 * sizeof(float), st, a);
 }

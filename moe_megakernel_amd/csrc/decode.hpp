@@ -17,6 +17,7 @@ struct Plan {
   int32_t expert[kMaxExperts + 1];
   int32_t first[kMaxExperts + 2];                     // into route; first[groups] = routes
   int32_t route[kMaxRoutes];
+  float weight[kMaxRoutes];                           // of the routes
 };
 
 struct Args {
