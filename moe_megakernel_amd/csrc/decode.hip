@@ -26,10 +26,7 @@ namespace decode {
 namespace {
 
 constexpr int kStep = 128;          // elements of the contraction per step (the ABI's multiple)
-#ifndef DEC_W1
-#define DEC_W1 4
-#endif
-constexpr int kFc1Waves = DEC_W1, kFc2Waves = 8;
+constexpr int kFc1Waves = 4;
 
 // Loads through global (not flat) addresses: the pointers may come out of a table in
 // memory, which hides their address space, and a flat load is waited for with every other
@@ -43,37 +40,105 @@ __device__ __forceinline__ uint32_t ld4(const uint8_t* p) {
   return *(const __attribute__((address_space(1))) uint32_t*)(uintptr_t)p;
 }
 
-// One step of 16 weight rows: lane (r = lane & 15, q = lane >> 4) has elements
-// 64 s + 16 q .. + 15 of row r, s = 0, 1.
+// One step is 128 elements of the contraction, four products of 32.  Lane (r, q) of a
+// product (r = lane & 15, q = lane >> 4) holds 8 elements of row r (weights) or column r
+// (tokens); which 8 is free as long as both operands agree:
+//   BF16 weights:  product j takes elements 32 j + 8 q .. + 7
+//   E4M3 weights:  products 2 s and 2 s + 1 take elements 64 s + 16 q .. + 7 and + 8 .. + 15, so
+//                  that a lane's 16 bytes serve two products and lie in one block of 32
+// Loading straight into that layout would give neighbouring lanes different rows, and the
+// address unit then handles one lane a clock: 64 clocks a load instead of 16 (measured on
+// E4M3 experts, 64 tokens, H 7168: 327 us against 244 us).  So a load takes 64 consecutive bytes
+// of 16 rows, four lanes a row, and each wave turns it round through 1 KB of LDS of its
+// own.  LDS operations of a wave run in order, so one such slot serves every load in turn and
+// needs no barrier.
+
+// Slot position (16-byte cells) of chunk c of row `row`: rows two apart land in different
+// banks, for the writes (2 rows, 4 chunks by 8 lanes) and the reads (8 rows, one chunk) alike.
+__device__ __forceinline__ int cell(int row, int c) { return 4 * row + (c ^ ((row >> 1) & 3)); }
+
+// The wave's turn-round slots: one for weights, two for tokens (E4M3 products take their
+// 8 elements from every other chunk of two loads).
+struct Turn {
+  uint4* w;
+  uint4* x;
+  uint32_t* scale;         // [R][16][kScaleRow] (MXFP8)
+  int put;                 // cell this lane's loads go to
+  int row, q;              // the lane's row and element group in a product
+};
+constexpr int kTurnCells = 3 * 64;
+
+// E8M0 scales of up to kScaleSteps steps of 16 rows: a row's four bytes of a step are far from
+// the next row's, so fetching them step by step would cost as many cache lines as the
+// weights; the four lanes of a row fetch four steps at once, and products read them here.
+constexpr int kScaleSteps = 16, kScaleRow = kScaleSteps + 1;      // words; the odd stride spreads rows over banks
+constexpr int kScaleCells = 16 * kScaleRow / 4;
+
+// A wave's LDS for row fragments 0 .. R - 1, in 16-byte cells.
+template <bool MX, int R>
+constexpr int wave_cells() { return kTurnCells + (MX ? R * kScaleCells : 0); }
+__device__ __forceinline__ Turn turn_of(uint4* scratch) {
+  const int lane = threadIdx.x & 63;
+  return {scratch, scratch + 64, reinterpret_cast<uint32_t*>(scratch + kTurnCells), cell(lane >> 2, lane & 3),
+          lane & 15, lane >> 4};
+}
+
+// 16 token columns, one step: lane l loads chunk l & 3 (16 bytes) of column l >> 2.
+struct XStep {
+  uint4 v[4];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = ld16(p + 64 * j);
+  }
+  // products 2 s and 2 s + 1
+  template <bool MX>
+  __device__ __forceinline__ void frags(const Turn& t, int s, bf16x8_t (&o)[2]) const {
+    t.x[t.put] = v[2 * s];
+    t.x[64 + t.put] = v[2 * s + 1];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)   // E4M3: elements 64 s + 16 q + 8 u .. are chunk 2 q + u of the eight
+      o[u] = __builtin_bit_cast(bf16x8_t, MX ? t.x[(t.q >> 1) * 64 + cell(t.row, 2 * (t.q & 1) + u)]
+                                             : t.x[u * 64 + cell(t.row, t.q)]);
+  }
+  static constexpr int kBytes = 2 * kStep;
+};
+
+// 16 weight rows, one step: lane l loads chunk l & 3 of row l >> 2.
 template <bool MX>
 struct WStep;
 template <>
 struct WStep<false> {
   uint4 v[4];
-  __device__ __forceinline__ void load(const uint8_t* p, const uint8_t*) {
-    v[0] = ld16(p);
-    v[1] = ld16(p + 16);
-    v[2] = ld16(p + 128);
-    v[3] = ld16(p + 144);
+  __device__ __forceinline__ void load(const uint8_t* p) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = ld16(p + 64 * j);
   }
-  // the 8 elements 64 s + 16 q + 8 u ..
-  __device__ __forceinline__ bf16x8_t frag(int s, int u, int) const {
-    return __builtin_bit_cast(bf16x8_t, v[2 * s + u]);
+  __device__ __forceinline__ void frags(const Turn& t, int s, int, bf16x8_t (&o)[2]) const {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      t.w[t.put] = v[2 * s + u];
+      o[u] = __builtin_bit_cast(bf16x8_t, t.w[cell(t.row, t.q)]);
+    }
   }
-  static constexpr int kBytes = 2 * kStep, kLane = 32;   // bytes per row and step; per q
+  static constexpr int kBytes = 2 * kStep;
 };
 template <>
 struct WStep<true> {
   uint4 v[2];
-  uint32_t sc;   // E8M0 of the row's four blocks of 32
-  __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* s) {
+  __device__ __forceinline__ void load(const uint8_t* p) {
     v[0] = ld16(p);
     v[1] = ld16(p + 64);
-    sc = ld4(s);
   }
-  __device__ __forceinline__ bf16x8_t frag(int s, int u, int q) const {
-    const float scale = __uint_as_float(((sc >> (16 * s + 8 * (q >> 1))) & 0xffu) << 23);
-    const uint32_t lo = u ? v[s].z : v[s].x, hi = u ? v[s].w : v[s].y;
+  // word: the step's place in t.scale (of row 0)
+  __device__ __forceinline__ void frags(const Turn& t, int s, int word, bf16x8_t (&o)[2]) const {
+    const uint32_t sr = t.scale[word + t.row * kScaleRow];
+    t.w[t.put] = v[s];
+    const uint4 b = t.w[cell(t.row, t.q)];
+    const float scale = __uint_as_float(((sr >> (16 * s + 8 * (t.q >> 1))) & 0xffu) << 23);
+    o[0] = decode8(b.x, b.y, scale);
+    o[1] = decode8(b.z, b.w, scale);
+  }
+  __device__ static __forceinline__ bf16x8_t decode8(uint32_t lo, uint32_t hi, float scale) {
     const u32x4_t r = {
         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false)),
         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true)),
@@ -81,45 +146,65 @@ struct WStep<true> {
         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true))};
     return __builtin_bit_cast(bf16x8_t, r);
   }
-  static constexpr int kBytes = kStep, kLane = 16;
+  static constexpr int kBytes = kStep;
 };
 
-// acc[g][f] += W_g (16 rows) X_f^T (16 columns) over n steps.  w, ws: the lane's rows at
-// their first element (scales: the rows' first block); x: the lane's columns at their first
-// element.  D steps are in flight; the steady loop has no conditions.
+// acc[g][f] += W_g (16 rows) X_f^T (16 columns) over n steps (MXFP8: at most kScaleSteps).
+// w, ws: the loading lane's rows at their first element (scales: the rows' first block); x: the
+// loading lane's columns at their first element.  D steps are in flight; the steady loop
+// has no conditions.
 template <bool MX, int R, int NF, int D>
-__device__ __forceinline__ void dot_steps(const uint8_t* const (&w)[R], const uint8_t* const (&ws)[R],
+__device__ __forceinline__ void dot_chunk(const Turn& t, const uint8_t* const (&w)[R], const uint8_t* const (&ws)[R],
                                           const uint8_t* const (&x)[NF], int n, f32x4_t (&acc)[R][NF]) {
-  const int q = (threadIdx.x & 63) >> 4;
   WStep<MX> wr[D][R];
-  WStep<false> xr[D][NF];
+  XStep xr[D][NF];
   auto load = [&](int d, int i) __attribute__((always_inline)) {
 #pragma unroll
-    for (int g = 0; g < R; ++g) wr[d][g].load(w[g] + (int64_t)i * WStep<MX>::kBytes, ws[g] + i * 4);
+    for (int g = 0; g < R; ++g) wr[d][g].load(w[g] + (int64_t)i * WStep<MX>::kBytes);
 #pragma unroll
-    for (int f = 0; f < NF; ++f) xr[d][f].load(x[f] + i * WStep<false>::kBytes, nullptr);
+    for (int f = 0; f < NF; ++f) xr[d][f].load(x[f] + i * XStep::kBytes);
   };
-  auto mul = [&](int d) __attribute__((always_inline)) {
+  auto mul = [&](int d, int i) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < 2; ++s) {
+      bf16x8_t b[NF][2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int f = 0; f < NF; ++f) xr[d][f].template frags<MX>(t, s, b[f]);
 #pragma unroll
-        for (int g = 0; g < R; ++g) {
-          const bf16x8_t a = wr[d][g].frag(s, u, q);
+      for (int g = 0; g < R; ++g) {
+        bf16x8_t a[2];
+        wr[d][g].frags(t, s, g * 16 * kScaleRow + i, a);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int f = 0; f < NF; ++f)
-            acc[g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, xr[d][f].frag(s, u, q), acc[g][f], 0, 0, 0);
-        }
+            acc[g][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u], b[f][u], acc[g][f], 0, 0, 0);
+      }
+    }
   };
+  [[maybe_unused]] uint32_t sc[R][kScaleSteps / 4];
+  const int lane = threadIdx.x & 63;
+  if constexpr (MX) {
+#pragma unroll
+    for (int g = 0; g < R; ++g)
+#pragma unroll
+      for (int m = 0; m < kScaleSteps / 4; ++m) sc[g][m] = ld4(ws[g] + 4 * min(4 * m + (lane & 3), n - 1));
+  }
 #pragma unroll
   for (int d = 0; d < D; ++d)
     if (d < n) load(d, d);
+  if constexpr (MX) {
+#pragma unroll
+    for (int g = 0; g < R; ++g)
+#pragma unroll
+      for (int m = 0; m < kScaleSteps / 4; ++m)
+        t.scale[(g * 16 + (lane >> 2)) * kScaleRow + 4 * m + (lane & 3)] = sc[g][m];
+  }
   int i = 0;
   for (; i + 2 * D <= n; i += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      mul(d);
+      mul(d, i + d);
       load(d, i + D + d);
       __builtin_amdgcn_sched_barrier(0);   // the next stage's products stay behind these loads
     }
@@ -127,35 +212,39 @@ __device__ __forceinline__ void dot_steps(const uint8_t* const (&w)[R], const ui
 #pragma unroll
   for (int d = 0; d < D; ++d)
     if (i + d < n) {
-      mul(d);
+      mul(d, i + d);
       if (i + D + d < n) load(d, i + D + d);
     }
 #pragma unroll
   for (int d = 0; d < D; ++d)
-    if (i + D + d < n) mul(d);
+    if (i + D + d < n) mul(d, i + D + d);
 }
 
-#ifndef DEC_D_BF
-#define DEC_D_BF 2
-#endif
-#ifndef DEC_D_MX
-#define DEC_D_MX 2
-#endif
-#ifndef DEC_R_BF
-#define DEC_R_BF 1
-#endif
-#ifndef DEC_R_MX
-#define DEC_R_MX 2
-#endif
-#ifndef DEC_D2_MX
-#define DEC_D2_MX 3
-#endif
-// Steps in flight: what fits 128 registers beside the accumulators and addresses.
-template <bool MX, int R, int NF>
-constexpr int depth() {
-  if (NF == 2) return 1;
-  return MX ? (R == 1 ? DEC_D2_MX : DEC_D_MX) : (R == 1 ? DEC_D_BF : 2);
+template <bool MX, int R, int NF, int D>
+__device__ __forceinline__ void dot_steps(const Turn& t, const uint8_t* const (&w)[R], const uint8_t* const (&ws)[R],
+                                          const uint8_t* const (&x)[NF], int n, f32x4_t (&acc)[R][NF]) {
+  if constexpr (!MX) {
+    dot_chunk<MX, R, NF, D>(t, w, ws, x, n, acc);
+  } else {
+    const uint8_t *wc[R], *wsc[R], *xc[NF];
+    for (int i0 = 0; i0 < n; i0 += kScaleSteps) {
+#pragma unroll
+      for (int g = 0; g < R; ++g) {
+        wc[g] = w[g] + (int64_t)i0 * WStep<MX>::kBytes;
+        wsc[g] = ws[g] + i0 * 4;
+      }
+#pragma unroll
+      for (int f = 0; f < NF; ++f) xc[f] = x[f] + (int64_t)i0 * XStep::kBytes;
+      dot_chunk<MX, R, NF, D>(t, wc, wsc, xc, min(kScaleSteps, n - i0), acc);
+    }
+  }
 }
+
+// Steps in flight by the number of column groups: what fits 128 registers (four waves a
+// SIMD) beside the accumulators and addresses.  Spills cost more than depth gains: E4M3 at 3
+// steps took 36 us where 2 take 30 (the second kernel, 7 tokens, H 4096, 96 experts).
+template <bool MX, int R, int NF>
+constexpr int depth() { return NF == 2 || R == 2 ? 1 : 2; }
 
 __device__ __forceinline__ float swiglu(float a, float b, float L) {
   if (L > 0.0f) {   // comparisons that keep a NaN
@@ -272,10 +361,10 @@ __device__ __forceinline__ void write_plan(const Args& a, const Fc1Shared& s, in
 
 // Columns c0 .. c0 + 16 NF - 1 (of `count`) of one tile.
 template <bool MX, int R, int W, int NF>
-__device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, float* red, int e, int i0, int c0,
+__device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint4* lds, int e, int i0, int c0,
                                          int count) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, q = lane >> 4;
+  const int r = lane >> 2, c4 = 16 * (lane & 3);   // the row and byte this lane loads
   const int steps = a.H / kStep;
   const int s0 = wave * steps / W, s1 = (wave + 1) * steps / W;
   const uint8_t *w[R], *ws[R];
@@ -290,28 +379,30 @@ __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, floa
       w[g] = m.data.row(e, row);
       if constexpr (MX) ws[g] = m.scale.row(e, row) + s0 * 4;
     }
-    w[g] += (int64_t)s0 * WStep<MX>::kBytes + q * WStep<MX>::kLane;
+    w[g] += (int64_t)s0 * WStep<MX>::kBytes + c4;
   }
   const uint8_t* x[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
     const int c = c0 + 16 * f + r < count ? c0 + 16 * f + r : c0;   // columns past the last repeat one
     const int t = e < 0 ? c : s.list[c] / a.K;
-    x[f] = reinterpret_cast<const uint8_t*>(a.x + (int64_t)t * a.H) + (int64_t)s0 * WStep<false>::kBytes +
-           q * WStep<false>::kLane;
+    x[f] = reinterpret_cast<const uint8_t*>(a.x + (int64_t)t * a.H) + (int64_t)s0 * XStep::kBytes + c4;
   }
   f32x4_t acc[R][NF];
 #pragma unroll
   for (int g = 0; g < R; ++g)
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[g][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  dot_steps<MX, R, NF, depth<MX, R, NF>()>(w, ws, x, s1 - s0, acc);
-  // [wave][column][row]: a lane has rows 4 q .. 4 q + 3 of column r
+  const Turn turn = turn_of(lds + wave * wave_cells<MX, R>());
+  dot_steps<MX, R, NF, depth<MX, R, NF>()>(turn, w, ws, x, s1 - s0, acc);
+  // [wave][column][row]: a lane has rows 4 q .. 4 q + 3 of column r.  Over the turn-round slots
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (int g = 0; g < R; ++g)
 #pragma unroll
     for (int f = 0; f < NF; ++f)
-      *reinterpret_cast<f32x4_t*>(red + ((wave * NF + f) * 16 + r) * (16 * R) + 16 * g + 4 * q) = acc[g][f];
+      *reinterpret_cast<f32x4_t*>(red + ((wave * NF + f) * 16 + turn.row) * (16 * R) + 16 * g + 4 * turn.q) = acc[g][f];
   __syncthreads();
   const int cols = min(16 * NF, count - c0);
   for (int o = threadIdx.x; o < 8 * R * cols; o += 64 * W) {
@@ -328,30 +419,33 @@ __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, floa
   }
 }
 
-// More than 32 tokens go in passes over the tile's weights, which the caches then hold.
+// More than 16 tokens go in passes over one fragment's weights, which the caches then hold.
 template <bool MX, int R, int W>
-__device__ __forceinline__ void fc1_group(const Args& a, const Fc1Shared& s, float* red, int e, int i0, int count) {
+__device__ __forceinline__ void fc1_group(const Args& a, const Fc1Shared& s, uint4* lds, int e, int i0, int count) {
   if (count <= 16) {
-    fc1_tile<MX, R, W, 1>(a, s, red, e, i0, 0, count);
+    fc1_tile<MX, R, W, 1>(a, s, lds, e, i0, 0, count);
     return;
   }
-  for (int c0 = 0; c0 < count; c0 += 32) {
-    if (c0) __syncthreads();
-    fc1_tile<MX, R, W, 2>(a, s, red, e, i0, c0, count);
-  }
+  for (int g = 0; g < R; ++g)
+    for (int c0 = 0; c0 < count; c0 += 32) {
+      if (g + c0) __syncthreads();
+      fc1_tile<MX, 1, W, 2>(a, s, lds, e, i0 + 8 * g, c0, count);
+    }
 }
 
 template <bool MX, int R, int W>
 __global__ __launch_bounds__(64 * W, 4) void k_decode_fc1(Args a) {
   __shared__ Fc1Shared s;
-  __shared__ __align__(16) float red[W * 2 * 256 * R];
+  // turn-round slots, then the partial sums of up to two column groups
+  constexpr int kCells = wave_cells<MX, R>() > 2 * R * 64 ? wave_cells<MX, R>() : 2 * R * 64;
+  __shared__ __align__(16) uint4 lds[W * kCells];
   const int tiles = a.I / (8 * R);
   constexpr int RS = MX ? 1 : R;                      // BF16 fragments take twice the registers
   const int shared_blocks = a.shared ? a.I / (8 * RS) : 0;
   const int routed_blocks = min(a.E, a.T * a.K) * tiles;
   if (blockIdx.x == 0) {
     read_table<64 * W>(a, s);
-    write_plan<64 * W>(a, s, reinterpret_cast<int*>(red));
+    write_plan<64 * W>(a, s, reinterpret_cast<int*>(lds));
     return;
   }
   int b = blockIdx.x - 1;
@@ -372,7 +466,7 @@ __global__ __launch_bounds__(64 * W, 4) void k_decode_fc1(Args a) {
     return;
   }
   if (b < shared_blocks) {
-    fc1_group<false, RS, W>(a, s, red, -1, b * 8 * RS, a.T);
+    fc1_group<false, RS, W>(a, s, lds, -1, b * 8 * RS, a.T);
     return;
   }
   b -= shared_blocks;
@@ -382,11 +476,11 @@ __global__ __launch_bounds__(64 * W, 4) void k_decode_fc1(Args a) {
   // every wave lists the routes for itself, to the same place with the same values
   const int count = each_route(a, s, e, [&](int p, int i) { s.list[p] = (int16_t)i; });
   __builtin_amdgcn_wave_barrier();
-  fc1_group<MX, R, W>(a, s, red, e, b % tiles * 8 * R, count);
+  fc1_group<MX, R, W>(a, s, lds, e, b % tiles * 8 * R, count);
 }
 
 // ---------------------------------------------------------------- FC2 + combine
-// A workgroup owns 16 output columns of every token.  Its 8 waves split the steps of all
+// A workgroup owns 16 output columns of every token.  Its W waves split the steps of all
 // experts in use evenly; each adds w_tk times what it has of an expert's product to an
 // accumulator [token][16] of its own in LDS, and the waves' accumulators are joined in
 // order at the end.
@@ -398,9 +492,9 @@ struct Fc2Shared {
 
 // Columns c0 .. of one expert, steps s0 .. s0 + n - 1.
 template <bool MX, int NF>
-__device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, float* acc_lds, int n0, int e, int first,
-                                         int c0, int count, int s0, int n) {
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+__device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, const Turn& turn, float* acc_lds, int n0,
+                                         int e, int first, int c0, int count, int s0, int n) {
+  const int lane = threadIdx.x & 63, r = lane >> 2, c4 = 16 * (lane & 3);   // the row and byte this lane loads
   const uint8_t *w[1], *ws[1] = {nullptr};
   if (e < 0) {
     w[0] = a.sdown.row(0, n0 + r);
@@ -408,26 +502,25 @@ __device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, floa
     w[0] = a.down.data.row(e, n0 + r);
     if constexpr (MX) ws[0] = a.down.scale.row(e, n0 + r) + s0 * 4;
   }
-  w[0] += (int64_t)s0 * WStep<MX>::kBytes + q * WStep<MX>::kLane;
+  w[0] += (int64_t)s0 * WStep<MX>::kBytes + c4;
   const uint8_t* x[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
     const int c = c0 + 16 * f + r < count ? c0 + 16 * f + r : c0;
     const int64_t hrow = e < 0 ? (int64_t)a.T * a.K + c : s.route[first + c];
-    x[f] = reinterpret_cast<const uint8_t*>(a.h + hrow * a.I) + (int64_t)s0 * WStep<false>::kBytes +
-           q * WStep<false>::kLane;
+    x[f] = reinterpret_cast<const uint8_t*>(a.h + hrow * a.I) + (int64_t)s0 * XStep::kBytes + c4;
   }
   f32x4_t acc[1][NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) acc[0][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  dot_steps<MX, 1, NF, depth<MX, 1, NF>()>(w, ws, x, n, acc);
+  dot_steps<MX, 1, NF, depth<MX, 1, NF>()>(turn, w, ws, x, n, acc);
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
-    const int c = c0 + 16 * f + r;
+    const int c = c0 + 16 * f + turn.row;
     if (c >= count) continue;
     const int tok = e < 0 ? c : s.route[first + c] / a.K;
     const float wt = e < 0 ? s.gate[c] : s.weight[first + c];
-    f32x4_t* o = reinterpret_cast<f32x4_t*>(acc_lds + tok * 16 + 4 * q);   // the wave's own
+    f32x4_t* o = reinterpret_cast<f32x4_t*>(acc_lds + tok * 16 + 4 * turn.q);   // the wave's own
     f32x4_t v = *o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += wt * acc[0][f][i];
@@ -436,19 +529,20 @@ __device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, floa
 }
 
 template <bool MX>
-__device__ __forceinline__ void fc2_group(const Args& a, const Fc2Shared& s, float* acc_lds, int n0, int e, int first,
-                                          int count, int s0, int n) {
+__device__ __forceinline__ void fc2_group(const Args& a, const Fc2Shared& s, const Turn& turn, float* acc_lds, int n0,
+                                          int e, int first, int count, int s0, int n) {
   if (count <= 16) {
-    fc2_part<MX, 1>(a, s, acc_lds, n0, e, first, 0, count, s0, n);
+    fc2_part<MX, 1>(a, s, turn, acc_lds, n0, e, first, 0, count, s0, n);
     return;
   }
-  for (int c0 = 0; c0 < count; c0 += 32) fc2_part<MX, 2>(a, s, acc_lds, n0, e, first, c0, count, s0, n);
+  for (int c0 = 0; c0 < count; c0 += 32) fc2_part<MX, 2>(a, s, turn, acc_lds, n0, e, first, c0, count, s0, n);
 }
 
-template <bool MX>
-__global__ __launch_bounds__(64 * kFc2Waves, 4) void k_decode_fc2(Args a) {
-  extern __shared__ __align__(16) float acc_all[];   // [kFc2Waves][T][16]
+template <bool MX, int W>
+__global__ __launch_bounds__(64 * W, 4) void k_decode_fc2(Args a) {
+  extern __shared__ __align__(16) float acc_all[];   // [W][T][16]
   __shared__ Fc2Shared s;
+  __shared__ __align__(16) uint4 slots[W * wave_cells<MX, 1>()];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // whole arrays, past the plan's ends too: no load waits for another
   const int routed = a.plan->groups;
@@ -459,33 +553,32 @@ __global__ __launch_bounds__(64 * kFc2Waves, 4) void k_decode_fc2(Args a) {
     s.weight[tid] = a.plan->weight[tid];
   }
   if (tid < a.T) s.gate[tid] = a.gw ? a.gate_s[tid] : 1.0f;
-  for (int i = tid; i < kFc2Waves * a.T * 16; i += 64 * kFc2Waves) acc_all[i] = 0.0f;
+  for (int i = tid; i < W * a.T * 16; i += 64 * W) acc_all[i] = 0.0f;
   __syncthreads();
 
   float* mine = acc_all + wave * a.T * 16;
+  const Turn turn = turn_of(slots + wave * wave_cells<MX, 1>());
   const int n0 = blockIdx.x * 16, steps = a.I / kStep;
-  const int groups = routed + (a.shared ? 1 : 0);
-  const int64_t total = (int64_t)groups * steps;
-  int64_t p = wave * total / kFc2Waves;
-  const int64_t end = (wave + 1) * total / kFc2Waves;
-  while (p < end) {
-    const int g = (int)(p / steps), s0 = (int)(p % steps);   // uniform in the wave
+  if (a.shared) {   // every wave takes its part: with many tokens these steps cost more than routed ones
+    const int s0 = wave * steps / W, s1 = (wave + 1) * steps / W;
+    if (s1 > s0) fc2_group<false>(a, s, turn, mine, n0, -1, 0, a.T, s0, s1 - s0);
+  }
+  const int64_t total = (int64_t)routed * steps;
+  int64_t p = wave * total / W;
+  const int64_t end = (wave + 1) * total / W;
+  while (p < end) {   // uniform in the wave
+    const int g = (int)(p / steps), s0 = (int)(p % steps);
     const int n = (int)min((int64_t)(steps - s0), end - p);
-    if (a.shared && g == 0) {
-      fc2_group<false>(a, s, mine, n0, -1, 0, a.T, s0, n);
-    } else {
-      const int u = g - (a.shared ? 1 : 0);
-      const int e = __builtin_amdgcn_readfirstlane(s.expert[u]), first = __builtin_amdgcn_readfirstlane(s.first[u]);
-      const int count = __builtin_amdgcn_readfirstlane(s.first[u + 1]) - first;
-      fc2_group<MX>(a, s, mine, n0, e, first, count, s0, n);
-    }
+    const int e = __builtin_amdgcn_readfirstlane(s.expert[g]), first = __builtin_amdgcn_readfirstlane(s.first[g]);
+    const int count = __builtin_amdgcn_readfirstlane(s.first[g + 1]) - first;
+    fc2_group<MX>(a, s, turn, mine, n0, e, first, count, s0, n);
     p += n;
   }
   __syncthreads();
-  for (int o = tid; o < a.T * 16; o += 64 * kFc2Waves) {
+  for (int o = tid; o < a.T * 16; o += 64 * W) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kFc2Waves; ++w) v += acc_all[w * a.T * 16 + o];
+    for (int w = 0; w < W; ++w) v += acc_all[w * a.T * 16 + o];
     a.out[(int64_t)(o >> 4) * a.H + n0 + (o & 15)] = (uint16_t)f2bf(v);
   }
 }
@@ -494,18 +587,27 @@ __global__ __launch_bounds__(64 * kFc2Waves, 4) void k_decode_fc2(Args a) {
 
 template <bool MX>
 void launch_fc1(hipStream_t st, const Args& a) {
-  constexpr int R = MX ? DEC_R_MX : DEC_R_BF, W = kFc1Waves;
+  // Two fragments a workgroup share the tokens' loads, which weigh twice as much beside E4M3
+  // as beside BF16: 371 us against 424 (64 tokens, H 7168, E4M3); BF16 loses a little to the
+  // coarser grid (151 us against 139, 19 tokens, H 4096).
+  constexpr int R = MX ? 2 : 1, W = kFc1Waves;
   const int tiles = a.I / (8 * R), used = a.E < a.T * a.K ? a.E : a.T * a.K;
   const int gate = a.gw ? (a.T + W - 1) / W : 0;
   const int shared = a.shared ? a.I / (8 * (MX ? 1 : R)) : 0;
   hipLaunchKernelGGL((k_decode_fc1<MX, R, W>), dim3((unsigned)(1 + shared + used * tiles + gate)), dim3(64 * W), 0,
                      st, a);
 }
+template <bool MX, int W>
+void launch_fc2_w(hipStream_t st, const Args& a) {
+  static_assert(64 * W >= kMaxRoutes && 64 * W >= kMaxExperts + 2, "the plan in one load a thread");
+  hipLaunchKernelGGL((k_decode_fc2<MX, W>), dim3(a.H / 16), dim3(64 * W), (size_t)W * a.T * 16 * sizeof(float), st, a);
+}
 template <bool MX>
 void launch_fc2(hipStream_t st, const Args& a) {
-  static_assert(64 * kFc2Waves >= kMaxRoutes && 64 * kFc2Waves >= kMaxExperts + 2, "the plan in one load a thread");
-  hipLaunchKernelGGL((k_decode_fc2<MX>), dim3(a.H / 16), dim3(64 * kFc2Waves),
-                     (size_t)kFc2Waves * a.T * 16 * sizeof(float), st, a);
+  // A grid of at most one workgroup a CU takes 16 waves in each: 28.5 us against 30.0 at
+  // H 4096 (7 tokens, E4M3); more workgroups than that run two to a CU.
+  if (a.H / 16 <= 256) launch_fc2_w<MX, 16>(st, a);
+  else launch_fc2_w<MX, 8>(st, a);
 }
 template void launch_fc1<false>(hipStream_t, const Args&);
 template void launch_fc1<true>(hipStream_t, const Args&);
