@@ -392,23 +392,26 @@ def _moe_dtype(dt, where: str) -> int:
     return code
 
 
-def _check(where, device, t, dtype, shape):
-    """t: a tensor of this dtype and shape on `device` (the first tensor's) whose last
-    dimension is dense.  A host tensor's address must never reach a kernel."""
+def _check(where, device, t, dtype, shape, dense=True):
+    """t: a tensor of this dtype and shape on GPU `device` (an index), contiguous or (dense
+    false) with a dense last dimension.  A host tensor's address must never reach a kernel."""
     if t is None:
         raise MoeError(MOE_ERR_NULL, where)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise MoeError(MOE_ERR_DTYPE, where)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise MoeError(MOE_ERR_SHAPE, where)
-    if not t.is_cuda or t.device != device or (t.stride(-1) != 1 and shape[-1] > 1):
+    if device < 0 or t.get_device() != device:
+        raise MoeError(MOE_ERR_LAYOUT, where)
+    if not t.is_contiguous() and (dense or (t.stride(-1) != 1 and shape[-1] > 1)):
         raise MoeError(MOE_ERR_LAYOUT, where)
 
 
-def _check_dense(where, device, t, dtype, shape):
-    _check(where, device, t, dtype, shape)
-    if not t.is_contiguous():
-        raise MoeError(MOE_ERR_LAYOUT, where)
+def _device(where, t) -> int:
+    """The GPU index of a call's first tensor (-1: not on a GPU)."""
+    if t is None:
+        raise MoeError(MOE_ERR_NULL, where)
+    return t.get_device()
 
 
 def _ld(t) -> int:
@@ -416,14 +419,14 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
-def _call(where, device, f):
-    """f(stream) on torch's current stream of `device`, with that device current."""
+def _call(where, device, fn, *args):
+    """fn(*args, stream) on torch's current stream of GPU `device`, with that GPU current."""
     import torch
-    if device.index is None or device.index == torch.cuda.current_device():
-        st = f(current_stream())
+    if device == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
-            st = f(current_stream())
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     if st != MOE_OK:
         raise MoeError(st, where)
 
@@ -443,40 +446,40 @@ class Router:
         if st != MOE_OK:
             raise MoeError(st, "Router")
 
-    def _problem(self, where, logits):
-        if logits is None:
-            raise MoeError(MOE_ERR_NULL, where)
+    def _problem(self, where, dev, logits):
         if logits.dim() != 2:
             raise MoeError(MOE_ERR_SHAPE, where)
         T, q = logits.shape[0], self.p
-        _check(where, logits.device, logits, self.dtype, (T, q.experts))
-        p = moe_router_problem(T, q.experts, q.topk, q.score, q.logits_dtype, q.flags, q.scale, _ld(logits))
-        return T, p
+        _check(where, dev, logits, self.dtype, (T, q.experts), False)
+        return moe_router_problem(T, q.experts, q.topk, q.score, q.logits_dtype, q.flags, q.scale, _ld(logits))
 
     def forward(self, logits, top_experts, router_weights, expert_bias=None):
         """Writes top_experts (int32) and router_weights (float32), both [tokens, topk]."""
         import torch
-        where, dev = "moe_router_forward", getattr(logits, "device", None)
-        T, p = self._problem(where, logits)
-        _check_dense(where, dev, top_experts, torch.int32, (T, p.topk))
-        _check_dense(where, dev, router_weights, torch.float32, (T, p.topk))
+        where = "moe_router_forward"
+        dev = _device(where, logits)
+        p = self._problem(where, dev, logits)
+        table = (p.tokens, p.topk)
+        _check(where, dev, top_experts, torch.int32, table)
+        _check(where, dev, router_weights, torch.float32, table)
         if expert_bias is not None:
-            _check_dense(where, dev, expert_bias, torch.float32, (p.experts,))
-        _call(where, dev, lambda s: moe_router_forward(p, _ptr(logits), _ptr(expert_bias), _ptr(top_experts),
-                                                       _ptr(router_weights), s))
+            _check(where, dev, expert_bias, torch.float32, (p.experts,))
+        _call(where, dev, load().moe_router_forward, p, logits.data_ptr(), _ptr(expert_bias),
+              top_experts.data_ptr(), router_weights.data_ptr())
         return top_experts, router_weights
 
     def backward(self, logits, top_experts, grad_router_weights, grad_logits):
         """Writes grad_logits [tokens, experts] in the logits' dtype."""
         import torch
-        where, dev = "moe_router_backward", getattr(logits, "device", None)
-        T, p = self._problem(where, logits)
-        _check_dense(where, dev, top_experts, torch.int32, (T, p.topk))
-        _check_dense(where, dev, grad_router_weights, torch.float32, (T, p.topk))
-        _check(where, dev, grad_logits, self.dtype, (T, p.experts))
-        _call(where, dev, lambda s: moe_router_backward(p, _ptr(logits), _ptr(top_experts),
-                                                        _ptr(grad_router_weights), _ptr(grad_logits),
-                                                        _ld(grad_logits), s))
+        where = "moe_router_backward"
+        dev = _device(where, logits)
+        p = self._problem(where, dev, logits)
+        table = (p.tokens, p.topk)
+        _check(where, dev, top_experts, torch.int32, table)
+        _check(where, dev, grad_router_weights, torch.float32, table)
+        _check(where, dev, grad_logits, self.dtype, (p.tokens, p.experts), False)
+        _call(where, dev, load().moe_router_backward, p, logits.data_ptr(), top_experts.data_ptr(),
+              grad_router_weights.data_ptr(), grad_logits.data_ptr(), _ld(grad_logits))
         return grad_logits
 
 
@@ -499,33 +502,33 @@ class Norm:
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
 
     def _problem(self, where, x, flags=0):
-        if x is None:
-            raise MoeError(MOE_ERR_NULL, where)
         if x.dim() != 2:
             raise MoeError(MOE_ERR_SHAPE, where)
         q = self.p
         p = moe_norm_problem(x.shape[0], q.cols, q.kind, q.dtype, q.param_dtype, q.grad_dtype, flags, q.eps)
-        return p, (x.shape[0], q.cols)
+        return p, (p.rows, p.cols)
 
     def _rows(self, where, device, t, shape):
-        _check(where, device, t, self.dtype, shape)
-        return moe_rows(_ptr(t), _ld(t))
+        _check(where, device, t, self.dtype, shape, False)
+        return moe_rows(t.data_ptr(), _ld(t))
 
     def forward(self, x, weight, bias, y, stats=None, residual=None, sum=None):
         """y = norm(x) or, with residual, sum = x + residual and y = norm(sum).  stats: float32
         [rows, 2], what backward needs."""
         import torch
-        where, dev = "moe_norm_forward", getattr(x, "device", None)
+        where = "moe_norm_forward"
+        dev = _device(where, x)
         p, shape = self._problem(where, x)
-        rows = [None if t is None else self._rows(where, dev, t, shape) for t in (residual, sum)]
         rx, ry = self._rows(where, dev, x, shape), self._rows(where, dev, y, shape)
-        _check_dense(where, dev, weight, self.param_dtype, (shape[1],))
+        rres = None if residual is None else self._rows(where, dev, residual, shape)
+        rsum = None if sum is None else self._rows(where, dev, sum, shape)
+        cols = (p.cols,)
+        _check(where, dev, weight, self.param_dtype, cols)
         if bias is not None:
-            _check_dense(where, dev, bias, self.param_dtype, (shape[1],))
+            _check(where, dev, bias, self.param_dtype, cols)
         if stats is not None:
-            _check_dense(where, dev, stats, torch.float32, (shape[0], 2))
-        _call(where, dev, lambda s: moe_norm_forward(p, rx, rows[0], _ptr(weight), _ptr(bias), rows[1], ry,
-                                                     _ptr(stats), s))
+            _check(where, dev, stats, torch.float32, (p.rows, 2))
+        _call(where, dev, load().moe_norm_forward, p, rx, rres, weight.data_ptr(), _ptr(bias), rsum, ry, _ptr(stats))
         return y
 
     def backward(self, grad_y, x, weight, stats, grad_x, grad_weight=None, grad_bias=None, grad_sum=None,
@@ -533,20 +536,21 @@ class Norm:
         """x: what was normalised (the forward's sum if it took a residual).  grad_weight and
         grad_bias [cols] are accumulated, or overwritten."""
         import torch
-        where, dev = "moe_norm_backward", getattr(x, "device", None)
+        where = "moe_norm_backward"
+        dev = _device(where, x)
         p, shape = self._problem(where, x, MOE_NORM_OVERWRITE_GRADS if overwrite else 0)
         rx, rdy, rdx = (self._rows(where, dev, t, shape) for t in (x, grad_y, grad_x))
         rgs = None if grad_sum is None else self._rows(where, dev, grad_sum, shape)
-        _check_dense(where, dev, weight, self.param_dtype, (shape[1],))
-        _check_dense(where, dev, stats, torch.float32, (shape[0], 2))
+        cols = (p.cols,)
+        _check(where, dev, weight, self.param_dtype, cols)
+        _check(where, dev, stats, torch.float32, (p.rows, 2))
         for g in (grad_weight, grad_bias):
             if g is not None:
-                _check_dense(where, dev, g, self.grad_dtype, (shape[1],))
-        if self.workspace.device != dev:
+                _check(where, dev, g, self.grad_dtype, cols)
+        if self.workspace.get_device() != dev:
             raise MoeError(MOE_ERR_WORKSPACE, where)
-        _call(where, dev, lambda s: moe_norm_backward(p, rdy, rx, _ptr(weight), _ptr(stats), rgs, rdx,
-                                                      _ptr(grad_weight), _ptr(grad_bias), _ptr(self.workspace),
-                                                      self.ws_bytes, s))
+        _call(where, dev, load().moe_norm_backward, p, rdy, rx, weight.data_ptr(), stats.data_ptr(), rgs, rdx,
+              _ptr(grad_weight), _ptr(grad_bias), self.workspace.data_ptr(), self.ws_bytes)
         return grad_x
 
 
@@ -566,22 +570,21 @@ class DecodeLayer:
 
     def forward(self, hidden, top_experts, router_weights, weights: moe_weights, out):
         import torch
-        where, dev = "moe_forward_decode", getattr(hidden, "device", None)
-        if hidden is None:
-            raise MoeError(MOE_ERR_NULL, where)
-        T, H, K = hidden.shape[0], self.p.hidden, self.p.topk
-        if T > self.p.tokens:
-            raise MoeError(MOE_ERR_SHAPE, where)
+        where = "moe_forward_decode"
+        dev = _device(where, hidden)
         p = moe_problem.from_buffer_copy(self.p)
-        p.tokens = T
-        _check_dense(where, dev, hidden, torch.bfloat16, (T, H))
-        _check_dense(where, dev, top_experts, torch.int32, (T, K))
-        _check_dense(where, dev, router_weights, torch.float32, (T, K))
-        _check_dense(where, dev, out, torch.bfloat16, (T, H))
-        if self.workspace.device != dev:
+        p.tokens = hidden.shape[0]
+        if p.tokens > self.p.tokens:
+            raise MoeError(MOE_ERR_SHAPE, where)
+        rows, table = (p.tokens, p.hidden), (p.tokens, p.topk)
+        _check(where, dev, hidden, torch.bfloat16, rows)
+        _check(where, dev, top_experts, torch.int32, table)
+        _check(where, dev, router_weights, torch.float32, table)
+        _check(where, dev, out, torch.bfloat16, rows)
+        if self.workspace.get_device() != dev:
             raise MoeError(MOE_ERR_WORKSPACE, where)
-        _call(where, dev, lambda s: moe_forward_decode(p, _ptr(hidden), _ptr(top_experts), _ptr(router_weights),
-                                                       weights, _ptr(out), _ptr(self.workspace), self.ws_bytes, s))
+        _call(where, dev, load().moe_forward_decode, p, hidden.data_ptr(), top_experts.data_ptr(),
+              router_weights.data_ptr(), weights, out.data_ptr(), self.workspace.data_ptr(), self.ws_bytes)
         return out
 
     def status_word(self):
