@@ -1,8 +1,8 @@
 // Layer norm and RMS norm of rows, forward and backward (C ABI: moe_norm_forward,
 // moe_norm_backward).
 //
-// Each row is held in the registers of `tpr` threads (a multiple of 64, 16 elements a
-// thread), so x is read once and every statistic is taken from registers:
+// Each row is held in the registers of `tpr` threads (a multiple of 64, EPT = 8 or 16
+// elements a thread), so x is read once and every statistic is taken from registers:
 //   m = sum x / N;  d = x - m;  delta = sum d / N;  var = sum d^2 / N - delta^2
 // mean = m + delta.  The second pass over the registers removes what rounding m cost: with
 // m already close, delta is tiny and var has no cancellation.
@@ -27,10 +27,9 @@ using namespace moe;
 
 namespace {
 
-constexpr int kEpt = 16;              // elements per thread
 constexpr int kNormThreads = 1024;    // largest workgroup
 constexpr int kNormGroups = 256;      // workgroups of the backward (partial rows): one per CU
-constexpr int kFinalCols = 32;        // columns per workgroup of the second kernel
+constexpr int kFinalCols = 32, kFinalLanes = 16;   // columns and row lanes of the second kernel's workgroups
 
 struct Rows {
   uint8_t* base;
@@ -46,7 +45,7 @@ struct NormArgs {
   int64_t rows;
   int N;                    // cols
   int tpr;                  // threads per row
-  int rms, wbf16;
+  int rms, wbf16, w16, b16;  // w16, b16: 16-byte aligned weight, bias
   int want_dw, want_db;
   float eps;
 };
@@ -58,24 +57,25 @@ __device__ __forceinline__ int col_of(int j, int i, int tpr) {
   return VEC ? 8 * (j + (i >> 3) * tpr) + (i & 7) : j + i * tpr;
 }
 
-template <bool VEC, bool BF16>
-struct Raw;   // a thread's part of a row as loaded
-template <>
-struct Raw<true, true> { uint4 q[2]; };
-template <>
-struct Raw<true, false> { float4 q[4]; };
-template <>
-struct Raw<false, true> { uint16_t q[16]; };
-template <>
-struct Raw<false, false> { float q[16]; };
+// A thread's EPT elements of a row as loaded.
+template <int EPT, bool VEC, bool BF16>
+struct Raw;
+template <int EPT>
+struct Raw<EPT, true, true> { uint4 q[EPT / 8]; };
+template <int EPT>
+struct Raw<EPT, true, false> { float4 q[EPT / 4]; };
+template <int EPT>
+struct Raw<EPT, false, true> { uint16_t q[EPT]; };
+template <int EPT>
+struct Raw<EPT, false, false> { float q[EPT]; };
 
-template <bool VEC, bool BF16>
-__device__ __forceinline__ Raw<VEC, BF16> ld_row(const Rows& m, int64_t r, int j, int tpr, int N) {
-  Raw<VEC, BF16> v;
+template <int EPT, bool VEC, bool BF16>
+__device__ __forceinline__ Raw<EPT, VEC, BF16> ld_row(const Rows& m, int64_t r, int j, int tpr, int N) {
+  Raw<EPT, VEC, BF16> v;
   const uint8_t* p = m.base + r * m.ld * (BF16 ? 2 : 4);
   if constexpr (VEC) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < EPT / 8; ++u) {
       const int c = 8 * (j + u * tpr);
       if constexpr (BF16) {
         v.q[u] = c < N ? *reinterpret_cast<const uint4*>(p + 2 * c) : make_uint4(0, 0, 0, 0);
@@ -87,7 +87,7 @@ __device__ __forceinline__ Raw<VEC, BF16> ld_row(const Rows& m, int64_t r, int j
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kEpt; ++i) {
+    for (int i = 0; i < EPT; ++i) {
       const int c = j + i * tpr;
       if constexpr (BF16) v.q[i] = c < N ? reinterpret_cast<const uint16_t*>(p)[c] : (uint16_t)0;
       else v.q[i] = c < N ? reinterpret_cast<const float*>(p)[c] : 0.0f;
@@ -96,31 +96,31 @@ __device__ __forceinline__ Raw<VEC, BF16> ld_row(const Rows& m, int64_t r, int j
   return v;
 }
 
-template <bool VEC, bool BF16>
-__device__ __forceinline__ void unpack(const Raw<VEC, BF16>& v, float (&f)[kEpt]) {
+template <int EPT, bool VEC, bool BF16>
+__device__ __forceinline__ void unpack(const Raw<EPT, VEC, BF16>& v, float (&f)[EPT]) {
   if constexpr (VEC && BF16) {
-    unpack_bf16x8(v.q[0], f);
-    unpack_bf16x8(v.q[1], f + 8);
+#pragma unroll
+    for (int u = 0; u < EPT / 8; ++u) unpack_bf16x8(v.q[u], f + 8 * u);
   } else if constexpr (VEC) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < EPT / 4; ++u) {
       f[4 * u] = v.q[u].x; f[4 * u + 1] = v.q[u].y; f[4 * u + 2] = v.q[u].z; f[4 * u + 3] = v.q[u].w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kEpt; ++i) {
+    for (int i = 0; i < EPT; ++i) {
       if constexpr (BF16) f[i] = bf2f(v.q[i]);
       else f[i] = v.q[i];
     }
   }
 }
 
-template <bool VEC, bool BF16>
-__device__ __forceinline__ void st_row(const Rows& m, int64_t r, int j, int tpr, int N, const float (&f)[kEpt]) {
+template <int EPT, bool VEC, bool BF16>
+__device__ __forceinline__ void st_row(const Rows& m, int64_t r, int j, int tpr, int N, const float (&f)[EPT]) {
   uint8_t* p = m.base + r * m.ld * (BF16 ? 2 : 4);
   if constexpr (VEC) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < EPT / 8; ++u) {
       const int c = 8 * (j + u * tpr);
       if (c >= N) continue;
       const float* s = f + 8 * u;
@@ -134,7 +134,7 @@ __device__ __forceinline__ void st_row(const Rows& m, int64_t r, int j, int tpr,
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kEpt; ++i) {
+    for (int i = 0; i < EPT; ++i) {
       const int c = j + i * tpr;
       if (c >= N) continue;
       if constexpr (BF16) reinterpret_cast<uint16_t*>(p)[c] = (uint16_t)f2bf(f[i]);
@@ -143,11 +143,18 @@ __device__ __forceinline__ void st_row(const Rows& m, int64_t r, int j, int tpr,
   }
 }
 
-// weight or bias of a thread's columns (0 past the end)
-template <bool VEC>
-__device__ __forceinline__ void ld_param(const void* w, int bf16, int j, int tpr, int N, float (&f)[kEpt]) {
+// weight or bias of a thread's columns (0 past the end); aligned: 16-byte pieces can be read
+template <int EPT, bool VEC>
+__device__ __forceinline__ void ld_param(const void* w, int bf16, int aligned, int j, int tpr, int N,
+                                         float (&f)[EPT]) {
+  const Rows m{const_cast<uint8_t*>(static_cast<const uint8_t*>(w)), 0};
+  if (VEC && aligned) {
+    if (bf16) unpack(ld_row<EPT, true, true>(m, 0, j, tpr, N), f);
+    else unpack(ld_row<EPT, true, false>(m, 0, j, tpr, N), f);
+    return;
+  }
 #pragma unroll
-  for (int i = 0; i < kEpt; ++i) {
+  for (int i = 0; i < EPT; ++i) {
     const int c = col_of<VEC>(j, i, tpr);
     f[i] = c < N ? (bf16 ? bf2f(static_cast<const uint16_t*>(w)[c]) : static_cast<const float*>(w)[c]) : 0.0f;
   }
@@ -176,49 +183,55 @@ __device__ __forceinline__ void group_sum2(float& a, float& b, int nw, float2* r
 
 // Forward: blockDim.x = row groups * tpr, the groups walk rows with a common trip count
 // (the barriers are the workgroup's).
-template <bool VEC, bool BF16>
+template <int EPT, bool VEC, bool BF16>
 __global__ __launch_bounds__(kNormThreads) void k_norm_fwd(NormArgs a) {
   __shared__ float2 red[2 * (kNormThreads / 64)];
   const int tpr = a.tpr, N = a.N, nw = tpr >> 6;
   const int j = threadIdx.x % tpr;
   const int rg = threadIdx.x / tpr, ng = blockDim.x / tpr;
-  float w[kEpt], b[kEpt];
-  ld_param<VEC>(a.w, a.wbf16, j, tpr, N, w);
+  const int64_t stride = (int64_t)gridDim.x * ng;
+  // the next row's loads are under way while a row is reduced and written
+  Raw<EPT, VEC, BF16> nx{}, nr{};
+  auto fetch = [&](int64_t r) __attribute__((always_inline)) {
+    if (r < a.rows) {
+      nx = ld_row<EPT, VEC, BF16>(a.x, r, j, tpr, N);
+      if (a.res.base) nr = ld_row<EPT, VEC, BF16>(a.res, r, j, tpr, N);
+    }
+  };
+  fetch((int64_t)blockIdx.x * ng + rg);
+  float w[EPT], b[EPT];
+  ld_param<EPT, VEC>(a.w, a.wbf16, a.w16, j, tpr, N, w);
 #pragma unroll
-  for (int i = 0; i < kEpt; ++i) b[i] = 0.0f;
-  if (a.b) ld_param<VEC>(a.b, a.wbf16, j, tpr, N, b);
+  for (int i = 0; i < EPT; ++i) b[i] = 0.0f;
+  if (a.b) ld_param<EPT, VEC>(a.b, a.wbf16, a.b16, j, tpr, N, b);
   const float inv_n = 1.0f / (float)N;
   int parity = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * ng; r0 < a.rows; r0 += (int64_t)gridDim.x * ng) {
+  for (int64_t r0 = (int64_t)blockIdx.x * ng; r0 < a.rows; r0 += stride) {
     const int64_t r = r0 + rg;
     const bool on = r < a.rows;
-    float v[kEpt];
+    float v[EPT], q[EPT];
+    unpack(nx, v);
+    if (a.res.base) {
+      unpack(nr, q);
 #pragma unroll
-    for (int i = 0; i < kEpt; ++i) v[i] = 0.0f;
-    if (on) {
-      unpack<VEC, BF16>(ld_row<VEC, BF16>(a.x, r, j, tpr, N), v);
-      if (a.res.base) {
-        float q[kEpt];
-        unpack<VEC, BF16>(ld_row<VEC, BF16>(a.res, r, j, tpr, N), q);
-#pragma unroll
-        for (int i = 0; i < kEpt; ++i) {
-          v[i] += q[i];
-          if constexpr (BF16) v[i] = bf2f(f2bf(v[i]));
-        }
-        st_row<VEC, BF16>(a.sum, r, j, tpr, N, v);
+      for (int i = 0; i < EPT; ++i) {
+        v[i] += q[i];
+        if constexpr (BF16) v[i] = bf2f(f2bf(v[i]));
       }
+      if (on) st_row<EPT, VEC, BF16>(a.sum, r, j, tpr, N, v);
     }
+    fetch(r + stride);
     float mean = 0.0f, s = 0.0f, s2 = 0.0f;
     if (!a.rms) {
 #pragma unroll
-      for (int i = 0; i < kEpt; ++i) s += v[i];
+      for (int i = 0; i < EPT; ++i) s += v[i];
       group_sum2(s, s2, nw, red, parity);
       parity ^= 1;
       mean = s / (float)N;
     }
     s = s2 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kEpt; ++i) {
+    for (int i = 0; i < EPT; ++i) {
       v[i] = col_of<VEC>(j, i, tpr) < N ? v[i] - mean : 0.0f;
       s += v[i];
       s2 += v[i] * v[i];
@@ -230,42 +243,57 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_fwd(NormArgs a) {
     if (on) {
       if (a.stats && j == 0) reinterpret_cast<float2*>(a.stats)[r] = make_float2(mean + delta, rstd);
 #pragma unroll
-      for (int i = 0; i < kEpt; ++i) v[i] = (v[i] - delta) * rstd * w[i] + b[i];
-      st_row<VEC, BF16>(a.y, r, j, tpr, N, v);
+      for (int i = 0; i < EPT; ++i) v[i] = (v[i] - delta) * rstd * w[i] + b[i];
+      st_row<EPT, VEC, BF16>(a.y, r, j, tpr, N, v);
     }
   }
 }
 
-template <bool VEC, bool BF16>
+template <int EPT, bool VEC, bool BF16>
 __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
-  extern __shared__ float join[];                        // [ng - 1][tpr * kEpt], reused
+  extern __shared__ float join[];                        // [ng - 1][tpr * EPT], reused
   __shared__ float2 red[2 * (kNormThreads / 64)];
   const int tpr = a.tpr, N = a.N, nw = tpr >> 6;
   const int j = threadIdx.x % tpr;
   const int rg = threadIdx.x / tpr, ng = blockDim.x / tpr;
-  float w[kEpt], dw[kEpt], db[kEpt];
-  ld_param<VEC>(a.w, a.wbf16, j, tpr, N, w);
+  const int64_t stride = (int64_t)gridDim.x * ng;
+  // The next row's loads are under way while a row is reduced and written (25 us against 35 at
+  // 4096 x 4096 BF16); 16 elements a thread leave no registers for that.
+  constexpr bool kAhead = EPT == 8;
+  Raw<EPT, VEC, BF16> nx{}, ndy{}, ngs{};
+  float2 nst = make_float2(0.0f, 0.0f);
+  auto fetch = [&](int64_t r) __attribute__((always_inline)) {
+    if (r < a.rows) {
+      nst = reinterpret_cast<const float2*>(a.stats)[r];
+      nx = ld_row<EPT, VEC, BF16>(a.x, r, j, tpr, N);
+      ndy = ld_row<EPT, VEC, BF16>(a.dy, r, j, tpr, N);
+      if (a.gsum.base) ngs = ld_row<EPT, VEC, BF16>(a.gsum, r, j, tpr, N);
+    } else {   // past the last row: nothing for the column sums
+      ndy = Raw<EPT, VEC, BF16>{};
+    }
+  };
+  if (kAhead) fetch((int64_t)blockIdx.x * ng + rg);
+  float w[EPT], dw[EPT], db[EPT];
+  ld_param<EPT, VEC>(a.w, a.wbf16, a.w16, j, tpr, N, w);
 #pragma unroll
-  for (int i = 0; i < kEpt; ++i) dw[i] = db[i] = 0.0f;
+  for (int i = 0; i < EPT; ++i) dw[i] = db[i] = 0.0f;
   const float inv_n = 1.0f / (float)N;
   int parity = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * ng; r0 < a.rows; r0 += (int64_t)gridDim.x * ng) {
+  for (int64_t r0 = (int64_t)blockIdx.x * ng; r0 < a.rows; r0 += stride) {
     const int64_t r = r0 + rg;
     const bool on = r < a.rows;
-    float xh[kEpt], g[kEpt], rstd = 0.0f;
+    if (!kAhead) fetch(r);
+    float xh[EPT], g[EPT];
+    unpack(nx, xh);
+    unpack(ndy, g);
+    const Raw<EPT, VEC, BF16> gs = ngs;
+    const float mean = nst.x, rstd = nst.y;
+    if (kAhead) fetch(r + stride);
 #pragma unroll
-    for (int i = 0; i < kEpt; ++i) xh[i] = g[i] = 0.0f;
-    if (on) {
-      unpack<VEC, BF16>(ld_row<VEC, BF16>(a.x, r, j, tpr, N), xh);
-      unpack<VEC, BF16>(ld_row<VEC, BF16>(a.dy, r, j, tpr, N), g);
-      const float2 st = reinterpret_cast<const float2*>(a.stats)[r];
-      rstd = st.y;
-#pragma unroll
-      for (int i = 0; i < kEpt; ++i) xh[i] = col_of<VEC>(j, i, tpr) < N ? (xh[i] - st.x) * rstd : 0.0f;
-    }
+    for (int i = 0; i < EPT; ++i) xh[i] = on && col_of<VEC>(j, i, tpr) < N ? (xh[i] - mean) * rstd : 0.0f;
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kEpt; ++i) {
+    for (int i = 0; i < EPT; ++i) {
       dw[i] += g[i] * xh[i];
       db[i] += g[i];
       g[i] *= w[i];
@@ -277,13 +305,13 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
     if (on) {
       const float m1 = a.rms ? 0.0f : s1 * inv_n, m2 = s2 * inv_n;
 #pragma unroll
-      for (int i = 0; i < kEpt; ++i) g[i] = rstd * (g[i] - m1 - xh[i] * m2);
+      for (int i = 0; i < EPT; ++i) g[i] = rstd * (g[i] - m1 - xh[i] * m2);
       if (a.gsum.base) {
-        unpack<VEC, BF16>(ld_row<VEC, BF16>(a.gsum, r, j, tpr, N), xh);
+        unpack(gs, xh);
 #pragma unroll
-        for (int i = 0; i < kEpt; ++i) g[i] += xh[i];
+        for (int i = 0; i < EPT; ++i) g[i] += xh[i];
       }
-      st_row<VEC, BF16>(a.dx, r, j, tpr, N, g);
+      st_row<EPT, VEC, BF16>(a.dx, r, j, tpr, N, g);
     }
   }
   if (!a.part) return;
@@ -297,15 +325,15 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
       __syncthreads();
       if (rg > 0) {
 #pragma unroll
-        for (int i = 0; i < kEpt; ++i) join[((rg - 1) * kEpt + i) * tpr + j] = which ? db[i] : dw[i];
+        for (int i = 0; i < EPT; ++i) join[((rg - 1) * EPT + i) * tpr + j] = which ? db[i] : dw[i];
       }
       __syncthreads();
     }
     if (rg == 0) {
 #pragma unroll
-      for (int i = 0; i < kEpt; ++i) {
+      for (int i = 0; i < EPT; ++i) {
         float v = which ? db[i] : dw[i];
-        for (int q = 0; q < ng - 1; ++q) v += join[(q * kEpt + i) * tpr + j];
+        for (int q = 0; q < ng - 1; ++q) v += join[(q * EPT + i) * tpr + j];
         const int c = col_of<VEC>(j, i, tpr);
         if (c < N) out[(which && a.want_dw ? N : 0) + c] = v;
       }
@@ -313,22 +341,34 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
   }
 }
 
-// grad[c] (+)= sum over the partial rows: kFinalCols columns a workgroup, 8 lanes of
-// rows per column joined in order.
-__global__ __launch_bounds__(256) void k_norm_bwd_final(const float* __restrict__ part, int groups, int width,
-                                                        int N, uint8_t* g0, uint8_t* g1, int bf16, int overwrite) {
-  __shared__ float red[8][kFinalCols];
+// grad[c] (+)= sum over the partial rows: kFinalCols columns a workgroup, kFinalLanes lanes
+// of rows per column, eight rows of a lane in flight, joined in order.
+__global__ __launch_bounds__(kFinalCols * kFinalLanes) void k_norm_bwd_final(const float* __restrict__ part,
+                                                                            int groups, int width, int N,
+                                                                            uint8_t* g0, uint8_t* g1, int bf16,
+                                                                            int overwrite) {
+  __shared__ float red[kFinalLanes][kFinalCols];
   const int cl = threadIdx.x % kFinalCols, q = threadIdx.x / kFinalCols;
   const int c = blockIdx.x * kFinalCols + cl;
   float v = 0.0f;
-  if (c < width)
-    for (int p = q; p < groups; p += 8) v += part[(int64_t)p * width + c];
+  if (c < width) {
+    for (int p = q; p < groups; p += 8 * kFinalLanes) {
+      float t[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int pu = p + u * kFinalLanes;
+        t[u] = pu < groups ? part[(int64_t)pu * width + c] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v += t[u];
+    }
+  }
   red[q][cl] = v;
   __syncthreads();
   if (q != 0 || c >= width) return;
   v = red[0][cl];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) v += red[i][cl];
+  for (int i = 1; i < kFinalLanes; ++i) v += red[i][cl];
   uint8_t* dst = c < N ? g0 : g1;
   const int cc = c < N ? c : c - N;
   if (bf16) {
@@ -372,13 +412,19 @@ bool rows16(const moe_norm_problem* p, const moe_rows* m) {
 
 Rows rows_of(const moe_rows* m) { return m ? Rows{static_cast<uint8_t*>(m->base), m->ld} : Rows{nullptr, 0}; }
 
-int threads_per_row(int64_t cols) { return 64 * (int)((cols + 64 * kEpt - 1) / (64 * kEpt)); }
+int threads_per_row(int64_t cols, int ept) { return 64 * (int)((cols + 64 * ept - 1) / (64 * ept)); }
 
-NormArgs norm_args(const moe_norm_problem* p) {
+// Elements per thread.  The forward in 16-byte pieces takes 16 (fewer waves meet at the
+// barriers: 89 us against 112 at 8192 x 7168 BF16); single elements at 16 a thread would
+// spill, as would the backward's accumulators, so those take 8 wherever 1024 threads then hold a row.
+int fwd_ept(int64_t cols, bool vec) { return !vec && cols <= 8 * kNormThreads ? 8 : 16; }
+int bwd_ept(int64_t cols) { return cols <= 8 * kNormThreads ? 8 : 16; }
+
+NormArgs norm_args(const moe_norm_problem* p, int ept) {
   NormArgs a{};
   a.rows = p->rows;
   a.N = (int)p->cols;
-  a.tpr = threads_per_row(p->cols);
+  a.tpr = threads_per_row(p->cols, ept);
   a.rms = p->kind == MOE_NORM_RMS;
   a.wbf16 = p->param_dtype == MOE_BF16;
   a.eps = p->eps;
@@ -386,17 +432,24 @@ NormArgs norm_args(const moe_norm_problem* p) {
 }
 
 template <class F>
-void with_variant(bool vec, bool bf16, F&& f) {
-  if (vec && bf16) f(std::true_type{}, std::true_type{});
-  else if (vec) f(std::true_type{}, std::false_type{});
-  else if (bf16) f(std::false_type{}, std::true_type{});
-  else f(std::false_type{}, std::false_type{});
+void with_variant(int ept, bool vec, bool bf16, F&& f) {
+  using E8 = std::integral_constant<int, 8>;
+  using E16 = std::integral_constant<int, 16>;
+  auto types = [&](auto e) {
+    if (vec && bf16) f(e, std::true_type{}, std::true_type{});
+    else if (vec) f(e, std::true_type{}, std::false_type{});
+    else if (bf16) f(e, std::false_type{}, std::true_type{});
+    else f(e, std::false_type{}, std::false_type{});
+  };
+  if (ept == 8) types(E8{});
+  else types(E16{});
 }
 
-// Row groups per backward workgroup: as many as 1024 threads hold, no more than the rows.
+// Row groups per backward workgroup: as many as 1024 threads hold, but first a workgroup for
+// each of the kNormGroups.
 int bwd_row_groups(const NormArgs& a) {
-  const int64_t fit = kNormThreads / a.tpr;
-  return (int)(a.rows < fit ? (a.rows > 0 ? a.rows : 1) : fit);
+  const int64_t fit = kNormThreads / a.tpr, want = (a.rows + kNormGroups - 1) / kNormGroups;
+  return (int)(want < 1 ? 1 : (want < fit ? want : fit));
 }
 int bwd_groups(const NormArgs& a) {
   const int64_t ng = bwd_row_groups(a), need = (a.rows + ng - 1) / ng;
@@ -422,11 +475,13 @@ moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const 
   if (!elem_aligned(weight, p->param_dtype) || !elem_aligned(bias, p->param_dtype)) return MOE_ERR_LAYOUT;
   if (reinterpret_cast<uintptr_t>(stats) & 7u) return MOE_ERR_LAYOUT;
   if (p->rows == 0) return MOE_OK;
-  NormArgs a = norm_args(p);
+  const bool vec = p->cols % 8 == 0 && rows16(p, x) && rows16(p, residual) && rows16(p, sum) && rows16(p, y);
+  const int ept = fwd_ept(p->cols, vec);
+  NormArgs a = norm_args(p, ept);
   a.x = rows_of(x); a.res = rows_of(residual); a.sum = rows_of(sum); a.y = rows_of(y);
   a.w = weight; a.b = bias;
+  a.w16 = aligned16(weight); a.b16 = aligned16(bias);
   a.stats = stats;
-  const bool vec = p->cols % 8 == 0 && rows16(p, x) && rows16(p, residual) && rows16(p, sum) && rows16(p, y);
   // about 256 threads a workgroup, and enough workgroups for 2048 threads per CU
   int ng = 256 / a.tpr;
   if (ng < 1) ng = 1;
@@ -435,15 +490,15 @@ moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const 
   const dim3 grid((unsigned)(need < most ? need : most)), block(ng * a.tpr);
   hipStream_t st = static_cast<hipStream_t>(stream);
   return launch("norm_fwd", st, [&] {
-    with_variant(vec, p->dtype == MOE_BF16, [&](auto v, auto bf) {
-      hipLaunchKernelGGL((k_norm_fwd<v(), bf()>), grid, block, 0, st, a);
+    with_variant(ept, vec, p->dtype == MOE_BF16, [&](auto e, auto v, auto bf) {
+      hipLaunchKernelGGL((k_norm_fwd<e(), v(), bf()>), grid, block, 0, st, a);
     });
   });
 }
 
 size_t moe_norm_workspace_bytes(const moe_norm_problem* p) {
   if (check_norm(p) != MOE_OK) return 0;
-  return align_up((size_t)bwd_groups(norm_args(p)) * 2 * p->cols * sizeof(float) + 1);
+  return align_up((size_t)bwd_groups(norm_args(p, bwd_ept(p->cols))) * 2 * p->cols * sizeof(float) + 1);
 }
 
 moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, const moe_rows* x,
@@ -463,9 +518,11 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, 
     if (!workspace || workspace_bytes < moe_norm_workspace_bytes(p)) return MOE_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MOE_ERR_LAYOUT;
   }
-  NormArgs a = norm_args(p);
+  const int ept = bwd_ept(p->cols);
+  NormArgs a = norm_args(p, ept);
   a.dy = rows_of(grad_y); a.x = rows_of(x); a.gsum = rows_of(grad_sum); a.dx = rows_of(grad_x);
   a.w = weight;
+  a.w16 = aligned16(weight);
   a.stats = const_cast<float*>(stats);
   a.part = sums ? static_cast<float*>(workspace) : nullptr;
   a.want_dw = grad_weight != nullptr;
@@ -475,9 +532,9 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, 
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (p->rows > 0) {
     MOE_TRY(launch("norm_bwd", st, [&] {
-      with_variant(vec, p->dtype == MOE_BF16, [&](auto v, auto bf) {
-        const size_t lds = sums ? (size_t)(ng - 1) * a.tpr * kEpt * sizeof(float) : 0;
-        hipLaunchKernelGGL((k_norm_bwd<v(), bf()>), dim3(groups), dim3(ng * a.tpr), lds, st, a);
+      with_variant(ept, vec, p->dtype == MOE_BF16, [&](auto e, auto v, auto bf) {
+        const size_t lds = sums ? (size_t)(ng - 1) * a.tpr * ept * sizeof(float) : 0;
+        hipLaunchKernelGGL((k_norm_bwd<e(), v(), bf()>), dim3(groups), dim3(ng * a.tpr), lds, st, a);
       });
     }));
   }
@@ -486,7 +543,7 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, 
   const int width = a.N * (a.want_dw + a.want_db);
   uint8_t* g0 = static_cast<uint8_t*>(grad_weight ? grad_weight : grad_bias);
   return launch("norm_bwd_final", st, [&] {
-    hipLaunchKernelGGL(k_norm_bwd_final, dim3((width + kFinalCols - 1) / kFinalCols), dim3(256), 0, st,
+    hipLaunchKernelGGL(k_norm_bwd_final, dim3((width + kFinalCols - 1) / kFinalCols), dim3(kFinalCols * kFinalLanes), 0, st,
                        (const float*)workspace, groups, width, a.N, g0, static_cast<uint8_t*>(grad_bias),
                        p->grad_dtype == MOE_BF16 ? 1 : 0, (p->flags & MOE_NORM_OVERWRITE_GRADS) ? 1 : 0);
   });

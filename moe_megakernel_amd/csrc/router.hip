@@ -11,8 +11,9 @@
 //
 // Without a bias the order of the scores is the order of the logits, so the logits
 // themselves are compared: no rounding can make or break a tie.  With a bias s + bias is
-// compared in 64 bits: in 32 bits scores near 1 differ by rounding alone and two correct
-// programs would choose different experts.
+// compared as in 64 bits: in 32 bits scores near 1 differ by rounding alone and two correct
+// programs would choose different experts.  (FP32 keys decide wherever they are far enough
+// apart to be sure; FP64 everywhere took 23.6 us at 65536 x 64, top-6.)
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -92,22 +93,22 @@ __device__ __forceinline__ void row_scores(const float (&l)[EPL], T (&s)[EPL]) {
   }
 }
 
-// One round: the largest key left in the row and the lowest expert that has it (E's
-// successor and a -inf key when nothing is left), then that expert's key is struck out.
+// One round: the largest key left in the row (to `best`) and the lowest expert that has it,
+// -1 when nothing but `lowest` is left; that expert's key is struck out.
 template <int EPL, typename T>
-__device__ __forceinline__ int take_best(T (&key)[EPL], int lane, T lowest) {
+__device__ __forceinline__ int take_best(T (&key)[EPL], int lane, T lowest, T& best) {
   T m = key[0];
 #pragma unroll
   for (int j = 1; j < EPL; ++j) m = key[j] > m ? key[j] : m;
   m = row16_max(m);
+  best = m;
   int e = 1 << 20;
 #pragma unroll
   for (int j = EPL - 1; j >= 0; --j) e = key[j] == m ? lane + 16 * j : e;
   e = row16_min(e);
-  const bool none = m == lowest;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) key[j] = (lane + 16 * j == e) ? lowest : key[j];
-  return none ? -1 : e;
+  return m == lowest ? -1 : e;
 }
 
 template <int EPL, bool BF16, bool SOFTMAX, bool BIAS>
@@ -124,25 +125,51 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_fwd(RouterArgs a) {
   row_scores<EPL, SOFTMAX, float>(l, s);
 
   int pick[kMaxTopk];
-  if constexpr (!BIAS) {
-    float key[EPL];
+  float key[EPL], best[kMaxTopk + 1];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) key[j] = l[j] == l[j] ? l[j] : ninf();
+  for (int j = 0; j < EPL; ++j) {
+    const int e = lane + 16 * j;
+    key[j] = BIAS && e < a.E ? s[j] + a.bias[e] : l[j];
+    // an expert whose logit is -inf or NaN, or whose key is NaN, is never chosen
+    if (!(l[j] > ninf()) || key[j] != key[j]) key[j] = ninf();
+  }
 #pragma unroll
-    for (int k = 0; k < kMaxTopk; ++k) pick[k] = k < a.K ? take_best<EPL, float>(key, lane, ninf()) : -1;
-  } else {
-    double key[EPL];
-    const double lowest = -__builtin_huge_val();
-    row_scores<EPL, SOFTMAX, double>(l, key);
+  for (int k = 0; k < kMaxTopk; ++k) pick[k] = k < a.K ? take_best<EPL, float>(key, lane, ninf(), best[k]) : -1;
+  if constexpr (BIAS) {
+    // FP32 keys are off by at most 32 u of a softmax score (u = 2^-24: the rounding of l - m
+    // times x exp(-x) <= 0.37, the function, the row sum and the division), 4 u of a sigmoid,
+    // and u of the key.  Where the keys down to the first one left out are further apart
+    // than twice that, FP64 keys have the same order; other rows (some in ten thousand) are
+    // decided again in FP64.
+    float next = key[0];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-      const int e = lane + 16 * j;
-      key[j] = e < a.E ? key[j] + (double)a.bias[e] : lowest;
-      // an expert whose logit is -inf or NaN, or whose key is NaN, is never chosen
-      if (!(l[j] > ninf()) || key[j] != key[j]) key[j] = lowest;
+    for (int j = 1; j < EPL; ++j) next = key[j] > next ? key[j] : next;
+    next = row16_max(next);
+    bool close = false;
+#pragma unroll
+    for (int k = 0; k < kMaxTopk; ++k) {
+      if (k < a.K) {
+        const float lower = k + 1 < a.K ? best[k + 1] : next;
+        const float off = (SOFTMAX ? 0x1p-18f : 0x1p-21f) + 0x1p-23f * (fabsf(best[k]) + fabsf(lower));
+        close |= lower > ninf() && !(best[k] - lower > off);
+      }
     }
+    if (__any(close)) {
+      double dkey[EPL], db;
+      const double lowest = -__builtin_huge_val();
+      row_scores<EPL, SOFTMAX, double>(l, dkey);
 #pragma unroll
-    for (int k = 0; k < kMaxTopk; ++k) pick[k] = k < a.K ? take_best<EPL, double>(key, lane, lowest) : -1;
+      for (int j = 0; j < EPL; ++j) {
+        const int e = lane + 16 * j;
+        dkey[j] = e < a.E ? dkey[j] + (double)a.bias[e] : lowest;
+        if (!(l[j] > ninf()) || dkey[j] != dkey[j]) dkey[j] = lowest;
+      }
+#pragma unroll
+      for (int k = 0; k < kMaxTopk; ++k) {
+        const int e = k < a.K ? take_best<EPL, double>(dkey, lane, lowest, db) : -1;
+        pick[k] = close ? e : pick[k];
+      }
+    }
   }
 
   // the chosen scores: each lane adds what it holds of pick k, then the row sums (one
@@ -157,14 +184,24 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_fwd(RouterArgs a) {
     sum += w[k];
   }
   const float f = a.normalize ? a.scale / (sum + kRouterEps) : a.scale;
+  int e = -1;
+  float v = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kMaxTopk; ++k) {
-    if (k < a.K && lane == k) {
-      a.top[t * a.K + k] = pick[k];
-      const float v = bad != 0.0f ? __builtin_nanf("") : w[k] * f;
-      a.rw[t * a.K + k] = pick[k] >= 0 ? v : 0.0f;
-    }
+  for (int k = 0; k < kMaxTopk; ++k) {   // lane k writes entry k
+    e = lane == k ? pick[k] : e;
+    v = lane == k ? w[k] : v;
   }
+  if (lane < a.K) {
+    a.top[t * a.K + lane] = e;
+    a.rw[t * a.K + lane] = e < 0 ? 0.0f : (bad != 0.0f ? __builtin_nanf("") : v * f);
+  }
+}
+
+// Orders this wave's LDS accesses for the compiler, which would otherwise take a value a lane
+// has just stored for granted; the hardware runs them in order.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // Gradient of sum_k gw_k w_k.  With cnt_e the times e stands in the table's row (0 or 1
@@ -174,22 +211,45 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_fwd(RouterArgs a) {
 //   softmax: dl_e = s_e (ds_e - sum_j ds_j s_j)     sigmoid: dl_e = ds_e s_e (1 - s_e)
 template <int EPL, bool BF16, bool SOFTMAX>
 __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
+  __shared__ int tags[kRouterRows * 16 * EPL];
+  __shared__ float grads[kRouterRows * 16 * EPL];
   const int lane = threadIdx.x & 15;
   const int64_t t = (int64_t)blockIdx.x * kRouterRows + (threadIdx.x >> 4);
   if (t >= a.tokens) return;
   float l[EPL], s[EPL], g[EPL], cnt[EPL];
   load_row<EPL, BF16>(a, t, lane, l);
+  // Lane k holds the row's entry k.  Its position (1 + k) and gradient go to the expert's
+  // place in LDS; the lanes then read their experts' places.  A lane that does not find its own
+  // position again shares its expert with another entry: such rows add entry by entry.
+  int me = lane < a.K ? a.top[t * a.K + lane] : -1;
+  const float mg = lane < a.K ? a.gw[t * a.K + lane] : 0.0f;
+  if (me >= a.E || me < 0) me = -1;   // skipped
+  int* tag = tags + (threadIdx.x >> 4) * (16 * EPL);
+  float* grad = grads + (threadIdx.x >> 4) * (16 * EPL);
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) g[j] = cnt[j] = 0.0f;
+  for (int j = 0; j < EPL; ++j) tag[lane + 16 * j] = 0;
+  wave_lds_fence();
+  if (me >= 0) {
+    tag[me] = lane + 1;
+    grad[me] = mg;
+  }
+  wave_lds_fence();
+  const bool twice = me >= 0 && tag[me] != lane + 1;
 #pragma unroll
-  for (int k = 0; k < kMaxTopk; ++k) {
-    if (k < a.K) {
-      int e = a.top[t * a.K + k];
-      if (e >= a.E) e = -1;
-      const float v = a.gw[t * a.K + k];
+  for (int j = 0; j < EPL; ++j) {
+    const bool hit = tag[lane + 16 * j] != 0;
+    g[j] = hit ? grad[lane + 16 * j] : 0.0f;
+    cnt[j] = hit ? 1.0f : 0.0f;
+  }
+  if (__any(twice)) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) g[j] = cnt[j] = 0.0f;
+    for (int k = 0; k < a.K; ++k) {
+      const int e = __shfl(me, k, 16);
+      const float v = __shfl(mg, k, 16);
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        const bool hit = lane + 16 * j == e;   // -1 and out-of-range entries hit nothing
+        const bool hit = lane + 16 * j == e;
         g[j] += hit ? v : 0.0f;
         cnt[j] += hit ? 1.0f : 0.0f;
       }

@@ -217,6 +217,25 @@ def test_backward_matches_formula(gpu_lib, score, dtype, normalize):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_close_keys_are_compared_in_64_bits(gpu_lib, score):
+    """Keys s + bias that FP32 cannot tell apart: the bias is chosen as -s rounded to FP32, so the
+    keys are the rounding errors (1e-8 and less) of every expert, in 64 bits all different."""
+    E, K = 40, 6
+    g = torch.Generator().manual_seed(4)
+    base = torch.randn(1, E, generator=g)
+    bias = -ref_scores(base, score)[0].float()
+    l = torch.cat([base, torch.randn(60, E, generator=g), base, base])
+    l[3] = 0.0                                        # equal scores: the bias decides, in order
+    l[-1, 5:9] = l[-1, 5]                             # some equal logits beside unequal biases
+    for b in (bias, torch.zeros(E), bias + 0.25):
+        rt, _ = ref_forward(l, K, score, True, 1.0, b)
+        top, w = torch.empty(63, K, dtype=torch.int32, device="cuda"), torch.empty(63, K, device="cuda")
+        mk.Router(E, K, score=score, normalize=True).forward(l.cuda(), top, w, expert_bias=b.cuda())
+        assert torch.equal(top.cpu(), rt)
+
+
+@pytest.mark.gpu
 def test_nan_rows(gpu_lib):
     l = torch.randn(4, 40, generator=torch.Generator().manual_seed(1))
     l[1, 5] = float("nan")
