@@ -51,6 +51,12 @@ __device__ __forceinline__ double row16_max(double v) {
   v = fmax(v, dpp_d<kDppHalfMirror>(v));
   return fmax(v, dpp_d<kDppMirror>(v));
 }
+__device__ __forceinline__ int row16_max(int v) {
+  v = max(v, dpp_i<kDppXor1>(v));
+  v = max(v, dpp_i<kDppXor2>(v));
+  v = max(v, dpp_i<kDppHalfMirror>(v));
+  return max(v, dpp_i<kDppMirror>(v));
+}
 __device__ __forceinline__ int row16_min(int v) {
   v = min(v, dpp_i<kDppXor1>(v));
   v = min(v, dpp_i<kDppXor2>(v));

@@ -88,10 +88,19 @@ __device__ __forceinline__ void row_scores(const float (&l)[EPL], T (&s)[EPL]) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       if constexpr (std::is_same<T, double>::value) s[j] = 1.0 / (1.0 + exp(-(double)l[j]));
-      else s[j] = 1.0f / (1.0f + expf(-l[j]));
+      else s[j] = __builtin_amdgcn_rcpf(1.0f + expf(-l[j]));
     }
   }
 }
+
+// Keys as integers in the same order (-0 becomes +0 first): integer maxima need no
+// canonical forms and fold into the DPP instruction.  kNoKey lies below every float's.
+constexpr int kNoKey = INT32_MIN;
+__device__ __forceinline__ int order_key(float v) {
+  const int b = __float_as_int(v + 0.0f);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float key_value(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
 // One round: the largest key left in the row (to `best`) and the lowest expert that has it,
 // -1 when nothing but `lowest` is left; that expert's key is struck out.
@@ -111,47 +120,55 @@ __device__ __forceinline__ int take_best(T (&key)[EPL], int lane, T lowest, T& b
   return m == lowest ? -1 : e;
 }
 
+// Orders this wave's LDS accesses for the compiler, which would otherwise take a value a lane
+// has just stored for granted; the hardware runs them in order.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 template <int EPL, bool BF16, bool SOFTMAX, bool BIAS>
 __global__ __launch_bounds__(kRouterThreads) void k_router_fwd(RouterArgs a) {
+  __shared__ float chosen[kRouterRows][kMaxTopk];
   const int lane = threadIdx.x & 15;
   const int64_t t = (int64_t)blockIdx.x * kRouterRows + (threadIdx.x >> 4);
   if (t >= a.tokens) return;   // whole 16-lane rows leave together
   float l[EPL], s[EPL];
   load_row<EPL, BF16>(a, t, lane, l);
-  float bad = 0.0f;
+  int bad = 0;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) bad = l[j] != l[j] ? 1.0f : bad;
+  for (int j = 0; j < EPL; ++j) bad = l[j] != l[j] ? 1 : bad;
   bad = row16_max(bad);
   row_scores<EPL, SOFTMAX, float>(l, s);
 
-  int pick[kMaxTopk];
-  float key[EPL], best[kMaxTopk + 1];
+  int pick[kMaxTopk], key[EPL], best[kMaxTopk];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = lane + 16 * j;
-    key[j] = BIAS && e < a.E ? s[j] + a.bias[e] : l[j];
-    // an expert whose logit is -inf or NaN, or whose key is NaN, is never chosen
-    if (!(l[j] > ninf()) || key[j] != key[j]) key[j] = ninf();
+    const float v = BIAS && e < a.E ? s[j] + a.bias[e] : l[j];
+    // an expert whose logit is -inf or NaN, or whose key is -inf or NaN, is never chosen
+    key[j] = l[j] > ninf() && v > ninf() ? order_key(v) : kNoKey;
   }
 #pragma unroll
-  for (int k = 0; k < kMaxTopk; ++k) pick[k] = k < a.K ? take_best<EPL, float>(key, lane, ninf(), best[k]) : -1;
+  for (int k = 0; k < kMaxTopk; ++k) pick[k] = k < a.K ? take_best<EPL, int>(key, lane, kNoKey, best[k]) : -1;
   if constexpr (BIAS) {
     // FP32 keys are off by at most 32 u of a softmax score (u = 2^-24: the rounding of l - m
-    // times x exp(-x) <= 0.37, the function, the row sum and the division), 4 u of a sigmoid,
+    // times x exp(-x) <= 0.37, the function, the row sum and the division), 8 u of a sigmoid,
     // and u of the key.  Where the keys down to the first one left out are further apart
     // than twice that, FP64 keys have the same order; other rows (some in ten thousand) are
     // decided again in FP64.
-    float next = key[0];
+    int next = key[0];
 #pragma unroll
-    for (int j = 1; j < EPL; ++j) next = key[j] > next ? key[j] : next;
+    for (int j = 1; j < EPL; ++j) next = max(next, key[j]);
     next = row16_max(next);
     bool close = false;
 #pragma unroll
     for (int k = 0; k < kMaxTopk; ++k) {
       if (k < a.K) {
-        const float lower = k + 1 < a.K ? best[k + 1] : next;
-        const float off = (SOFTMAX ? 0x1p-18f : 0x1p-21f) + 0x1p-23f * (fabsf(best[k]) + fabsf(lower));
-        close |= lower > ninf() && !(best[k] - lower > off);
+        const int low = k + 1 < a.K ? best[k + 1 < kMaxTopk ? k + 1 : k] : next;
+        const float hi = key_value(best[k]), lo = key_value(low);
+        const float off = (SOFTMAX ? 0x1p-18f : 0x1p-20f) + 0x1p-23f * (fabsf(hi) + fabsf(lo));
+        close |= low != kNoKey && !(hi - lo > off);
       }
     }
     if (__any(close)) {
@@ -172,36 +189,29 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_fwd(RouterArgs a) {
     }
   }
 
-  // the chosen scores: each lane adds what it holds of pick k, then the row sums (one
-  // lane has the value, the others zero)
-  float w[kMaxTopk], sum = 0.0f;
+  // the lane that holds pick k leaves its score for lane k, which writes entry k
+  float* mine = chosen[threadIdx.x >> 4];
+  if (lane < kMaxTopk) mine[lane] = 0.0f;
+  wave_lds_fence();
+  int e = -1;
 #pragma unroll
   for (int k = 0; k < kMaxTopk; ++k) {
-    float v = 0.0f;
+    if (k < a.K) {
+      float v = s[0];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) v = (lane + 16 * j == pick[k]) ? s[j] : v;
-    w[k] = k < a.K ? row16_sum(v) : 0.0f;
-    sum += w[k];
+      for (int j = 1; j < EPL; ++j) v = (pick[k] >> 4) == j ? s[j] : v;
+      if ((pick[k] & 15) == lane && pick[k] >= 0) mine[k] = v;
+      e = lane == k ? pick[k] : e;
+    }
   }
+  wave_lds_fence();
+  const float w = lane < a.K ? mine[lane] : 0.0f;
+  const float sum = row16_sum(w);
   const float f = a.normalize ? a.scale / (sum + kRouterEps) : a.scale;
-  int e = -1;
-  float v = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kMaxTopk; ++k) {   // lane k writes entry k
-    e = lane == k ? pick[k] : e;
-    v = lane == k ? w[k] : v;
-  }
   if (lane < a.K) {
     a.top[t * a.K + lane] = e;
-    a.rw[t * a.K + lane] = e < 0 ? 0.0f : (bad != 0.0f ? __builtin_nanf("") : v * f);
+    a.rw[t * a.K + lane] = e < 0 ? 0.0f : (bad ? __builtin_nanf("") : w * f);
   }
-}
-
-// Orders this wave's LDS accesses for the compiler, which would otherwise take a value a lane
-// has just stored for granted; the hardware runs them in order.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
 }
 
 // Gradient of sum_k gw_k w_k.  With cnt_e the times e stands in the table's row (0 or 1
