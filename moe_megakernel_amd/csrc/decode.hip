@@ -240,12 +240,6 @@ __device__ __forceinline__ void dot_steps(const Turn& t, const uint8_t* const (&
   }
 }
 
-// Steps in flight by the number of column groups: what fits 128 registers (four waves a
-// SIMD) beside the accumulators and addresses.  Spills cost more than depth gains: E4M3 at 3
-// steps took 36 us where 2 take 30 (the second kernel, 7 tokens, H 4096, 96 experts).
-template <bool MX, int R, int NF>
-constexpr int depth() { return NF == 2 || R == 2 ? 1 : 2; }
-
 __device__ __forceinline__ float swiglu(float a, float b, float L) {
   if (L > 0.0f) {   // comparisons that keep a NaN
     a = a > L ? L : a;
@@ -322,6 +316,31 @@ __device__ __forceinline__ int each_route(const Args& a, const Fc1Shared& s, int
   return pos;
 }
 
+// The same for a table of at most kSmallTable entries, by one wave in registers: the expert of
+// group g (here in the order of first appearance: any fixed order serves, as long as every
+// workgroup takes the same), its routes to s.list and their number to count.
+constexpr int kSmallTable = 32;
+__device__ __forceinline__ int small_group(const Args& a, Fc1Shared& s, int g, int& count) {
+  const int lane = threadIdx.x & 63, n = a.T * a.K;
+  int e = lane < n ? a.top[lane] : -1;
+  if (e < 0 || e >= a.E) e = -1;
+  const int row0 = lane - lane % a.K;
+  bool first = e >= 0, again = false;   // first of its expert; listed again in its row
+  for (int j = 0; j < n; ++j) {
+    const bool same = j < lane && __builtin_amdgcn_readlane(e, j) == e;
+    first &= !same;
+    again |= same && j >= row0;
+  }
+  uint64_t m = __ballot(first);
+  if (g >= __popcll(m)) return -1;
+  for (; g > 0; --g) m &= m - 1;
+  e = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)m) - 1) == e && !again ? e : -1;
+  m = __ballot(e >= 0);
+  if (e >= 0) s.list[__popcll(m & ((1ull << lane) - 1))] = (int16_t)lane;
+  count = __popcll(m);
+  return __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)m) - 1);
+}
+
 // The first workgroup leaves the plan for the second kernel: one wave a group counts and
 // then lists its routes, at the sum of the counts of the groups before it.
 template <int NT>
@@ -360,7 +379,7 @@ __device__ __forceinline__ void write_plan(const Args& a, const Fc1Shared& s, in
 }
 
 // Columns c0 .. c0 + 16 NF - 1 (of `count`) of one tile.
-template <bool MX, int R, int W, int NF>
+template <bool MX, int R, int W, int NF, int D>
 __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint4* lds, int e, int i0, int c0,
                                          int count) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -394,7 +413,7 @@ __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[g][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const Turn turn = turn_of(lds + wave * wave_cells<MX, R>());
-  dot_steps<MX, R, NF, depth<MX, R, NF>()>(turn, w, ws, x, s1 - s0, acc);
+  dot_steps<MX, R, NF, D>(turn, w, ws, x, s1 - s0, acc);
   // [wave][column][row]: a lane has rows 4 q .. 4 q + 3 of column r.  Over the turn-round slots
   __syncthreads();
   float* red = reinterpret_cast<float*>(lds);
@@ -420,21 +439,21 @@ __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint
 }
 
 // More than 16 tokens go in passes over one fragment's weights, which the caches then hold.
-template <bool MX, int R, int W>
+template <bool MX, int R, int W, int D>
 __device__ __forceinline__ void fc1_group(const Args& a, const Fc1Shared& s, uint4* lds, int e, int i0, int count) {
   if (count <= 16) {
-    fc1_tile<MX, R, W, 1>(a, s, lds, e, i0, 0, count);
+    fc1_tile<MX, R, W, 1, D>(a, s, lds, e, i0, 0, count);
     return;
   }
   for (int g = 0; g < R; ++g)
     for (int c0 = 0; c0 < count; c0 += 32) {
       if (g + c0) __syncthreads();
-      fc1_tile<MX, 1, W, 2>(a, s, lds, e, i0 + 8 * g, c0, count);
+      fc1_tile<MX, 1, W, 2, 1>(a, s, lds, e, i0 + 8 * g, c0, count);
     }
 }
 
-template <bool MX, int R, int W>
-__global__ __launch_bounds__(64 * W, 4) void k_decode_fc1(Args a) {
+template <bool MX, int R, int W, int D, int OCC>
+__global__ __launch_bounds__(64 * W, OCC) void k_decode_fc1(Args a) {
   __shared__ Fc1Shared s;
   // turn-round slots, then the partial sums of up to two column groups
   constexpr int kCells = wave_cells<MX, R>() > 2 * R * 64 ? wave_cells<MX, R>() : 2 * R * 64;
@@ -466,43 +485,54 @@ __global__ __launch_bounds__(64 * W, 4) void k_decode_fc1(Args a) {
     return;
   }
   if (b < shared_blocks) {
-    fc1_group<false, RS, W>(a, s, lds, -1, b * 8 * RS, a.T);
+    fc1_group<false, RS, W, 2>(a, s, lds, -1, b * 8 * RS, a.T);
     return;
   }
   b -= shared_blocks;
-  read_table<64 * W>(a, s);
-  const int e = __builtin_amdgcn_readfirstlane(group_expert(s, b / tiles));
-  if (e < 0) return;
-  // every wave lists the routes for itself, to the same place with the same values
-  const int count = each_route(a, s, e, [&](int p, int i) { s.list[p] = (int16_t)i; });
+  int e, count;   // every wave lists the routes for itself, to the same place with the same values
+  if (a.T * a.K <= kSmallTable) {
+    e = small_group(a, s, b / tiles, count);
+    if (e < 0) return;
+  } else {
+    read_table<64 * W>(a, s);
+    e = __builtin_amdgcn_readfirstlane(group_expert(s, b / tiles));
+    if (e < 0) return;
+    count = each_route(a, s, e, [&](int p, int i) { s.list[p] = (int16_t)i; });
+  }
   __builtin_amdgcn_wave_barrier();
-  fc1_group<MX, R, W>(a, s, lds, e, b % tiles * 8 * R, count);
+  fc1_group<MX, R, W, D>(a, s, lds, e, b % tiles * 8 * R, count);
 }
 
 // ---------------------------------------------------------------- FC2 + combine
-// A workgroup owns 16 output columns of every token.  Its W waves split the steps of all
+// A workgroup owns 16 R output columns of every token.  Its W waves split the steps of all
 // experts in use evenly; each adds w_tk times what it has of an expert's product to an
-// accumulator [token][16] of its own in LDS, and the waves' accumulators are joined in
+// accumulator [token][16 R] of its own in LDS, and the waves' accumulators are joined in
 // order at the end.
 struct Fc2Shared {
   int32_t expert[kMaxExperts + 1], first[kMaxExperts + 2];
   int16_t route[kMaxRoutes];
-  float weight[kMaxRoutes], gate[kMaxTokens];
+  float weight[kMaxRoutes];
 };
 
-// Columns c0 .. of one expert, steps s0 .. s0 + n - 1.
-template <bool MX, int NF>
-__device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, const Turn& turn, float* acc_lds, int n0,
+// Columns c0 .. of one expert (e < 0: the shared one), steps s0 .. s0 + n - 1; row fragments
+// g0 .. g0 + R - 1 of the workgroup's RT.
+template <bool MX, int R, int RT, int NF, int D>
+__device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, const Turn& turn, float* acc_lds, int g0,
                                          int e, int first, int c0, int count, int s0, int n) {
   const int lane = threadIdx.x & 63, r = lane >> 2, c4 = 16 * (lane & 3);   // the row and byte this lane loads
-  const uint8_t *w[1], *ws[1] = {nullptr};
-  if (e < 0) {
-    w[0] = a.sdown.row(0, n0 + r);
-  } else {
-    w[0] = a.down.data.row(e, n0 + r);
-    if constexpr (MX) ws[0] = a.down.scale.row(e, n0 + r) + s0 * 4;
+  const uint8_t *w[R], *ws[R];
+#pragma unroll
+  for (int g = 0; g < R; ++g) {
+    const int row = ((int)blockIdx.x * RT + g0 + g) * 16 + r;
+    ws[g] = nullptr;
+    if (e < 0) {
+      w[g] = a.sdown.row(0, row);
+    } else {
+      w[g] = a.down.data.row(e, row);
+      if constexpr (MX) ws[g] = a.down.scale.row(e, row) + s0 * 4;
+    }
+    w[g] += (int64_t)s0 * WStep<MX>::kBytes + c4;
   }
-  w[0] += (int64_t)s0 * WStep<MX>::kBytes + c4;
   const uint8_t* x[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
@@ -510,59 +540,74 @@ __device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, cons
     const int64_t hrow = e < 0 ? (int64_t)a.T * a.K + c : s.route[first + c];
     x[f] = reinterpret_cast<const uint8_t*>(a.h + hrow * a.I) + (int64_t)s0 * XStep::kBytes + c4;
   }
-  f32x4_t acc[1][NF];
+  f32x4_t acc[R][NF];
 #pragma unroll
-  for (int f = 0; f < NF; ++f) acc[0][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  dot_steps<MX, 1, NF, depth<MX, 1, NF>()>(turn, w, ws, x, n, acc);
+  for (int g = 0; g < R; ++g)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) acc[g][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  dot_steps<MX, R, NF, D>(turn, w, ws, x, n, acc);
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
     const int c = c0 + 16 * f + turn.row;
     if (c >= count) continue;
     const int tok = e < 0 ? c : s.route[first + c] / a.K;
-    const float wt = e < 0 ? s.gate[c] : s.weight[first + c];
-    f32x4_t* o = reinterpret_cast<f32x4_t*>(acc_lds + tok * 16 + 4 * turn.q);   // the wave's own
-    f32x4_t v = *o;
+    const float wt = e < 0 ? (a.gw ? a.gate_s[c] : 1.0f) : s.weight[first + c];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += wt * acc[0][f][i];
-    *o = v;
+    for (int g = 0; g < R; ++g) {
+      f32x4_t* o = reinterpret_cast<f32x4_t*>(acc_lds + (tok * RT + g0 + g) * 16 + 4 * turn.q);   // the wave's own
+      f32x4_t v = *o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += wt * acc[g][f][i];
+      *o = v;
+    }
   }
 }
 
-template <bool MX>
-__device__ __forceinline__ void fc2_group(const Args& a, const Fc2Shared& s, const Turn& turn, float* acc_lds, int n0,
-                                          int e, int first, int count, int s0, int n) {
+// Up to 16 tokens: all R fragments together; more: passes over one fragment's weights.
+template <bool MX, int R, int RT, int D>
+__device__ __forceinline__ void fc2_group(const Args& a, const Fc2Shared& s, const Turn& turn, float* acc_lds, int e,
+                                          int first, int count, int s0, int n) {
   if (count <= 16) {
-    fc2_part<MX, 1>(a, s, turn, acc_lds, n0, e, first, 0, count, s0, n);
+    for (int g = 0; g < RT; g += R) fc2_part<MX, R, RT, 1, D>(a, s, turn, acc_lds, g, e, first, 0, count, s0, n);
     return;
   }
-  for (int c0 = 0; c0 < count; c0 += 32) fc2_part<MX, 2>(a, s, turn, acc_lds, n0, e, first, c0, count, s0, n);
+  for (int g = 0; g < RT; ++g)
+    for (int c0 = 0; c0 < count; c0 += 32)
+      fc2_part<MX, 1, RT, 2, 1>(a, s, turn, acc_lds, g, e, first, c0, count, s0, n);
 }
 
-template <bool MX, int W>
-__global__ __launch_bounds__(64 * W, 4) void k_decode_fc2(Args a) {
-  extern __shared__ __align__(16) float acc_all[];   // [W][T][16]
+template <bool MX, int W, int R, int D, int OCC>
+__global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
+  extern __shared__ __align__(16) float acc_all[];   // [W][T][16 R]
   __shared__ Fc2Shared s;
-  __shared__ __align__(16) uint4 slots[W * wave_cells<MX, 1>()];
+  __shared__ __align__(16) uint4 slots[W * wave_cells<MX, R>()];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // whole arrays, past the plan's ends too: no load waits for another
+  // the plan's whole arrays, past their ends too: no load waits for another, and none is
+  // waited for before the shared expert is done
   const int routed = a.plan->groups;
-  if (tid <= kMaxExperts) s.expert[tid] = a.plan->expert[tid];
-  if (tid < kMaxExperts + 2) s.first[tid] = a.plan->first[tid];
+  int plan_e = 0, plan_f = 0, plan_r = 0;
+  float plan_w = 0.0f;
+  if (tid <= kMaxExperts) plan_e = a.plan->expert[tid];
+  if (tid < kMaxExperts + 2) plan_f = a.plan->first[tid];
   if (tid < a.T * a.K) {
-    s.route[tid] = (int16_t)a.plan->route[tid];
-    s.weight[tid] = a.plan->weight[tid];
+    plan_r = a.plan->route[tid];
+    plan_w = a.plan->weight[tid];
   }
-  if (tid < a.T) s.gate[tid] = a.gw ? a.gate_s[tid] : 1.0f;
-  for (int i = tid; i < W * a.T * 16; i += 64 * W) acc_all[i] = 0.0f;
-  __syncthreads();
-
-  float* mine = acc_all + wave * a.T * 16;
-  const Turn turn = turn_of(slots + wave * wave_cells<MX, 1>());
-  const int n0 = blockIdx.x * 16, steps = a.I / kStep;
+  float* mine = acc_all + wave * a.T * 16 * R;
+  for (int i = tid & 63; i < a.T * 4 * R; i += 64) reinterpret_cast<f32x4_t*>(mine)[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const Turn turn = turn_of(slots + wave * wave_cells<MX, R>());
+  const int steps = a.I / kStep;
   if (a.shared) {   // every wave takes its part: with many tokens these steps cost more than routed ones
     const int s0 = wave * steps / W, s1 = (wave + 1) * steps / W;
-    if (s1 > s0) fc2_group<false>(a, s, turn, mine, n0, -1, 0, a.T, s0, s1 - s0);
+    if (s1 > s0) fc2_group<false, 1, R, 2>(a, s, turn, mine, -1, 0, a.T, s0, s1 - s0);
   }
+  if (tid <= kMaxExperts) s.expert[tid] = plan_e;
+  if (tid < kMaxExperts + 2) s.first[tid] = plan_f;
+  if (tid < a.T * a.K) {
+    s.route[tid] = (int16_t)plan_r;
+    s.weight[tid] = plan_w;
+  }
+  __syncthreads();
   const int64_t total = (int64_t)routed * steps;
   int64_t p = wave * total / W;
   const int64_t end = (wave + 1) * total / W;
@@ -571,43 +616,50 @@ __global__ __launch_bounds__(64 * W, 4) void k_decode_fc2(Args a) {
     const int n = (int)min((int64_t)(steps - s0), end - p);
     const int e = __builtin_amdgcn_readfirstlane(s.expert[g]), first = __builtin_amdgcn_readfirstlane(s.first[g]);
     const int count = __builtin_amdgcn_readfirstlane(s.first[g + 1]) - first;
-    fc2_group<MX>(a, s, turn, mine, n0, e, first, count, s0, n);
+    fc2_group<MX, R, R, D>(a, s, turn, mine, e, first, count, s0, n);
     p += n;
   }
   __syncthreads();
-  for (int o = tid; o < a.T * 16; o += 64 * W) {
+  for (int o = tid; o < a.T * 16 * R; o += 64 * W) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += acc_all[w * a.T * 16 + o];
-    a.out[(int64_t)(o >> 4) * a.H + n0 + (o & 15)] = (uint16_t)f2bf(v);
+    for (int w = 0; w < W; ++w) v += acc_all[w * a.T * 16 * R + o];
+    a.out[(int64_t)(o / (16 * R)) * a.H + blockIdx.x * 16 * R + o % (16 * R)] = (uint16_t)f2bf(v);
   }
 }
 
 }  // namespace
 
+// Steps in flight (D) and waves a SIMD (OCC) fit the register file: four waves leave 128
+// registers each.  Spills and fewer waves cost more than depth gains: one token of BF16 at H 4096
+// takes 28.2 us as it is, 30.2 with three steps in flight and 29.1 with eight waves a
+// workgroup in the first kernel.
 template <bool MX>
 void launch_fc1(hipStream_t st, const Args& a) {
   // Two fragments a workgroup share the tokens' loads, which weigh twice as much beside E4M3
   // as beside BF16: 371 us against 424 (64 tokens, H 7168, E4M3); BF16 loses a little to the
   // coarser grid (151 us against 139, 19 tokens, H 4096).
-  constexpr int R = MX ? 2 : 1, W = kFc1Waves;
+  constexpr int R = MX ? 2 : 1, W = kFc1Waves, D = MX ? 1 : 2;
   const int tiles = a.I / (8 * R), used = a.E < a.T * a.K ? a.E : a.T * a.K;
   const int gate = a.gw ? (a.T + W - 1) / W : 0;
   const int shared = a.shared ? a.I / (8 * (MX ? 1 : R)) : 0;
-  hipLaunchKernelGGL((k_decode_fc1<MX, R, W>), dim3((unsigned)(1 + shared + used * tiles + gate)), dim3(64 * W), 0,
-                     st, a);
+  hipLaunchKernelGGL((k_decode_fc1<MX, R, W, D, 4>), dim3((unsigned)(1 + shared + used * tiles + gate)), dim3(64 * W),
+                     0, st, a);
 }
-template <bool MX, int W>
-void launch_fc2_w(hipStream_t st, const Args& a) {
+template <bool MX, int W, int R, int OCC>
+void launch_fc2_as(hipStream_t st, const Args& a) {
   static_assert(64 * W >= kMaxRoutes && 64 * W >= kMaxExperts + 2, "the plan in one load a thread");
-  hipLaunchKernelGGL((k_decode_fc2<MX, W>), dim3(a.H / 16), dim3(64 * W), (size_t)W * a.T * 16 * sizeof(float), st, a);
+  hipLaunchKernelGGL((k_decode_fc2<MX, W, R, 2, OCC>), dim3(a.H / (16 * R)), dim3(64 * W),
+                     (size_t)W * a.T * 16 * R * sizeof(float), st, a);
 }
 template <bool MX>
 void launch_fc2(hipStream_t st, const Args& a) {
-  // A grid of at most one workgroup a CU takes 16 waves in each: 28.5 us against 30.0 at
-  // H 4096 (7 tokens, E4M3); more workgroups than that run two to a CU.
-  if (a.H / 16 <= 256) launch_fc2_w<MX, 16>(st, a);
-  else launch_fc2_w<MX, 8>(st, a);
+  // Up to H 4096 a fragment and 16 waves a workgroup, at most one workgroup a CU: 28.5 us
+  // against 30.0 with 8 waves (7 tokens, H 4096, E4M3).  Above, two fragments share the tokens'
+  // loads and 8 waves hold them: 185 us against 222 at H 7168 (64 tokens, E4M3), 122 against
+  // 154 at H 5120 (16 tokens); the same with BF16 at H 7168.
+  if (a.H / 16 <= 256) launch_fc2_as<MX, 16, 1, 4>(st, a);
+  else launch_fc2_as<MX, 8, 2, 2>(st, a);
 }
 template void launch_fc1<false>(hipStream_t, const Args&);
 template void launch_fc1<true>(hipStream_t, const Args&);

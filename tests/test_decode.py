@@ -230,6 +230,8 @@ CASES = [
     dict(T=64, H=256, I=128, E=2, K=1, kind="one"),
     dict(T=64, H=512, I=256, E=40, K=8, kind="short", limit=0.4),
     dict(T=31, H=256, I=1024, E=64, K=6, sep=True),
+    dict(T=9, H=4224, I=2304, E=3, K=2, limit=1.0),              # two row fragments; more than 16 steps
+    dict(T=37, H=4352, I=128, E=4, K=2, layout="table", gate=True),
     dict(T=64, H=128, I=128, E=255, K=8, kind="invalid", shared=False),
 ]
 
