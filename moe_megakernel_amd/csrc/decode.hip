@@ -438,28 +438,37 @@ __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint
   }
 }
 
-// More than 16 tokens go in passes over one fragment's weights, which the caches then hold.
-template <bool MX, int R, int W, int D>
+// More than 16 tokens: without MANY in passes of 32 over one fragment's weights, which the
+// caches then hold; with MANY (two waves a SIMD, so twice the registers) all at once.
+template <bool MX, int R, int W, int D, bool MANY>
 __device__ __forceinline__ void fc1_group(const Args& a, const Fc1Shared& s, uint4* lds, int e, int i0, int count) {
   if (count <= 16) {
     fc1_tile<MX, R, W, 1, D>(a, s, lds, e, i0, 0, count);
-    return;
+  } else if constexpr (MANY) {
+    if (count <= 32) fc1_tile<MX, R, W, 2, 1>(a, s, lds, e, i0, 0, count);
+    else fc1_tile<MX, R, W, 4, 1>(a, s, lds, e, i0, 0, count);
+  } else {
+    for (int g = 0; g < R; ++g)
+      for (int c0 = 0; c0 < count; c0 += 32) {
+        if (g + c0) __syncthreads();
+        fc1_tile<MX, 1, W, 2, 1>(a, s, lds, e, i0 + 8 * g, c0, count);
+      }
   }
-  for (int g = 0; g < R; ++g)
-    for (int c0 = 0; c0 < count; c0 += 32) {
-      if (g + c0) __syncthreads();
-      fc1_tile<MX, 1, W, 2, 1>(a, s, lds, e, i0 + 8 * g, c0, count);
-    }
 }
 
-template <bool MX, int R, int W, int D, int OCC>
-__global__ __launch_bounds__(64 * W, OCC) void k_decode_fc1(Args a) {
+// Row fragments a workgroup of the shared expert takes: BF16 needs twice the registers.
+template <bool MX, int R, bool MANY>
+constexpr int shared_frags() { return MX && !MANY ? 1 : R; }
+
+template <bool MX, int R, int W, int D, bool MANY>
+__global__ __launch_bounds__(64 * W, MANY ? 2 : 4) void k_decode_fc1(Args a) {
   __shared__ Fc1Shared s;
-  // turn-round slots, then the partial sums of up to two column groups
-  constexpr int kCells = wave_cells<MX, R>() > 2 * R * 64 ? wave_cells<MX, R>() : 2 * R * 64;
+  // turn-round slots, then the partial sums of up to four column groups
+  constexpr int kSums = (MANY ? 4 : 2) * R * 64;
+  constexpr int kCells = wave_cells<MX, R>() > kSums ? wave_cells<MX, R>() : kSums;
   __shared__ __align__(16) uint4 lds[W * kCells];
   const int tiles = a.I / (8 * R);
-  constexpr int RS = MX ? 1 : R;                      // BF16 fragments take twice the registers
+  constexpr int RS = shared_frags<MX, R, MANY>();
   const int shared_blocks = a.shared ? a.I / (8 * RS) : 0;
   const int routed_blocks = min(a.E, a.T * a.K) * tiles;
   if (blockIdx.x == 0) {
@@ -485,7 +494,7 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc1(Args a) {
     return;
   }
   if (b < shared_blocks) {
-    fc1_group<false, RS, W, 2>(a, s, lds, -1, b * 8 * RS, a.T);
+    fc1_group<false, RS, W, 2, MANY>(a, s, lds, -1, b * 8 * RS, a.T);
     return;
   }
   b -= shared_blocks;
@@ -500,7 +509,7 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc1(Args a) {
     count = each_route(a, s, e, [&](int p, int i) { s.list[p] = (int16_t)i; });
   }
   __builtin_amdgcn_wave_barrier();
-  fc1_group<MX, R, W, D>(a, s, lds, e, b % tiles * 8 * R, count);
+  fc1_group<MX, R, W, D, MANY>(a, s, lds, e, b % tiles * 8 * R, count);
 }
 
 // ---------------------------------------------------------------- FC2 + combine
@@ -563,20 +572,21 @@ __device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, cons
   }
 }
 
-// Up to 16 tokens: all R fragments together; more: passes over one fragment's weights.
-template <bool MX, int R, int RT, int D>
+// All RT fragments of the workgroup together (R at a time up to 16 tokens: the shared expert's
+// BF16 rows take more registers than E4M3's).  MANY: a batch of more than 16 tokens.
+template <bool MX, int R, int RT, int D, bool MANY>
 __device__ __forceinline__ void fc2_group(const Args& a, const Fc2Shared& s, const Turn& turn, float* acc_lds, int e,
                                           int first, int count, int s0, int n) {
-  if (count <= 16) {
+  if (!MANY || count <= 16) {
     for (int g = 0; g < RT; g += R) fc2_part<MX, R, RT, 1, D>(a, s, turn, acc_lds, g, e, first, 0, count, s0, n);
-    return;
+  } else if (count <= 32) {
+    fc2_part<MX, RT, RT, 2, 1>(a, s, turn, acc_lds, 0, e, first, 0, count, s0, n);
+  } else {
+    fc2_part<MX, RT, RT, 4, 1>(a, s, turn, acc_lds, 0, e, first, 0, count, s0, n);
   }
-  for (int g = 0; g < RT; ++g)
-    for (int c0 = 0; c0 < count; c0 += 32)
-      fc2_part<MX, 1, RT, 2, 1>(a, s, turn, acc_lds, g, e, first, c0, count, s0, n);
 }
 
-template <bool MX, int W, int R, int D, int OCC>
+template <bool MX, int W, int R, int D, int OCC, bool MANY>
 __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
   extern __shared__ __align__(16) float acc_all[];   // [W][T][16 R]
   __shared__ Fc2Shared s;
@@ -599,7 +609,7 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
   const int steps = a.I / kStep;
   if (a.shared) {   // every wave takes its part: with many tokens these steps cost more than routed ones
     const int s0 = wave * steps / W, s1 = (wave + 1) * steps / W;
-    if (s1 > s0) fc2_group<false, 1, R, 2>(a, s, turn, mine, -1, 0, a.T, s0, s1 - s0);
+    if (s1 > s0) fc2_group<false, 1, R, 2, MANY>(a, s, turn, mine, -1, 0, a.T, s0, s1 - s0);
   }
   if (tid <= kMaxExperts) s.expert[tid] = plan_e;
   if (tid < kMaxExperts + 2) s.first[tid] = plan_f;
@@ -616,7 +626,7 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
     const int n = (int)min((int64_t)(steps - s0), end - p);
     const int e = __builtin_amdgcn_readfirstlane(s.expert[g]), first = __builtin_amdgcn_readfirstlane(s.first[g]);
     const int count = __builtin_amdgcn_readfirstlane(s.first[g + 1]) - first;
-    fc2_group<MX, R, R, D>(a, s, turn, mine, e, first, count, s0, n);
+    fc2_group<MX, R, R, D, MANY>(a, s, turn, mine, e, first, count, s0, n);
     p += n;
   }
   __syncthreads();
@@ -634,32 +644,48 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
 // registers each.  Spills and fewer waves cost more than depth gains: one token of BF16 at H 4096
 // takes 28.2 us as it is, 30.2 with three steps in flight and 29.1 with eight waves a
 // workgroup in the first kernel.
-template <bool MX>
-void launch_fc1(hipStream_t st, const Args& a) {
-  // Two fragments a workgroup share the tokens' loads, which weigh twice as much beside E4M3
-  // as beside BF16: 371 us against 424 (64 tokens, H 7168, E4M3); BF16 loses a little to the
-  // coarser grid (151 us against 139, 19 tokens, H 4096).
-  constexpr int R = MX ? 2 : 1, W = kFc1Waves, D = MX ? 1 : 2;
+template <bool MX, int R, int D, bool MANY>
+void launch_fc1_as(hipStream_t st, const Args& a) {
+  constexpr int W = kFc1Waves;
   const int tiles = a.I / (8 * R), used = a.E < a.T * a.K ? a.E : a.T * a.K;
   const int gate = a.gw ? (a.T + W - 1) / W : 0;
-  const int shared = a.shared ? a.I / (8 * (MX ? 1 : R)) : 0;
-  hipLaunchKernelGGL((k_decode_fc1<MX, R, W, D, 4>), dim3((unsigned)(1 + shared + used * tiles + gate)), dim3(64 * W),
-                     0, st, a);
+  const int shared = a.shared ? a.I / (8 * shared_frags<MX, R, MANY>()) : 0;
+  hipLaunchKernelGGL((k_decode_fc1<MX, R, W, D, MANY>), dim3((unsigned)(1 + shared + used * tiles + gate)),
+                     dim3(64 * W), 0, st, a);
 }
-template <bool MX, int W, int R, int OCC>
+template <bool MX>
+void launch_fc1(hipStream_t st, const Args& a) {
+  // More than 14 tokens an expert on average (and more than 16 in all): every row fragment
+  // takes up to 64 tokens at once, on two waves a SIMD.  64 tokens over 6 BF16 experts of H 4096:
+  // 38 us against 54; over 32 experts top-6 (12 each), E4M3: 89 against 80.
+  // Otherwise two fragments a workgroup share the tokens' loads with E4M3, where they weigh
+  // twice as much as beside BF16: 371 us against 424 (64 tokens, H 7168, E4M3); BF16 loses a
+  // little to the coarser grid (151 us against 139, 19 tokens, H 4096).
+  if (a.T > 16 && a.T * a.K > 14 * a.E) launch_fc1_as<MX, 2, 1, true>(st, a);
+  else launch_fc1_as<MX, MX ? 2 : 1, MX ? 1 : 2, false>(st, a);
+}
+template <bool MX, int W, int R, int OCC, bool MANY>
 void launch_fc2_as(hipStream_t st, const Args& a) {
   static_assert(64 * W >= kMaxRoutes && 64 * W >= kMaxExperts + 2, "the plan in one load a thread");
-  hipLaunchKernelGGL((k_decode_fc2<MX, W, R, 2, OCC>), dim3(a.H / (16 * R)), dim3(64 * W),
+  hipLaunchKernelGGL((k_decode_fc2<MX, W, R, 2, OCC, MANY>), dim3(a.H / (16 * R)), dim3(64 * W),
                      (size_t)W * a.T * 16 * R * sizeof(float), st, a);
 }
 template <bool MX>
 void launch_fc2(hipStream_t st, const Args& a) {
-  // Up to H 4096 a fragment and 16 waves a workgroup, at most one workgroup a CU: 28.5 us
-  // against 30.0 with 8 waves (7 tokens, H 4096, E4M3).  Above, two fragments share the tokens'
-  // loads and 8 waves hold them: 185 us against 222 at H 7168 (64 tokens, E4M3), 122 against
-  // 154 at H 5120 (16 tokens); the same with BF16 at H 7168.
-  if (a.H / 16 <= 256) launch_fc2_as<MX, 16, 1, 4>(st, a);
-  else launch_fc2_as<MX, 8, 2, 2>(st, a);
+  // Up to H 4096 a fragment a workgroup, at most one workgroup a CU; up to 16 tokens then with
+  // 16 waves: 28.5 us against 30.0 with 8 (7 tokens, H 4096, E4M3).  Above, two fragments share
+  // the tokens' loads: 185 us against 222 at H 7168 (64 tokens, E4M3), 122 against 154 at H 5120
+  // (16 tokens), the same with BF16 at H 7168.  More than 16 tokens run on two waves a SIMD, which
+  // leaves the registers for up to 64 tokens an expert: 24 us against 27 (64 tokens over 6 E4M3
+  // experts of H 4096), 81.5 against 83.5 over 96.
+  const bool many = a.T > 16;
+  if (a.H / 16 <= 256) {
+    if (many) launch_fc2_as<MX, 8, 1, 2, true>(st, a);
+    else launch_fc2_as<MX, 16, 1, 4, false>(st, a);
+  } else {
+    if (many) launch_fc2_as<MX, 8, 2, 2, true>(st, a);
+    else launch_fc2_as<MX, 8, 2, 2, false>(st, a);
+  }
 }
 template void launch_fc1<false>(hipStream_t, const Args&);
 template void launch_fc1<true>(hipStream_t, const Args&);
