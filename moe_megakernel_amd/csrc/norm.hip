@@ -153,15 +153,24 @@ __device__ __forceinline__ void ld_param(const void* w, int bf16, int aligned, i
     else unpack(ld_row<EPT, true, false>(m, 0, j, tpr, N), f);
     return;
   }
+  if (bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(w);
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) {
-    const int c = col_of<VEC>(j, i, tpr);
-    f[i] = c < N ? (bf16 ? bf2f(static_cast<const uint16_t*>(w)[c]) : static_cast<const float*>(w)[c]) : 0.0f;
+    for (int i = 0; i < EPT; ++i) {
+      const int c = col_of<VEC>(j, i, tpr);
+      f[i] = bf2f(c < N ? p[c] : (uint16_t)0);
+    }
+  } else {
+    const float* p = static_cast<const float*>(w);
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = col_of<VEC>(j, i, tpr);
+      f[i] = c < N ? p[c] : 0.0f;
+    }
   }
 }
 
-// Sums of a and b over the `nw` waves of a row group, every thread of it gets both: the
-// waves in order.  `red` holds two floats per wave of the workgroup and call parity, so
+// Sums of a and b over the `nw` (at most 16) waves of a row group, every thread of it gets both.  `red` holds two floats per wave of the workgroup and call parity, so
 // one barrier a call is enough (a slot is rewritten two calls later, behind the next
 // call's barrier).
 __device__ __forceinline__ void group_sum2(float& a, float& b, int nw, float2* red, int parity) {
@@ -172,13 +181,11 @@ __device__ __forceinline__ void group_sum2(float& a, float& b, int nw, float2* r
   float2* slot = red + parity * (kNormThreads / 64);
   if ((threadIdx.x & 63) == 0) slot[w] = make_float2(a, b);
   __syncthreads();
-  const int w0 = w - w % nw;
-  a = b = 0.0f;
-  for (int q = 0; q < nw; ++q) {
-    const float2 v = slot[w0 + q];
-    a += v.x;
-    b += v.y;
-  }
+  const int l = threadIdx.x & 15;          // every 16 lanes add the group's sums up alike
+  float2 v = make_float2(0.0f, 0.0f);
+  if (l < nw) v = slot[w - w % nw + l];
+  a = row16_sum(v.x);
+  b = row16_sum(v.y);
 }
 
 // Forward: blockDim.x = row groups * tpr, the groups walk rows with a common trip count
