@@ -392,10 +392,11 @@ typedef struct {
 
 /*  x, residual  residual may be NULL; with it `sum` is required, without it `sum` must be NULL
  *  weight, bias [cols], bias may be NULL
- *  sum          written: the row that was normalised.  May be x or residual itself (same
- *               base and ld); no other output may overlap an input
+ *  sum          written: the row that was normalised
  *  y            written
- *  stats        float [rows][2], written: mean and rstd, for the backward; NULL if not needed */
+ *  stats        float [rows][2], 8-byte aligned, written: mean and rstd, for the backward; NULL if
+ *               not needed
+ * sum and y may each be x or residual (same base and ld); other overlaps are not allowed. */
 moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const moe_rows* residual,
                             const void* weight, const void* bias, const moe_rows* sum, const moe_rows* y,
                             float* stats, void* stream);
@@ -408,7 +409,8 @@ size_t moe_norm_workspace_bytes(const moe_norm_problem* p);
  *  x            what was normalised: the forward's x, or its sum if a residual was given
  *  stats        the forward's
  *  grad_sum     gradient that reaches `sum` (or x) past the norm; NULL if none
- *  grad_x       overwritten: the gradient of x, and of residual, which share it
+ *  grad_x       overwritten: the gradient of x, and of residual, which share it.  May be
+ *               grad_y, x or grad_sum (same base and ld); other overlaps are not allowed
  *  grad_weight, grad_bias  [cols], accumulated (or overwritten, see the flag): FP32, or BF16
  *               with the rounding of a BF16 main_grad (the call's contribution is rounded
  *               before it is added).  Either may be NULL and is then not computed

@@ -233,6 +233,11 @@ CASES = [
     dict(T=9, H=4224, I=2304, E=3, K=2, limit=1.0),              # two row fragments; more than 16 steps
     dict(T=37, H=4352, I=128, E=4, K=2, layout="table", gate=True),
     dict(T=64, H=128, I=128, E=255, K=8, kind="invalid", shared=False),
+    dict(T=2, H=8448, I=128, E=2, K=1),                          # more than 16 steps a wave in the first product
+    dict(T=6, H=256, I=128, E=7, K=4, kind="invalid"),           # tables small enough for registers
+    dict(T=8, H=256, I=256, E=30, K=4, kind="short", gate=True),
+    dict(T=16, H=256, I=128, E=5, K=2, kind="one"),
+    dict(T=50, H=256, I=128, E=5, K=4, kind="invalid", limit=0.4),
 ]
 
 
@@ -260,6 +265,26 @@ def test_matches_formula(gpu_lib, i, routed):
 @pytest.mark.parametrize("routed", ["bf16", "mxfp8"])
 def test_full_width(gpu_lib, routed):
     dp, W = problem(5, 4096, 1024, 10, 4, routed=routed, seed=40)
+    run(dp)
+    torch.cuda.synchronize()
+    check(dp, W)
+
+
+@pytest.mark.gpu
+def test_expert_offsets_past_32_bits(gpu_lib):
+    """Experts 2.4 GB apart: byte offsets pass 2^32 from the second expert on."""
+    dp, W = problem(9, 256, 128, 3, 2, seed=47)
+    gap = 1_200_000_000 // 8 * 8
+    for name, rows, cols in (("fc1", 256, 256), ("fc2", 256, 128)):
+        big = torch.empty(2 * gap + rows * cols, dtype=torch.bfloat16, device="cuda")
+        for e in range(3):
+            big[e * gap:e * gap + rows * cols].view(rows, cols).copy_(getattr(dp, name)[e])
+        dp._keep.append(big)
+        m = mk.mat(base=big, expert_stride=gap, ld=cols)
+        if name == "fc1":
+            dp.weights.routed_gate.data = dp.weights.routed_up.data = m
+        else:
+            dp.weights.routed_down.data = m
     run(dp)
     torch.cuda.synchronize()
     check(dp, W)

@@ -337,6 +337,26 @@ def test_sum_in_place(gpu_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("R,N", [(1, 64), (70, 4096), (1030, 264), (300, 2055), (5, 16384)])
+def test_outputs_in_place_of_inputs(gpu_lib, R, N):
+    """y over x, grad_x over grad_y, x or grad_sum: the same bits as into memory of their own."""
+    x, w, b, dy, gs = (t.cuda() for t in make(R, N, BF, BF, seed=13))
+    n = mk.Norm(N)
+    y, stats, dx, dw, db = (torch.empty_like(x), torch.empty(R, 2, device="cuda"), torch.empty_like(x),
+                            torch.empty(N, device="cuda"), torch.empty(N, device="cuda"))
+    n.forward(x, w, b, y, stats)
+    t = x.clone()
+    n.forward(t, w, b, t)
+    assert torch.equal(t, y)
+    n.backward(dy, x, w, stats, dx, dw, db, grad_sum=gs, overwrite=True)
+    for i in range(3):
+        c = [dy.clone(), x.clone(), gs.clone()]
+        dw2, db2 = torch.empty_like(dw), torch.empty_like(db)
+        n.backward(c[0], c[1], w, stats, c[i], dw2, db2, grad_sum=c[2], overwrite=True)
+        assert torch.equal(c[i], dx) and torch.equal(dw2, dw) and torch.equal(db2, db)
+
+
+@pytest.mark.gpu
 def test_row_offsets_past_32_bits(gpu_lib):
     """Five rows a gigabyte apart: byte offsets pass 2^32."""
     N, ld = 264, (1 << 29) + 8
