@@ -392,9 +392,22 @@ def _moe_dtype(dt, where: str) -> int:
     return code
 
 
-def _check(where, device, t, dtype, shape, dense=True):
-    """t: a tensor of this dtype and shape on GPU `device` (an index), contiguous or (dense
-    false) with a dense last dimension.  A host tensor's address must never reach a kernel."""
+def _check(where, device, t, dtype, shape):
+    """t: a contiguous tensor of this dtype and shape on GPU `device` (an index).  A host
+    tensor's address must never reach a kernel."""
+    if t is None:
+        raise MoeError(MOE_ERR_NULL, where)
+    if t.dtype is not dtype:
+        raise MoeError(MOE_ERR_DTYPE, where)
+    if t.shape != shape:
+        raise MoeError(MOE_ERR_SHAPE, where)
+    if device < 0 or t.get_device() != device or not t.is_contiguous():
+        raise MoeError(MOE_ERR_LAYOUT, where)
+
+
+def _check_rows(where, device, t, dtype, shape) -> int:
+    """As _check for a matrix whose rows may lie apart; returns the elements between rows (of a
+    single row: at least its length, its stride means nothing)."""
     if t is None:
         raise MoeError(MOE_ERR_NULL, where)
     if t.dtype is not dtype:
@@ -403,8 +416,11 @@ def _check(where, device, t, dtype, shape, dense=True):
         raise MoeError(MOE_ERR_SHAPE, where)
     if device < 0 or t.get_device() != device:
         raise MoeError(MOE_ERR_LAYOUT, where)
-    if not t.is_contiguous() and (dense or (t.stride(-1) != 1 and shape[-1] > 1)):
+    if t.is_contiguous():
+        return shape[1]
+    if t.stride(1) != 1 and shape[1] > 1:
         raise MoeError(MOE_ERR_LAYOUT, where)
+    return t.stride(0) if shape[0] > 1 else shape[1]
 
 
 def _device(where, t) -> int:
@@ -412,11 +428,6 @@ def _device(where, t) -> int:
     if t is None:
         raise MoeError(MOE_ERR_NULL, where)
     return t.get_device()
-
-
-def _ld(t) -> int:
-    """Elements between rows; a single row's stride means nothing."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def _call(where, device, fn, *args):
@@ -450,8 +461,8 @@ class Router:
         if logits.dim() != 2:
             raise MoeError(MOE_ERR_SHAPE, where)
         T, q = logits.shape[0], self.p
-        _check(where, dev, logits, self.dtype, (T, q.experts), False)
-        return moe_router_problem(T, q.experts, q.topk, q.score, q.logits_dtype, q.flags, q.scale, _ld(logits))
+        ld = _check_rows(where, dev, logits, self.dtype, (T, q.experts))
+        return moe_router_problem(T, q.experts, q.topk, q.score, q.logits_dtype, q.flags, q.scale, ld)
 
     def forward(self, logits, top_experts, router_weights, expert_bias=None):
         """Writes top_experts (int32) and router_weights (float32), both [tokens, topk]."""
@@ -477,9 +488,9 @@ class Router:
         table = (p.tokens, p.topk)
         _check(where, dev, top_experts, torch.int32, table)
         _check(where, dev, grad_router_weights, torch.float32, table)
-        _check(where, dev, grad_logits, self.dtype, (p.tokens, p.experts), False)
+        ld = _check_rows(where, dev, grad_logits, self.dtype, (p.tokens, p.experts))
         _call(where, dev, load().moe_router_backward, p, logits.data_ptr(), top_experts.data_ptr(),
-              grad_router_weights.data_ptr(), grad_logits.data_ptr(), _ld(grad_logits))
+              grad_router_weights.data_ptr(), grad_logits.data_ptr(), ld)
         return grad_logits
 
 
@@ -509,8 +520,7 @@ class Norm:
         return p, (p.rows, p.cols)
 
     def _rows(self, where, device, t, shape):
-        _check(where, device, t, self.dtype, shape, False)
-        return moe_rows(t.data_ptr(), _ld(t))
+        return moe_rows(t.data_ptr(), _check_rows(where, device, t, self.dtype, shape))
 
     def forward(self, x, weight, bias, y, stats=None, residual=None, sum=None):
         """y = norm(x) or, with residual, sum = x + residual and y = norm(sum).  stats: float32
