@@ -254,64 +254,84 @@ __device__ __forceinline__ float swiglu(float a, float b, float L) {
 // Grid: [plan] [shared expert's tiles] [min(E, T K) experts' tiles] [gate scores, 4 tokens each].
 struct Fc1Shared {
   uint32_t mask[8];
-  int16_t id[kMaxRoutes];          // expert of each route, -1: none, -2: outside [-1, E)
+  int16_t raw[kMaxRoutes];         // the table; -2: outside [-1, E)
+  int16_t id[kMaxRoutes];          // expert of each route; < 0: none
   int16_t list[kMaxTokens];        // the group's routes
 };
 
-// Reads the table and marks the experts in use.
+// A wave's copy of the routes' experts: lane l has routes 64 u + l.
+constexpr int kRouteRegs = kMaxRoutes / 64;
+struct Routes {
+  int id[kRouteRegs];
+};
+
+// Reads the table, drops invalid entries (outside [0, E), or listed before in their row) and
+// marks the experts in use.  Returns whether this thread saw an invalid entry.
 template <int NT>
-__device__ __forceinline__ void read_table(const Args& a, Fc1Shared& s) {
+__device__ __forceinline__ bool read_table(const Args& a, Fc1Shared& s, Routes& rt) {
+  constexpr int U = kMaxRoutes / NT;
   const int tid = threadIdx.x, n = a.T * a.K;
-  int e[(kMaxRoutes + NT - 1) / NT];
+  int e[U];
 #pragma unroll
-  for (int u = 0; u < (kMaxRoutes + NT - 1) / NT; ++u) {
+  for (int u = 0; u < U; ++u) {
     const int i = tid + u * NT;
     e[u] = i < n ? a.top[i] : -1;
     if (e[u] < -1 || e[u] >= a.E) e[u] = -2;
-    if (i < n) s.id[i] = (int16_t)e[u];
+    s.raw[i] = (int16_t)e[u];
   }
   if (tid < 8) s.mask[tid] = 0;
   __syncthreads();
+  bool invalid = false;
 #pragma unroll
-  for (int u = 0; u < (kMaxRoutes + NT - 1) / NT; ++u)
-    if (e[u] >= 0) atomicOr(&s.mask[e[u] >> 5], 1u << (e[u] & 31));
+  for (int u = 0; u < U; ++u) {
+    const int i = tid + u * NT, k = i % a.K;
+    bool again = false;
+#pragma unroll
+    for (int d = 1; d < kMaxTopk; ++d) again |= d <= k && s.raw[d <= k ? i - d : i] == e[u];
+    const bool ok = e[u] >= 0 && !again;
+    invalid |= e[u] == -2 || (e[u] >= 0 && again);
+    s.id[i] = (int16_t)(ok ? e[u] : -1);
+    if (ok) atomicOr(&s.mask[e[u] >> 5], 1u << (e[u] & 31));
+  }
   __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kRouteRegs; ++u) rt.id[u] = s.id[64 * u + (tid & 63)];
+  return invalid;
 }
 
 // Expert of group g (ascending), or -1 past the last.
 __device__ __forceinline__ int group_expert(const Fc1Shared& s, int g) {
+  uint32_t m[8];
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m[w] = s.mask[w];
+  int e = -1;
+#pragma unroll
   for (int w = 0; w < 8; ++w) {
-    uint32_t m = s.mask[w];
-    const int c = __popc(m);
-    if (g < c) {
-      for (; g > 0; --g) m &= m - 1;
-      return 32 * w + __ffs(m) - 1;
+    const int c = __popc(m[w]);
+    if (g >= 0 && g < c) {
+      uint32_t v = m[w];
+      for (int q = g; q > 0; --q) v &= v - 1;
+      e = 32 * w + __ffs(v) - 1;
     }
-    g -= c;
+    g -= c;                        // below zero once found
   }
-  return -1;
-}
-
-// Route i goes to expert e, and no earlier entry of its row does (an expert listed again
-// in a row is dropped).
-__device__ __forceinline__ bool takes(const Args& a, const Fc1Shared& s, int i, int e) {
-  if (i >= a.T * a.K || s.id[i] != e) return false;
-  for (int j = i - i % a.K; j < i; ++j)
-    if (s.id[j] == e) return false;
-  return true;
+  return e;
 }
 
 // Calls f(position, route) for the routes of expert e in order, one lane each; returns their
 // number.  One wave.
 template <class F>
-__device__ __forceinline__ int each_route(const Args& a, const Fc1Shared& s, int e, F&& f) {
-  const int lane = threadIdx.x & 63, n = a.T * a.K;
+__device__ __forceinline__ int each_route(const Routes& rt, int n, int e, F&& f) {
+  const int lane = threadIdx.x & 63;
   int pos = 0;
-  for (int i0 = 0; i0 < n; i0 += 64) {
-    const bool hit = takes(a, s, i0 + lane, e);
-    const uint64_t m = __ballot(hit);
-    if (hit) f(pos + __popcll(m & ((1ull << lane) - 1)), i0 + lane);
-    pos += __popcll(m);
+#pragma unroll
+  for (int u = 0; u < kRouteRegs; ++u) {
+    if (64 * u < n) {
+      const bool hit = rt.id[u] == e;
+      const uint64_t m = __ballot(hit);
+      if (hit) f(pos + __popcll(m & ((1ull << lane) - 1)), 64 * u + lane);
+      pos += __popcll(m);
+    }
   }
   return pos;
 }
@@ -341,37 +361,40 @@ __device__ __forceinline__ int small_group(const Args& a, Fc1Shared& s, int g, i
   return __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)m) - 1);
 }
 
-// The first workgroup leaves the plan for the second kernel: one wave a group counts and
-// then lists its routes, at the sum of the counts of the groups before it.
+// The first workgroup leaves the plan for the second kernel: the routes of each expert are
+// counted, and one wave a group lists them at the sum of the counts of the groups before it.
 template <int NT>
-__device__ __forceinline__ void write_plan(const Args& a, const Fc1Shared& s, int* cnt /* LDS [kMaxExperts + 2] */) {
+__device__ __forceinline__ void write_plan(const Args& a, const Fc1Shared& s, const Routes& rt, bool bad,
+                                           int* cnt /* LDS [kMaxExperts + 2] */) {
   const int tid = threadIdx.x, n = a.T * a.K, lane = tid & 63, wave = tid >> 6;
+  int* invalid = cnt + kMaxExperts + 1;
+  for (int e = tid; e < kMaxExperts + 2; e += NT) cnt[e] = 0;
+  for (int i = tid; i < a.tiles2; i += NT) a.arrived[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += NT)
+    if (s.id[i] >= 0) atomicAdd(&cnt[s.id[i]], 1);
+  if (bad) *invalid = 1;
   int groups = 0;
   for (int w = 0; w < 8; ++w) groups += __popc(s.mask[w]);
-  int* invalid = cnt + kMaxExperts + 1;
-  if (tid == 0) *invalid = 0;
-  __syncthreads();
-  for (int g = wave; g < groups; g += NT / 64) {
-    const int c = each_route(a, s, group_expert(s, g), [](int, int) {});
-    if (lane == 0) cnt[g] = c;
-  }
-  for (int i = tid; i < n; i += NT)
-    if (s.id[i] == -2 || (s.id[i] >= 0 && !takes(a, s, i, s.id[i]))) *invalid = 1;
   __syncthreads();
   if (tid == 0) {
     a.plan->status = *invalid ? 9 /* MOE_ERR_ROUTE_INVALID */ : 0;
     a.plan->groups = groups;
   }
   for (int g = wave; g <= groups; g += NT / 64) {
+    const int e = group_expert(s, g);       // -1 for the end mark: all routes lie before it
     int before = 0;
-    for (int f = lane; f < g; f += 64) before += cnt[f];
+#pragma unroll
+    for (int f0 = 0; f0 <= kMaxExperts; f0 += 64) {
+      const int f = f0 + lane;
+      if (f < (e < 0 ? kMaxExperts : e)) before += cnt[f];
+    }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) before += __shfl_xor(before, o);
     if (lane == 0) a.plan->first[g] = before;
-    if (g == groups) break;
-    const int e = group_expert(s, g);
+    if (e < 0) break;
     if (lane == 0) a.plan->expert[g] = e;
-    each_route(a, s, e, [&](int p, int i) {
+    each_route(rt, n, e, [&](int p, int i) {
       a.plan->route[before + p] = i;
       a.plan->weight[before + p] = a.rw[i];
     });
@@ -472,8 +495,9 @@ __global__ __launch_bounds__(64 * W, MANY ? 2 : 4) void k_decode_fc1(Args a) {
   const int shared_blocks = a.shared ? a.I / (8 * RS) : 0;
   const int routed_blocks = min(a.E, a.T * a.K) * tiles;
   if (blockIdx.x == 0) {
-    read_table<64 * W>(a, s);
-    write_plan<64 * W>(a, s, reinterpret_cast<int*>(lds));
+    Routes rt;
+    const bool bad = read_table<64 * W>(a, s, rt);
+    write_plan<64 * W>(a, s, rt, bad, reinterpret_cast<int*>(lds));
     return;
   }
   int b = blockIdx.x - 1;
@@ -503,10 +527,11 @@ __global__ __launch_bounds__(64 * W, MANY ? 2 : 4) void k_decode_fc1(Args a) {
     e = small_group(a, s, b / tiles, count);
     if (e < 0) return;
   } else {
-    read_table<64 * W>(a, s);
+    Routes rt;
+    read_table<64 * W>(a, s, rt);
     e = __builtin_amdgcn_readfirstlane(group_expert(s, b / tiles));
     if (e < 0) return;
-    count = each_route(a, s, e, [&](int p, int i) { s.list[p] = (int16_t)i; });
+    count = each_route(rt, a.T * a.K, e, [&](int p, int i) { s.list[p] = (int16_t)i; });
   }
   __builtin_amdgcn_wave_barrier();
   fc1_group<MX, R, W, D, MANY>(a, s, lds, e, b % tiles * 8 * R, count);
@@ -516,7 +541,9 @@ __global__ __launch_bounds__(64 * W, MANY ? 2 : 4) void k_decode_fc1(Args a) {
 // A workgroup owns 16 R output columns of every token.  Its W waves split the steps of all
 // experts in use evenly; each adds w_tk times what it has of an expert's product to an
 // accumulator [token][16 R] of its own in LDS, and the waves' accumulators are joined in
-// order at the end.
+// order at the end.  Where H is too short to give every CU a workgroup, `split` workgroups
+// share the columns: each leaves its sums in the workspace, and the last one to arrive adds
+// them up in order.
 struct Fc2Shared {
   int32_t expert[kMaxExperts + 1], first[kMaxExperts + 2];
   int16_t route[kMaxRoutes];
@@ -606,9 +633,9 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
   float* mine = acc_all + wave * a.T * 16 * R;
   for (int i = tid & 63; i < a.T * 4 * R; i += 64) reinterpret_cast<f32x4_t*>(mine)[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const Turn turn = turn_of(slots + wave * wave_cells<MX, R>());
-  const int steps = a.I / kStep;
+  const int steps = a.I / kStep, part = blockIdx.y * W + wave, parts = W * a.split;
   if (a.shared) {   // every wave takes its part: with many tokens these steps cost more than routed ones
-    const int s0 = wave * steps / W, s1 = (wave + 1) * steps / W;
+    const int s0 = part * steps / parts, s1 = (part + 1) * steps / parts;
     if (s1 > s0) fc2_group<false, 1, R, 2, MANY>(a, s, turn, mine, -1, 0, a.T, s0, s1 - s0);
   }
   if (tid <= kMaxExperts) s.expert[tid] = plan_e;
@@ -619,8 +646,8 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
   }
   __syncthreads();
   const int64_t total = (int64_t)routed * steps;
-  int64_t p = wave * total / W;
-  const int64_t end = (wave + 1) * total / W;
+  int64_t p = part * total / parts;
+  const int64_t end = (part + 1) * total / parts;
   while (p < end) {   // uniform in the wave
     const int g = (int)(p / steps), s0 = (int)(p % steps);
     const int n = (int)min((int64_t)(steps - s0), end - p);
@@ -630,11 +657,35 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
     p += n;
   }
   __syncthreads();
-  for (int o = tid; o < a.T * 16 * R; o += 64 * W) {
+  const int outs = a.T * 16 * R;
+  auto put = [&](int o, float v) __attribute__((always_inline)) {
+    a.out[(int64_t)(o / (16 * R)) * a.H + blockIdx.x * 16 * R + o % (16 * R)] = (uint16_t)f2bf(v);
+  };
+  float* sums = a.sums + (int64_t)blockIdx.x * a.split * outs;     // [split][T][16 R]
+  for (int o = tid; o < outs; o += 64 * W) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) v += acc_all[w * a.T * 16 * R + o];
-    a.out[(int64_t)(o / (16 * R)) * a.H + blockIdx.x * 16 * R + o % (16 * R)] = (uint16_t)f2bf(v);
+    for (int w = 0; w < W; ++w) v += acc_all[w * outs + o];
+    if (a.split == 1) put(o, v);
+    else __hip_atomic_store(sums + (int64_t)blockIdx.y * outs + o, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (a.split == 1) return;
+  // The sums go through device-scope stores and loads, which the XCDs' caches do not keep to
+  // themselves, so all that is needed is that a wave's stores are done before its workgroup is
+  // counted.  (Device-scope fences instead would write back a whole L2 in every workgroup: 58 us
+  // for a second kernel of 36 tokens at H 512 that takes 17 this way.)
+  __shared__ int last;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (tid == 0) last = __hip_atomic_fetch_add(a.arrived + blockIdx.x, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                       == a.split - 1;
+  __syncthreads();
+  if (!last) return;
+  for (int o = tid; o < outs; o += 64 * W) {
+    float v = 0.0f;
+    for (int y = 0; y < a.split; ++y)
+      v += __hip_atomic_load(sums + (int64_t)y * outs + o, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    put(o, v);
   }
 }
 
@@ -667,23 +718,17 @@ void launch_fc1(hipStream_t st, const Args& a) {
 template <bool MX, int W, int R, int OCC, bool MANY>
 void launch_fc2_as(hipStream_t st, const Args& a) {
   static_assert(64 * W >= kMaxRoutes && 64 * W >= kMaxExperts + 2, "the plan in one load a thread");
-  hipLaunchKernelGGL((k_decode_fc2<MX, W, R, 2, OCC, MANY>), dim3(a.H / (16 * R)), dim3(64 * W),
+  hipLaunchKernelGGL((k_decode_fc2<MX, W, R, 2, OCC, MANY>), dim3(a.tiles2, a.split), dim3(64 * W),
                      (size_t)W * a.T * 16 * R * sizeof(float), st, a);
 }
 template <bool MX>
 void launch_fc2(hipStream_t st, const Args& a) {
-  // Up to H 4096 a fragment a workgroup, at most one workgroup a CU; up to 16 tokens then with
-  // 16 waves: 28.5 us against 30.0 with 8 (7 tokens, H 4096, E4M3).  Above, two fragments share
-  // the tokens' loads: 185 us against 222 at H 7168 (64 tokens, E4M3), 122 against 154 at H 5120
-  // (16 tokens), the same with BF16 at H 7168.  More than 16 tokens run on two waves a SIMD, which
-  // leaves the registers for up to 64 tokens an expert: 24 us against 27 (64 tokens over 6 E4M3
-  // experts of H 4096), 81.5 against 83.5 over 96.
-  const bool many = a.T > 16;
-  if (a.H / 16 <= 256) {
-    if (many) launch_fc2_as<MX, 8, 1, 2, true>(st, a);
+  const Fc2Shape f = fc2_shape(a.T, a.H, a.I, a.E, a.K);
+  if (f.frags == 1) {
+    if (f.waves == 8) launch_fc2_as<MX, 8, 1, 2, true>(st, a);
     else launch_fc2_as<MX, 16, 1, 4, false>(st, a);
   } else {
-    if (many) launch_fc2_as<MX, 8, 2, 2, true>(st, a);
+    if (a.T > 16) launch_fc2_as<MX, 8, 2, 2, true>(st, a);
     else launch_fc2_as<MX, 8, 2, 2, false>(st, a);
   }
 }

@@ -20,6 +20,31 @@ struct Plan {
   float weight[kMaxRoutes];                           // of the routes
 };
 
+// The second kernel's launch: row fragments (16 output columns each) and waves a workgroup, and
+// workgroups that share a workgroup's columns.
+//   Up to H 4096 one fragment, at most one workgroup a CU; up to 16 tokens then 16 waves: 28.5 us
+// against 30.0 with 8 (7 tokens, H 4096, E4M3).  Above, two fragments share the tokens' loads:
+// 185 us against 222 at H 7168 (64 tokens, E4M3), 122 against 154 at H 5120 (16 tokens), the same
+// with BF16 at H 7168.  More than 16 tokens run on two waves a SIMD, which leaves the registers for
+// up to 64 tokens an expert: 24 us against 27 (64 tokens over 6 E4M3 experts of H 4096), 81.5
+// against 83.5 over 96.
+//   A short H is split where that leaves every wave at least 8 steps.  `split` does not fall as T
+// grows, so a workspace sized for T serves every smaller batch.
+struct Fc2Shape {
+  int frags, waves, split;
+};
+inline Fc2Shape fc2_shape(int64_t T, int64_t H, int64_t I, int64_t E, int64_t K) {
+  Fc2Shape f;
+  f.frags = H / 16 <= 256 ? 1 : 2;
+  f.waves = T > 16 || f.frags == 2 ? 8 : 16;
+  const int64_t tiles = H / (16 * f.frags), experts = E < T * K ? E : T * K;
+  int64_t split = 256 / tiles;
+  const int64_t fed = experts * (I / 128) / (8 * f.waves);
+  if (split > fed) split = fed;
+  f.split = split < 1 ? 1 : (int)split;
+  return f;
+}
+
 struct Args {
   const uint16_t* x;          // [T][H]
   const int32_t* top;         // [T][K]
@@ -34,6 +59,9 @@ struct Args {
   float* gate_s;              // [T] sigmoid(x . gw)
   uint16_t* h;                // [T K + T][I]: routed rows by route, then the shared expert's
   uint16_t* out;              // [T][H]
+  int tiles2, split;          // the second kernel's grid
+  int32_t* arrived;           // [tiles2], zeroed by the first kernel
+  float* sums;                // [tiles2][split][T][16 frags] when split > 1
 };
 
 template <bool MX>

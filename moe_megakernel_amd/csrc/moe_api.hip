@@ -170,9 +170,11 @@ FwdLayout fwd_layout(const Dims& d) {
 size_t fwd_workspace(const Dims& d) { return fwd_layout(d).total; }
 
 // Workspace of the few-token forward: the plan (its first word is the status), the gate
-// scores and h (routed rows by route, then the shared expert's).
+// scores, h (routed rows by route, then the shared expert's) and the sums of a split second
+// product with their arrival counts.
 struct DecodeLayout {
-  size_t plan, gate_s, h, total;
+  size_t plan, gate_s, h, arrived, sums, total;
+  decode::Fc2Shape fc2;
 };
 
 DecodeLayout decode_layout(const Dims& d) {
@@ -182,6 +184,9 @@ DecodeLayout decode_layout(const Dims& d) {
   L.plan = take(sizeof(decode::Plan));
   L.gate_s = take(4 * d.T);
   L.h = take(2 * d.R * d.I);
+  L.fc2 = decode::fc2_shape(d.T, d.H, d.I, d.E, d.K);
+  L.arrived = take(4 * d.H / (16 * L.fc2.frags));
+  L.sums = take(L.fc2.split > 1 ? 4 * d.T * d.H * L.fc2.split : 0);
   L.total = o;
   return L;
 }
@@ -733,6 +738,10 @@ moe_status moe_forward_decode(const moe_problem* p, const void* hidden, const in
   a.gate_s = reinterpret_cast<float*>(W + L.gate_s);
   a.h = reinterpret_cast<uint16_t*>(W + L.h);
   a.out = static_cast<uint16_t*>(out);
+  a.tiles2 = (int)(d.H / (16 * L.fc2.frags));
+  a.split = L.fc2.split;
+  a.arrived = reinterpret_cast<int32_t*>(W + L.arrived);
+  a.sums = reinterpret_cast<float*>(W + L.sums);
   MOE_TRY(launch("decode_fc1", st, [&] {
     if (d.mx) decode::launch_fc1<true>(st, a);
     else decode::launch_fc1<false>(st, a);

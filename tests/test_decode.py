@@ -84,6 +84,14 @@ def test_bad_arguments_are_refused():
     assert _call(_p(tokens=0), x=None, top=None, rw=None, out=None) == mk.MOE_OK
 
 
+def test_workspace_serves_smaller_batches():
+    """A DecodeLayer of T tokens calls with fewer: their workspace must not be larger."""
+    for H, I, E, K in ((128, 2048, 16, 8), (256, 2304, 20, 4), (4096, 1024, 96, 4), (7168, 2048, 64, 6), (512, 128, 255, 1)):
+        for dt in (mk.MOE_BF16, mk.MOE_MXFP8_E4M3):
+            need = [mk.moe_decode_workspace_bytes(_p(t, H, I, E, K, dt)) for t in range(65)]
+            assert all(n > 0 for n in need) and need == sorted(need)
+
+
 def test_binding_refuses_host_and_mismatched_tensors():
     p = _p()
     layer = mk.DecodeLayer(p, device="cpu")
@@ -238,6 +246,9 @@ CASES = [
     dict(T=8, H=256, I=256, E=30, K=4, kind="short", gate=True),
     dict(T=16, H=256, I=128, E=5, K=2, kind="one"),
     dict(T=50, H=256, I=128, E=5, K=4, kind="invalid", limit=0.4),
+    dict(T=20, H=128, I=2048, E=16, K=8, kind="short"),          # second product shared by 4 workgroups a column tile
+    dict(T=12, H=256, I=2304, E=20, K=4, gate=True),             # by 2
+    dict(T=64, H=384, I=1024, E=12, K=6, layout="table", kind="invalid"),
 ]
 
 
