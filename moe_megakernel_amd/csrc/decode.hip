@@ -299,27 +299,44 @@ __device__ __forceinline__ bool read_table(const Args& a, Fc1Shared& s, Routes& 
   return invalid;
 }
 
-// Expert of group g (ascending), or -1 past the last.
-__device__ __forceinline__ int group_expert(const Fc1Shared& s, int g) {
-  uint32_t m[8];
+// Position of set bit g (from 0) of v, which has more than g.
+__device__ __forceinline__ int select_bit(uint32_t v, int g) {
+  int pos = 0;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) m[w] = s.mask[w];
-  int e = -1;
+  for (int h = 16; h > 0; h >>= 1) {
+    const int c = __popc(v & ((1u << h) - 1));
+    if (g >= c) {
+      g -= c;
+      v >>= h;
+      pos += h;
+    }
+  }
+  return pos;
+}
+
+// Expert of group g (ascending; g uniform in the workgroup), or -1 past the last.
+__device__ __forceinline__ int group_expert(const Fc1Shared& s, int g) {
+  uint32_t m[8], v = 0;
+  int word = -1;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m[w] = __builtin_amdgcn_readfirstlane(s.mask[w]);
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
     const int c = __popc(m[w]);
-    if (g >= 0 && g < c) {
-      uint32_t v = m[w];
-      for (int q = g; q > 0; --q) v &= v - 1;
-      e = 32 * w + __ffs(v) - 1;
+    if (word < 0) {
+      if (g < c) {
+        word = w;
+        v = m[w];
+      } else {
+        g -= c;
+      }
     }
-    g -= c;                        // below zero once found
   }
-  return e;
+  return word < 0 ? -1 : 32 * word + select_bit(v, g);
 }
 
-// Calls f(position, route) for the routes of expert e in order, one lane each; returns their
-// number.  One wave.
+// Calls f(u, position) for the routes (64 u + lane) of expert e in order, one lane each;
+// returns their number.  One wave.
 template <class F>
 __device__ __forceinline__ int each_route(const Routes& rt, int n, int e, F&& f) {
   const int lane = threadIdx.x & 63;
@@ -329,7 +346,7 @@ __device__ __forceinline__ int each_route(const Routes& rt, int n, int e, F&& f)
     if (64 * u < n) {
       const bool hit = rt.id[u] == e;
       const uint64_t m = __ballot(hit);
-      if (hit) f(pos + __popcll(m & ((1ull << lane) - 1)), 64 * u + lane);
+      if (hit) f(u, pos + __popcll(m & ((1ull << lane) - 1)));
       pos += __popcll(m);
     }
   }
@@ -361,43 +378,96 @@ __device__ __forceinline__ int small_group(const Args& a, Fc1Shared& s, int g, i
   return __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)m) - 1);
 }
 
-// The first workgroup leaves the plan for the second kernel: the routes of each expert are
-// counted, and one wave a group lists them at the sum of the counts of the groups before it.
+// The first workgroup leaves the plan for the second kernel, a stable counting sort: each
+// wave ranks the routes of its chunks of 64 among the chunk's routes to the same expert
+// (eight ballots, one a bit of the expert's number), thread e turns the chunks' counts of expert e
+// and those of the experts before it into places, and every route goes to its place.
+struct PlanShared {
+  int place[kRouteRegs][256];      // of each chunk and expert: the count, then the first place
+  int wave[4], invalid;
+};
 template <int NT>
-__device__ __forceinline__ void write_plan(const Args& a, const Fc1Shared& s, const Routes& rt, bool bad,
-                                           int* cnt /* LDS [kMaxExperts + 2] */) {
+__device__ __forceinline__ void write_plan(const Args& a, const Fc1Shared& s, bool bad, PlanShared& p) {
+  static_assert(NT == 256, "one thread an expert");
+  constexpr int C = kRouteRegs / 4;              // chunks of a wave
   const int tid = threadIdx.x, n = a.T * a.K, lane = tid & 63, wave = tid >> 6;
-  int* invalid = cnt + kMaxExperts + 1;
-  for (int e = tid; e < kMaxExperts + 2; e += NT) cnt[e] = 0;
+  int id[C], rank[C];
+  float w[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = 64 * (wave + 4 * c) + lane;
+    id[c] = s.id[i];                             // -1 past the table's end
+    w[c] = i < n ? a.rw[i] : 0.0f;
+  }
+#pragma unroll
+  for (int c = 0; c < kRouteRegs; ++c) p.place[c][tid] = 0;
+  if (tid == 0) p.invalid = 0;
   for (int i = tid; i < a.tiles2; i += NT) a.arrived[i] = 0;
   __syncthreads();
-  for (int i = tid; i < n; i += NT)
-    if (s.id[i] >= 0) atomicAdd(&cnt[s.id[i]], 1);
-  if (bad) *invalid = 1;
-  int groups = 0;
-  for (int w = 0; w < 8; ++w) groups += __popc(s.mask[w]);
-  __syncthreads();
-  if (tid == 0) {
-    a.plan->status = *invalid ? 9 /* MOE_ERR_ROUTE_INVALID */ : 0;
-    a.plan->groups = groups;
-  }
-  for (int g = wave; g <= groups; g += NT / 64) {
-    const int e = group_expert(s, g);       // -1 for the end mark: all routes lie before it
-    int before = 0;
 #pragma unroll
-    for (int f0 = 0; f0 <= kMaxExperts; f0 += 64) {
-      const int f = f0 + lane;
-      if (f < (e < 0 ? kMaxExperts : e)) before += cnt[f];
+  for (int c = 0; c < C; ++c) {
+    uint64_t same = ~0ull;
+#pragma unroll
+    for (int bit = 0; bit < 8; ++bit) {
+      const bool one = (id[c] >> bit) & 1;
+      const uint64_t m = __ballot(one);
+      same &= one ? m : ~m;
     }
+    same &= __ballot(id[c] >= 0);                // -1 has the bits of expert 255, which does not exist
+    rank[c] = __popcll(same & ((1ull << lane) - 1));
+    if (id[c] >= 0 && rank[c] == 0) p.place[wave + 4 * c][id[c]] = __popcll(same);
+  }
+  if (bad) p.invalid = 1;
+  __syncthreads();
+  int count = 0, in_chunk[kRouteRegs];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) before += __shfl_xor(before, o);
-    if (lane == 0) a.plan->first[g] = before;
-    if (e < 0) break;
-    if (lane == 0) a.plan->expert[g] = e;
-    each_route(rt, n, e, [&](int p, int i) {
-      a.plan->route[before + p] = i;
-      a.plan->weight[before + p] = a.rw[i];
-    });
+  for (int c = 0; c < kRouteRegs; ++c) {
+    in_chunk[c] = p.place[c][tid];
+    count += in_chunk[c];
+  }
+  int before = count;                            // inclusive over the wave, then exclusive over all
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(before, o);
+    before += lane >= o ? v : 0;
+  }
+  if (lane == 63) p.wave[wave] = before;
+  __syncthreads();
+  before -= count;
+  int group = 0, groups = 0, routes = 0;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (v < wave) before += p.wave[v];
+    routes += p.wave[v];
+  }
+#pragma unroll
+  for (int v = 0; v < 8; ++v) {
+    const uint32_t m = s.mask[v];
+    groups += __popc(m);
+    group += v < (tid >> 5) ? __popc(m) : (v == (tid >> 5) ? __popc(m & ((1u << (tid & 31)) - 1)) : 0);
+  }
+  if (tid == 0) {
+    a.plan->status = p.invalid ? 9 /* MOE_ERR_ROUTE_INVALID */ : 0;
+    a.plan->groups = groups;
+    a.plan->first[groups] = routes;
+  }
+  if (count > 0) {
+    a.plan->expert[group] = tid;
+    a.plan->first[group] = before;
+  }
+#pragma unroll
+  for (int c = 0; c < kRouteRegs; ++c) {
+    p.place[c][tid] = before;
+    before += in_chunk[c];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (id[c] >= 0) {
+      const int to = p.place[wave + 4 * c][id[c]] + rank[c];
+      a.plan->route[to] = 64 * (wave + 4 * c) + lane;
+      a.plan->weight[to] = w[c];
+    }
   }
 }
 
@@ -483,21 +553,22 @@ __device__ __forceinline__ void fc1_group(const Args& a, const Fc1Shared& s, uin
 template <bool MX, int R, bool MANY>
 constexpr int shared_frags() { return MX && !MANY ? 1 : R; }
 
-template <bool MX, int R, int W, int D, bool MANY>
+template <bool MX, int R, int W, int D, bool MANY, bool LOOP>
 __global__ __launch_bounds__(64 * W, MANY ? 2 : 4) void k_decode_fc1(Args a) {
   __shared__ Fc1Shared s;
   // turn-round slots, then the partial sums of up to four column groups
   constexpr int kSums = (MANY ? 4 : 2) * R * 64;
   constexpr int kCells = wave_cells<MX, R>() > kSums ? wave_cells<MX, R>() : kSums;
   __shared__ __align__(16) uint4 lds[W * kCells];
-  const int tiles = a.I / (8 * R);
+  const int tiles = a.I / (8 * R * (LOOP ? a.reps : 1));   // workgroups an expert
   constexpr int RS = shared_frags<MX, R, MANY>();
   const int shared_blocks = a.shared ? a.I / (8 * RS) : 0;
   const int routed_blocks = min(a.E, a.T * a.K) * tiles;
   if (blockIdx.x == 0) {
     Routes rt;
     const bool bad = read_table<64 * W>(a, s, rt);
-    write_plan<64 * W>(a, s, rt, bad, reinterpret_cast<int*>(lds));
+    static_assert(sizeof(PlanShared) <= sizeof(lds), "the plan's scratch");
+    write_plan<64 * W>(a, s, bad, *reinterpret_cast<PlanShared*>(lds));
     return;
   }
   int b = blockIdx.x - 1;
@@ -531,10 +602,17 @@ __global__ __launch_bounds__(64 * W, MANY ? 2 : 4) void k_decode_fc1(Args a) {
     read_table<64 * W>(a, s, rt);
     e = __builtin_amdgcn_readfirstlane(group_expert(s, b / tiles));
     if (e < 0) return;
-    count = each_route(rt, a.T * a.K, e, [&](int p, int i) { s.list[p] = (int16_t)i; });
+    count = each_route(rt, a.T * a.K, e, [&](int u, int p) { s.list[p] = (int16_t)(64 * u + (threadIdx.x & 63)); });
   }
   __builtin_amdgcn_wave_barrier();
-  fc1_group<MX, R, W, D, MANY>(a, s, lds, e, b % tiles * 8 * R, count);
+  if constexpr (!LOOP) {
+    fc1_group<MX, R, W, D, MANY>(a, s, lds, e, b % tiles * 8 * R, count);
+  } else {
+    for (int t = 0; t < a.reps; ++t) {
+      if (t) __syncthreads();      // the sums of the last tile have been read
+      fc1_group<MX, R, W, D, MANY>(a, s, lds, e, (b % tiles * a.reps + t) * 8 * R, count);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- FC2 + combine
@@ -698,11 +776,29 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
 template <bool MX, int R, int D, bool MANY>
 void launch_fc1_as(hipStream_t st, const Args& a) {
   constexpr int W = kFc1Waves;
-  const int tiles = a.I / (8 * R), used = a.E < a.T * a.K ? a.E : a.T * a.K;
+  const int used = a.E < a.T * a.K ? a.E : a.T * a.K;
+  // A workgroup's start (reading the table, finding its expert) costs about what 64 KB of weights
+  // do: short BF16 rows take several tiles, as long as that leaves every CU four workgroups (36
+  // tokens over 77 experts of H 512: 33 us against 45).  The loop costs registers: longer rows
+  // do without it, and E4M3, which has none to spare, at any length (30 tokens over 53 experts of
+  // H 1024: 46 us, 50 with the loop).
+  constexpr bool kLoops = !MX && !MANY;
+  Args b = a;
+  b.reps = 1;
+  const int64_t bytes = (int64_t)a.H * 32 * R;
+  while (kLoops && b.reps < 8 && bytes * b.reps < (64 << 10) && (int64_t)used * (a.I / (16 * R * b.reps)) >= 1024)
+    b.reps *= 2;
+  const int tiles = a.I / (8 * R * b.reps);
   const int gate = a.gw ? (a.T + W - 1) / W : 0;
   const int shared = a.shared ? a.I / (8 * shared_frags<MX, R, MANY>()) : 0;
-  hipLaunchKernelGGL((k_decode_fc1<MX, R, W, D, MANY>), dim3((unsigned)(1 + shared + used * tiles + gate)),
-                     dim3(64 * W), 0, st, a);
+  const dim3 grid((unsigned)(1 + shared + used * tiles + gate)), block(64 * W);
+  if constexpr (kLoops) {
+    if (b.reps > 1) {
+      hipLaunchKernelGGL((k_decode_fc1<MX, R, W, D, MANY, true>), grid, block, 0, st, b);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((k_decode_fc1<MX, R, W, D, MANY, false>), grid, block, 0, st, b);
 }
 template <bool MX>
 void launch_fc1(hipStream_t st, const Args& a) {

@@ -59,6 +59,7 @@ struct Args {
   float* gate_s;              // [T] sigmoid(x . gw)
   uint16_t* h;                // [T K + T][I]: routed rows by route, then the shared expert's
   uint16_t* out;              // [T][H]
+  int reps;                   // tiles of a workgroup of the first kernel (set by its launcher)
   int tiles2, split;          // the second kernel's grid
   int32_t* arrived;           // [tiles2], zeroed by the first kernel
   float* sums;                // [tiles2][split][T][16 frags] when split > 1
