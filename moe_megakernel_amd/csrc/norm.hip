@@ -41,12 +41,13 @@ struct NormArgs {
   Rows dy, gsum, dx;        // backward (x: what was normalised)
   const void *w, *b;
   float* stats;
-  float* part;              // backward: [groups][nsum][cols]
+  float* part;              // backward: [groups][nsum][cols], null if there is one group or no sum
+  uint8_t *gw, *gb;         // backward: weight's and bias's gradient (null: not wanted)
+  int g16, overwrite;       // BF16 gradients; not accumulated
   int64_t rows;
   int N;                    // cols
   int tpr;                  // threads per row
   int rms, wbf16, w16, b16;  // w16, b16: 16-byte aligned weight, bias
-  int want_dw, want_db;
   float eps;
 };
 
@@ -256,9 +257,25 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_fwd(NormArgs a) {
   }
 }
 
+// grad[c] (+)= v
+__device__ __forceinline__ void add_grad(uint8_t* grad, int bf16, int overwrite, int c, float v) {
+  if (bf16) {
+    uint16_t* o = reinterpret_cast<uint16_t*>(grad) + c;
+    float r = bf2f(f2bf(v));
+    if (!overwrite) r = bf2f(*o) + r;
+    *o = (uint16_t)f2bf(r);
+  } else {
+    float* o = reinterpret_cast<float*>(grad) + c;
+    *o = overwrite ? v : *o + v;
+  }
+}
+
 template <int EPT, bool VEC, bool BF16>
 __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
-  extern __shared__ float join[];                        // [ng - 1][tpr * EPT], reused
+  // EPT 8: the row groups' sums, [ng][tpr * 8], one gradient after the other.  EPT 16 (one row
+  // group): both gradients' running sums, [32][tpr], which would not fit the registers.
+  extern __shared__ float join[];
+  constexpr bool kLdsSums = EPT == 16;
   __shared__ float2 red[2 * (kNormThreads / 64)];
   const int tpr = a.tpr, N = a.N, nw = tpr >> 6;
   const int j = threadIdx.x % tpr;
@@ -280,10 +297,16 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
     }
   };
   if (kAhead) fetch((int64_t)blockIdx.x * ng + rg);
-  float w[EPT], dw[EPT], db[EPT];
+  float w[EPT];
   ld_param<EPT, VEC>(a.w, a.wbf16, a.w16, j, tpr, N, w);
+  float dw[kLdsSums ? 1 : EPT], db[kLdsSums ? 1 : EPT];
+  if constexpr (kLdsSums) {
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) dw[i] = db[i] = 0.0f;
+    for (int i = 0; i < 2 * EPT; ++i) join[i * tpr + j] = 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) dw[i] = db[i] = 0.0f;
+  }
   const float inv_n = 1.0f / (float)N;
   int parity = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * ng; r0 < a.rows; r0 += stride) {
@@ -301,8 +324,13 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      dw[i] += g[i] * xh[i];
-      db[i] += g[i];
+      if constexpr (kLdsSums) {
+        join[i * tpr + j] += g[i] * xh[i];
+        join[(EPT + i) * tpr + j] += g[i];
+      } else {
+        dw[i] += g[i] * xh[i];
+        db[i] += g[i];
+      }
       g[i] *= w[i];
       s1 += g[i];
       s2 += g[i] * xh[i];
@@ -321,28 +349,37 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
       st_row<EPT, VEC, BF16>(a.dx, r, j, tpr, N, g);
     }
   }
-  if (!a.part) return;
-  // join the row groups in order, then one partial row of this workgroup
-  const int nsum = a.want_dw + a.want_db;
-  float* out = a.part + (int64_t)blockIdx.x * nsum * N;
+  if (!a.gw && !a.gb) return;
+  // join the row groups in order; then a partial row of this workgroup, or, if it is the
+  // only one, the gradients
+  float* out = a.part ? a.part + (int64_t)blockIdx.x * ((a.gw ? N : 0) + (a.gb ? N : 0)) : nullptr;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    if (!(which ? a.want_db : a.want_dw)) continue;
-    if (ng > 1) {
-      __syncthreads();
-      if (rg > 0) {
+    uint8_t* grad = which ? a.gb : a.gw;
+    if (!grad) continue;
+    auto put = [&](int i, int jj, float v) __attribute__((always_inline)) {
+      const int c = col_of<VEC>(jj, i, tpr);
+      if (c >= N) return;
+      if (out) out[(which && a.gw ? N : 0) + c] = v;
+      else add_grad(grad, a.g16, a.overwrite, c, v);
+    };
+    if constexpr (kLdsSums) {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) join[((rg - 1) * EPT + i) * tpr + j] = which ? db[i] : dw[i];
-      }
-      __syncthreads();
-    }
-    if (rg == 0) {
+      for (int i = 0; i < EPT; ++i) put(i, j, join[(which * EPT + i) * tpr + j]);
+    } else if (ng == 1) {
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        float v = which ? db[i] : dw[i];
-        for (int q = 0; q < ng - 1; ++q) v += join[(q * EPT + i) * tpr + j];
-        const int c = col_of<VEC>(j, i, tpr);
-        if (c < N) out[(which && a.want_dw ? N : 0) + c] = v;
+      for (int i = 0; i < EPT; ++i) put(i, j, which ? db[i] : dw[i]);
+    } else {
+      const int row = tpr * EPT;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) join[rg * row + i * tpr + j] = which ? db[i] : dw[i];
+      __syncthreads();
+      for (int k = threadIdx.x; k < row; k += blockDim.x) {
+        float v = 0.0f;
+#pragma unroll 4
+        for (int q = 0; q < ng; ++q) v += join[q * row + k];
+        put(k / tpr, k % tpr, v);
       }
     }
   }
@@ -376,17 +413,7 @@ __global__ __launch_bounds__(kFinalCols * kFinalLanes) void k_norm_bwd_final(con
   v = red[0][cl];
 #pragma unroll
   for (int i = 1; i < kFinalLanes; ++i) v += red[i][cl];
-  uint8_t* dst = c < N ? g0 : g1;
-  const int cc = c < N ? c : c - N;
-  if (bf16) {
-    uint16_t* o = reinterpret_cast<uint16_t*>(dst) + cc;
-    float r = bf2f(f2bf(v));
-    if (!overwrite) r = bf2f(*o) + r;
-    *o = (uint16_t)f2bf(r);
-  } else {
-    float* o = reinterpret_cast<float*>(dst) + cc;
-    *o = overwrite ? v : *o + v;
-  }
+  add_grad(c < N ? g0 : g1, bf16, overwrite, c < N ? c : c - N, v);
 }
 
 // ---------------------------------------------------------------- host side
@@ -452,15 +479,29 @@ void with_variant(int ept, bool vec, bool bf16, F&& f) {
   else types(E16{});
 }
 
-// Row groups per backward workgroup: as many as 1024 threads hold, but first a workgroup for
-// each of the kNormGroups.
-int bwd_row_groups(const NormArgs& a) {
-  const int64_t fit = kNormThreads / a.tpr, want = (a.rows + kNormGroups - 1) / kNormGroups;
-  return (int)(want < 1 ? 1 : (want < fit ? want : fit));
-}
-int bwd_groups(const NormArgs& a) {
-  const int64_t ng = bwd_row_groups(a), need = (a.rows + ng - 1) / ng;
-  return (int)(need < kNormGroups ? need : kNormGroups);
+// The backward's launch: row groups a workgroup, workgroups, LDS bytes.  Up to twice the rows
+// that one workgroup holds stay in one, which writes the gradients itself (no second kernel);
+// otherwise first a workgroup for each of the kNormGroups, then row groups up to 1024 threads.
+struct BwdShape {
+  int ept, ng, groups;
+  size_t lds;
+};
+BwdShape bwd_shape(const moe_norm_problem* p) {
+  BwdShape b;
+  b.ept = bwd_ept(p->cols);
+  const int tpr = threads_per_row(p->cols, b.ept);
+  const int64_t fit = kNormThreads / tpr, rows = p->rows > 0 ? p->rows : 1;
+  if (rows <= 2 * fit) {
+    b.ng = (int)(rows < fit ? rows : fit);
+    b.groups = 1;
+  } else {
+    const int64_t want = (rows + kNormGroups - 1) / kNormGroups;
+    b.ng = (int)(want < fit ? want : fit);
+    const int64_t need = (rows + b.ng - 1) / b.ng;
+    b.groups = (int)(need < kNormGroups ? need : kNormGroups);
+  }
+  b.lds = sizeof(float) * tpr * (b.ept == 16 ? 32 : (b.ng > 1 ? 8 * b.ng : 0));
+  return b;
 }
 
 }  // namespace
@@ -505,7 +546,7 @@ moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const 
 
 size_t moe_norm_workspace_bytes(const moe_norm_problem* p) {
   if (check_norm(p) != MOE_OK) return 0;
-  return align_up((size_t)bwd_groups(norm_args(p, bwd_ept(p->cols))) * 2 * p->cols * sizeof(float) + 1);
+  return align_up((size_t)bwd_shape(p).groups * 2 * p->cols * sizeof(float) + 1);
 }
 
 moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, const moe_rows* x,
@@ -525,34 +566,33 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, 
     if (!workspace || workspace_bytes < moe_norm_workspace_bytes(p)) return MOE_ERR_WORKSPACE;
     if (!aligned16(workspace)) return MOE_ERR_LAYOUT;
   }
-  const int ept = bwd_ept(p->cols);
-  NormArgs a = norm_args(p, ept);
+  const BwdShape b = bwd_shape(p);
+  NormArgs a = norm_args(p, b.ept);
   a.dy = rows_of(grad_y); a.x = rows_of(x); a.gsum = rows_of(grad_sum); a.dx = rows_of(grad_x);
   a.w = weight;
   a.w16 = aligned16(weight);
   a.stats = const_cast<float*>(stats);
-  a.part = sums ? static_cast<float*>(workspace) : nullptr;
-  a.want_dw = grad_weight != nullptr;
-  a.want_db = grad_bias != nullptr;
+  a.part = sums && b.groups > 1 ? static_cast<float*>(workspace) : nullptr;
+  a.gw = static_cast<uint8_t*>(grad_weight);
+  a.gb = static_cast<uint8_t*>(grad_bias);
+  a.g16 = p->grad_dtype == MOE_BF16;
+  a.overwrite = (p->flags & MOE_NORM_OVERWRITE_GRADS) != 0;
   const bool vec = p->cols % 8 == 0 && rows16(p, grad_y) && rows16(p, x) && rows16(p, grad_sum) && rows16(p, grad_x);
-  const int ng = bwd_row_groups(a), groups = bwd_groups(a);
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (p->rows > 0) {
     MOE_TRY(launch("norm_bwd", st, [&] {
-      with_variant(ept, vec, p->dtype == MOE_BF16, [&](auto e, auto v, auto bf) {
-        const size_t lds = sums ? (size_t)(ng - 1) * a.tpr * ept * sizeof(float) : 0;
-        hipLaunchKernelGGL((k_norm_bwd<e(), v(), bf()>), dim3(groups), dim3(ng * a.tpr), lds, st, a);
+      with_variant(b.ept, vec, p->dtype == MOE_BF16, [&](auto e, auto v, auto bf) {
+        hipLaunchKernelGGL((k_norm_bwd<e(), v(), bf()>), dim3(b.groups), dim3(b.ng * a.tpr), b.lds, st, a);
       });
     }));
+    if (!a.part) return MOE_OK;
   }
   if (!sums) return MOE_OK;
-  // also with no rows: an overwriting call leaves zeros
-  const int width = a.N * (a.want_dw + a.want_db);
-  uint8_t* g0 = static_cast<uint8_t*>(grad_weight ? grad_weight : grad_bias);
+  // with no rows: an overwriting call leaves zeros
+  const int width = a.N * ((a.gw ? 1 : 0) + (a.gb ? 1 : 0)), groups = p->rows > 0 ? b.groups : 0;
   return launch("norm_bwd_final", st, [&] {
-    hipLaunchKernelGGL(k_norm_bwd_final, dim3((width + kFinalCols - 1) / kFinalCols), dim3(kFinalCols * kFinalLanes), 0, st,
-                       (const float*)workspace, groups, width, a.N, g0, static_cast<uint8_t*>(grad_bias),
-                       p->grad_dtype == MOE_BF16 ? 1 : 0, (p->flags & MOE_NORM_OVERWRITE_GRADS) ? 1 : 0);
+    hipLaunchKernelGGL(k_norm_bwd_final, dim3((width + kFinalCols - 1) / kFinalCols), dim3(kFinalCols * kFinalLanes), 0,
+                       st, (const float*)workspace, groups, width, a.N, a.gw ? a.gw : a.gb, a.gb, a.g16, a.overwrite);
   });
 }
 
