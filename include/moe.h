@@ -383,8 +383,8 @@ typedef struct {
 #define MOE_NORM_MAX_COLS 16384
 
 /* A matrix [rows][cols] of the problem's dtype, rows `ld` >= cols elements apart.  Any
- * element-aligned base and any ld are taken; rows that are all 16-byte aligned (and cols a
- * multiple of 8) are read and written in 16-byte pieces. */
+ * element-aligned base and any ld are taken; rows that are all 16-byte aligned and hold
+ * whole 16-byte pieces are read and written in those. */
 typedef struct {
   void* base;
   int64_t ld;

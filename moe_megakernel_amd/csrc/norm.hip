@@ -51,11 +51,16 @@ struct NormArgs {
   float eps;
 };
 
-// Columns of a thread: VEC (rows 16-byte aligned, N % 8 == 0) two pieces of 8 elements at
-// pieces j and j + tpr; otherwise single elements j + i tpr.  col < 0: past the end.
-template <bool VEC>
+// Columns of a thread: VEC (rows 16-byte aligned, whole pieces) pieces of 16 bytes, 8 BF16 or 4
+// FP32 elements, at pieces j, j + tpr, ..: neighbouring lanes read neighbouring pieces (with 8
+// FP32 elements a lane, 32 bytes apart, 4453 x 3584 took 73 us in the backward).  Otherwise
+// single elements j + i tpr.
+template <bool BF16>
+constexpr int piece() { return BF16 ? 8 : 4; }
+template <bool VEC, bool BF16>
 __device__ __forceinline__ int col_of(int j, int i, int tpr) {
-  return VEC ? 8 * (j + (i >> 3) * tpr) + (i & 7) : j + i * tpr;
+  constexpr int P = piece<BF16>();
+  return VEC ? P * (j + i / P * tpr) + i % P : j + i * tpr;
 }
 
 // A thread's EPT elements of a row as loaded.
@@ -76,15 +81,10 @@ __device__ __forceinline__ Raw<EPT, VEC, BF16> ld_row(const Rows& m, int64_t r, 
   const uint8_t* p = m.base + r * m.ld * (BF16 ? 2 : 4);
   if constexpr (VEC) {
 #pragma unroll
-    for (int u = 0; u < EPT / 8; ++u) {
-      const int c = 8 * (j + u * tpr);
-      if constexpr (BF16) {
-        v.q[u] = c < N ? *reinterpret_cast<const uint4*>(p + 2 * c) : make_uint4(0, 0, 0, 0);
-      } else {
-        const float4 z = make_float4(0, 0, 0, 0);
-        v.q[2 * u] = c < N ? *reinterpret_cast<const float4*>(p + 4 * c) : z;
-        v.q[2 * u + 1] = c < N ? *reinterpret_cast<const float4*>(p + 4 * c + 16) : z;
-      }
+    for (int u = 0; u < EPT / piece<BF16>(); ++u) {
+      const int c = piece<BF16>() * (j + u * tpr);
+      if constexpr (BF16) v.q[u] = c < N ? *reinterpret_cast<const uint4*>(p + 2 * c) : make_uint4(0, 0, 0, 0);
+      else v.q[u] = c < N ? *reinterpret_cast<const float4*>(p + 4 * c) : make_float4(0, 0, 0, 0);
     }
   } else {
 #pragma unroll
@@ -121,16 +121,15 @@ __device__ __forceinline__ void st_row(const Rows& m, int64_t r, int j, int tpr,
   uint8_t* p = m.base + r * m.ld * (BF16 ? 2 : 4);
   if constexpr (VEC) {
 #pragma unroll
-    for (int u = 0; u < EPT / 8; ++u) {
-      const int c = 8 * (j + u * tpr);
+    for (int u = 0; u < EPT / piece<BF16>(); ++u) {
+      const int c = piece<BF16>() * (j + u * tpr);
       if (c >= N) continue;
-      const float* s = f + 8 * u;
+      const float* s = f + piece<BF16>() * u;
       if constexpr (BF16) {
         *reinterpret_cast<uint4*>(p + 2 * c) = make_uint4(pack_bf2(s[0], s[1]), pack_bf2(s[2], s[3]),
                                                           pack_bf2(s[4], s[5]), pack_bf2(s[6], s[7]));
       } else {
         *reinterpret_cast<float4*>(p + 4 * c) = make_float4(s[0], s[1], s[2], s[3]);
-        *reinterpret_cast<float4*>(p + 4 * c + 16) = make_float4(s[4], s[5], s[6], s[7]);
       }
     }
   } else {
@@ -144,31 +143,46 @@ __device__ __forceinline__ void st_row(const Rows& m, int64_t r, int j, int tpr,
   }
 }
 
-// weight or bias of a thread's columns (0 past the end); aligned: 16-byte pieces can be read
-template <int EPT, bool VEC>
-__device__ __forceinline__ void ld_param(const void* w, int bf16, int aligned, int j, int tpr, int N,
-                                         float (&f)[EPT]) {
-  const Rows m{const_cast<uint8_t*>(static_cast<const uint8_t*>(w)), 0};
+// weight or bias of a thread's columns (0 past the end), PBF: stored as BF16; aligned:
+// 16-byte aligned, so whole pieces can be read
+template <int EPT, bool VEC, bool BF16, bool PBF>
+__device__ __forceinline__ void ld_param_as(const void* w, int aligned, int j, int tpr, int N, float (&f)[EPT]) {
+  constexpr int P = piece<BF16>();
   if (VEC && aligned) {
-    if (bf16) unpack(ld_row<EPT, true, true>(m, 0, j, tpr, N), f);
-    else unpack(ld_row<EPT, true, false>(m, 0, j, tpr, N), f);
+#pragma unroll
+    for (int u = 0; u < EPT / P; ++u) {
+      const int c = P * (j + u * tpr);
+      float* o = f + P * u;
+#pragma unroll
+      for (int i = 0; i < P; ++i) o[i] = 0.0f;
+      if (c >= N) continue;
+      if constexpr (PBF && P == 8) {
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c), o);
+      } else if constexpr (PBF) {
+        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + c);
+        o[0] = lo_bf(q.x); o[1] = hi_bf(q.x); o[2] = lo_bf(q.y); o[3] = hi_bf(q.y);
+      } else {
+#pragma unroll
+        for (int h = 0; h < P; h += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + h);
+          o[h] = q.x; o[h + 1] = q.y; o[h + 2] = q.z; o[h + 3] = q.w;
+        }
+      }
+    }
     return;
   }
-  if (bf16) {
-    const uint16_t* p = static_cast<const uint16_t*>(w);
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int c = col_of<VEC>(j, i, tpr);
-      f[i] = bf2f(c < N ? p[c] : (uint16_t)0);
-    }
-  } else {
-    const float* p = static_cast<const float*>(w);
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int c = col_of<VEC>(j, i, tpr);
-      f[i] = c < N ? p[c] : 0.0f;
-    }
+  for (int i = 0; i < EPT; ++i) {
+    const int c = col_of<VEC, BF16>(j, i, tpr);
+    if constexpr (PBF) f[i] = bf2f(c < N ? static_cast<const uint16_t*>(w)[c] : (uint16_t)0);
+    else f[i] = c < N ? static_cast<const float*>(w)[c] : 0.0f;
   }
+}
+template <int EPT, bool VEC, bool BF16>
+__device__ __forceinline__ void ld_param(const void* w, int pbf, int aligned, int j, int tpr, int N,
+                                         float (&f)[EPT]) {
+  if (pbf) ld_param_as<EPT, VEC, BF16, true>(w, aligned, j, tpr, N, f);
+  else ld_param_as<EPT, VEC, BF16, false>(w, aligned, j, tpr, N, f);
 }
 
 // Sums of a and b over the `nw` (at most 16) waves of a row group, every thread of it gets both.  `red` holds two floats per wave of the workgroup and call parity, so
@@ -208,10 +222,10 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_fwd(NormArgs a) {
   };
   fetch((int64_t)blockIdx.x * ng + rg);
   float w[EPT], b[EPT];
-  ld_param<EPT, VEC>(a.w, a.wbf16, a.w16, j, tpr, N, w);
+  ld_param<EPT, VEC, BF16>(a.w, a.wbf16, a.w16, j, tpr, N, w);
 #pragma unroll
   for (int i = 0; i < EPT; ++i) b[i] = 0.0f;
-  if (a.b) ld_param<EPT, VEC>(a.b, a.wbf16, a.b16, j, tpr, N, b);
+  if (a.b) ld_param<EPT, VEC, BF16>(a.b, a.wbf16, a.b16, j, tpr, N, b);
   const float inv_n = 1.0f / (float)N;
   int parity = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * ng; r0 < a.rows; r0 += stride) {
@@ -240,7 +254,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_fwd(NormArgs a) {
     s = s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      v[i] = col_of<VEC>(j, i, tpr) < N ? v[i] - mean : 0.0f;
+      v[i] = col_of<VEC, BF16>(j, i, tpr) < N ? v[i] - mean : 0.0f;
       s += v[i];
       s2 += v[i] * v[i];
     }
@@ -298,7 +312,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
   };
   if (kAhead) fetch((int64_t)blockIdx.x * ng + rg);
   float w[EPT];
-  ld_param<EPT, VEC>(a.w, a.wbf16, a.w16, j, tpr, N, w);
+  ld_param<EPT, VEC, BF16>(a.w, a.wbf16, a.w16, j, tpr, N, w);
   float dw[kLdsSums ? 1 : EPT], db[kLdsSums ? 1 : EPT];
   if constexpr (kLdsSums) {
 #pragma unroll
@@ -320,7 +334,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
     const float mean = nst.x, rstd = nst.y;
     if (kAhead) fetch(r + stride);
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) xh[i] = on && col_of<VEC>(j, i, tpr) < N ? (xh[i] - mean) * rstd : 0.0f;
+    for (int i = 0; i < EPT; ++i) xh[i] = on && col_of<VEC, BF16>(j, i, tpr) < N ? (xh[i] - mean) * rstd : 0.0f;
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
@@ -358,7 +372,7 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_bwd(NormArgs a) {
     uint8_t* grad = which ? a.gb : a.gw;
     if (!grad) continue;
     auto put = [&](int i, int jj, float v) __attribute__((always_inline)) {
-      const int c = col_of<VEC>(jj, i, tpr);
+      const int c = col_of<VEC, BF16>(jj, i, tpr);
       if (c >= N) return;
       if (out) out[(which && a.gw ? N : 0) + c] = v;
       else add_grad(grad, a.g16, a.overwrite, c, v);
@@ -444,6 +458,10 @@ bool rows16(const moe_norm_problem* p, const moe_rows* m) {
   return !m || (aligned16(m->base) && (m->ld * (p->dtype == MOE_BF16 ? 2 : 4)) % 16 == 0);
 }
 
+bool whole_pieces(const moe_norm_problem* p) {
+  return p->cols % (p->dtype == MOE_BF16 ? piece<true>() : piece<false>()) == 0;
+}
+
 Rows rows_of(const moe_rows* m) { return m ? Rows{static_cast<uint8_t*>(m->base), m->ld} : Rows{nullptr, 0}; }
 
 int threads_per_row(int64_t cols, int ept) { return 64 * (int)((cols + 64 * ept - 1) / (64 * ept)); }
@@ -523,7 +541,7 @@ moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const 
   if (!elem_aligned(weight, p->param_dtype) || !elem_aligned(bias, p->param_dtype)) return MOE_ERR_LAYOUT;
   if (reinterpret_cast<uintptr_t>(stats) & 7u) return MOE_ERR_LAYOUT;
   if (p->rows == 0) return MOE_OK;
-  const bool vec = p->cols % 8 == 0 && rows16(p, x) && rows16(p, residual) && rows16(p, sum) && rows16(p, y);
+  const bool vec = whole_pieces(p) && rows16(p, x) && rows16(p, residual) && rows16(p, sum) && rows16(p, y);
   const int ept = fwd_ept(p->cols, vec);
   NormArgs a = norm_args(p, ept);
   a.x = rows_of(x); a.res = rows_of(residual); a.sum = rows_of(sum); a.y = rows_of(y);
@@ -577,7 +595,7 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, 
   a.gb = static_cast<uint8_t*>(grad_bias);
   a.g16 = p->grad_dtype == MOE_BF16;
   a.overwrite = (p->flags & MOE_NORM_OVERWRITE_GRADS) != 0;
-  const bool vec = p->cols % 8 == 0 && rows16(p, grad_y) && rows16(p, x) && rows16(p, grad_sum) && rows16(p, grad_x);
+  const bool vec = whole_pieces(p) && rows16(p, grad_y) && rows16(p, x) && rows16(p, grad_sum) && rows16(p, grad_x);
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (p->rows > 0) {
     MOE_TRY(launch("norm_bwd", st, [&] {
