@@ -302,6 +302,26 @@ def test_expert_offsets_past_32_bits(gpu_lib):
 
 
 @pytest.mark.gpu
+def test_scales_of_all_sizes(gpu_lib):
+    """E8M0 bytes far apart beside each other, and all-zero blocks with byte 0 (2^-127)."""
+    dp, W = problem(11, 512, 384, 5, 3, routed="mxfp8", seed=48, swiglu_limit=2.0)
+    fc1, fc1s, _, _, fc2, fc2s = dp._keep[:6]
+    rng = np.random.default_rng(5)
+    for key, t, ts in (("fc1", fc1, fc1s), ("fc2", fc2, fc2s)):
+        for e in range(5):
+            codes, sc = dp.np_routed[e][key], dp.np_routed[e][key + "_s"]
+            sc += rng.integers(-12, 3, sc.shape).astype(np.uint8)
+            zero = rng.random(sc.shape) < 0.1
+            sc[zero] = 0
+            codes[np.repeat(zero, 32, axis=1)] = 0
+            t[e].copy_(torch.from_numpy(codes))
+            ts[e].copy_(torch.from_numpy(sc))
+    run(dp)
+    torch.cuda.synchronize()
+    check(dp, W)
+
+
+@pytest.mark.gpu
 def test_agrees_with_the_training_forward(gpu_lib):
     """BF16: the same roundings as moe_forward_topk, so the outputs differ by at most FP32
     summation order and the BF16 steps it tips: h may move by a step (2^-7 of itself), as may out."""
