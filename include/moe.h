@@ -286,14 +286,18 @@ moe_status moe_forward_noalloc(const moe_problem* p, const void* hidden, const f
  * that read the weights of each expert in use once.  Requires MOE_FLAG_TOPK_ROUTING; with
  * MOE_FLAG_RECOMPUTE it returns MOE_ERR_UNSUPPORTED, and with more than
  * MOE_DECODE_MAX_TOKENS tokens MOE_ERR_SHAPE.  Arguments as for moe_forward_topk, without
- * `saved`: no backward can follow.  The result is moe_forward_topk's with BF16 weights, up to
- * the order of the FP32 sums.  With MXFP8 weights it differs: the weights are decoded
- * exactly and multiply the BF16 activations, which are not quantised.
+ * `saved`: no backward can follow.  intermediate is at most MOE_DECODE_MAX_INTERMEDIATE
+ * (MOE_ERR_SHAPE above).  The result with BF16 weights is moe_forward_topk's, up to the order
+ * of the FP32 sums and without its rounding of each expert's output to BF16 before they are
+ * added.  With MXFP8 weights it differs: the weights are decoded to BF16 (exactly,
+ * unless smaller than 2^-126 or past BF16's largest) and multiply the BF16 activations,
+ * which are not quantised.
  *  workspace   moe_decode_workspace_bytes(p) bytes, 16-byte aligned, overwritten in every
  *              call.  Its first int32 is the status word afterwards: 0 or
  *              MOE_ERR_ROUTE_INVALID (invalid entries are dropped, as moe_forward_topk does)
  * With no tokens nothing is enqueued and nothing is written. */
 #define MOE_DECODE_MAX_TOKENS 64
+#define MOE_DECODE_MAX_INTERMEDIATE 65536
 size_t moe_decode_workspace_bytes(const moe_problem* p);
 moe_status moe_forward_decode(const moe_problem* p, const void* hidden, const int32_t* top_experts,
                               const float* router_weights, const moe_weights* w, void* out,
@@ -335,7 +339,7 @@ moe_status moe_backward(const moe_problem* p, const void* grad_out, const void* 
 typedef enum { MOE_ROUTER_SOFTMAX = 1, MOE_ROUTER_SIGMOID = 2 } moe_router_score;
 #define MOE_ROUTER_NORMALIZE 1u
 typedef struct {
-  int64_t tokens;        /* T in [0, 2^30]                                                */
+  int64_t tokens;        /* T in [0, 2^27]                                                */
   int32_t experts;       /* E in [1, 255]                                                 */
   int32_t topk;          /* K in [1, min(8, E)]                                           */
   int32_t score;         /* moe_router_score                                              */
@@ -396,7 +400,8 @@ typedef struct {
  *  y            written
  *  stats        float [rows][2], 8-byte aligned, written: mean and rstd, for the backward; NULL if
  *               not needed
- * sum and y may each be x or residual (same base and ld); other overlaps are not allowed. */
+ * sum and y may each be x or residual (same base and ld), not both the same; other overlaps
+ * are not allowed. */
 moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const moe_rows* residual,
                             const void* weight, const void* bias, const moe_rows* sum, const moe_rows* y,
                             float* stats, void* stream);

@@ -33,10 +33,11 @@ MOE_NORM_MAX_COLS = 16384
 EXPORTED = ("moe_saved_bytes", "moe_workspace_bytes", "moe_saved_view", "moe_forward",
             "moe_forward_topk", "moe_forward_noalloc", "moe_backward", "moe_status_str",
             "moe_kernel_timer_enable", "moe_kernel_timer_read", "moe_mx_staging_view",
-            "moe_decode_workspace_bytes", "moe_forward_decode", "moe_router_forward", "moe_router_backward", "moe_norm_forward", "moe_norm_backward",
-            "moe_norm_workspace_bytes")
+            "moe_decode_workspace_bytes", "moe_forward_decode", "moe_router_forward", "moe_router_backward",
+            "moe_norm_forward", "moe_norm_backward", "moe_norm_workspace_bytes")
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 MOE_DECODE_MAX_TOKENS = 64
+MOE_DECODE_MAX_INTERMEDIATE = 65536
 
 
 class moe_problem(C.Structure):
@@ -576,12 +577,15 @@ class DecodeLayer:
         if self.ws_bytes == 0:
             raise MoeError(MOE_ERR_UNSUPPORTED if 0 <= p.tokens <= MOE_DECODE_MAX_TOKENS else MOE_ERR_SHAPE,
                            "moe_decode_workspace_bytes")
-        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        # zeros: the status word before the first call
+        self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=device)
 
     def forward(self, hidden, top_experts, router_weights, weights: moe_weights, out):
         import torch
         where = "moe_forward_decode"
         dev = _device(where, hidden)
+        if hidden.dim() != 2:
+            raise MoeError(MOE_ERR_SHAPE, where)
         p = moe_problem.from_buffer_copy(self.p)
         p.tokens = hidden.shape[0]
         if p.tokens > self.p.tokens:
@@ -598,6 +602,7 @@ class DecodeLayer:
         return out
 
     def status_word(self):
-        """The last call's status word, a device int32 [1]: 0 or MOE_ERR_ROUTE_INVALID."""
+        """The status word of the last call that had tokens, a device int32 [1]: 0 or
+        MOE_ERR_ROUTE_INVALID."""
         import torch
         return self.workspace[:4].view(torch.int32)

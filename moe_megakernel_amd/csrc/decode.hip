@@ -18,7 +18,8 @@
 // table, first loads, last sums).
 //
 // MXFP8 weights are decoded to BF16 in registers, which is exact (E4M3 has 3 fraction
-// bits and the scale is a power of two); the tokens stay BF16.  h is rounded to BF16, as
+// bits and the scale is a power of two) wherever the product is a normal BF16 number; the tokens
+// stay BF16.  h is rounded to BF16, as
 // moe_forward stores it.  Accumulators, the SwiGLU and the combine are FP32, and the output is
 // rounded once.  Every sum has a fixed order.
 #include <hip/hip_runtime.h>
@@ -453,7 +454,7 @@ __device__ __forceinline__ void write_plan(const Args& a, const Fc1Shared& s, bo
     group += v < (tid >> 5) ? __popc(m) : (v == (tid >> 5) ? __popc(m & ((1u << (tid & 31)) - 1)) : 0);
   }
   if (tid == 0) {
-    a.plan->status = p.invalid ? 9 /* MOE_ERR_ROUTE_INVALID */ : 0;
+    a.plan->status = p.invalid ? kRouteInvalid : 0;
     a.plan->groups = groups;
     a.plan->first[groups] = routes;
   }

@@ -8,11 +8,12 @@ namespace decode {
 
 constexpr int kMaxTokens = 64;                        // MOE_DECODE_MAX_TOKENS
 constexpr int kMaxRoutes = kMaxTokens * kMaxTopk;
+constexpr int kRouteInvalid = 9;                      // MOE_ERR_ROUTE_INVALID
 
 // What the first kernel's block 0 leaves for the second: the distinct experts in
 // ascending order and each one's routes (t K + k) in ascending order.
 struct Plan {
-  int32_t status;                                     // 0 or MOE_ERR_ROUTE_INVALID
+  int32_t status;                                     // 0 or kRouteInvalid
   int32_t groups;                                     // distinct experts
   int32_t expert[kMaxExperts + 1];
   int32_t first[kMaxExperts + 2];                     // into route; first[groups] = routes

@@ -213,6 +213,7 @@ moe_status check_decode(const moe_problem* p) {
   MOE_TRY(check_problem(p));
   if (!(p->flags & MOE_FLAG_TOPK_ROUTING) || (p->flags & MOE_FLAG_RECOMPUTE)) return MOE_ERR_UNSUPPORTED;
   if (p->tokens > MOE_DECODE_MAX_TOKENS) return MOE_ERR_SHAPE;
+  if (p->intermediate > MOE_DECODE_MAX_INTERMEDIATE) return MOE_ERR_SHAPE;   // a launch holds 2^32 threads
   return MOE_OK;
 }
 
@@ -700,6 +701,7 @@ moe_status moe_forward_decode(const moe_problem* p, const void* hidden, const in
                               const float* router_weights, const moe_weights* w, void* out, void* workspace,
                               size_t workspace_bytes, void* stream) {
   static_assert(decode::kMaxTokens == MOE_DECODE_MAX_TOKENS, "token limit of the kernels and of the ABI");
+  static_assert(decode::kRouteInvalid == MOE_ERR_ROUTE_INVALID, "status word of the kernels and of the ABI");
   MOE_TRY(check_decode(p));
   MOE_TRY(check_weights(p, w));
   const Dims d = dims_of(p);

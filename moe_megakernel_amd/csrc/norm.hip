@@ -185,9 +185,9 @@ __device__ __forceinline__ void ld_param(const void* w, int pbf, int aligned, in
   else ld_param_as<EPT, VEC, BF16, false>(w, aligned, j, tpr, N, f);
 }
 
-// Sums of a and b over the `nw` (at most 16) waves of a row group, every thread of it gets both.  `red` holds two floats per wave of the workgroup and call parity, so
-// one barrier a call is enough (a slot is rewritten two calls later, behind the next
-// call's barrier).
+// Sums of a and b over the `nw` (at most 16) waves of a row group; every thread of it gets
+// both.  `red` holds two floats per wave of the workgroup and call parity, so one barrier a call
+// is enough (a slot is rewritten two calls later, behind the next call's barrier).
 __device__ __forceinline__ void group_sum2(float& a, float& b, int nw, float2* red, int parity) {
   a = wave_sum(a);
   b = wave_sum(b);
@@ -483,18 +483,19 @@ NormArgs norm_args(const moe_norm_problem* p, int ept) {
   return a;
 }
 
-template <class F>
+// FWD: the forward has no variant of 8 elements a thread in 16-byte pieces (fwd_ept).
+template <bool FWD, class F>
 void with_variant(int ept, bool vec, bool bf16, F&& f) {
   using E8 = std::integral_constant<int, 8>;
   using E16 = std::integral_constant<int, 16>;
-  auto types = [&](auto e) {
-    if (vec && bf16) f(e, std::true_type{}, std::true_type{});
-    else if (vec) f(e, std::true_type{}, std::false_type{});
-    else if (bf16) f(e, std::false_type{}, std::true_type{});
-    else f(e, std::false_type{}, std::false_type{});
+  auto types = [&](auto e, auto v) {
+    if (bf16) f(e, v, std::true_type{});
+    else f(e, v, std::false_type{});
   };
-  if (ept == 8) types(E8{});
-  else types(E16{});
+  if (!vec && ept == 8) types(E8{}, std::false_type{});
+  else if (!vec) types(E16{}, std::false_type{});
+  else if (FWD || ept == 16) types(E16{}, std::true_type{});
+  else if constexpr (!FWD) types(E8{}, std::true_type{});
 }
 
 // The backward's launch: row groups a workgroup, workgroups, LDS bytes.  Up to twice the rows
@@ -536,6 +537,7 @@ moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const 
   if (residual) {
     MOE_TRY(check_rows(p, residual));
     MOE_TRY(check_rows(p, sum));
+    if (p->rows > 0 && sum->base == y->base) return MOE_ERR_LAYOUT;   // one would overwrite the other
   }
   if (!weight) return MOE_ERR_NULL;
   if (!elem_aligned(weight, p->param_dtype) || !elem_aligned(bias, p->param_dtype)) return MOE_ERR_LAYOUT;
@@ -556,7 +558,7 @@ moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const 
   const dim3 grid((unsigned)(need < most ? need : most)), block(ng * a.tpr);
   hipStream_t st = static_cast<hipStream_t>(stream);
   return launch("norm_fwd", st, [&] {
-    with_variant(ept, vec, p->dtype == MOE_BF16, [&](auto e, auto v, auto bf) {
+    with_variant<true>(ept, vec, p->dtype == MOE_BF16, [&](auto e, auto v, auto bf) {
       hipLaunchKernelGGL((k_norm_fwd<e(), v(), bf()>), grid, block, 0, st, a);
     });
   });
@@ -599,7 +601,7 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, 
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (p->rows > 0) {
     MOE_TRY(launch("norm_bwd", st, [&] {
-      with_variant(b.ept, vec, p->dtype == MOE_BF16, [&](auto e, auto v, auto bf) {
+      with_variant<false>(b.ept, vec, p->dtype == MOE_BF16, [&](auto e, auto v, auto bf) {
         hipLaunchKernelGGL((k_norm_bwd<e(), v(), bf()>), dim3(b.groups), dim3(b.ng * a.tpr), b.lds, st, a);
       });
     }));

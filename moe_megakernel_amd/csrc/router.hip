@@ -302,7 +302,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
 
 moe_status check_router(const moe_router_problem* p) {
   if (!p) return MOE_ERR_NULL;
-  if (p->tokens < 0 || p->tokens > ((int64_t)1 << 30)) return MOE_ERR_SHAPE;
+  if (p->tokens < 0 || p->tokens > ((int64_t)1 << 27)) return MOE_ERR_SHAPE;   // a launch holds 2^32 threads, 16 a row
   if (p->experts < 1 || p->experts > kMaxExperts) return MOE_ERR_SHAPE;
   if (p->topk < 1 || p->topk > kMaxTopk || p->topk > p->experts) return MOE_ERR_SHAPE;
   if (p->logits_dtype != MOE_BF16 && p->logits_dtype != MOE_FP32) return MOE_ERR_DTYPE;

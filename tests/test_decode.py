@@ -49,7 +49,8 @@ def _p(tokens=4, hidden=256, inter=128, experts=8, topk=2, dt=mk.MOE_BF16, flags
 
 @pytest.mark.parametrize("kw,status", [
     (dict(tokens=-1), mk.MOE_ERR_SHAPE), (dict(tokens=mk.MOE_DECODE_MAX_TOKENS + 1), mk.MOE_ERR_SHAPE),
-    (dict(hidden=130), mk.MOE_ERR_SHAPE), (dict(inter=64), mk.MOE_ERR_SHAPE), (dict(experts=256), mk.MOE_ERR_SHAPE),
+    (dict(hidden=130), mk.MOE_ERR_SHAPE), (dict(inter=64), mk.MOE_ERR_SHAPE),
+    (dict(inter=mk.MOE_DECODE_MAX_INTERMEDIATE + 128), mk.MOE_ERR_SHAPE), (dict(experts=256), mk.MOE_ERR_SHAPE),
     (dict(topk=9, experts=16), mk.MOE_ERR_SHAPE), (dict(flags=mk.MOE_FLAG_HAS_SHARED), mk.MOE_ERR_UNSUPPORTED),
     (dict(flags=TABLE | mk.MOE_FLAG_RECOMPUTE), mk.MOE_ERR_UNSUPPORTED),
     (dict(flags=TABLE | mk.MOE_FLAG_SHARED_GATE), mk.MOE_ERR_UNSUPPORTED), (dict(flags=TABLE | 64), mk.MOE_ERR_UNSUPPORTED),
@@ -100,6 +101,7 @@ def test_binding_refuses_host_and_mismatched_tensors():
     for args, status in (((x, top, rw, w, x.clone()), mk.MOE_ERR_LAYOUT), ((x.float(), top, rw, w, x.clone()), mk.MOE_ERR_DTYPE),
                          ((torch.zeros(5, 256, dtype=torch.bfloat16), top, rw, w, x.clone()), mk.MOE_ERR_SHAPE),
                          ((x[:, :128], top, rw, w, x.clone()), mk.MOE_ERR_SHAPE),
+                         ((x[0, 0], top, rw, w, x.clone()), mk.MOE_ERR_SHAPE),
                          ((None, top, rw, w, x.clone()), mk.MOE_ERR_NULL)):
         with pytest.raises(mk.MoeError) as ei:
             layer.forward(*args)
@@ -322,16 +324,46 @@ def test_scales_of_all_sizes(gpu_lib):
 
 
 @pytest.mark.gpu
+def test_scales_at_the_ends(gpu_lib):
+    """E8M0 bytes 0 (2^-127) and 254 (2^127) beside ordinary ones, and 255, which is NaN."""
+    dp, W = problem(5, 256, 128, 3, 3, routed="mxfp8", seed=49, shared=False)
+    _, _, _, _, fc2, fc2s = dp._keep[:6]
+    for e in range(3):
+        codes, sc = dp.np_routed[e]["fc2"], dp.np_routed[e]["fc2_s"]
+        codes[7], sc[7] = 0x7E, 0                   # 448 * 2^-127
+        codes[9], sc[9] = 0, 127
+        codes[9, 40], sc[9, 1] = 0x08, 254          # 2^-6 * 2^127
+        fc2[e].copy_(torch.from_numpy(codes))
+        fc2s[e].copy_(torch.from_numpy(sc))
+    run(dp)
+    torch.cuda.synchronize()
+    check(dp, W)
+    want = dp.out.clone()
+    fc2s[1][20, 2] = 255
+    run(dp)
+    torch.cuda.synchronize()
+    keep = [c for c in range(256) if c != 20]
+    assert torch.equal(dp.out[:, keep], want[:, keep]) and bool(torch.isnan(dp.out[:, 20]).all())
+
+
+@pytest.mark.gpu
 def test_agrees_with_the_training_forward(gpu_lib):
-    """BF16: the same roundings as moe_forward_topk, so the outputs differ by at most FP32
-    summation order and the BF16 steps it tips: h may move by a step (2^-7 of itself), as may out."""
+    """BF16: h and the output are rounded as in moe_forward_topk (each within tol and 2^-8 of
+    itself); that one also rounds every expert's output, within 2^-8 of it, before they are added."""
     dp, W = problem(40, 512, 256, 12, 3, seed=41, kind="short", shared_gate=True)
     run(dp)
     got = dp.out.double().cpu()
     dp.forward()
     want = dp.out.double().cpu()
-    _, tol = reference(dp.np_x, clean_table(dp.np_top, 12), np.nan_to_num(dp.np_rw), 12, W)
-    assert bool(((got - want).abs() <= 2 * (tol + H8 * (want.abs() + tol))).all())
+    top, rw = clean_table(dp.np_top, 12), np.nan_to_num(dp.np_rw)
+    both, tol = reference(dp.np_x, top, rw, 12, W)
+    shared = reference(dp.np_x, np.full_like(top, -1), rw, 12, W)[0]
+    each = shared.abs()                                # sum of the magnitudes of the experts' terms
+    for k in range(3):
+        one = np.full_like(top, -1)
+        one[:, k] = top[:, k]
+        each += (reference(dp.np_x, one, rw, 12, W)[0] - shared).abs()
+    assert bool(((got - want).abs() <= 2 * (tol + H8 * (both.abs() + tol)) + H8 * (each + tol)).all())
 
 
 @pytest.mark.gpu

@@ -134,6 +134,7 @@ def test_bad_arguments_are_refused():
     assert _fwd(p, res=(PTR, 64)) == mk.MOE_ERR_NULL            # residual without sum
     assert _fwd(p, sum=(PTR, 64)) == mk.MOE_ERR_LAYOUT          # sum without residual
     assert _fwd(p, res=(PTR, 64), sum=(PTR, 8)) == mk.MOE_ERR_LAYOUT
+    assert _fwd(p, res=(PTR, 64), sum=(2 * PTR, 64), y=(2 * PTR, 64)) == mk.MOE_ERR_LAYOUT
     assert _fwd(p, w=PTR + 1) == mk.MOE_ERR_LAYOUT
     assert _fwd(p, b=PTR + 1) == mk.MOE_ERR_LAYOUT
     assert _fwd(p, stats=PTR + 4) == mk.MOE_ERR_LAYOUT
