@@ -64,11 +64,12 @@ __device__ __forceinline__ int row16_min(int v) {
   return min(v, dpp_i<kDppMirror>(v));
 }
 
-// Sum over the wave's 64 lanes: the 16-lane rows, then the rows of each half, then the halves.
-__device__ __forceinline__ float wave_sum(float v) {
-  v = row16_sum(v);
+// From the sums of 16-lane rows to those of each half of the wave, and from those to the wave's.
+__device__ __forceinline__ float add_row_pairs(float v) {
   auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+__device__ __forceinline__ float add_halves(float v) {
   auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
