@@ -13,7 +13,11 @@
 // themselves are compared: no rounding can make or break a tie.  With a bias s + bias is
 // compared as in 64 bits: in 32 bits scores near 1 differ by rounding alone and two correct
 // programs would choose different experts.  (FP32 keys decide wherever they are far enough
-// apart to be sure; FP64 everywhere took 23.6 us at 65536 x 64, top-6.)
+// apart to be sure; FP64 everywhere took 11 us more at 65536 x 64, top-6.)
+//
+// 65536 x 64 sigmoid scores with a bias, top-6: 12.3 us (4.0 us for its bytes at the rate of a
+// large copy); the backward of 65536 x 97 BF16 logits, top-8: 10.3 us (6.0 us).  Bound by vector
+// instructions: at 4 clocks a wave, the forward's are most of its time.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -54,13 +58,30 @@ __device__ __forceinline__ float ld_logit(const void* base, int64_t i) {
 
 __device__ __forceinline__ float ninf() { return -__builtin_huge_valf(); }
 
-// EPL registers of a row: logits (-inf past the last expert).
+// exp(x) = 2^p (1 + r ln 2), p = x log2(e) rounded and r what that left of it: off by 5 u (u =
+// 2^-24; the hardware's 2^p 2 u), a third of the instructions of the library's, which also keeps
+// results below 2^-126.  NaN passes; below -150 the result is 0 either way.
+__device__ __forceinline__ float exp_(float x) {
+  x = x < -150.0f ? -150.0f : x;
+  const float p = x * 1.44269504f;
+  const float r = fmaf(x, 1.44269504f, -p) + x * 1.92596300e-8f;   // log2(e) in two floats
+  const float e = __builtin_amdgcn_exp2f(p);
+  return fmaf(e, r * 0.693147181f, e);
+}
+__device__ __forceinline__ float sigmoid_(float x) {   // 0 where it would not be a normal number; NaN passes
+  const float s = __builtin_amdgcn_rcpf(1.0f + exp_(-x));
+  return x < -87.0f ? 0.0f : s;
+}
+
+// EPL registers of a row: logits (-inf past the last expert).  Every lane loads, past the
+// end the last expert's: without branches all loads are under way together.
 template <int EPL, bool BF16>
 __device__ __forceinline__ void load_row(const RouterArgs& a, int64_t t, int lane, float (&l)[EPL]) {
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = lane + 16 * j;
-    l[j] = e < a.E ? ld_logit<BF16>(a.logits, t * a.ld + e) : ninf();
+    const float v = ld_logit<BF16>(a.logits, t * a.ld + min(e, a.E - 1));
+    l[j] = e < a.E ? v : ninf();
   }
 }
 
@@ -77,7 +98,7 @@ __device__ __forceinline__ void row_scores(const float (&l)[EPL], T (&s)[EPL]) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       if constexpr (std::is_same<T, double>::value) s[j] = l[j] == ninf() ? 0.0 : exp((double)l[j] - (double)m);
-      else s[j] = l[j] == ninf() ? 0.0f : expf(l[j] - m);
+      else s[j] = l[j] == ninf() ? 0.0f : exp_(l[j] - m);
       z += s[j];
     }
     z = row16_sum(z);
@@ -88,7 +109,7 @@ __device__ __forceinline__ void row_scores(const float (&l)[EPL], T (&s)[EPL]) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       if constexpr (std::is_same<T, double>::value) s[j] = 1.0 / (1.0 + exp(-(double)l[j]));
-      else s[j] = __builtin_amdgcn_rcpf(1.0f + expf(-l[j]));
+      else s[j] = sigmoid_(l[j]);
     }
   }
 }
@@ -102,22 +123,47 @@ __device__ __forceinline__ int order_key(float v) {
 }
 __device__ __forceinline__ float key_value(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
-// One round: the largest key left in the row (to `best`) and the lowest expert that has it,
-// -1 when nothing but `lowest` is left; that expert's key is struck out.
+// A chosen expert and its score.
+struct Entry {
+  int e;
+  float s;
+};
+
+// One round: the largest key left in the row (to `best`); the lane that holds it, for the
+// lowest expert if several do, strikes it out and leaves its expert and score in `to` (if
+// `write`).  Nothing happens when only `lowest` is left.
 template <int EPL, typename T>
-__device__ __forceinline__ int take_best(T (&key)[EPL], int lane, T lowest, T& best) {
+__device__ __forceinline__ void take_best(T (&key)[EPL], const float (&s)[EPL], int lane, int rows, T lowest, T& best,
+                                          Entry* to, bool write) {
   T m = key[0];
 #pragma unroll
   for (int j = 1; j < EPL; ++j) m = key[j] > m ? key[j] : m;
   m = row16_max(m);
   best = m;
-  int e = 1 << 20;
+  int e = 1 << 20, hits = 0;
+  float v = 0.0f;
 #pragma unroll
-  for (int j = EPL - 1; j >= 0; --j) e = key[j] == m ? lane + 16 * j : e;
-  e = row16_min(e);
+  for (int j = EPL - 1; j >= 0; --j) {
+    const bool hit = key[j] == m;
+    hits += __popcll(__ballot(hit));
+    e = hit ? lane + 16 * j : e;
+    v = hit ? s[j] : v;
+  }
+  if (hits == rows) {   // one in each of the wave's rows: it is known where it is found
+    bool own = false;
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) key[j] = (lane + 16 * j == e) ? lowest : key[j];
-  return m == lowest ? -1 : e;
+    for (int j = 0; j < EPL; ++j) {
+      const bool hit = key[j] == m;
+      own |= hit;
+      key[j] = hit ? lowest : key[j];
+    }
+    if (own && write) *to = Entry{e, v};
+  } else {              // the rows agree on the lowest expert
+    const bool own = e == row16_min(e) && e < (1 << 20) && m != lowest;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = own && lane + 16 * j == e ? lowest : key[j];
+    if (own && write) *to = Entry{e, v};
+  }
 }
 
 // Orders this wave's LDS accesses for the compiler, which would otherwise take a value a lane
@@ -129,28 +175,38 @@ __device__ __forceinline__ void wave_lds_fence() {
 
 template <int EPL, bool BF16, bool SOFTMAX, bool BIAS>
 __global__ __launch_bounds__(kRouterThreads) void k_router_fwd(RouterArgs a) {
-  __shared__ float chosen[kRouterRows][kMaxTopk];
+  __shared__ Entry chosen[kRouterRows][kMaxTopk];
   const int lane = threadIdx.x & 15;
   const int64_t t = (int64_t)blockIdx.x * kRouterRows + (threadIdx.x >> 4);
   if (t >= a.tokens) return;   // whole 16-lane rows leave together
   float l[EPL], s[EPL];
+  [[maybe_unused]] float bias[EPL];
   load_row<EPL, BF16>(a, t, lane, l);
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) bias[j] = a.bias[min(lane + 16 * j, a.E - 1)];
+  }
   int bad = 0;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) bad = l[j] != l[j] ? 1 : bad;
   bad = row16_max(bad);
   row_scores<EPL, SOFTMAX, float>(l, s);
 
-  int pick[kMaxTopk], key[EPL], best[kMaxTopk];
+  Entry* mine = chosen[threadIdx.x >> 4];
+  if (lane < kMaxTopk) mine[lane] = Entry{-1, 0.0f};
+  wave_lds_fence();
+  const int rows = __popcll(__ballot(true)) >> 4;
+  int key[EPL], best[kMaxTopk];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const int e = lane + 16 * j;
-    const float v = BIAS && e < a.E ? s[j] + a.bias[e] : l[j];
+    const float v = BIAS ? s[j] + bias[j] : l[j];
     // an expert whose logit is -inf or NaN, or whose key is -inf or NaN, is never chosen
     key[j] = l[j] > ninf() && v > ninf() ? order_key(v) : kNoKey;
   }
 #pragma unroll
-  for (int k = 0; k < kMaxTopk; ++k) pick[k] = k < a.K ? take_best<EPL, int>(key, lane, kNoKey, best[k]) : -1;
+  for (int k = 0; k < kMaxTopk; ++k)
+    if (k < a.K) take_best<EPL, int>(key, s, lane, rows, kNoKey, best[k], mine + k, true);
   if constexpr (BIAS) {
     // FP32 keys are off by at most 32 u of a softmax score (u = 2^-24: the rounding of l - m
     // times x exp(-x) <= 0.37, the function, the row sum and the division), 8 u of a sigmoid,
@@ -160,17 +216,19 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_fwd(RouterArgs a) {
     int next = key[0];
 #pragma unroll
     for (int j = 1; j < EPL; ++j) next = max(next, key[j]);
-    next = row16_max(next);
-    bool close = false;
+    // the smallest gap and the largest magnitude; kNoKey is a NaN here, which fminf and fmaxf ignore
+    float low = key_value(row16_max(next)), gap = __builtin_huge_valf(), most = fabsf(low);
 #pragma unroll
-    for (int k = 0; k < kMaxTopk; ++k) {
+    for (int k = kMaxTopk - 1; k >= 0; --k) {
       if (k < a.K) {
-        const int low = k + 1 < a.K ? best[k + 1 < kMaxTopk ? k + 1 : k] : next;
-        const float hi = key_value(best[k]), lo = key_value(low);
-        const float off = (SOFTMAX ? 0x1p-18f : 0x1p-20f) + 0x1p-23f * (fabsf(hi) + fabsf(lo));
-        close |= low != kNoKey && !(hi - lo > off);
+        const float hi = key_value(best[k]);
+        gap = fminf(gap, hi - low);
+        most = fmaxf(most, fabsf(hi));
+        low = hi;
       }
     }
+    // (no gap at all: nothing to confuse.  !(>) holds for infinite magnitudes too)
+    const bool close = gap < __builtin_huge_valf() && !(gap > (SOFTMAX ? 0x1p-18f : 0x1p-20f) + 0x1p-22f * most);
     if (__any(close)) {
       double dkey[EPL], db;
       const double lowest = -__builtin_huge_val();
@@ -178,34 +236,24 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_fwd(RouterArgs a) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
         const int e = lane + 16 * j;
-        dkey[j] = e < a.E ? dkey[j] + (double)a.bias[e] : lowest;
+        dkey[j] = e < a.E ? dkey[j] + (double)bias[j] : lowest;
         if (!(l[j] > ninf()) || dkey[j] != dkey[j]) dkey[j] = lowest;
       }
 #pragma unroll
       for (int k = 0; k < kMaxTopk; ++k) {
-        const int e = k < a.K ? take_best<EPL, double>(dkey, lane, lowest, db) : -1;
-        pick[k] = close ? e : pick[k];
+        if (k < a.K) {
+          if (close && lane == 0) mine[k] = Entry{-1, 0.0f};
+          wave_lds_fence();
+          take_best<EPL, double>(dkey, s, lane, rows, lowest, db, mine + k, close);
+        }
       }
     }
   }
 
-  // the lane that holds pick k leaves its score for lane k, which writes entry k
-  float* mine = chosen[threadIdx.x >> 4];
-  if (lane < kMaxTopk) mine[lane] = 0.0f;
   wave_lds_fence();
-  int e = -1;
-#pragma unroll
-  for (int k = 0; k < kMaxTopk; ++k) {
-    if (k < a.K) {
-      float v = s[0];
-#pragma unroll
-      for (int j = 1; j < EPL; ++j) v = (pick[k] >> 4) == j ? s[j] : v;
-      if ((pick[k] & 15) == lane && pick[k] >= 0) mine[k] = v;
-      e = lane == k ? pick[k] : e;
-    }
-  }
-  wave_lds_fence();
-  const float w = lane < a.K ? mine[lane] : 0.0f;
+  const Entry entry = lane < a.K ? mine[lane] : Entry{-1, 0.0f};   // lane k writes entry k
+  const int e = entry.e;
+  const float w = entry.s;
   const float sum = row16_sum(w);
   const float f = a.normalize ? a.scale / (sum + kRouterEps) : a.scale;
   if (lane < a.K) {
@@ -293,7 +341,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
     const int e = lane + 16 * j;
     if (e < a.E) {
       // 1 - sigmoid(l) as sigmoid(-l): the difference would cancel near 1
-      const float d = SOFTMAX ? s[j] * (g[j] - dot) : g[j] * s[j] / (1.0f + expf(l[j]));
+      const float d = SOFTMAX ? s[j] * (g[j] - dot) : g[j] * s[j] * sigmoid_(-l[j]);
       if constexpr (BF16) static_cast<uint16_t*>(a.dl)[t * a.ld_dl + e] = (uint16_t)f2bf(d);
       else static_cast<float*>(a.dl)[t * a.ld_dl + e] = d;
     }
