@@ -387,7 +387,7 @@ typedef struct {
 #define MOE_NORM_MAX_COLS 16384
 
 /* A matrix [rows][cols] of the problem's dtype, rows `ld` >= cols elements apart.  Any
- * element-aligned base and any ld are taken; rows that are all 16-byte aligned and hold
+ * element-aligned base and any ld are taken; rows that are all 4-byte aligned and hold
  * whole 16-byte pieces are read and written in those. */
 typedef struct {
   void* base;

@@ -16,9 +16,9 @@
 //
 // Bound by memory from some thousand rows on: RMS norm with a residual, 8192 x 7168 BF16, 89 us
 // (5.3 TB/s; a large copy runs at 5.0); layer norm's backward, 4096 x 4096 BF16, 25 us and 3.6 for
-// the second kernel (20 at the copy's rate; the partial rows add a sixth to the bytes).  Rows
-// of FP32 that are not 16-byte aligned, backward of 1023 x 2055: 15 us (7), bound by the number of
-// loads.  Below that by the launch: one row of 4096 takes 3 us on the GPU.
+// the second kernel (20 at the copy's rate; the partial rows add a sixth to the bytes).  FP32
+// rows that are no whole pieces, backward of 1023 x 2055: 15 us (7), bound by the number of loads.
+// Below that by the launch: one row of 4096 takes 3 us on the GPU.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -57,10 +57,13 @@ struct NormArgs {
   float eps;
 };
 
-// Columns of a thread: VEC (rows 16-byte aligned, whole pieces) pieces of 16 bytes, 8 BF16 or 4
-// FP32 elements, at pieces j, j + tpr, ..: neighbouring lanes read neighbouring pieces (with 8
-// FP32 elements a lane, 32 bytes apart, 4453 x 3584 took 73 us in the backward).  Otherwise
-// single elements j + i tpr.
+// Columns of a thread: VEC (whole pieces, rows 4-byte aligned, as all of FP32 are) pieces of 16
+// bytes, 8 BF16 or 4 FP32 elements, at pieces j, j + tpr, ..: neighbouring lanes read neighbouring
+// pieces (with 8 FP32 elements a lane, 32 bytes apart, 4453 x 3584 took 73 us in the backward).
+// Global memory takes 16 bytes at any multiple of 4: 8192 x 4096 BF16 at a stride of 4098 takes 32
+// us in the forward and 50 in the backward, 30 and 48 at 4096, 52 and 56 by elements.  Otherwise
+// single elements j + i tpr; pieces with a shorter last one gained nothing over those for FP32
+// (4096 x 2047: 20 us and 32, against 16 and 28).
 template <bool BF16>
 constexpr int piece() { return BF16 ? 8 : 4; }
 template <bool VEC, bool BF16>
@@ -69,13 +72,19 @@ __device__ __forceinline__ int col_of(int j, int i, int tpr) {
   return VEC ? P * (j + i / P * tpr) + i % P : j + i * tpr;
 }
 
+// 16 bytes at a multiple of 4
+typedef uint32_t piece_t __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ uint4 ld_piece(const void* p) {
+  const piece_t v = *static_cast<const piece_t*>(p);
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void st_piece(void* p, uint4 v) { *static_cast<piece_t*>(p) = piece_t{v.x, v.y, v.z, v.w}; }
+
 // A thread's EPT elements of a row as loaded.
 template <int EPT, bool VEC, bool BF16>
 struct Raw;
-template <int EPT>
-struct Raw<EPT, true, true> { uint4 q[EPT / 8]; };
-template <int EPT>
-struct Raw<EPT, true, false> { float4 q[EPT / 4]; };
+template <int EPT, bool BF16>
+struct Raw<EPT, true, BF16> { uint4 q[EPT / piece<BF16>()]; };
 template <int EPT>
 struct Raw<EPT, false, true> { uint16_t q[EPT]; };
 template <int EPT>
@@ -89,8 +98,7 @@ __device__ __forceinline__ Raw<EPT, VEC, BF16> ld_row(const Rows& m, int64_t r, 
 #pragma unroll
     for (int u = 0; u < EPT / piece<BF16>(); ++u) {
       const int c = piece<BF16>() * (j + u * tpr);
-      if constexpr (BF16) v.q[u] = c < N ? *reinterpret_cast<const uint4*>(p + 2 * c) : make_uint4(0, 0, 0, 0);
-      else v.q[u] = c < N ? *reinterpret_cast<const float4*>(p + 4 * c) : make_float4(0, 0, 0, 0);
+      v.q[u] = c < N ? ld_piece(p + c * (BF16 ? 2 : 4)) : make_uint4(0, 0, 0, 0);
     }
   } else {
 #pragma unroll
@@ -111,7 +119,10 @@ __device__ __forceinline__ void unpack(const Raw<EPT, VEC, BF16>& v, float (&f)[
   } else if constexpr (VEC) {
 #pragma unroll
     for (int u = 0; u < EPT / 4; ++u) {
-      f[4 * u] = v.q[u].x; f[4 * u + 1] = v.q[u].y; f[4 * u + 2] = v.q[u].z; f[4 * u + 3] = v.q[u].w;
+      f[4 * u] = __uint_as_float(v.q[u].x);
+      f[4 * u + 1] = __uint_as_float(v.q[u].y);
+      f[4 * u + 2] = __uint_as_float(v.q[u].z);
+      f[4 * u + 3] = __uint_as_float(v.q[u].w);
     }
   } else {
 #pragma unroll
@@ -132,10 +143,11 @@ __device__ __forceinline__ void st_row(const Rows& m, int64_t r, int j, int tpr,
       if (c >= N) continue;
       const float* s = f + piece<BF16>() * u;
       if constexpr (BF16) {
-        *reinterpret_cast<uint4*>(p + 2 * c) = make_uint4(pack_bf2(s[0], s[1]), pack_bf2(s[2], s[3]),
-                                                          pack_bf2(s[4], s[5]), pack_bf2(s[6], s[7]));
+        st_piece(p + 2 * c, make_uint4(pack_bf2(s[0], s[1]), pack_bf2(s[2], s[3]), pack_bf2(s[4], s[5]),
+                                       pack_bf2(s[6], s[7])));
       } else {
-        *reinterpret_cast<float4*>(p + 4 * c) = make_float4(s[0], s[1], s[2], s[3]);
+        st_piece(p + 4 * c, make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]),
+                                       __float_as_uint(s[3])));
       }
     }
   } else {
@@ -465,9 +477,9 @@ moe_status check_rows(const moe_norm_problem* p, const moe_rows* m) {
   return MOE_OK;
 }
 
-// every row 16-byte aligned (m: an optional matrix may be null)
-bool rows16(const moe_norm_problem* p, const moe_rows* m) {
-  return !m || (aligned16(m->base) && (m->ld * (p->dtype == MOE_BF16 ? 2 : 4)) % 16 == 0);
+// every row 4-byte aligned (m: an optional matrix may be null)
+bool rows4(const moe_norm_problem* p, const moe_rows* m) {
+  return !m || p->dtype == MOE_FP32 || (aligned4(m->base) && m->ld % 2 == 0);
 }
 
 bool whole_pieces(const moe_norm_problem* p) {
@@ -562,7 +574,7 @@ moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const 
   if (!elem_aligned(weight, p->param_dtype) || !elem_aligned(bias, p->param_dtype)) return MOE_ERR_LAYOUT;
   if (reinterpret_cast<uintptr_t>(stats) & 7u) return MOE_ERR_LAYOUT;
   if (p->rows == 0) return MOE_OK;
-  const bool vec = whole_pieces(p) && rows16(p, x) && rows16(p, residual) && rows16(p, sum) && rows16(p, y);
+  const bool vec = whole_pieces(p) && rows4(p, x) && rows4(p, residual) && rows4(p, sum) && rows4(p, y);
   const int ept = fwd_ept(p->cols, vec);
   NormArgs a = norm_args(p, ept);
   a.x = rows_of(x); a.res = rows_of(residual); a.sum = rows_of(sum); a.y = rows_of(y);
@@ -616,7 +628,7 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, 
   a.gb = static_cast<uint8_t*>(grad_bias);
   a.g16 = p->grad_dtype == MOE_BF16;
   a.overwrite = (p->flags & MOE_NORM_OVERWRITE_GRADS) != 0;
-  const bool vec = whole_pieces(p) && rows16(p, grad_y) && rows16(p, x) && rows16(p, grad_sum) && rows16(p, grad_x);
+  const bool vec = whole_pieces(p) && rows4(p, grad_y) && rows4(p, x) && rows4(p, grad_sum) && rows4(p, grad_x);
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (p->rows > 0) {
     MOE_TRY(launch("norm_bwd", st, [&] {

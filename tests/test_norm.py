@@ -211,7 +211,8 @@ def check_backward(dy, x, w, stats, kind, gsum, dx, dw, db):
 BF, F32 = torch.bfloat16, torch.float32
 SIZES = [(1, 1), (1, 8), (3, 2), (5, 7), (1, 4096), (2, 63), (17, 64), (33, 65), (16, 1024), (17, 1032), (9, 1023),
          (300, 128), (1025, 384), (7, 7168), (40, 260), (3, 12300), (513, 4096), (3, 16384), (4, 16383), (2, 8200), (260, 2055),
-         (77, 200), (600, 256), (129, 249), (2000, 100), (20000, 72)]                # rows that share a wave
+         (77, 200), (600, 256), (129, 249), (2000, 100), (20000, 72),                   # rows that share a wave
+         (50, 134), (9, 4095), (65, 1038), (6, 14), (300, 4098)]                    # a last piece of 2, 4, 6 and 3 elements
 
 
 def _run_forward(n, x, w, b, res, kind, pad, offset):
