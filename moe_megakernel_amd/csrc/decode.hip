@@ -246,6 +246,12 @@ __device__ __forceinline__ void dot_steps(const Turn& t, const uint8_t* const (&
   }
 }
 
+// Orders a wave's LDS accesses for the compiler; the hardware runs them in order.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 __device__ __forceinline__ float swiglu(float a, float b, float L) {
   if (L > 0.0f) {   // comparisons that keep a NaN
     a = a > L ? L : a;
@@ -255,9 +261,9 @@ __device__ __forceinline__ float swiglu(float a, float b, float L) {
 }
 
 // ---------------------------------------------------------------- FC1 + SwiGLU
-// A workgroup computes 8 R intermediate columns of one expert for all its tokens (or `reps` times
-// that, in turn): each fragment of 16 rows is 8 gate and 8 up rows in turn, so that a pair ends
-// in one lane's neighbouring sums, and its 4 waves split the contraction.
+// A tile is 8 R intermediate columns of one expert for all its tokens: each fragment of 16 rows is
+// 8 gate and 8 up rows in turn, so that a pair ends in one lane's neighbouring sums.  A
+// workgroup's 4 waves split the contraction of one tile, or (COLS) take a tile each.
 // Grid: [plan] [shared expert's tiles] [min(E, T K) experts' tiles] [gate scores, 4 tokens each].
 struct Fc1Shared {
   uint32_t mask[8];
@@ -478,14 +484,16 @@ __device__ __forceinline__ void write_plan(const Args& a, const Fc1Shared& s, bo
   }
 }
 
-// Columns c0 .. c0 + 16 NF - 1 (of `count`) of one tile.
-template <bool MX, int R, int W, int NF, int D>
-__device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint4* lds, int e, int i0, int c0,
-                                         int count) {
+// Token columns c0 .. c0 + 16 NF - 1 (of `count`) of the tile at i0 (COLS: of wave w's, w tiles
+// on).  `cells`: 16-byte cells of lds a wave has.
+template <bool MX, int R, int W, int NF, int D, bool COLS>
+__device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint4* lds, int cells, int e, int i0,
+                                         int c0, int count) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane >> 2, c4 = 16 * (lane & 3);   // the row and byte this lane loads
   const int steps = a.H / kStep;
-  const int s0 = wave * steps / W, s1 = (wave + 1) * steps / W;
+  const int s0 = COLS ? 0 : wave * steps / W, s1 = COLS ? steps : (wave + 1) * steps / W;
+  if (COLS) i0 += wave * 8 * R;
   const uint8_t *w[R], *ws[R];
 #pragma unroll
   for (int g = 0; g < R; ++g) {
@@ -512,23 +520,29 @@ __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint
   for (int g = 0; g < R; ++g)
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[g][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const Turn turn = turn_of(lds + wave * wave_cells<MX, R>());
+  const Turn turn = turn_of(lds + wave * cells);
   dot_steps<MX, R, NF, D>(turn, w, ws, x, s1 - s0, acc);
   // [wave][column][row]: a lane has rows 4 q .. 4 q + 3 of column r.  Over the turn-round slots
-  __syncthreads();
   float* red = reinterpret_cast<float*>(lds);
+  if constexpr (COLS) {
+    red += (wave * cells - wave * NF * R * 64) * 4;   // the wave's own slots
+    wave_lds_fence();
+  } else {
+    __syncthreads();
+  }
 #pragma unroll
   for (int g = 0; g < R; ++g)
 #pragma unroll
     for (int f = 0; f < NF; ++f)
       *reinterpret_cast<f32x4_t*>(red + ((wave * NF + f) * 16 + turn.row) * (16 * R) + 16 * g + 4 * turn.q) = acc[g][f];
-  __syncthreads();
+  if constexpr (COLS) wave_lds_fence();
+  else __syncthreads();
   const int cols = min(16 * NF, count - c0);
-  for (int o = threadIdx.x; o < 8 * R * cols; o += 64 * W) {
+  for (int o = COLS ? lane : threadIdx.x; o < 8 * R * cols; o += COLS ? 64 : 64 * W) {
     const int c = o / (8 * R), p = o % (8 * R);
     float g = 0.0f, u = 0.0f;
 #pragma unroll
-    for (int v = 0; v < W; ++v) {
+    for (int v = COLS ? wave : 0; v < (COLS ? wave + 1 : W); ++v) {
       const float2 z = *reinterpret_cast<const float2*>(red + (v * NF * 16 + c) * (16 * R) + 2 * p);
       g += z.x;
       u += z.y;
@@ -540,18 +554,20 @@ __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint
 
 // More than 16 tokens: without MANY in passes of 32 over one fragment's weights, which the
 // caches then hold; with MANY (two waves a SIMD, so twice the registers) all at once.
-template <bool MX, int R, int W, int D, bool MANY>
-__device__ __forceinline__ void fc1_group(const Args& a, const Fc1Shared& s, uint4* lds, int e, int i0, int count) {
+template <bool MX, int R, int W, int D, bool MANY, bool COLS>
+__device__ __forceinline__ void fc1_group(const Args& a, const Fc1Shared& s, uint4* lds, int cells, int e, int i0,
+                                          int count) {
   if (count <= 16) {
-    fc1_tile<MX, R, W, 1, D>(a, s, lds, e, i0, 0, count);
+    fc1_tile<MX, R, W, 1, D, COLS>(a, s, lds, cells, e, i0, 0, count);
   } else if constexpr (MANY) {
-    if (count <= 32) fc1_tile<MX, R, W, 2, 1>(a, s, lds, e, i0, 0, count);
-    else fc1_tile<MX, R, W, 4, 1>(a, s, lds, e, i0, 0, count);
+    if (count <= 32) fc1_tile<MX, R, W, 2, 1, COLS>(a, s, lds, cells, e, i0, 0, count);
+    else fc1_tile<MX, R, W, 4, 1, COLS>(a, s, lds, cells, e, i0, 0, count);
   } else {
     for (int g = 0; g < R; ++g)
       for (int c0 = 0; c0 < count; c0 += 32) {
-        if (g + c0) __syncthreads();
-        fc1_tile<MX, 1, W, 2, 1>(a, s, lds, e, i0 + 8 * g, c0, count);
+        if (!COLS && g + c0) __syncthreads();
+        if (COLS) wave_lds_fence();
+        fc1_tile<MX, 1, W, 2, 1, COLS>(a, s, lds, cells, e, i0 + (COLS ? 8 * W : 8) * g, c0, count);
       }
   }
 }
@@ -560,16 +576,17 @@ __device__ __forceinline__ void fc1_group(const Args& a, const Fc1Shared& s, uin
 template <bool MX, int R, bool MANY>
 constexpr int shared_frags() { return MX && !MANY ? 1 : R; }
 
-template <bool MX, int R, int W, int D, bool MANY, bool LOOP>
+template <bool MX, int R, int W, int D, bool MANY, bool COLS>
 __global__ __launch_bounds__(64 * W, MANY ? 2 : 4) void k_decode_fc1(Args a) {
   __shared__ Fc1Shared s;
   // turn-round slots, then the partial sums of up to four column groups
   constexpr int kSums = (MANY ? 4 : 2) * R * 64;
   constexpr int kCells = wave_cells<MX, R>() > kSums ? wave_cells<MX, R>() : kSums;
   __shared__ __align__(16) uint4 lds[W * kCells];
-  const int tiles = a.I / (8 * R * (LOOP ? a.reps : 1));   // workgroups an expert
+  constexpr int T = COLS ? W : 1;                          // column tiles of a workgroup
+  const int tiles = a.I / (8 * R * T);                     // workgroups an expert
   constexpr int RS = shared_frags<MX, R, MANY>();
-  const int shared_blocks = a.shared ? a.I / (8 * RS) : 0;
+  const int shared_blocks = a.shared ? a.I / (8 * RS * T) : 0;
   const int routed_blocks = min(a.E, a.T * a.K) * tiles;
   if (blockIdx.x == 0) {
     Routes rt;
@@ -596,7 +613,7 @@ __global__ __launch_bounds__(64 * W, MANY ? 2 : 4) void k_decode_fc1(Args a) {
     return;
   }
   if (b < shared_blocks) {
-    fc1_group<false, RS, W, 2, MANY>(a, s, lds, -1, b * 8 * RS, a.T);
+    fc1_group<false, RS, W, 2, MANY, COLS>(a, s, lds, kCells, -1, b * 8 * RS * T, a.T);
     return;
   }
   b -= shared_blocks;
@@ -612,14 +629,7 @@ __global__ __launch_bounds__(64 * W, MANY ? 2 : 4) void k_decode_fc1(Args a) {
     count = each_route(rt, a.T * a.K, e, [&](int u, int p) { s.list[p] = (int16_t)(64 * u + (threadIdx.x & 63)); });
   }
   __builtin_amdgcn_wave_barrier();
-  if constexpr (!LOOP) {
-    fc1_group<MX, R, W, D, MANY>(a, s, lds, e, b % tiles * 8 * R, count);
-  } else {
-    for (int t = 0; t < a.reps; ++t) {
-      if (t) __syncthreads();      // the sums of the last tile have been read
-      fc1_group<MX, R, W, D, MANY>(a, s, lds, e, (b % tiles * a.reps + t) * 8 * R, count);
-    }
-  }
+  fc1_group<MX, R, W, D, MANY, COLS>(a, s, lds, kCells, e, b % tiles * 8 * R * T, count);
 }
 
 // ---------------------------------------------------------------- FC2 + combine
@@ -784,28 +794,21 @@ template <bool MX, int R, int D, bool MANY>
 void launch_fc1_as(hipStream_t st, const Args& a) {
   constexpr int W = kFc1Waves;
   const int used = a.E < a.T * a.K ? a.E : a.T * a.K;
-  // A workgroup's start (reading the table, finding its expert) costs about what 64 KB of weights
-  // do: short BF16 rows take several tiles, as long as that leaves every CU four workgroups (36
-  // tokens over 77 experts of H 512: 33 us against 45).  The loop costs registers: longer rows
-  // do without it, and E4M3, which has none to spare, at any length (30 tokens over 53 experts of
-  // H 1024: 46 us, 50 with the loop).
-  constexpr bool kLoops = !MX && !MANY;
-  Args b = a;
-  b.reps = 1;
-  const int64_t bytes = (int64_t)a.H * 32 * R;
-  while (kLoops && b.reps < 8 && bytes * b.reps < (64 << 10) && (int64_t)used * (a.I / (16 * R * b.reps)) >= 1024)
-    b.reps *= 2;
-  const int tiles = a.I / (8 * R * b.reps);
+  // A workgroup's start (reading the table, finding its expert) costs about what 64 KB of
+  // weights do, and four waves that split a short contraction have little to add up: up to H
+  // 1792 each wave takes columns of its own, as long as that leaves 128 workgroups.  36 tokens over
+  // 77 BF16 experts of H 512: 33 us against 41; 64 over 16 E4M3 experts of H 512: 21 against 28;
+  // over 64 of H 1664, top-8: 81 against 94.  Longer rows leave too few workgroups to even out (16
+  // tokens, 32 BF16 experts of H 2048: 76 against 71), as does a smaller layer (55 tokens, 7 E4M3
+  // experts of H 512, I 512: 22 against 20).
+  const bool cols = a.H <= 14 * kStep && (int64_t)used * (a.I / (8 * R * W)) >= 128;
+  const int T = cols ? W : 1;
+  const int tiles = a.I / (8 * R * T);
   const int gate = a.gw ? (a.T + W - 1) / W : 0;
-  const int shared = a.shared ? a.I / (8 * shared_frags<MX, R, MANY>()) : 0;
+  const int shared = a.shared ? a.I / (8 * shared_frags<MX, R, MANY>() * T) : 0;
   const dim3 grid((unsigned)(1 + shared + used * tiles + gate)), block(64 * W);
-  if constexpr (kLoops) {
-    if (b.reps > 1) {
-      hipLaunchKernelGGL((k_decode_fc1<MX, R, W, D, MANY, true>), grid, block, 0, st, b);
-      return;
-    }
-  }
-  hipLaunchKernelGGL((k_decode_fc1<MX, R, W, D, MANY, false>), grid, block, 0, st, b);
+  if (cols) hipLaunchKernelGGL((k_decode_fc1<MX, R, W, D, MANY, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_decode_fc1<MX, R, W, D, MANY, false>), grid, block, 0, st, a);
 }
 template <bool MX>
 void launch_fc1(hipStream_t st, const Args& a) {

@@ -29,8 +29,9 @@ struct Plan {
 // with BF16 at H 7168.  More than 16 tokens run on two waves a SIMD, which leaves the registers for
 // up to 64 tokens an expert: 24 us against 27 (64 tokens over 6 E4M3 experts of H 4096), 81.5
 // against 83.5 over 96.
-//   A short H is split where that leaves every wave at least 8 steps.  `split` does not fall as T
-// grows, so a workspace sized for T serves every smaller batch.
+//   A short H is split where that leaves every wave at least 2 steps (56 tokens over 7 BF16 experts
+// of H 1280, I 640: 25 us against 27 with 8).  `split` does not fall as T grows, so a workspace
+// sized for T serves every smaller batch.
 struct Fc2Shape {
   int frags, waves, split;
 };
@@ -40,7 +41,7 @@ inline Fc2Shape fc2_shape(int64_t T, int64_t H, int64_t I, int64_t E, int64_t K)
   f.waves = T > 16 || f.frags == 2 ? 8 : 16;
   const int64_t tiles = H / (16 * f.frags), experts = E < T * K ? E : T * K;
   int64_t split = 256 / tiles;
-  const int64_t fed = experts * (I / 128) / (8 * f.waves);
+  const int64_t fed = experts * (I / 128) / (2 * f.waves);
   if (split > fed) split = fed;
   f.split = split < 1 ? 1 : (int)split;
   return f;
@@ -60,7 +61,6 @@ struct Args {
   float* gate_s;              // [T] sigmoid(x . gw)
   uint16_t* h;                // [T K + T][I]: routed rows by route, then the shared expert's
   uint16_t* out;              // [T][H]
-  int reps;                   // tiles of a workgroup of the first kernel (set by its launcher)
   int tiles2, split;          // the second kernel's grid
   int32_t* arrived;           // [tiles2], zeroed by the first kernel
   float* sums;                // [tiles2][split][T][16 frags] when split > 1

@@ -251,6 +251,8 @@ CASES = [
     dict(T=20, H=128, I=2048, E=16, K=8, kind="short"),          # second product shared by 4 workgroups a column tile
     dict(T=12, H=256, I=2304, E=20, K=4, gate=True),             # by 2
     dict(T=64, H=384, I=1024, E=12, K=6, layout="table", kind="invalid"),
+    dict(T=40, H=256, I=1024, E=40, K=2, kind="one", gate=True),  # short rows: a tile a wave, tokens in passes of 32
+    dict(T=18, H=1792, I=512, E=10, K=3, limit=0.4),
 ]
 
 
