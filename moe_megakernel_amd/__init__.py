@@ -425,16 +425,33 @@ def _check_rows(where, device, t, dtype, shape) -> int:
 
 
 def _device(where, t) -> int:
-    """The GPU index of a call's first tensor (-1: not on a GPU)."""
+    """The GPU index of a call's first tensor (-1: not on a GPU), which is a matrix."""
     if t is None:
         raise MoeError(MOE_ERR_NULL, where)
+    if t.dim() != 2:
+        raise MoeError(MOE_ERR_SHAPE, where)
     return t.get_device()
+
+
+class _Problems(dict):
+    """Problem structs by what of them changes from call to call (the sizes): a call of a size
+    met before does not build one again.  Nothing writes to a struct once it is made."""
+
+    def __init__(self, make):
+        super().__init__()
+        self.make = make
+
+    def __missing__(self, key):
+        if len(self) >= 256:
+            self.clear()
+        p = self[key] = self.make(*key)
+        return p
 
 
 def _call(where, device, fn, *args):
     """fn(*args, stream) on torch's current stream of GPU `device`, with that GPU current."""
     import torch
-    if device == torch.cuda.current_device():
+    if device == torch._C._cuda_getDevice():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
@@ -457,26 +474,22 @@ class Router:
         st = moe_router_forward(self.p, None, None, None, None, None)    # no tokens: checks the options
         if st != MOE_OK:
             raise MoeError(st, "Router")
-
-    def _problem(self, where, dev, logits):
-        if logits.dim() != 2:
-            raise MoeError(MOE_ERR_SHAPE, where)
-        T, q = logits.shape[0], self.p
-        ld = _check_rows(where, dev, logits, self.dtype, (T, q.experts))
-        return moe_router_problem(T, q.experts, q.topk, q.score, q.logits_dtype, q.flags, q.scale, ld)
+        self.experts, self.topk, q = experts, topk, self.p
+        self._problems = _Problems(lambda T, ld: moe_router_problem(
+            T, q.experts, q.topk, q.score, q.logits_dtype, q.flags, q.scale, ld))
 
     def forward(self, logits, top_experts, router_weights, expert_bias=None):
         """Writes top_experts (int32) and router_weights (float32), both [tokens, topk]."""
         import torch
         where = "moe_router_forward"
-        dev = _device(where, logits)
-        p = self._problem(where, dev, logits)
-        table = (p.tokens, p.topk)
+        dev, T = _device(where, logits), logits.shape[0]
+        ld = _check_rows(where, dev, logits, self.dtype, (T, self.experts))
+        table = (T, self.topk)
         _check(where, dev, top_experts, torch.int32, table)
         _check(where, dev, router_weights, torch.float32, table)
         if expert_bias is not None:
-            _check(where, dev, expert_bias, torch.float32, (p.experts,))
-        _call(where, dev, load().moe_router_forward, p, logits.data_ptr(), _ptr(expert_bias),
+            _check(where, dev, expert_bias, torch.float32, (self.experts,))
+        _call(where, dev, load().moe_router_forward, self._problems[T, ld], logits.data_ptr(), _ptr(expert_bias),
               top_experts.data_ptr(), router_weights.data_ptr())
         return top_experts, router_weights
 
@@ -484,14 +497,14 @@ class Router:
         """Writes grad_logits [tokens, experts] in the logits' dtype."""
         import torch
         where = "moe_router_backward"
-        dev = _device(where, logits)
-        p = self._problem(where, dev, logits)
-        table = (p.tokens, p.topk)
+        dev, T = _device(where, logits), logits.shape[0]
+        ld = _check_rows(where, dev, logits, self.dtype, (T, self.experts))
+        table = (T, self.topk)
         _check(where, dev, top_experts, torch.int32, table)
         _check(where, dev, grad_router_weights, torch.float32, table)
-        ld = _check_rows(where, dev, grad_logits, self.dtype, (p.tokens, p.experts))
-        _call(where, dev, load().moe_router_backward, p, logits.data_ptr(), top_experts.data_ptr(),
-              grad_router_weights.data_ptr(), grad_logits.data_ptr(), ld)
+        ld_grad = _check_rows(where, dev, grad_logits, self.dtype, (T, self.experts))
+        _call(where, dev, load().moe_router_backward, self._problems[T, ld], logits.data_ptr(),
+              top_experts.data_ptr(), grad_router_weights.data_ptr(), grad_logits.data_ptr(), ld_grad)
         return grad_logits
 
 
@@ -512,34 +525,31 @@ class Norm:
         if self.ws_bytes == 0:
             raise MoeError(MOE_ERR_SHAPE if kind in ("layer", "rms") else MOE_ERR_UNSUPPORTED, "Norm")
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
-
-    def _problem(self, where, x, flags=0):
-        if x.dim() != 2:
-            raise MoeError(MOE_ERR_SHAPE, where)
-        q = self.p
-        p = moe_norm_problem(x.shape[0], q.cols, q.kind, q.dtype, q.param_dtype, q.grad_dtype, flags, q.eps)
-        return p, (p.rows, p.cols)
+        self.cols, q = cols, self.p
+        self._problems = _Problems(lambda rows, flags: moe_norm_problem(
+            rows, q.cols, q.kind, q.dtype, q.param_dtype, q.grad_dtype, flags, q.eps))
 
     def _rows(self, where, device, t, shape):
-        return moe_rows(t.data_ptr(), _check_rows(where, device, t, self.dtype, shape))
+        ld = _check_rows(where, device, t, self.dtype, shape)
+        return moe_rows(t.data_ptr(), ld)
 
     def forward(self, x, weight, bias, y, stats=None, residual=None, sum=None):
         """y = norm(x) or, with residual, sum = x + residual and y = norm(sum).  stats: float32
         [rows, 2], what backward needs."""
         import torch
         where = "moe_norm_forward"
-        dev = _device(where, x)
-        p, shape = self._problem(where, x)
+        dev, shape = _device(where, x), (x.shape[0], self.cols)
         rx, ry = self._rows(where, dev, x, shape), self._rows(where, dev, y, shape)
         rres = None if residual is None else self._rows(where, dev, residual, shape)
         rsum = None if sum is None else self._rows(where, dev, sum, shape)
-        cols = (p.cols,)
+        cols = (self.cols,)
         _check(where, dev, weight, self.param_dtype, cols)
         if bias is not None:
             _check(where, dev, bias, self.param_dtype, cols)
         if stats is not None:
-            _check(where, dev, stats, torch.float32, (p.rows, 2))
-        _call(where, dev, load().moe_norm_forward, p, rx, rres, weight.data_ptr(), _ptr(bias), rsum, ry, _ptr(stats))
+            _check(where, dev, stats, torch.float32, (shape[0], 2))
+        _call(where, dev, load().moe_norm_forward, self._problems[shape[0], 0], rx, rres, weight.data_ptr(),
+              _ptr(bias), rsum, ry, _ptr(stats))
         return y
 
     def backward(self, grad_y, x, weight, stats, grad_x, grad_weight=None, grad_bias=None, grad_sum=None,
@@ -548,20 +558,20 @@ class Norm:
         grad_bias [cols] are accumulated, or overwritten."""
         import torch
         where = "moe_norm_backward"
-        dev = _device(where, x)
-        p, shape = self._problem(where, x, MOE_NORM_OVERWRITE_GRADS if overwrite else 0)
+        dev, shape = _device(where, x), (x.shape[0], self.cols)
         rx, rdy, rdx = (self._rows(where, dev, t, shape) for t in (x, grad_y, grad_x))
         rgs = None if grad_sum is None else self._rows(where, dev, grad_sum, shape)
-        cols = (p.cols,)
+        cols = (self.cols,)
         _check(where, dev, weight, self.param_dtype, cols)
-        _check(where, dev, stats, torch.float32, (p.rows, 2))
+        _check(where, dev, stats, torch.float32, (shape[0], 2))
         for g in (grad_weight, grad_bias):
             if g is not None:
                 _check(where, dev, g, self.grad_dtype, cols)
         if self.workspace.get_device() != dev:
             raise MoeError(MOE_ERR_WORKSPACE, where)
-        _call(where, dev, load().moe_norm_backward, p, rdy, rx, weight.data_ptr(), stats.data_ptr(), rgs, rdx,
-              _ptr(grad_weight), _ptr(grad_bias), self.workspace.data_ptr(), self.ws_bytes)
+        _call(where, dev, load().moe_norm_backward,
+              self._problems[shape[0], MOE_NORM_OVERWRITE_GRADS if overwrite else 0], rdy, rx, weight.data_ptr(),
+              stats.data_ptr(), rgs, rdx, _ptr(grad_weight), _ptr(grad_bias), self.workspace.data_ptr(), self.ws_bytes)
         return grad_x
 
 
@@ -580,24 +590,27 @@ class DecodeLayer:
         # zeros: the status word before the first call
         self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=device)
 
+        def problem_of(tokens):
+            q = moe_problem.from_buffer_copy(self.p)
+            q.tokens = tokens
+            return q
+        self.hidden, self.topk = p.hidden, p.topk
+        self._problems = _Problems(problem_of)
+
     def forward(self, hidden, top_experts, router_weights, weights: moe_weights, out):
         import torch
         where = "moe_forward_decode"
-        dev = _device(where, hidden)
-        if hidden.dim() != 2:
+        dev, T = _device(where, hidden), hidden.shape[0]
+        if T > self.p.tokens:
             raise MoeError(MOE_ERR_SHAPE, where)
-        p = moe_problem.from_buffer_copy(self.p)
-        p.tokens = hidden.shape[0]
-        if p.tokens > self.p.tokens:
-            raise MoeError(MOE_ERR_SHAPE, where)
-        rows, table = (p.tokens, p.hidden), (p.tokens, p.topk)
+        rows, table = (T, self.hidden), (T, self.topk)
         _check(where, dev, hidden, torch.bfloat16, rows)
         _check(where, dev, top_experts, torch.int32, table)
         _check(where, dev, router_weights, torch.float32, table)
         _check(where, dev, out, torch.bfloat16, rows)
         if self.workspace.get_device() != dev:
             raise MoeError(MOE_ERR_WORKSPACE, where)
-        _call(where, dev, load().moe_forward_decode, p, hidden.data_ptr(), top_experts.data_ptr(),
+        _call(where, dev, load().moe_forward_decode, self._problems[T,], hidden.data_ptr(), top_experts.data_ptr(),
               router_weights.data_ptr(), weights, out.data_ptr(), self.workspace.data_ptr(), self.ws_bytes)
         return out
 
