@@ -412,3 +412,77 @@ def test_graph_replay_side_stream_and_repeatability(gpu_lib):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(outs, want)), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N", [1000, 1003, 1500, 3584, 7168, 12300])
+def test_constant_rows_far_from_zero(gpu_lib, N, dtype):
+    """Rows of one value c, far above the spread that eps allows for.  The first mean is off by at
+    most 40 u c (and half a step of c), so d = c - mean is exact, a multiple of half a step of c and at
+    most 81 of those: the sum of N of them is exact (81 N < 2^24) and so is its Nth, which is d
+    itself.  What is left is a variance of 0: y is the bias, the mean c and rstd 1 / sqrt(eps),
+    off by the rounding of the root and of the quotient, u each."""
+    g = torch.Generator().manual_seed(N)
+    R, eps = 256, 1e-12
+    c = torch.exp(torch.empty(R).uniform_(9.2, 11.6, generator=g))         # 1e4 .. 1.1e5
+    c[:4] = torch.tensor([11572.6005859375, 31307.4, 26514.5, -20000.3])
+    x = c.to(dtype)[:, None].expand(R, N).contiguous()
+    w, b = 1 + 0.2 * torch.randn(N, generator=g), 0.3 * torch.randn(N, generator=g)
+    y, stats, _ = _run_forward(mk.Norm(N, eps=eps, dtype=dtype, param_dtype=F32), x, w, b, None, "layer", 0, 0)
+    assert torch.equal(y, b.to(dtype)[None].expand(R, N))
+    assert torch.equal(stats[:, 0], x[:, 0].float())
+    want = 1.0 / float(torch.tensor(eps, dtype=F32).double().sqrt())
+    assert bool((stats[:, 1].double() / want - 1).abs().max() <= 3 * U)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [1000, 1003, 3584, 7168, 12300])
+def test_rows_of_two_neighbouring_values(gpu_lib, N):
+    """c and the next number above it, a step (2 u c at most) apart, half of each or a few among the rest.
+    As for constant rows all differences and their sum are exact, |delta| <= 81 half steps; its
+    division is off by u |delta| <= 41 u steps and each centred value by that and u of itself.
+    The variance is then off by its sum's 40 u and twice those 41 u steps over its root, at most."""
+    g = torch.Generator().manual_seed(N + 1)
+    R, eps = 64, 1e-12
+    c = torch.exp(torch.empty(R, 1).uniform_(9.3, 10.3, generator=g))      # 1.1e4 .. 3e4
+    step = torch.exp2(torch.floor(torch.log2(c)) - 23)
+    share = torch.tensor([0.5, 0.02])[torch.arange(R) % 2][:, None]
+    on = torch.rand(R, N, generator=g) < share
+    on[:, 0] = True
+    x = c + step * on
+    assert bool(((x == c) | on).all()) and bool((x[:, 0] > c[:, 0]).all())
+    w, b = 1 + 0.2 * torch.randn(N, generator=g), 0.3 * torch.randn(N, generator=g)
+    y, stats, _ = _run_forward(mk.Norm(N, eps=eps, dtype=F32), x, w, b, None, "layer", 0, 0)
+    ref, xh, mu, rstd = ref_forward(x, w, b, "layer", float(torch.tensor(eps, dtype=F32)))
+    off = 41 * U * step.double() * rstd                       # of (x - mean) rstd
+    rel = 64 * U + 2 * off + off ** 2                         # of rstd
+    assert bool(((stats[:, 1:].double() / rstd - 1).abs() <= rel).all())
+    assert bool(((stats[:, :1].double() - mu).abs() <= 41 * U * step.double() + 2 * U * mu.abs()).all())
+    tol = (off + (rel + 4 * U) * xh.abs()) * w.double().abs() + 2 * U * (ref.abs() + b.double().abs())
+    assert bool(((y.double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [97, 200, 1000, 1003, 1400, 1900, 3584, 7168])
+def test_constant_rows_beside_ordinary_ones(gpu_lib, N):
+    """Rows that share a wave or a workgroup with rows of one value (and with one that holds a
+    NaN) get the results they get beside others, bit for bit; every second of them has a spread of a
+    few steps of its mean."""
+    R, eps = 96, 1e-12
+    x, w, b, _, _ = make(R, N, F32, F32, seed=21)
+    n = mk.Norm(N, eps=eps, dtype=F32)
+    y, stats, _ = _run_forward(n, x, w, b, None, "layer", 0, 0)
+    check_forward(x, w, b, y, stats, "layer", eps=eps)
+    g = torch.Generator().manual_seed(N)
+    x[1::2] = 20000 + torch.randint(0, 16, (R // 2, N), generator=g) * torch.rand(R // 2, 1, generator=g) * 2.0 ** -9   # steps
+    alone, stats, _ = _run_forward(n, x, w, b, None, "layer", 0, 0)
+    flat = torch.rand(R, generator=g) < 0.4
+    c = torch.exp(torch.empty(R, 1).uniform_(9.3, 11.5, generator=g))
+    mixed = torch.where(flat[:, None], c, x)
+    mixed[5, N // 2], flat[5] = float("nan"), True
+    y, st, _ = _run_forward(n, mixed, w, b, None, "layer", 0, 0)
+    assert bool(torch.isnan(y[5]).all())
+    assert torch.equal(y[~flat], alone[~flat]) and torch.equal(st[~flat], stats[~flat])
+    flat[5] = False
+    assert torch.equal(y[flat], b[None].expand(int(flat.sum()), N))
