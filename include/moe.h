@@ -407,7 +407,8 @@ moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const 
                             float* stats, void* stream);
 
 /* Workspace bytes of moe_norm_backward (0 on invalid input): the column sums of up to 256
- * groups of rows.  The size does not depend on rows beyond that. */
+ * groups of rows.  The size never falls as rows grow and is the same from 256 rows on: what
+ * suffices for some rows suffices for fewer. */
 size_t moe_norm_workspace_bytes(const moe_norm_problem* p);
 
 /* Backward of sum(grad_y * y) + sum(grad_sum * sum).

@@ -637,7 +637,11 @@ moe_status moe_norm_forward(const moe_norm_problem* p, const moe_rows* x, const 
 
 size_t moe_norm_workspace_bytes(const moe_norm_problem* p) {
   if (check_norm(p) != MOE_OK) return 0;
-  return align_up((size_t)bwd_shape(p).groups * 2 * p->cols * sizeof(float) + 1);
+  // Not the launch's own number of partial rows, which falls where a workgroup takes another row
+  // group (256 rows of 4096 in 256 workgroups, 257 in 129): a workspace sized for some rows has to serve
+  // every smaller batch.
+  const int64_t groups = bwd_shape(p).groups == 1 ? 1 : (p->rows < kNormGroups ? p->rows : kNormGroups);
+  return align_up((size_t)groups * 2 * p->cols * sizeof(float) + 1);
 }
 
 moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, const moe_rows* x,

@@ -157,6 +157,15 @@ def test_workspace_does_not_grow_with_rows():
         assert 0 < mk.moe_norm_workspace_bytes(_problem(rows=rows, cols=4096)) <= big
 
 
+def test_workspace_serves_smaller_batches():
+    """A workspace sized for some rows takes a call with fewer of them."""
+    for cols in (1, 96, 1000, 1024, 2055, 4096, 7168, 8200, 16384):
+        for dtype in (mk.MOE_BF16, mk.MOE_FP32):
+            need = [mk.moe_norm_workspace_bytes(_problem(rows=r, cols=cols, dtype=dtype)) for r in
+                    [*range(1100), 2047, 2048, 2049, 5000, 1 << 15, 1 << 20, 1 << 30]]
+            assert all(n > 0 for n in need) and need == sorted(need), (cols, dtype)
+
+
 def test_binding_refuses_host_and_mismatched_tensors():
     n = mk.Norm(64, device="cpu")
     x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.ones(64, dtype=torch.bfloat16)
