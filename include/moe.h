@@ -283,13 +283,14 @@ moe_status moe_forward_noalloc(const moe_problem* p, const void* hidden, const f
                                void* saved, void* stream);
 
 /* Forward of a few tokens (serving: one token of each of several streams), in two kernels
- * that read the weights of each expert in use once.  Requires MOE_FLAG_TOPK_ROUTING; with
+ * built around one read of the weights of each expert in use (an expert with more than 32 tokens
+ * reads them again, mostly from the caches).  Requires MOE_FLAG_TOPK_ROUTING; with
  * MOE_FLAG_RECOMPUTE it returns MOE_ERR_UNSUPPORTED, and with more than
  * MOE_DECODE_MAX_TOKENS tokens MOE_ERR_SHAPE.  Arguments as for moe_forward_topk, without
  * `saved`: no backward can follow.  intermediate is at most MOE_DECODE_MAX_INTERMEDIATE
  * (MOE_ERR_SHAPE above).  The result with BF16 weights is moe_forward_topk's, up to the order
- * of the FP32 sums and without its rounding of each expert's output to BF16 before they are
- * added.  With MXFP8 weights it differs: the weights are decoded to BF16 (exactly,
+ * of the FP32 sums and without its roundings of h and of each expert's output to BF16 (h is held
+ * to 2^-16 of itself).  With MXFP8 weights it differs: the weights are decoded to BF16 (exactly,
  * unless smaller than 2^-126 or past BF16's largest) and multiply the BF16 activations,
  * which are not quantised.
  *  workspace   moe_decode_workspace_bytes(p) bytes, 16-byte aligned, overwritten in every

@@ -11,20 +11,25 @@
 //
 // What it reaches (read floor: the weights in use at 6.35 TB/s, what a plain read kernel gets):
 //   1 token, 96 BF16 experts top-4, H 4096, I 1024, shared expert    28 us, floor 20
-//   7 tokens, the same with E4M3 experts                             72 us, floor 55
-//   19 tokens, BF16, no shared expert                               201 us, floor 196
-//   64 tokens, 64 E4M3 experts top-6, H 7168, I 2048                529 us, floor 471
-// Bound by the weight stream; at one token by the two kernels' start and end (about 4 us each:
-// table, first loads, last sums).
+//   7 tokens, the same with E4M3 experts                             70 us, floor 55
+//   19 tokens, BF16, no shared expert                               215 us, floor 196
+//   64 tokens, 64 E4M3 experts top-6, H 7168, I 2048                570 us, floor 471
+// Bound by the weight stream, in the last case with the reads of h; at one token by the two kernels'
+// start and end (about 4 us each: table, first loads, last sums).
 //
 // MXFP8 weights are decoded to BF16 in registers, which is exact (E4M3 has 3 fraction
 // bits and the scale is a power of two) wherever the product is a normal BF16 number; the tokens
-// stay BF16.  h is rounded to BF16, as
-// moe_forward stores it.  Accumulators, the SwiGLU and the combine are FP32, and the output is
-// rounded once.  Every sum has a fixed order.
+// stay BF16.  h is held in two BF16 parts, 16 of its 24 bits, so that nothing but the output is
+// rounded to BF16: its error against 64 bits is 0.166% of its size, a plain FP32 form's too, and
+// 0.235% with h in one part.  That costs at most 2.5% up to 16 tokens (empty columns of a fragment
+// hold the second part) and 5% with BF16 weights up to 32 tokens an expert, but with many tokens and
+// E4M3 the doubled reads of h show: 570 us against 528 in the last case above, 171 against 139 where
+// experts get 33 of 64 tokens.  Accumulators, the SwiGLU and the combine are FP32.  Every sum has a
+// fixed order.
 #include <hip/hip_runtime.h>
 
 #include "decode.hpp"
+#include "reduce.hpp"
 
 namespace moe {
 namespace decode {
@@ -89,12 +94,14 @@ __device__ __forceinline__ Turn turn_of(uint4* scratch) {
           lane & 15, lane >> 4};
 }
 
-// 16 token columns, one step: lane l loads chunk l & 3 (16 bytes) of column l >> 2.
+// 16 token columns, one step: lane l loads chunk l & 3 (16 bytes) of column l >> 2.  A column's
+// 64-byte pieces are PITCH bytes apart.
+template <int PITCH>
 struct XStep {
   uint4 v[4];
   __device__ __forceinline__ void load(const uint8_t* p) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = ld16(p + 64 * j);
+    for (int j = 0; j < 4; ++j) v[j] = ld16(p + PITCH * j);
   }
   // products 2 s and 2 s + 1
   template <bool MX>
@@ -106,8 +113,10 @@ struct XStep {
       o[u] = __builtin_bit_cast(bf16x8_t, MX ? t.x[(t.q >> 1) * 64 + cell(t.row, 2 * (t.q & 1) + u)]
                                              : t.x[u * 64 + cell(t.row, t.q)]);
   }
-  static constexpr int kBytes = 2 * kStep;
+  static constexpr int kBytes = 4 * PITCH;
 };
+constexpr int kXPitch = 64;       // x: rows of consecutive elements
+constexpr int kHPitch = 128;      // h: see h_index
 
 // 16 weight rows, one step: lane l loads chunk l & 3 of row l >> 2.
 template <bool MX>
@@ -159,16 +168,16 @@ struct WStep<true> {
 // w, ws: the loading lane's rows at their first element (scales: the rows' first block); x: the
 // loading lane's columns at their first element.  D steps are in flight; the steady loop
 // has no conditions.
-template <bool MX, int R, int NF, int D>
+template <bool MX, int R, int NF, int D, int PITCH>
 __device__ __forceinline__ void dot_chunk(const Turn& t, const uint8_t* const (&w)[R], const uint8_t* const (&ws)[R],
                                           const uint8_t* const (&x)[NF], int n, f32x4_t (&acc)[R][NF]) {
   WStep<MX> wr[D][R];
-  XStep xr[D][NF];
+  XStep<PITCH> xr[D][NF];
   auto load = [&](int d, int i) __attribute__((always_inline)) {
 #pragma unroll
     for (int g = 0; g < R; ++g) wr[d][g].load(w[g] + (int64_t)i * WStep<MX>::kBytes);
 #pragma unroll
-    for (int f = 0; f < NF; ++f) xr[d][f].load(x[f] + i * XStep::kBytes);
+    for (int f = 0; f < NF; ++f) xr[d][f].load(x[f] + i * XStep<PITCH>::kBytes);
   };
   auto mul = [&](int d, int i) __attribute__((always_inline)) {
 #pragma unroll
@@ -226,11 +235,11 @@ __device__ __forceinline__ void dot_chunk(const Turn& t, const uint8_t* const (&
     if (i + D + d < n) mul(d, i + D + d);
 }
 
-template <bool MX, int R, int NF, int D>
+template <bool MX, int R, int NF, int D, int PITCH>
 __device__ __forceinline__ void dot_steps(const Turn& t, const uint8_t* const (&w)[R], const uint8_t* const (&ws)[R],
                                           const uint8_t* const (&x)[NF], int n, f32x4_t (&acc)[R][NF]) {
   if constexpr (!MX) {
-    dot_chunk<MX, R, NF, D>(t, w, ws, x, n, acc);
+    dot_chunk<MX, R, NF, D, PITCH>(t, w, ws, x, n, acc);
   } else {
     const uint8_t *wc[R], *wsc[R], *xc[NF];
     for (int i0 = 0; i0 < n; i0 += kScaleSteps) {
@@ -240,8 +249,8 @@ __device__ __forceinline__ void dot_steps(const Turn& t, const uint8_t* const (&
         wsc[g] = ws[g] + i0 * 4;
       }
 #pragma unroll
-      for (int f = 0; f < NF; ++f) xc[f] = x[f] + (int64_t)i0 * XStep::kBytes;
-      dot_chunk<MX, R, NF, D>(t, wc, wsc, xc, min(kScaleSteps, n - i0), acc);
+      for (int f = 0; f < NF; ++f) xc[f] = x[f] + (int64_t)i0 * XStep<PITCH>::kBytes;
+      dot_chunk<MX, R, NF, D, PITCH>(t, wc, wsc, xc, min(kScaleSteps, n - i0), acc);
     }
   }
 }
@@ -258,6 +267,15 @@ __device__ __forceinline__ float swiglu(float a, float b, float L) {
     b = b > L ? L : (b < -L ? -L : b);
   }
   return a * sigmoidf_(a) * b;
+}
+
+// h's two parts are its rounding to BF16 and what that left (of an infinite or NaN h: 0), 32 upper
+// parts and then their 32 lower ones in each 128-byte line.  The second product takes both as columns
+// of one fragment, so a load touches each line once, as a whole (parts in two rows, half a line a
+// load: 308 us against 291 with 12 tokens for each of 32 BF16 experts of H 7168).
+constexpr int kHLower = 32;
+__device__ __forceinline__ int64_t h_index(int64_t row, int i, int I) {
+  return row * 2 * I + (i >> 5) * 64 + (i & 31);
 }
 
 // ---------------------------------------------------------------- FC1 + SwiGLU
@@ -513,7 +531,7 @@ __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint
   for (int f = 0; f < NF; ++f) {
     const int c = c0 + 16 * f + r < count ? c0 + 16 * f + r : c0;   // columns past the last repeat one
     const int t = e < 0 ? c : s.list[c] / a.K;
-    x[f] = reinterpret_cast<const uint8_t*>(a.x + (int64_t)t * a.H) + (int64_t)s0 * XStep::kBytes + c4;
+    x[f] = reinterpret_cast<const uint8_t*>(a.x + (int64_t)t * a.H) + (int64_t)s0 * XStep<kXPitch>::kBytes + c4;
   }
   f32x4_t acc[R][NF];
 #pragma unroll
@@ -521,7 +539,7 @@ __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[g][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const Turn turn = turn_of(lds + wave * cells);
-  dot_steps<MX, R, NF, D>(turn, w, ws, x, s1 - s0, acc);
+  dot_steps<MX, R, NF, D, kXPitch>(turn, w, ws, x, s1 - s0, acc);
   // [wave][column][row]: a lane has rows 4 q .. 4 q + 3 of column r.  Over the turn-round slots
   float* red = reinterpret_cast<float*>(lds);
   if constexpr (COLS) {
@@ -548,7 +566,10 @@ __device__ __forceinline__ void fc1_tile(const Args& a, const Fc1Shared& s, uint
       u += z.y;
     }
     const int64_t hrow = e < 0 ? (int64_t)a.T * a.K + c0 + c : s.list[c0 + c];
-    a.h[hrow * a.I + i0 + p] = (uint16_t)f2bf(swiglu(g, u, a.limit));
+    const float h = swiglu(g, u, a.limit), hi = bf2f(f2bf(h));
+    uint16_t* to = a.h + h_index(hrow, i0 + p, a.I);
+    to[0] = (uint16_t)f2bf(h);
+    to[kHLower] = (uint16_t)f2bf(fabsf(hi) < __builtin_huge_valf() ? h - hi : 0.0f);
   }
 }
 
@@ -645,8 +666,9 @@ struct Fc2Shared {
   float weight[kMaxRoutes];
 };
 
-// Columns c0 .. of one expert (e < 0: the shared one), steps s0 .. s0 + n - 1; row fragments
-// g0 .. g0 + R - 1 of the workgroup's RT.
+// Tokens c0 .. c0 + 8 NF - 1 of one expert (e < 0: the shared one), steps s0 .. s0 + n - 1; row
+// fragments g0 .. g0 + R - 1 of the workgroup's RT.  A column fragment is 8 tokens: columns 0 .. 7 are
+// the upper parts of their h, 8 .. 15 the lower ones, and their sums are added at the end.
 template <bool MX, int R, int RT, int NF, int D>
 __device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, const Turn& turn, float* acc_lds, int g0,
                                          int e, int first, int c0, int count, int s0, int n) {
@@ -667,20 +689,27 @@ __device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, cons
   const uint8_t* x[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
-    const int c = c0 + 16 * f + r < count ? c0 + 16 * f + r : c0;
+    const int c = c0 + 8 * f + (r & 7) < count ? c0 + 8 * f + (r & 7) : c0;
     const int64_t hrow = e < 0 ? (int64_t)a.T * a.K + c : s.route[first + c];
-    x[f] = reinterpret_cast<const uint8_t*>(a.h + hrow * a.I) + (int64_t)s0 * XStep::kBytes + c4;
+    x[f] = reinterpret_cast<const uint8_t*>(a.h + h_index(hrow, 0, a.I) + (r >> 3) * kHLower) +
+           (int64_t)s0 * XStep<kHPitch>::kBytes + c4;
   }
   f32x4_t acc[R][NF];
 #pragma unroll
   for (int g = 0; g < R; ++g)
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[g][f] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  dot_steps<MX, R, NF, D>(turn, w, ws, x, n, acc);
+  dot_steps<MX, R, NF, D, kHPitch>(turn, w, ws, x, n, acc);
+#pragma unroll
+  for (int g = 0; g < R; ++g)
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[g][f][i] += dpp_f<kDppRor8>(acc[g][f][i]);
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
-    const int c = c0 + 16 * f + turn.row;
-    if (c >= count) continue;
+    const int c = c0 + 8 * f + turn.row;
+    if (c >= count || turn.row >= 8) continue;
     const int tok = e < 0 ? c : s.route[first + c] / a.K;
     const float wt = e < 0 ? (a.gw ? a.gate_s[c] : 1.0f) : s.weight[first + c];
 #pragma unroll
@@ -694,22 +723,27 @@ __device__ __forceinline__ void fc2_part(const Args& a, const Fc2Shared& s, cons
   }
 }
 
-// All RT fragments of the workgroup together (R at a time up to 16 tokens: the shared expert's
-// BF16 rows take more registers than E4M3's).  MANY: a batch of more than 16 tokens.
+// All RT fragments of the workgroup together (R at a time up to 8 tokens: the shared expert's
+// BF16 rows take more registers than E4M3's).  More than 32 tokens go in passes over the weights,
+// which the caches then hold.  MANY: a batch of more than 16 tokens, or short rows.  (Two column
+// fragments with two steps in flight: 183 us against 189 with 12 of 64 tokens for each of 32 E4M3
+// experts of H 7168.)
 template <bool MX, int R, int RT, int D, bool MANY>
 __device__ __forceinline__ void fc2_group(const Args& a, const Fc2Shared& s, const Turn& turn, float* acc_lds, int e,
                                           int first, int count, int s0, int n) {
-  if (!MANY || count <= 16) {
+  if (count <= 8) {
     for (int g = 0; g < RT; g += R) fc2_part<MX, R, RT, 1, D>(a, s, turn, acc_lds, g, e, first, 0, count, s0, n);
-  } else if (count <= 32) {
-    fc2_part<MX, RT, RT, 2, 1>(a, s, turn, acc_lds, 0, e, first, 0, count, s0, n);
+  } else if (!MANY || count <= 16) {
+    fc2_part<MX, RT, RT, 2, MANY ? D : 1>(a, s, turn, acc_lds, 0, e, first, 0, count, s0, n);
   } else {
-    fc2_part<MX, RT, RT, 4, 1>(a, s, turn, acc_lds, 0, e, first, 0, count, s0, n);
+    for (int c0 = 0; c0 < count; c0 += 32)
+      fc2_part<MX, RT, RT, 4, 1>(a, s, turn, acc_lds, 0, e, first, c0, count, s0, n);
   }
 }
 
-template <bool MX, int W, int R, int D, int OCC, bool MANY>
-__global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
+template <bool MX, int R, bool MANY>
+__global__ __launch_bounds__(64 * kFc2Waves, 2) void k_decode_fc2(Args a) {
+  constexpr int W = kFc2Waves, D = 2;
   extern __shared__ __align__(16) float acc_all[];   // [W][T][16 R]
   __shared__ Fc2Shared s;
   __shared__ __align__(16) uint4 slots[W * wave_cells<MX, R>()];
@@ -731,7 +765,7 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
   const int steps = a.I / kStep, part = blockIdx.y * W + wave, parts = W * a.split;
   if (a.shared) {   // every wave takes its part: with many tokens these steps cost more than routed ones
     const int s0 = part * steps / parts, s1 = (part + 1) * steps / parts;
-    if (s1 > s0) fc2_group<false, 1, R, 2, MANY>(a, s, turn, mine, -1, 0, a.T, s0, s1 - s0);
+    if (s1 > s0) fc2_group<false, 1, R, D, MANY>(a, s, turn, mine, -1, 0, a.T, s0, s1 - s0);
   }
   if (tid <= kMaxExperts) s.expert[tid] = plan_e;
   if (tid < kMaxExperts + 2) s.first[tid] = plan_f;
@@ -786,8 +820,8 @@ __global__ __launch_bounds__(64 * W, OCC) void k_decode_fc2(Args a) {
 
 }  // namespace
 
-// Steps in flight (D) and waves a SIMD (OCC) fit the register file: four waves leave 128
-// registers each.  Spills and fewer waves cost more than depth gains: one token of BF16 at H 4096
+// Steps in flight (D) and waves a SIMD fit the register file: four waves leave 128 registers
+// each.  Spills and fewer waves cost more than depth gains: one token of BF16 at H 4096
 // takes 28.2 us as it is, 30.2 with three steps in flight and 29.1 with eight waves a
 // workgroup in the first kernel.
 template <bool MX, int R, int D, bool MANY>
@@ -821,22 +855,20 @@ void launch_fc1(hipStream_t st, const Args& a) {
   if (a.T > 16 && a.T * a.K > 14 * a.E) launch_fc1_as<MX, 2, 1, true>(st, a);
   else launch_fc1_as<MX, MX ? 2 : 1, MX ? 1 : 2, false>(st, a);
 }
-template <bool MX, int W, int R, int OCC, bool MANY>
+template <bool MX, int R, bool MANY>
 void launch_fc2_as(hipStream_t st, const Args& a) {
+  constexpr int W = kFc2Waves;
   static_assert(64 * W >= kMaxRoutes && 64 * W >= kMaxExperts + 2, "the plan in one load a thread");
-  hipLaunchKernelGGL((k_decode_fc2<MX, W, R, 2, OCC, MANY>), dim3(a.tiles2, a.split), dim3(64 * W),
+  hipLaunchKernelGGL((k_decode_fc2<MX, R, MANY>), dim3(a.tiles2, a.split), dim3(64 * W),
                      (size_t)W * a.T * 16 * R * sizeof(float), st, a);
 }
 template <bool MX>
 void launch_fc2(hipStream_t st, const Args& a) {
-  const Fc2Shape f = fc2_shape(a.T, a.H, a.I, a.E, a.K);
-  if (f.frags == 1) {
-    if (f.waves == 8) launch_fc2_as<MX, 8, 1, 2, true>(st, a);
-    else launch_fc2_as<MX, 16, 1, 4, false>(st, a);
-  } else {
-    if (a.T > 16) launch_fc2_as<MX, 8, 2, 2, true>(st, a);
-    else launch_fc2_as<MX, 8, 2, 2, false>(st, a);
-  }
+  // Two fragments for up to 16 tokens leave out what only more need: 146 us against 152 (16 tokens over
+  // 32 E4M3 experts of H 5120), 252 against 259 (BF16).  With one fragment that gains nothing.
+  if (fc2_shape(a.T, a.H, a.I, a.E, a.K).frags == 1) launch_fc2_as<MX, 1, true>(st, a);
+  else if (a.T > 16) launch_fc2_as<MX, 2, true>(st, a);
+  else launch_fc2_as<MX, 2, false>(st, a);
 }
 template void launch_fc1<false>(hipStream_t, const Args&);
 template void launch_fc1<true>(hipStream_t, const Args&);

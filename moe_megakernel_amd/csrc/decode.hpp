@@ -21,27 +21,25 @@ struct Plan {
   float weight[kMaxRoutes];                           // of the routes
 };
 
-// The second kernel's launch: row fragments (16 output columns each) and waves a workgroup, and
-// workgroups that share a workgroup's columns.
-//   Up to H 4096 one fragment, at most one workgroup a CU; up to 16 tokens then 16 waves: 28.5 us
-// against 30.0 with 8 (7 tokens, H 4096, E4M3).  Above, two fragments share the tokens' loads:
-// 185 us against 222 at H 7168 (64 tokens, E4M3), 122 against 154 at H 5120 (16 tokens), the same
-// with BF16 at H 7168.  More than 16 tokens run on two waves a SIMD, which leaves the registers for
-// up to 64 tokens an expert: 24 us against 27 (64 tokens over 6 E4M3 experts of H 4096), 81.5
-// against 83.5 over 96.
+// The second kernel's launch: row fragments a workgroup (16 output columns each), and workgroups
+// that share a workgroup's columns.  Its 8 waves are two a SIMD, which leaves the registers for two
+// steps of h's two parts in flight.
+//   Up to H 4096 one fragment, at most one workgroup a CU.  Above, two fragments share the tokens'
+// loads: 226 us against 283 at H 7168 (64 tokens over 64 E4M3 experts), 66 against 87 (64 over 16
+// BF16), 98 against 109 at H 5120 (16 over 32 BF16).
 //   A short H is split where that leaves every wave at least 2 steps (56 tokens over 7 BF16 experts
-// of H 1280, I 640: 25 us against 27 with 8).  `split` does not fall as T grows, so a workspace
+// of H 1280, I 640: 13.4 us against 15.2 with 8).  `split` does not fall as T grows, so a workspace
 // sized for T serves every smaller batch.
+constexpr int kFc2Waves = 8;
 struct Fc2Shape {
-  int frags, waves, split;
+  int frags, split;
 };
 inline Fc2Shape fc2_shape(int64_t T, int64_t H, int64_t I, int64_t E, int64_t K) {
   Fc2Shape f;
   f.frags = H / 16 <= 256 ? 1 : 2;
-  f.waves = T > 16 || f.frags == 2 ? 8 : 16;
   const int64_t tiles = H / (16 * f.frags), experts = E < T * K ? E : T * K;
   int64_t split = 256 / tiles;
-  const int64_t fed = experts * (I / 128) / (2 * f.waves);
+  const int64_t fed = experts * (I / 128) / (2 * kFc2Waves);
   if (split > fed) split = fed;
   f.split = split < 1 ? 1 : (int)split;
   return f;
@@ -59,7 +57,7 @@ struct Args {
   const uint16_t* gw;         // shared output gate's weight [H], or null
   Plan* plan;
   float* gate_s;              // [T] sigmoid(x . gw)
-  uint16_t* h;                // [T K + T][I]: routed rows by route, then the shared expert's
+  uint16_t* h;                // [T K + T][2 I]: routed rows by route, then the shared expert's; two parts
   uint16_t* out;              // [T][H]
   int tiles2, split;          // the second kernel's grid
   int32_t* arrived;           // [tiles2], zeroed by the first kernel

@@ -170,8 +170,8 @@ FwdLayout fwd_layout(const Dims& d) {
 size_t fwd_workspace(const Dims& d) { return fwd_layout(d).total; }
 
 // Workspace of the few-token forward: the plan (its first word is the status), the gate
-// scores, h (routed rows by route, then the shared expert's) and the sums of a split second
-// product with their arrival counts.
+// scores, h (routed rows by route, then the shared expert's, each in two BF16 parts) and the
+// sums of a split second product with their arrival counts.
 struct DecodeLayout {
   size_t plan, gate_s, h, arrived, sums, total;
   decode::Fc2Shape fc2;
@@ -183,7 +183,7 @@ DecodeLayout decode_layout(const Dims& d) {
   auto take = [&](size_t bytes) { size_t r = o; o = align_up(o + bytes); return r; };
   L.plan = take(sizeof(decode::Plan));
   L.gate_s = take(4 * d.T);
-  L.h = take(2 * d.R * d.I);
+  L.h = take(4 * d.R * d.I);
   L.fc2 = decode::fc2_shape(d.T, d.H, d.I, d.E, d.K);
   L.arrived = take(4 * d.H / (16 * L.fc2.frags));
   L.sums = take(L.fc2.split > 1 ? 4 * d.T * d.H * L.fc2.split : 0);

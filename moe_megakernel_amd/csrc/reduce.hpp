@@ -26,6 +26,7 @@ __device__ __forceinline__ double dpp_d(double v) {
 // The four permutations that fold a row of 16 lanes: lanes xor 1, lanes xor 2, the mirror
 // of 8 lanes and the mirror of 16.
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+constexpr int kDppRor8 = 0x128;   // rotated by 8: lanes xor 8
 
 __device__ __forceinline__ float row16_sum(float v) {
   v += dpp_f<kDppXor1>(v);

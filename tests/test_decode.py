@@ -4,7 +4,8 @@ the stored weights (MXFP8 decoded, activations unquantised).
 Tolerances.  u = 2^-24.  A product of length n is accumulated in FP32 over at most 32 products
 inside a matrix instruction, n / 128 steps and 8 partial sums: (40 + n / 128) u of the sum
 of its magnitudes.  The SwiGLU passes errors of a and b on with factors of at most
-1.1 |b| and |silu(a)| and adds 32 u |h| (exp and reciprocal).  h is rounded to BF16: each term
+1.1 |b| and |silu(a)| and adds 32 u |h| (exp and reciprocal).  h may be rounded to BF16 (it is held
+closer, which test_h_is_not_rounded_to_bf16 checks): each term
 w W h of the output is off by at most 2^-8 of itself, independently, so by
 Hoeffding's inequality their sum stays within 6 sqrt(sum of squares) 2^-8 except once in 10^7
 elements at the largest possible spread (a rounding error's actual spread is 1/sqrt(3) of it).
@@ -448,3 +449,63 @@ def test_two_layers_on_two_streams(gpu_lib):
     torch.cuda.synchronize()
     check(a, Wa)
     check(b, Wb)
+
+
+def reference_in_two_parts(x_bits, top, rw, E, W):
+    """As reference, for an h that is held in two BF16 parts: the upper one leaves at most 2^-8 of h, and
+    the lower one's rounding 2^-8 of that.  (Below 2^-118 the lower part runs out of exponents.)"""
+    out, tol = reference(x_bits, top, rw, E, W)
+    x = torch.from_numpy(O.bf16_decode(x_bits))
+    t_top, t_rw = torch.from_numpy(top), torch.from_numpy(rw).double()
+    mag, sq = torch.zeros_like(out), torch.zeros_like(out)
+
+    def add(t, w, mats):
+        wg, wu, wd = (torch.from_numpy(np.ascontiguousarray(m)) for m in mats)
+        a, b = x[t] @ wg.T, x[t] @ wu.T
+        if W.swiglu_limit > 0:
+            a, b = a.clamp(max=W.swiglu_limit), b.clamp(-W.swiglu_limit, W.swiglu_limit)
+        h = a * torch.sigmoid(a) * b
+        mag.index_add_(0, t, w.abs()[:, None] * (h.abs() @ wd.abs().T))
+        sq.index_add_(0, t, w[:, None] ** 2 * (h ** 2 @ (wd ** 2).T))
+
+    for e in range(E):
+        t, k = (t_top == e).nonzero(as_tuple=True)
+        if t.numel():
+            add(t, t_rw[t, k], W.routed(e))
+    if W.shared is not None:
+        s = torch.ones(x.shape[0], dtype=torch.float64)
+        if W.shared_gate is not None:
+            s = torch.sigmoid(x @ torch.from_numpy(W.shared_gate))
+        add(torch.arange(x.shape[0]), s, W.shared)
+    return out, tol - 6 * H8 * sq.sqrt() + H8 ** 2 * mag
+
+
+PARTS = [
+    dict(T=1, H=256, I=256, E=4, K=2),
+    dict(T=8, H=384, I=640, E=3, K=2, kind="one"),
+    dict(T=13, H=384, I=256, E=3, K=3, gate=True),               # 9 to 16 tokens an expert
+    dict(T=16, H=4224, I=256, E=3, K=2, limit=0.4),              # two row fragments
+    dict(T=24, H=256, I=384, E=4, K=2),
+    dict(T=30, H=512, I=256, E=2, K=2, kind="short"),            # 17 to 32
+    dict(T=64, H=256, I=1024, E=2, K=1, limit=0.4),
+    dict(T=64, H=4224, I=256, E=4, K=3),                         # more than 32, two row fragments
+    dict(T=64, H=4224, I=384, E=5, K=2, kind="one", shared=False),
+    dict(T=64, H=7168, I=128, E=40, K=4, kind="invalid"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("routed", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("i", range(len(PARTS)))
+def test_h_is_not_rounded_to_bf16(gpu_lib, i, routed):
+    """The output is off by FP32 sums and its own rounding only."""
+    c = dict(PARTS[i])
+    kw = dict(shared=c.pop("shared", True), shared_gate=c.pop("gate", False), swiglu_limit=c.pop("limit", 0.0))
+    dp, W = problem(routed=routed, seed=70 + i, **c, **kw)
+    run(dp)
+    torch.cuda.synchronize()
+    top = clean_table(dp.np_top, c["E"])
+    ref, tol = reference_in_two_parts(dp.np_x, top, np.nan_to_num(dp.np_rw), c["E"], W)
+    tol = tol + H8 * (ref.abs() + tol)
+    off = (dp.out.cpu().double() - ref).abs()
+    assert bool((off <= tol).all()), (int((off > tol).sum()), float((off / tol.clamp(min=1e-30)).max()))
