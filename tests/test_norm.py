@@ -495,3 +495,38 @@ def test_constant_rows_beside_ordinary_ones(gpu_lib, N):
     assert torch.equal(y[~flat], alone[~flat]) and torch.equal(st[~flat], stats[~flat])
     flat[5] = False
     assert torch.equal(y[flat], b[None].expand(int(flat.sum()), N))
+
+
+LAYOUTS = [
+    # R, N, pad, offset: rows of whole 16-byte pieces that are 4-byte aligned only (BF16)
+    (1, 8, 2, 2), (37, 64, 2, 0), (130, 128, 6, 2), (600, 256, 2, 2), (70, 384, 2, 4), (65, 1032, 2, 2), (300, 4096, 2, 2),
+    (5, 7168, 6, 2),
+    # more than 8192 columns: contiguous, 4-byte aligned, by elements
+    (3, 8200, 0, 0), (300, 8208, 0, 0), (5, 12304, 0, 0), (4, 16384, 0, 0), (4, 12304, 2, 2), (6, 16384, 2, 0),
+    (3, 8201, 0, 0), (270, 9001, 1, 0), (3, 16383, 3, 1), (4, 16384, 1, 1),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dtype,pdtype", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("i", range(len(LAYOUTS)))
+def test_layouts_match_formula(gpu_lib, i, dtype, pdtype, kind):
+    dev, (R, N, pad, offset) = "cuda", LAYOUTS[i]
+    x, w, b, dy, gs = make(R, N, dtype, pdtype, seed=200 + i)
+    n = mk.Norm(N, kind=kind, dtype=dtype, param_dtype=pdtype)
+    y, stats, _ = _run_forward(n, x, w, b, None, kind, pad, offset)
+    check_forward(x, w, b, y, stats, kind)
+    y, stats, s = _run_forward(n, x, w, None, dy, kind, pad, offset)
+    assert torch.equal(s, (x.float() + dy.float()).to(dtype))
+    check_forward(s, w, None, y, stats, kind)
+    _, _, mu, rstd = ref_forward(x, w, None, kind, 1e-5)
+    stats = torch.cat([mu, rstd], 1).float()
+    xv, dyv, gsv = (padded(t.to(dev), pad, offset)[0] for t in (x, dy, gs))
+    for gsum in (None, gs):
+        dxv, dxb = padded(torch.zeros(R, N, dtype=dtype, device=dev), pad, offset)
+        dw, db = (torch.full((N,), float("nan"), device=dev) for _ in range(2))
+        n.backward(dyv, xv, w.to(dev), stats.to(dev), dxv, dw, db, grad_sum=None if gsum is None else gsv, overwrite=True)
+        torch.cuda.synchronize()
+        assert untouched(dxv, dxb, offset)
+        check_backward(dy, x, w, stats, kind, gsum, dxv.cpu(), dw.cpu(), db.cpu())
