@@ -29,6 +29,13 @@ __device__ __forceinline__ uint32_t f2bf(float f) { return pack_bf2(f, 0.0f) & 0
 __device__ __forceinline__ float lo_bf(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_bf(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Orders this wave's LDS accesses for the compiler, which would otherwise take a value a lane
+// has just stored for granted; the hardware runs them in order.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // logistic function with the hardware reciprocal (1 ulp) instead of an IEEE division
 __device__ __forceinline__ float sigmoidf_(float a) { return __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
 

@@ -255,12 +255,6 @@ __device__ __forceinline__ void dot_steps(const Turn& t, const uint8_t* const (&
   }
 }
 
-// Orders a wave's LDS accesses for the compiler; the hardware runs them in order.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 __device__ __forceinline__ float swiglu(float a, float b, float L) {
   if (L > 0.0f) {   // comparisons that keep a NaN
     a = a > L ? L : a;

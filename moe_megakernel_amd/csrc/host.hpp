@@ -16,6 +16,10 @@ constexpr size_t kAlign = 256;
 inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// at a multiple of its elements' size (MOE_BF16 or MOE_FP32)
+inline bool elem_aligned(const void* p, int32_t dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == MOE_BF16 ? 1u : 3u)) == 0;
+}
 
 // ---------------------------------------------------------------- kernel timer
 struct TimedLaunch {
