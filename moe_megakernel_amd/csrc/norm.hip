@@ -19,8 +19,9 @@
 // Bound by memory from some thousand rows on: RMS norm with a residual, 8192 x 7168 BF16, 89 us
 // (5.3 TB/s; a large copy runs at 5.0); layer norm's backward, 4096 x 4096 BF16, 25 us and 3.6 for
 // the second kernel (20 at the copy's rate; the partial rows add a sixth to the bytes).  FP32
-// rows that are no whole pieces, backward of 1023 x 2055: 15 us (7), bound by the number of loads.
-// Below that by the launch: one row of 4096 takes 3 us on the GPU.
+// rows that are no whole pieces, backward of 1023 x 2055: 15 us (7), single elements, a fifth of the
+// threads without one and a third of the row places empty in the second trip.  Below that by the
+// launch: one row of 4096 takes 3 us on the GPU.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
