@@ -522,8 +522,8 @@ class Norm:
         self.p = moe_norm_problem(1 << 30, cols, code, _moe_dtype(self.dtype, "Norm"),
                                   _moe_dtype(self.param_dtype, "Norm"), _moe_dtype(self.grad_dtype, "Norm"), 0, eps)
         self.ws_bytes = moe_norm_workspace_bytes(self.p)
-        if self.ws_bytes == 0:
-            raise MoeError(MOE_ERR_SHAPE if kind in ("layer", "rms") else MOE_ERR_UNSUPPORTED, "Norm")
+        if self.ws_bytes == 0:      # refused: a call without arguments says why
+            raise MoeError(moe_norm_forward(self.p, None, None, None, None, None, None, None, None), "Norm")
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
         self.cols, q = cols, self.p
         self._problems = _Problems(lambda rows, flags: moe_norm_problem(
@@ -584,8 +584,8 @@ class DecodeLayer:
         import torch
         self.p = moe_problem.from_buffer_copy(p)
         self.ws_bytes = moe_decode_workspace_bytes(self.p)
-        if self.ws_bytes == 0:
-            raise MoeError(MOE_ERR_UNSUPPORTED if 0 <= p.tokens <= MOE_DECODE_MAX_TOKENS else MOE_ERR_SHAPE,
+        if self.ws_bytes == 0:      # refused: a call without arguments says why
+            raise MoeError(moe_forward_decode(self.p, None, None, None, moe_weights(), None, None, 0, None),
                            "moe_decode_workspace_bytes")
         # zeros: the status word before the first call
         self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=device)

@@ -509,3 +509,14 @@ def test_h_is_not_rounded_to_bf16(gpu_lib, i, routed):
     tol = tol + H8 * (ref.abs() + tol)
     off = (dp.out.cpu().double() - ref).abs()
     assert bool((off <= tol).all()), (int((off > tol).sum()), float((off / tol.clamp(min=1e-30)).max()))
+
+
+def test_layer_names_the_status_of_a_refused_problem():
+    """The same status as moe_forward_decode returns for the problem."""
+    for kw, status in ((dict(inter=mk.MOE_DECODE_MAX_INTERMEDIATE + 128), mk.MOE_ERR_SHAPE), (dict(hidden=130), mk.MOE_ERR_SHAPE),
+                       (dict(tokens=-1), mk.MOE_ERR_SHAPE), (dict(topk=9, experts=16), mk.MOE_ERR_SHAPE),
+                       (dict(dt=mk.MOE_FP32), mk.MOE_ERR_DTYPE), (dict(L=-1.0), mk.MOE_ERR_UNSUPPORTED),
+                       (dict(flags=TABLE | mk.MOE_FLAG_RECOMPUTE), mk.MOE_ERR_UNSUPPORTED)):
+        with pytest.raises(mk.MoeError) as ei:
+            mk.DecodeLayer(_p(**kw), device="cpu")
+        assert ei.value.status == status, kw

@@ -530,3 +530,12 @@ def test_layouts_match_formula(gpu_lib, i, dtype, pdtype, kind):
         torch.cuda.synchronize()
         assert untouched(dxv, dxb, offset)
         check_backward(dy, x, w, stats, kind, gsum, dxv.cpu(), dw.cpu(), db.cpu())
+
+
+def test_norm_names_the_status_of_refused_options():
+    """The same status as moe_norm_forward returns for them."""
+    for kw, status in ((dict(eps=-1.0), mk.MOE_ERR_UNSUPPORTED), (dict(eps=float("nan")), mk.MOE_ERR_UNSUPPORTED),
+                       (dict(cols=mk.MOE_NORM_MAX_COLS + 1), mk.MOE_ERR_SHAPE), (dict(cols=-1), mk.MOE_ERR_SHAPE)):
+        with pytest.raises(mk.MoeError) as ei:
+            mk.Norm(**{"cols": 64, "device": "cpu", **kw})
+        assert ei.value.status == status, kw
