@@ -460,7 +460,16 @@ def _call(where, device, fn, *args):
         raise MoeError(st, where)
 
 
-class Router:
+class _Fixed:
+    """An operator whose options are fixed at construction."""
+
+    @property
+    def p(self):
+        """A copy of the problem struct."""
+        return type(self._p).from_buffer_copy(self._p)
+
+
+class Router(_Fixed):
     """The router's decision on logits [tokens, experts] (torch tensors, FP32 or BF16): the
     table moe_forward_topk and DecodeLayer take, and the gradient back to the logits.
     Holds options only; every buffer is the caller's."""
@@ -469,12 +478,12 @@ class Router:
         import torch
         self.dtype = dtype or torch.float32
         kind = {"softmax": MOE_ROUTER_SOFTMAX, "sigmoid": MOE_ROUTER_SIGMOID}.get(score, 0)
-        self.p = moe_router_problem(0, experts, topk, kind, _moe_dtype(self.dtype, "Router"),
-                                    MOE_ROUTER_NORMALIZE if normalize else 0, scale, experts)
-        st = moe_router_forward(self.p, None, None, None, None, None)    # no tokens: checks the options
+        self._p = moe_router_problem(0, experts, topk, kind, _moe_dtype(self.dtype, "Router"),
+                                     MOE_ROUTER_NORMALIZE if normalize else 0, scale, experts)
+        st = moe_router_forward(self._p, None, None, None, None, None)    # no tokens: checks the options
         if st != MOE_OK:
             raise MoeError(st, "Router")
-        self.experts, self.topk, q = experts, topk, self.p
+        self.experts, self.topk, q = experts, topk, self._p
         self._problems = _Problems(lambda T, ld: moe_router_problem(
             T, q.experts, q.topk, q.score, q.logits_dtype, q.flags, q.scale, ld))
 
@@ -508,7 +517,7 @@ class Router:
         return grad_logits
 
 
-class Norm:
+class Norm(_Fixed):
     """Layer norm (kind "layer") or RMS norm ("rms") of rows [rows, cols].  Holds the options
     and the backward's workspace (its size covers any number of rows); two backward calls
     of one Norm must not overlap on the GPU."""
@@ -519,13 +528,13 @@ class Norm:
         self.param_dtype = param_dtype or self.dtype
         self.grad_dtype = grad_dtype or torch.float32
         code = {"layer": MOE_NORM_LAYER, "rms": MOE_NORM_RMS}.get(kind, 0)
-        self.p = moe_norm_problem(1 << 30, cols, code, _moe_dtype(self.dtype, "Norm"),
-                                  _moe_dtype(self.param_dtype, "Norm"), _moe_dtype(self.grad_dtype, "Norm"), 0, eps)
-        self.ws_bytes = moe_norm_workspace_bytes(self.p)
+        self._p = moe_norm_problem(1 << 30, cols, code, _moe_dtype(self.dtype, "Norm"),
+                                   _moe_dtype(self.param_dtype, "Norm"), _moe_dtype(self.grad_dtype, "Norm"), 0, eps)
+        self.ws_bytes = moe_norm_workspace_bytes(self._p)
         if self.ws_bytes == 0:      # refused: a call without arguments says why
-            raise MoeError(moe_norm_forward(self.p, None, None, None, None, None, None, None, None), "Norm")
+            raise MoeError(moe_norm_forward(self._p, None, None, None, None, None, None, None, None), "Norm")
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
-        self.cols, q = cols, self.p
+        self.cols, q = cols, self._p
         self._problems = _Problems(lambda rows, flags: moe_norm_problem(
             rows, q.cols, q.kind, q.dtype, q.param_dtype, q.grad_dtype, flags, q.eps))
 
@@ -575,23 +584,23 @@ class Norm:
         return grad_x
 
 
-class DecodeLayer:
+class DecodeLayer(_Fixed):
     """The layer's forward for a few tokens.  Holds the problem (its `tokens` is the largest
     batch; a call takes any number up to it) and the workspace; two calls of one DecodeLayer
     must not overlap on the GPU."""
 
     def __init__(self, p: moe_problem, device="cuda"):
         import torch
-        self.p = moe_problem.from_buffer_copy(p)
-        self.ws_bytes = moe_decode_workspace_bytes(self.p)
+        self._p = moe_problem.from_buffer_copy(p)
+        self.ws_bytes = moe_decode_workspace_bytes(self._p)
         if self.ws_bytes == 0:      # refused: a call without arguments says why
-            raise MoeError(moe_forward_decode(self.p, None, None, None, moe_weights(), None, None, 0, None),
+            raise MoeError(moe_forward_decode(self._p, None, None, None, moe_weights(), None, None, 0, None),
                            "moe_decode_workspace_bytes")
         # zeros: the status word before the first call
         self.workspace = torch.zeros(self.ws_bytes, dtype=torch.uint8, device=device)
 
         def problem_of(tokens):
-            q = moe_problem.from_buffer_copy(self.p)
+            q = moe_problem.from_buffer_copy(self._p)
             q.tokens = tokens
             return q
         self.hidden, self.topk = p.hidden, p.topk
@@ -601,7 +610,7 @@ class DecodeLayer:
         import torch
         where = "moe_forward_decode"
         dev, T = _device(where, hidden), hidden.shape[0]
-        if T > self.p.tokens:
+        if T > self._p.tokens:
             raise MoeError(MOE_ERR_SHAPE, where)
         rows, table = (T, self.hidden), (T, self.topk)
         _check(where, dev, hidden, torch.bfloat16, rows)

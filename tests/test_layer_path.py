@@ -128,3 +128,16 @@ def test_serving_step_captured(gpu_lib):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((s, hidden, top, rw, out), want)), i
         assert int(layer.status_word()) == 0
+
+
+def test_options_are_fixed_at_construction():
+    """What a caller writes into `p` of an operator changes no call, of a size met before or not."""
+    def decode():
+        return mk.DecodeLayer(mk.problem(8, 256, 128, 8, 2, flags=mk.MOE_FLAG_TOPK_ROUTING), device="cpu")
+
+    for op, first, later, field in ((decode(), (2,), (3,), "swiglu_limit"), (mk.Norm(64, device="cpu"), (2, 0), (3, 0), "eps"),
+                                    (mk.Router(8, 2), (2, 8), (3, 8), "scale")):
+        before = getattr(op._problems[first], field)
+        setattr(op.p, field, 7.0)
+        assert getattr(op._problems[first], field) == getattr(op._problems[later], field) == before
+        assert getattr(op.p, field) == before
