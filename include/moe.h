@@ -59,7 +59,8 @@ typedef enum {
                                   or listed twice in one row (moe_forward_topk)            */
 } moe_status;
 
-typedef enum { MOE_BF16 = 1, MOE_FP32 = 2, MOE_MXFP8_E4M3 = 3 } moe_dtype;
+/* MOE_MXINT8: 8-bit integers in blocks of 32 (moe_checkpoint_store). */
+typedef enum { MOE_BF16 = 1, MOE_FP32 = 2, MOE_MXFP8_E4M3 = 3, MOE_MXINT8 = 4 } moe_dtype;
 
 /* Set: the shared expert is fused into the same launches (PR #6572, Summary: the
  * backend runs dispatch, routed and shared experts, and combine).  Clear: routed-only
@@ -427,6 +428,94 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, 
                              const void* weight, const float* stats, const moe_rows* grad_sum,
                              const moe_rows* grad_x, void* grad_weight, void* grad_bias, void* workspace,
                              size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------- activation checkpoints
+ * Rows of values kept in 8 bits between a forward and its backward: blocks of 32 along a row
+ * (the last may be short), signed 8-bit codes and one power of two a block (MXINT8 of the OCP
+ * microscaling formats):
+ *   value = code 2^(s - 133), s the smallest byte in [0, 254] for which the block's largest
+ *   magnitude is at most 127 steps; code = value / step to nearest, ties to even
+ * so a value is off by at most half a step, 2^-7 of the block's largest.  Values above 127.5
+ * 2^121 are stored as 127 2^121, parts of values below 2^-133 are dropped.  A block that holds an infinity or NaN has s = 255 and
+ * loads as NaN throughout.  Loading into BF16 is exact. */
+typedef struct {
+  int64_t rows;          /* in [0, 2^31]                                                  */
+  int64_t cols;          /* in [1, MOE_CHECKPOINT_MAX_COLS]                               */
+  int32_t dtype;         /* MOE_BF16 or MOE_FP32, of the values                           */
+} moe_checkpoint_problem;
+#define MOE_CHECKPOINT_MAX_COLS (1 << 24)
+
+/*  x       [rows][cols], any element-aligned base and any ld >= cols
+ *  codes   int8 [rows][cols], written (store) or read (load)
+ *  scales  uint8 [rows][ceil(cols / 32)]
+ * Buffers must not overlap.  Rows of whole 16-byte pieces at 16-byte alignment move in those. */
+moe_status moe_checkpoint_store(const moe_checkpoint_problem* p, const moe_rows* x, void* codes, void* scales,
+                                void* stream);
+moe_status moe_checkpoint_load(const moe_checkpoint_problem* p, const void* codes, const void* scales,
+                               const moe_rows* x, void* stream);
+
+/* ------------------------------------------------------------------- gated feed-forward block
+ * The dense block of a layer without experts, and the shared expert of a caller that runs it
+ * itself (routed-only mode), forward and backward:
+ *   a = x gate^T, b = x up^T, h = act(a) b, out = h down^T
+ *   act(a) = a / (1 + e^-a) (MOE_FFN_SILU) or a / (1 + e^-z), z = 2 sqrt(2 / pi) (a + 0.044715 a^3)
+ *   (MOE_FFN_GELU, the tanh form)
+ * x, out and the weights are BF16; sums are FP32; h, and in the backward da, db and h again,
+ * are rounded to BF16 once each as operands of the next product, outputs once.
+ * What a training forward keeps (`saved`) is a and b in BF16, or a, b and x in 8 bits
+ * (MOE_MXINT8, as moe_checkpoint_store writes them; a and b from their FP32 sums); the backward takes
+ * the gradient at the values kept. */
+typedef enum { MOE_FFN_SILU = 1, MOE_FFN_GELU = 2 } moe_ffn_activation;
+/* Set: the backward overwrites the weight gradients instead of accumulating. */
+#define MOE_FFN_OVERWRITE_GRADS 1u
+typedef struct {
+  int64_t tokens;        /* T in [0, 2^24]                                                */
+  int64_t hidden;        /* H in [64, 2^17], multiple of 64                               */
+  int64_t intermediate;  /* I in [64, 2^17], multiple of 64                               */
+  int32_t activation;    /* moe_ffn_activation                                            */
+  int32_t saved_dtype;   /* 0 (nothing kept, forward only), MOE_BF16 or MOE_MXINT8        */
+  int32_t grad_dtype;    /* MOE_FP32 or MOE_BF16: the weight gradients                    */
+  uint32_t flags;        /* MOE_FFN_OVERWRITE_GRADS or 0                                  */
+} moe_ffn_problem;
+/* T (H + 2 I) is at most 2^38 as well (a launch holds 2^32 threads; MOE_ERR_SHAPE above). */
+
+/* Byte offsets inside `saved`: ab [T][2I] (a at column j, b at I + j) in BF16, or int8 codes with
+ * their scale bytes ab_scales [T][2I / 32], and x codes [T][H] with x_scales [T][H / 32] (the last
+ * three are 0 with MOE_BF16).  `saved` may be copied elsewhere. */
+typedef struct {
+  size_t ab, ab_scales, x, x_scales;
+} moe_ffn_saved_layout;
+
+/* Bytes of `saved` (0 on invalid input and with saved_dtype 0) and of the workspace of the forward
+ * (for_backward = 0) or backward (0 on invalid input).  Neither falls as tokens grow: what
+ * suffices for some tokens suffices for fewer. */
+size_t moe_ffn_saved_bytes(const moe_ffn_problem* p);
+size_t moe_ffn_workspace_bytes(const moe_ffn_problem* p, int for_backward);
+moe_status moe_ffn_saved_view(const moe_ffn_problem* p, moe_ffn_saved_layout* layout);
+
+/*  x [T][H], gate and up [I][H], down [H][I], out [T][H]: BF16, 16-byte aligned, ld a multiple of 8
+ *    (gate and up may be row views of one tensor).  With MOE_MXINT8 x may not be out.
+ *  saved       moe_ffn_saved_bytes(p), 16-byte aligned, written; NULL with saved_dtype 0
+ *  workspace   moe_ffn_workspace_bytes(p, 0), 16-byte aligned
+ * No output may overlap an input.  With no tokens nothing is enqueued. */
+moe_status moe_ffn_forward(const moe_ffn_problem* p, const moe_rows* x, const moe_rows* gate, const moe_rows* up,
+                           const moe_rows* down, const moe_rows* out, void* saved, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Backward of sum(grad_out * out).
+ *  x           the forward's, with MOE_BF16; NULL with MOE_MXINT8, whose `saved` holds it
+ *  saved       the forward's
+ *  grad_x      BF16 [T][H], overwritten; NULL: not computed
+ *  grad_gate, grad_up [I][H], grad_down [H][I]  FP32 or BF16 (16-byte aligned, ld a multiple of 4 or 8),
+ *              accumulated or overwritten (also with no tokens); a BF16 gradient with the rounding of a
+ *              BF16 main_grad (the call's contribution is rounded before it is added).  NULL: not
+ *              computed (grad_gate and grad_up both or neither).  At least one output is needed
+ *  workspace   moe_ffn_workspace_bytes(p, 1), 16-byte aligned
+ * Sums run in a fixed order: the same call gives the same bits. */
+moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, const moe_rows* x,
+                            const moe_rows* gate, const moe_rows* up, const moe_rows* down, const void* saved,
+                            const moe_rows* grad_x, const moe_rows* grad_gate, const moe_rows* grad_up,
+                            const moe_rows* grad_down, void* workspace, size_t workspace_bytes, void* stream);
 
 /* A static description of a status code. */
 const char* moe_status_str(moe_status s);

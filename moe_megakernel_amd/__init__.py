@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe_mi355x.so")
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_LAYOUT = 0, 1, 2, 3, 4
 MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_ROUTE_OVERFLOW, MOE_ERR_HIP = 5, 6, 7, 8
 MOE_ERR_ROUTE_INVALID = 9
-MOE_BF16, MOE_FP32, MOE_MXFP8_E4M3 = 1, 2, 3
+MOE_BF16, MOE_FP32, MOE_MXFP8_E4M3, MOE_MXINT8 = 1, 2, 3, 4
 MOE_FLAG_HAS_SHARED = 1
 MOE_FLAG_RECOMPUTE = 2
 MOE_FLAG_TOPK_ROUTING = 4
@@ -29,12 +29,17 @@ MOE_ROUTER_NORMALIZE = 1
 MOE_NORM_LAYER, MOE_NORM_RMS = 1, 2
 MOE_NORM_OVERWRITE_GRADS = 1
 MOE_NORM_MAX_COLS = 16384
+MOE_CHECKPOINT_MAX_COLS = 1 << 24
+MOE_FFN_SILU, MOE_FFN_GELU = 1, 2
+MOE_FFN_OVERWRITE_GRADS = 1
 
 EXPORTED = ("moe_saved_bytes", "moe_workspace_bytes", "moe_saved_view", "moe_forward",
             "moe_forward_topk", "moe_forward_noalloc", "moe_backward", "moe_status_str",
             "moe_kernel_timer_enable", "moe_kernel_timer_read", "moe_mx_staging_view",
             "moe_decode_workspace_bytes", "moe_forward_decode", "moe_router_forward", "moe_router_backward",
-            "moe_norm_forward", "moe_norm_backward", "moe_norm_workspace_bytes")
+            "moe_norm_forward", "moe_norm_backward", "moe_norm_workspace_bytes", "moe_checkpoint_store",
+            "moe_checkpoint_load", "moe_ffn_saved_bytes", "moe_ffn_workspace_bytes", "moe_ffn_saved_view",
+            "moe_ffn_forward", "moe_ffn_backward")
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 MOE_DECODE_MAX_TOKENS = 64
 MOE_DECODE_MAX_INTERMEDIATE = 65536
@@ -92,6 +97,19 @@ class moe_norm_problem(C.Structure):
     _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("kind", C.c_int32), ("dtype", C.c_int32),
                 ("param_dtype", C.c_int32), ("grad_dtype", C.c_int32), ("flags", C.c_uint32),
                 ("eps", C.c_float)]
+
+
+class moe_checkpoint_problem(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("dtype", C.c_int32)]
+
+
+class moe_ffn_problem(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("hidden", C.c_int64), ("intermediate", C.c_int64), ("activation", C.c_int32),
+                ("saved_dtype", C.c_int32), ("grad_dtype", C.c_int32), ("flags", C.c_uint32)]
+
+
+class moe_ffn_saved_layout(C.Structure):
+    _fields_ = [(n, C.c_size_t) for n in ("ab", "ab_scales", "x", "x_scales")]
 
 
 class moe_rows(C.Structure):
@@ -155,6 +173,22 @@ def load(path: str | None = None):
     lib.moe_norm_backward.restype = C.c_int
     lib.moe_norm_workspace_bytes.argtypes = [P(moe_norm_problem)]
     lib.moe_norm_workspace_bytes.restype = C.c_size_t
+    lib.moe_checkpoint_store.argtypes = [P(moe_checkpoint_problem), P(moe_rows), C.c_void_p, C.c_void_p, C.c_void_p]
+    lib.moe_checkpoint_store.restype = C.c_int
+    lib.moe_checkpoint_load.argtypes = [P(moe_checkpoint_problem), C.c_void_p, C.c_void_p, P(moe_rows), C.c_void_p]
+    lib.moe_checkpoint_load.restype = C.c_int
+    lib.moe_ffn_saved_bytes.argtypes = [P(moe_ffn_problem)]
+    lib.moe_ffn_saved_bytes.restype = C.c_size_t
+    lib.moe_ffn_workspace_bytes.argtypes = [P(moe_ffn_problem), C.c_int]
+    lib.moe_ffn_workspace_bytes.restype = C.c_size_t
+    lib.moe_ffn_saved_view.argtypes = [P(moe_ffn_problem), P(moe_ffn_saved_layout)]
+    lib.moe_ffn_saved_view.restype = C.c_int
+    lib.moe_ffn_forward.argtypes = [P(moe_ffn_problem)] + [P(moe_rows)] * 5 + [C.c_void_p, C.c_void_p, C.c_size_t,
+                                                                             C.c_void_p]
+    lib.moe_ffn_forward.restype = C.c_int
+    lib.moe_ffn_backward.argtypes = [P(moe_ffn_problem)] + [P(moe_rows)] * 5 + [C.c_void_p] + [P(moe_rows)] * 4 + [
+        C.c_void_p, C.c_size_t, C.c_void_p]
+    lib.moe_ffn_backward.restype = C.c_int
     if path is None:
         _lib = lib
     return lib
@@ -264,6 +298,48 @@ def moe_norm_backward(p, grad_y, x, weight, stats, grad_sum, grad_x, grad_weight
     device addresses; returns the status."""
     return load().moe_norm_backward(C.byref(p), _ref(grad_y), _ref(x), weight, stats, _ref(grad_sum), _ref(grad_x),
                                     grad_weight, grad_bias, workspace, workspace_bytes, stream)
+
+
+def moe_checkpoint_store(p, x, codes, scales, stream) -> int:
+    """Raw call: x is a moe_rows (or None), the rest integer device addresses; returns the status."""
+    return load().moe_checkpoint_store(C.byref(p), _ref(x), codes, scales, stream)
+
+
+def moe_checkpoint_load(p, codes, scales, x, stream) -> int:
+    """Raw call: x is a moe_rows (or None), the rest integer device addresses; returns the status."""
+    return load().moe_checkpoint_load(C.byref(p), codes, scales, _ref(x), stream)
+
+
+def moe_ffn_saved_bytes(p: moe_ffn_problem) -> int:
+    return int(load().moe_ffn_saved_bytes(C.byref(p)))
+
+
+def moe_ffn_workspace_bytes(p: moe_ffn_problem, for_backward: bool) -> int:
+    return int(load().moe_ffn_workspace_bytes(C.byref(p), int(bool(for_backward))))
+
+
+def moe_ffn_saved_view(p: moe_ffn_problem) -> moe_ffn_saved_layout:
+    out = moe_ffn_saved_layout()
+    st = load().moe_ffn_saved_view(C.byref(p), C.byref(out))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_ffn_saved_view")
+    return out
+
+
+def moe_ffn_forward(p, x, gate, up, down, out, saved, workspace, workspace_bytes, stream) -> int:
+    """Raw call: x, gate, up, down and out are moe_rows (or None), the rest integer device
+    addresses; returns the status."""
+    return load().moe_ffn_forward(C.byref(p), _ref(x), _ref(gate), _ref(up), _ref(down), _ref(out), saved, workspace,
+                                  workspace_bytes, stream)
+
+
+def moe_ffn_backward(p, grad_out, x, gate, up, down, saved, grad_x, grad_gate, grad_up, grad_down, workspace,
+                     workspace_bytes, stream) -> int:
+    """Raw call: the matrices are moe_rows (or None), the rest integer device addresses; returns
+    the status."""
+    return load().moe_ffn_backward(C.byref(p), _ref(grad_out), _ref(x), _ref(gate), _ref(up), _ref(down), saved,
+                                   _ref(grad_x), _ref(grad_gate), _ref(grad_up), _ref(grad_down), workspace,
+                                   workspace_bytes, stream)
 
 
 def moe_kernel_timer_enable(on: bool) -> None:
@@ -628,3 +704,123 @@ class DecodeLayer(_Fixed):
         MOE_ERR_ROUTE_INVALID."""
         import torch
         return self.workspace[:4].view(torch.int32)
+
+
+class Checkpoint(_Fixed):
+    """Rows of BF16 or FP32 values to and from 8-bit checkpoints (MXINT8, blocks of 32 along a
+    row).  Holds the type only; every buffer is the caller's."""
+
+    def __init__(self, dtype=None):
+        import torch
+        self.dtype = dtype or torch.bfloat16
+        self._p = moe_checkpoint_problem(0, 1, _moe_dtype(self.dtype, "Checkpoint"))
+        q = self._p
+        self._problems = _Problems(lambda rows, cols: moe_checkpoint_problem(rows, cols, q.dtype))
+
+    def _buffers(self, where, x, codes, scales):
+        import torch
+        dev, (R, N) = _device(where, x), x.shape
+        if N == 0:
+            raise MoeError(MOE_ERR_SHAPE, where)
+        rows = moe_rows(x.data_ptr(), _check_rows(where, dev, x, self.dtype, (R, N)))
+        _check(where, dev, codes, torch.int8, (R, N))
+        _check(where, dev, scales, torch.uint8, (R, (N + 31) // 32))
+        return dev, self._problems[R, N], rows
+
+    def store(self, x, codes, scales):
+        """Writes codes (int8 [rows, cols]) and scales (uint8 [rows, ceil(cols / 32)]) of x."""
+        where = "moe_checkpoint_store"
+        dev, p, rows = self._buffers(where, x, codes, scales)
+        _call(where, dev, load().moe_checkpoint_store, p, rows, codes.data_ptr(), scales.data_ptr())
+        return codes, scales
+
+    def load(self, codes, scales, x):
+        """Writes the values that codes and scales stand for into x."""
+        where = "moe_checkpoint_load"
+        dev, p, rows = self._buffers(where, x, codes, scales)
+        _call(where, dev, load().moe_checkpoint_load, p, codes.data_ptr(), scales.data_ptr(), rows)
+        return x
+
+
+class FeedForward(_Fixed):
+    """The gated feed-forward block out = (act(x gate^T) * (x up^T)) down^T on BF16 tensors, for up
+    to `tokens` rows a call.  activation: "silu" or "gelu" (tanh form).  saved: what a training
+    forward keeps for the backward, "bf16" or "int8" (x too, in 8 bits), or "none".  Holds the
+    options and one workspace; two calls of one FeedForward must not overlap on the GPU."""
+
+    def __init__(self, hidden, intermediate, tokens, activation="silu", saved="none", grad_dtype=None, device="cuda"):
+        import torch
+        self.grad_dtype = grad_dtype or torch.float32
+        act = {"silu": MOE_FFN_SILU, "gelu": MOE_FFN_GELU}.get(activation, 0)
+        keep = {"none": 0, "bf16": MOE_BF16, "int8": MOE_MXINT8}.get(saved, -1)
+        self._p = moe_ffn_problem(tokens, hidden, intermediate, act, keep, _moe_dtype(self.grad_dtype, "FeedForward"), 0)
+        self.ws_bytes = max(moe_ffn_workspace_bytes(self._p, False), moe_ffn_workspace_bytes(self._p, True))
+        if self.ws_bytes == 0:      # refused: a call without arguments says why
+            raise MoeError(moe_ffn_forward(self._p, None, None, None, None, None, None, None, 0, None), "FeedForward")
+        self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=device)
+        self.hidden, self.intermediate, self.tokens, self.saved, q = hidden, intermediate, tokens, saved, self._p
+        self._problems = _Problems(lambda T, flags: moe_ffn_problem(
+            T, q.hidden, q.intermediate, q.activation, q.saved_dtype, q.grad_dtype, flags))
+
+    def saved_bytes(self, tokens):
+        """Bytes of the uint8 tensor that a forward of so many tokens fills for its backward."""
+        return moe_ffn_saved_bytes(self._problems[tokens, 0])
+
+    def saved_views(self, saved, tokens):
+        """Views of `saved`: "ab" [tokens, 2 intermediate] (a, then b) and with "int8" also
+        "ab_scales", "x" and "x_scales"."""
+        import torch
+        L, T, H, I = moe_ffn_saved_view(self._problems[tokens, 0]), tokens, self.hidden, self.intermediate
+
+        def view(off, cols, dt):
+            n = T * cols * dt.itemsize
+            return saved[off:off + n].view(dt).view(T, cols)
+        if self.saved == "bf16":
+            return {"ab": view(L.ab, 2 * I, torch.bfloat16)}
+        return {"ab": view(L.ab, 2 * I, torch.int8), "ab_scales": view(L.ab_scales, 2 * I // 32, torch.uint8),
+                "x": view(L.x, H, torch.int8), "x_scales": view(L.x_scales, H // 32, torch.uint8)}
+
+    def _common(self, where, x, gate, up, down, saved, flags=0):
+        import torch
+        dev, T, H, I, bf = _device(where, x), x.shape[0], self.hidden, self.intermediate, torch.bfloat16
+        if T > self.tokens:
+            raise MoeError(MOE_ERR_SHAPE, where)
+        ms = [moe_rows(t.data_ptr() if t is not None else 0, _check_rows(where, dev, t, bf, shape))
+              for t, shape in ((x, (T, H)), (gate, (I, H)), (up, (I, H)), (down, (H, I)))]
+        p = self._problems[T, flags]
+        if saved is not None:
+            if saved.dtype is not torch.uint8 or saved.numel() < moe_ffn_saved_bytes(p):
+                raise MoeError(MOE_ERR_WORKSPACE, where)
+            if saved.get_device() != dev or not saved.is_contiguous():
+                raise MoeError(MOE_ERR_LAYOUT, where)
+        if self.workspace.get_device() != dev:
+            raise MoeError(MOE_ERR_WORKSPACE, where)
+        return dev, T, p, ms
+
+    def forward(self, x, gate, up, down, out, saved=None):
+        """Writes out, and with saved="bf16" or "int8" the tensor `saved` (saved_bytes(tokens) bytes)."""
+        import torch
+        where = "moe_ffn_forward"
+        dev, T, p, ms = self._common(where, x, gate, up, down, saved)
+        ro = moe_rows(out.data_ptr() if out is not None else 0,
+                      _check_rows(where, dev, out, torch.bfloat16, (T, self.hidden)))
+        _call(where, dev, load().moe_ffn_forward, p, *ms, ro, _ptr(saved) or None, self.workspace.data_ptr(),
+              self.ws_bytes)
+        return out
+
+    def backward(self, grad_out, x, gate, up, down, saved, grad_x=None, grad_gate=None, grad_up=None, grad_down=None,
+                 overwrite=False):
+        """x: the forward's (None with saved="int8").  The gradients given are computed: grad_x is
+        overwritten, those of the weights (grad_dtype) are accumulated, or overwritten."""
+        import torch
+        where = "moe_ffn_backward"
+        H, I, bf = self.hidden, self.intermediate, torch.bfloat16
+        dev, T, p, ms = self._common(where, grad_out, gate, up, down, saved, MOE_FFN_OVERWRITE_GRADS if overwrite else 0)
+        opt = lambda t, dt, shape: None if t is None else moe_rows(t.data_ptr(), _check_rows(where, dev, t, dt, shape))
+        rx = opt(x, bf, (T, H))
+        gx, gg, gu, gd = (opt(t, dt, shape) for t, dt, shape in (
+            (grad_x, bf, (T, H)), (grad_gate, self.grad_dtype, (I, H)), (grad_up, self.grad_dtype, (I, H)),
+            (grad_down, self.grad_dtype, (H, I))))
+        _call(where, dev, load().moe_ffn_backward, p, ms[0], rx, *ms[1:], _ptr(saved) or None, gx, gg, gu, gd,
+              self.workspace.data_ptr(), self.ws_bytes)
+        return grad_x

@@ -26,6 +26,9 @@ SOURCES = [
     ("decode.hip", []),                      # the forward of a few tokens
     ("norm.hip", []),                        # layer norm and RMS norm
     ("router.hip", []),                      # the router's choice of experts
+    ("checkpoint.hip", []),                  # activation checkpoints in 8 bits
+    ("ffn_api.hip", []),                     # the gated feed-forward block: checks and launches
+    ("ffn.hip", []),                         # its products over many tokens
 ]
 
 FLAGS = [

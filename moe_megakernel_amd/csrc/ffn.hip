@@ -1,0 +1,241 @@
+// The gated feed-forward block: kernels over tiles of many tokens.
+//
+//   k_ffn_up     h = act(a) b, a = x gate^T, b = x up^T     both products in one tile, a and b kept
+//   k_ffn_rows   out = h down^T; grad_x = da gate + db up
+//   k_ffn_dh     dh = dy down; da = dh b act'(a), db = dh act(a), h again
+//   k_ffn_wgrad  grad_down (+)= dy^T h; grad_gate, grad_up (+)= da^T x, db^T x
+//
+// Sums are FP32 (the matrix unit's accumulators).  Rounded to BF16, each once: h (the second
+// product's operand; the output's own rounding is as large), a and b where they are kept so, da and
+// db (operands again), and the outputs.
+#include <hip/hip_runtime.h>
+
+#include "dense.hpp"
+#include "ffn.hpp"
+#include "mxint8.hpp"
+
+namespace moe {
+namespace ffn {
+
+using namespace dense;
+
+namespace {
+
+using Large = Tile<256, 256, 2, 2, 2, 1>;
+
+// act(a) = a s(z(a)) with the logistic function s: SiLU z = a, GELU (tanh form)
+// z = 2 sqrt(2 / pi) (a + 0.044715 a^3).
+constexpr float kZ1 = 1.5957691216057308f, kZ3 = 1.5957691216057308f * 0.044715f;
+template <int ACT>
+__device__ __forceinline__ float act(float a) {
+  return a * sigmoidf_(ACT == kSilu ? a : a * (kZ1 + kZ3 * a * a));
+}
+// act(a) and act'(a) = s (1 + a (1 - s) z'(a))
+template <int ACT>
+__device__ __forceinline__ void act_grad(float a, float& f, float& d) {
+  const float s = sigmoidf_(ACT == kSilu ? a : a * (kZ1 + kZ3 * a * a));
+  f = a * s;
+  d = s + f * (1.0f - s) * (ACT == kSilu ? 1.0f : kZ1 + 3.0f * kZ3 * a * a);
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));
+}
+
+template <class TL, int ACT, int SAVED>
+__global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_up(UpArgs p) {
+  static_assert(TL::WNC % 64 == 0, "gate / up pairs in a wave");
+  __shared__ __align__(16) uint8_t lds[TL::LDS];
+  constexpr int TI = TL::TN / 2;            // columns of h a tile
+  const TileAt at = tile_at((p.T + TL::TM - 1) / TL::TM, (p.I + TI - 1) / TI);
+  if (!at.ok) return;
+  const int m0 = at.m * TL::TM, i0 = at.n * TI, rows = min(TL::TM, p.T - m0), cols = min(TI, p.I - i0);
+  Acc<TL> acc;
+  zero_acc<TL>(acc);
+  const uint16_t* x = p.x.p + (int64_t)m0 * p.x.ld;
+  const uint16_t *wg = p.gate.p + (int64_t)i0 * p.gate.ld, *wu = p.up.p + (int64_t)i0 * p.up.ld;
+  auto fa = [&](int r) { return x + (int64_t)r * p.x.ld; };
+  // 32 gate rows, 32 up rows in turn: a lane's accumulators of blocks 2j and 2j + 1 are a and b of the
+  // same elements; cols is a multiple of 64, so the rows that exist come first
+  auto fb = [&](int r) {
+    const int64_t i = (r >> 6) * 32 + (r & 31);
+    return (r >> 5) & 1 ? wu + i * p.up.ld : wg + i * p.gate.ld;
+  };
+  tile_product<TL, KC, KC>(acc, p.H, fa, rows, fb, 2 * cols, lds);
+  each_piece<TL, true>(acc, lds, rows, cols, [&](int row, int col, const float* a, const float* b) {
+    const int64_t R = m0 + row;
+    const int i = i0 + col;
+    float h[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = act<ACT>(a[k]) * b[k];
+    *reinterpret_cast<uint4*>(p.h.p + R * p.h.ld + i) = pack8(h);
+    if constexpr (SAVED == kBf16) {
+      uint16_t* ab = reinterpret_cast<uint16_t*>(p.kept.ab) + R * 2 * p.I + i;
+      *reinterpret_cast<uint4*>(ab) = pack8(a);
+      *reinterpret_cast<uint4*>(ab + p.I) = pack8(b);
+    }
+    if constexpr (SAVED == kInt8) {   // the four lanes of a quad hold a block of 32
+      const float(&av)[8] = *reinterpret_cast<const float(*)[8]>(a);
+      const float(&bv)[8] = *reinterpret_cast<const float(*)[8]>(b);
+      const int sa = int8_scale_byte(quad_max_u(abs_bits8(av))), sb = int8_scale_byte(quad_max_u(abs_bits8(bv)));
+      uint8_t* ab = p.kept.ab + R * 2 * p.I + i;
+      *reinterpret_cast<uint2*>(ab) = int8_codes8(av, sa);
+      *reinterpret_cast<uint2*>(ab + p.I) = int8_codes8(bv, sb);
+      if ((i & 31) == 0) {
+        uint8_t* sc = p.kept.scales + R * (p.I / 16) + i / 32;
+        sc[0] = (uint8_t)sa;
+        sc[p.I / 32] = (uint8_t)sb;
+      }
+    }
+  });
+}
+
+// BM = KC: b0 rows are the result's columns; RC: b0 rows run along K, those from ksplit on in b1
+template <class TL, int BM>
+__global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_rows(RowsArgs p) {
+  __shared__ __align__(16) uint8_t lds[TL::LDS];
+  const TileAt at = tile_at((p.T + TL::TM - 1) / TL::TM, (p.N + TL::TN - 1) / TL::TN);
+  if (!at.ok) return;
+  const int m0 = at.m * TL::TM, n0 = at.n * TL::TN, rows = min(TL::TM, p.T - m0), cols = min(TL::TN, p.N - n0);
+  Acc<TL> acc;
+  zero_acc<TL>(acc);
+  const uint16_t* a = p.a.p + (int64_t)m0 * p.a.ld;
+  auto fa = [&](int r) { return a + (int64_t)r * p.a.ld; };
+  auto fb = [&](int r) {
+    if constexpr (BM == KC) return p.b0.p + (int64_t)(n0 + r) * p.b0.ld;
+    else return (r < p.ksplit ? p.b0.p + (int64_t)r * p.b0.ld : p.b1.p + (int64_t)(r - p.ksplit) * p.b1.ld) + n0;
+  };
+  tile_product<TL, KC, BM>(acc, p.K, fa, rows, fb, cols, lds);
+  each_piece<TL, false>(acc, lds, rows, cols, [&](int row, int col, const float* v) {
+    *reinterpret_cast<uint4*>(p.c.p + (int64_t)(m0 + row) * p.c.ld + n0 + col) = pack8(v);
+  });
+}
+
+template <class TL, int ACT, int SAVED>
+__global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_dh(DhArgs p) {
+  __shared__ __align__(16) uint8_t lds[TL::LDS];
+  const TileAt at = tile_at((p.T + TL::TM - 1) / TL::TM, (p.I + TL::TN - 1) / TL::TN);
+  if (!at.ok) return;
+  const int m0 = at.m * TL::TM, n0 = at.n * TL::TN, rows = min(TL::TM, p.T - m0), cols = min(TL::TN, p.I - n0);
+  Acc<TL> acc;
+  zero_acc<TL>(acc);
+  const uint16_t *dy = p.dy.p + (int64_t)m0 * p.dy.ld, *wd = p.down.p + n0;
+  auto fa = [&](int r) { return dy + (int64_t)r * p.dy.ld; };
+  auto fb = [&](int k) { return wd + (int64_t)k * p.down.ld; };
+  tile_product<TL, KC, RC>(acc, p.H, fa, rows, fb, cols, lds);
+  each_piece<TL, false>(acc, lds, rows, cols, [&](int row, int col, const float* dh) {
+    const int64_t R = m0 + row;
+    const int i = n0 + col;
+    float a[8], b[8], da[8], db[8], h[8];
+    if constexpr (SAVED == kBf16) {
+      const uint16_t* ab = reinterpret_cast<const uint16_t*>(p.kept.ab) + R * 2 * p.I + i;
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(ab), a);
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(ab + p.I), b);
+    } else {
+      const uint8_t *ab = p.kept.ab + R * 2 * p.I + i, *sc = p.kept.scales + R * (p.I / 16) + i / 32;
+      int8_values8(*reinterpret_cast<const uint2*>(ab), int8_step(sc[0]), a);
+      int8_values8(*reinterpret_cast<const uint2*>(ab + p.I), int8_step(sc[p.I / 32]), b);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float f, d;
+      act_grad<ACT>(a[k], f, d);
+      da[k] = dh[k] * b[k] * d;
+      db[k] = dh[k] * f;
+      h[k] = f * b[k];
+    }
+    uint16_t* dab = p.dab + R * 2 * p.I + i;
+    *reinterpret_cast<uint4*>(dab) = pack8(da);
+    *reinterpret_cast<uint4*>(dab + p.I) = pack8(db);
+    *reinterpret_cast<uint4*>(p.h + R * p.I + i) = pack8(h);
+  });
+}
+
+// FP32 or BF16 gradients; an accumulated BF16 gradient takes the rounded contribution, as a BF16
+// main_grad does.
+template <class TL, bool F32, bool OVER>
+__global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_wgrad(WgradArgs p) {
+  __shared__ __align__(16) uint8_t lds[TL::LDS];
+  const TileAt at = tile_at((p.M + TL::TM - 1) / TL::TM, (p.N + TL::TN - 1) / TL::TN);
+  if (!at.ok) return;
+  const int m0 = at.m * TL::TM, n0 = at.n * TL::TN, rows = min(TL::TM, p.M - m0), cols = min(TL::TN, p.N - n0);
+  Acc<TL> acc;
+  zero_acc<TL>(acc);
+  auto fa = [&](int k) { return p.a.p + (int64_t)k * p.a.ld + m0; };
+  auto fb = [&](int k) { return p.b.p + (int64_t)k * p.b.ld + n0; };
+  tile_product<TL, RC, RC>(acc, p.T, fa, rows, fb, cols, lds);
+  each_piece<TL, false>(acc, lds, rows, cols, [&](int row, int col, const float* v) {
+    const int m = m0 + row;
+    const int64_t at0 = m < p.msplit ? (int64_t)m * p.ldc0 : (int64_t)(m - p.msplit) * p.ldc1;
+    void* c = m < p.msplit ? p.c0 : p.c1;
+    if constexpr (F32) {
+      f32x4_t* to = reinterpret_cast<f32x4_t*>(static_cast<float*>(c) + at0 + n0 + col);
+      f32x4_t r[2] = {f32x4_t{v[0], v[1], v[2], v[3]}, f32x4_t{v[4], v[5], v[6], v[7]}};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) to[u] = OVER ? r[u] : to[u] + r[u];
+    } else {
+      uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(c) + at0 + n0 + col);
+      uint4 r = pack8(v);
+      if constexpr (!OVER) {
+        float old[8], add[8];
+        unpack_bf16x8(*to, old);
+        unpack_bf16x8(r, add);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) old[k] += add[k];
+        r = pack8(old);
+      }
+      *to = r;
+    }
+  });
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <class TL, class A>
+dim3 grid_of(const A& a, int64_t m, int64_t n, int tn) {
+  return dim3(tile_grid(ceil_div(m, TL::TM) * ceil_div(n, tn)));
+}
+
+template <class TL, int ACT>
+void up_as(hipStream_t st, const UpArgs& a) {
+  const dim3 grid = grid_of<TL>(a, a.T, a.I, TL::TN / 2), block(TL::NTH);
+  if (a.saved == kNone) hipLaunchKernelGGL((k_ffn_up<TL, ACT, kNone>), grid, block, 0, st, a);
+  else if (a.saved == kBf16) hipLaunchKernelGGL((k_ffn_up<TL, ACT, kBf16>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_ffn_up<TL, ACT, kInt8>), grid, block, 0, st, a);
+}
+template <class TL, int ACT>
+void dh_as(hipStream_t st, const DhArgs& a) {
+  const dim3 grid = grid_of<TL>(a, a.T, a.I, TL::TN), block(TL::NTH);
+  if (a.saved == kBf16) hipLaunchKernelGGL((k_ffn_dh<TL, ACT, kBf16>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_ffn_dh<TL, ACT, kInt8>), grid, block, 0, st, a);
+}
+template <class TL, bool F32>
+void wgrad_as(hipStream_t st, const WgradArgs& a) {
+  const dim3 grid = grid_of<TL>(a, a.M, a.N, TL::TN), block(TL::NTH);
+  if (a.overwrite) hipLaunchKernelGGL((k_ffn_wgrad<TL, F32, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_ffn_wgrad<TL, F32, false>), grid, block, 0, st, a);
+}
+
+}  // namespace
+
+void launch_up(hipStream_t st, const UpArgs& a) {
+  if (a.act == kSilu) up_as<Large, kSilu>(st, a);
+  else up_as<Large, kGelu>(st, a);
+}
+void launch_down(hipStream_t st, const RowsArgs& a) {
+  hipLaunchKernelGGL((k_ffn_rows<Large, KC>), grid_of<Large>(a, a.T, a.N, Large::TN), dim3(Large::NTH), 0, st, a);
+}
+void launch_dx(hipStream_t st, const RowsArgs& a) {
+  hipLaunchKernelGGL((k_ffn_rows<Large, RC>), grid_of<Large>(a, a.T, a.N, Large::TN), dim3(Large::NTH), 0, st, a);
+}
+void launch_dh(hipStream_t st, const DhArgs& a) {
+  if (a.act == kSilu) dh_as<Large, kSilu>(st, a);
+  else dh_as<Large, kGelu>(st, a);
+}
+void launch_wgrad(hipStream_t st, const WgradArgs& a) {
+  if (a.fp32) wgrad_as<Large, true>(st, a);
+  else wgrad_as<Large, false>(st, a);
+}
+
+}  // namespace ffn
+}  // namespace moe

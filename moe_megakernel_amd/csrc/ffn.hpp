@@ -1,0 +1,59 @@
+// The gated feed-forward block: arguments and launchers of its kernels.
+#pragma once
+#include "common.hpp"
+
+namespace moe {
+namespace ffn {
+
+enum Act { kSilu = 1, kGelu = 2 };          // moe_ffn_activation
+enum Saved { kNone = 0, kBf16 = 1, kInt8 = 4 };   // 0 or moe_dtype
+
+// A BF16 matrix, rows ld elements apart.
+struct Mat {
+  uint16_t* p;
+  int64_t ld;
+};
+
+// What the forward keeps of a = x gate^T and b = x up^T: BF16 [T][2I], or codes [T][2I] and scale
+// bytes [T][2I / 32]; a at column j, b at I + j.
+struct Kept {
+  uint8_t* ab;
+  uint8_t* scales;
+};
+
+// h = act(a) b
+struct UpArgs {
+  Mat x, gate, up, h;
+  Kept kept;
+  int T, H, I, act, saved;
+};
+// out = h down^T (K = I), or grad_x = dab [gate; up] (K = 2I, b1 the second half's rows)
+struct RowsArgs {
+  Mat a, b0, b1, c;
+  int T, N, K, ksplit;
+};
+// dh = dy down; dab = [da | db]; h again for the weight gradient
+struct DhArgs {
+  Mat dy, down;
+  Kept kept;
+  uint16_t* dab;         // [T][2I]
+  uint16_t* h;           // [T][I]
+  int T, H, I, act, saved;
+};
+// c[m][n] (+)= sum_t a[t][m] b[t][n]; rows m >= msplit go to c1
+struct WgradArgs {
+  Mat a, b;
+  void *c0, *c1;
+  int64_t ldc0, ldc1;
+  int M, N, T, msplit;
+  int fp32, overwrite;
+};
+
+void launch_up(hipStream_t st, const UpArgs& a);
+void launch_down(hipStream_t st, const RowsArgs& a);
+void launch_dh(hipStream_t st, const DhArgs& a);
+void launch_dx(hipStream_t st, const RowsArgs& a);
+void launch_wgrad(hipStream_t st, const WgradArgs& a);
+
+}  // namespace ffn
+}  // namespace moe
