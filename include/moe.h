@@ -517,6 +517,65 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
                             const moe_rows* grad_x, const moe_rows* grad_gate, const moe_rows* grad_up,
                             const moe_rows* grad_down, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------- 8-bit products, blocks of 128
+ * The blockwise recipe of 8-bit training and serving: E4M3 codes with one FP32 scale for each 128
+ * values along the contraction, of a row (activations, gradients) or of 128 x 128 values
+ * (weights), next to the layer's MXFP8 with one power of two for each 32.
+ *
+ * Quantiser:  scale = m / 448, code = E4M3(448 v / m) to nearest even, m the block's largest
+ * magnitude; value = code scale.  A block of zeros has scale 1; one that holds an infinity or NaN has
+ * scale NaN and codes 0. */
+typedef enum { MOE_FP8_ROWS = 1, MOE_FP8_TILES = 2 } moe_fp8_blocks;
+#define MOE_FP8_TRANSPOSE 1u   /* write the transposed matrix's codes and scales              */
+#define MOE_FP8_ACCUMULATE 2u  /* moe_fp8_matmul: add to out                                  */
+typedef struct {
+  int64_t rows;          /* R in [0, 2^31]                                                */
+  int64_t cols;          /* C in [1, 2^24]                                                */
+  int32_t kind;          /* moe_fp8_blocks: 128 values of a row, or 128 x 128              */
+  int32_t dtype;         /* MOE_BF16 or MOE_FP32, of x                                    */
+  uint32_t flags;        /* MOE_FP8_TRANSPOSE or 0                                        */
+} moe_fp8_quantize_problem;
+
+/*  x       [R][C], any element-aligned base and any ld >= C (rows of whole 16-byte pieces at 16-byte
+ *          alignment move in those)
+ *  With Y = x, or x^T with MOE_FP8_TRANSPOSE, [P][Q]:
+ *  codes   [P][Q16], Q16 = Q rounded up to a multiple of 16, zero codes past Q; 16-byte aligned
+ *  scales  float: MOE_FP8_ROWS [ceil(Q / 128)][P] (blocks of 128 along Q; a block's scales for
+ *          all rows lie side by side), MOE_FP8_TILES [ceil(P / 128)][ceil(Q / 128)]
+ * A weight gradient's operands are the transposed MOE_FP8_ROWS of the tokens' rows, a data
+ * gradient's weight the transposed MOE_FP8_TILES. */
+moe_status moe_fp8_quantize(const moe_fp8_quantize_problem* p, const moe_rows* x, void* codes, float* scales,
+                            void* stream);
+
+/* Product of rows in groups, each group with a weight of its own (the tokens of each expert, sorted
+ * by expert), or of one group:
+ *   out[m][n] = sum_b a_scales[b][m] S(g, n, b) sum_{k in block b} a[m][k] b[g][n][k],  m in group g
+ * FP32 sums, rounded once. */
+typedef struct {
+  int64_t rows;          /* M in [0, 2^24]                                                */
+  int64_t cols;          /* N in [1, 2^20]                                                */
+  int64_t depth;         /* K in [16, 2^24], a multiple of 16; the last block may be short */
+  int32_t groups;        /* G in [1, MOE_FP8_MAX_GROUPS]                                  */
+  int32_t scales;        /* moe_fp8_blocks of b: MOE_FP8_TILES, or MOE_FP8_ROWS with one group */
+  int32_t out_dtype;     /* MOE_BF16 or MOE_FP32                                          */
+  uint32_t flags;        /* MOE_FP8_ACCUMULATE or 0                                       */
+} moe_fp8_matmul_problem;
+#define MOE_FP8_MAX_GROUPS 256
+/* (M / 64 + 1 + G) (N / 128 + 1) is at most 2^22 as well (MOE_ERR_SHAPE above). */
+
+/*  a         E4M3 [M][K], 16-byte aligned, ld a multiple of 16
+ *  a_scales  float [ceil(K / 128)][M]
+ *  b         E4M3 [G][N][K]: base (16-byte aligned), ld and expert_stride multiples of 16; no table
+ *  b_scales  float: MOE_FP8_TILES [G][ceil(N / 128)][ceil(K / 128)], MOE_FP8_ROWS [ceil(K / 128)][N]
+ *  offsets   int32 [G + 1] on the device, ascending: group g is rows offsets[g] .. offsets[g + 1] - 1
+ *            (the layer's routing state holds such a table); NULL with one group: all rows.  Rows
+ *            outside every group are not read and not written.  Entries outside [0, M] count
+ *            as the nearest end; descending ones leave rows of out unspecified
+ *  out       [M][N], any element-aligned base and any ld >= N; must not overlap an input.
+ *            Accumulation into BF16 rounds the product first, as a BF16 main_grad does */
+moe_status moe_fp8_matmul(const moe_fp8_matmul_problem* p, const moe_rows* a, const float* a_scales, const moe_mat* b,
+                          const float* b_scales, const int32_t* offsets, const moe_rows* out, void* stream);
+
 /* A static description of a status code. */
 const char* moe_status_str(moe_status s);
 

@@ -32,6 +32,9 @@ MOE_NORM_MAX_COLS = 16384
 MOE_CHECKPOINT_MAX_COLS = 1 << 24
 MOE_FFN_SILU, MOE_FFN_GELU = 1, 2
 MOE_FFN_OVERWRITE_GRADS = 1
+MOE_FP8_ROWS, MOE_FP8_TILES = 1, 2
+MOE_FP8_TRANSPOSE, MOE_FP8_ACCUMULATE = 1, 2
+MOE_FP8_MAX_GROUPS = 256
 
 EXPORTED = ("moe_saved_bytes", "moe_workspace_bytes", "moe_saved_view", "moe_forward",
             "moe_forward_topk", "moe_forward_noalloc", "moe_backward", "moe_status_str",
@@ -39,7 +42,7 @@ EXPORTED = ("moe_saved_bytes", "moe_workspace_bytes", "moe_saved_view", "moe_for
             "moe_decode_workspace_bytes", "moe_forward_decode", "moe_router_forward", "moe_router_backward",
             "moe_norm_forward", "moe_norm_backward", "moe_norm_workspace_bytes", "moe_checkpoint_store",
             "moe_checkpoint_load", "moe_ffn_saved_bytes", "moe_ffn_workspace_bytes", "moe_ffn_saved_view",
-            "moe_ffn_forward", "moe_ffn_backward")
+            "moe_ffn_forward", "moe_ffn_backward", "moe_fp8_quantize", "moe_fp8_matmul")
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 MOE_DECODE_MAX_TOKENS = 64
 MOE_DECODE_MAX_INTERMEDIATE = 65536
@@ -110,6 +113,16 @@ class moe_ffn_problem(C.Structure):
 
 class moe_ffn_saved_layout(C.Structure):
     _fields_ = [(n, C.c_size_t) for n in ("ab", "ab_scales", "x", "x_scales")]
+
+
+class moe_fp8_quantize_problem(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("kind", C.c_int32), ("dtype", C.c_int32),
+                ("flags", C.c_uint32)]
+
+
+class moe_fp8_matmul_problem(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("depth", C.c_int64), ("groups", C.c_int32),
+                ("scales", C.c_int32), ("out_dtype", C.c_int32), ("flags", C.c_uint32)]
 
 
 class moe_rows(C.Structure):
@@ -189,6 +202,11 @@ def load(path: str | None = None):
     lib.moe_ffn_backward.argtypes = [P(moe_ffn_problem)] + [P(moe_rows)] * 5 + [C.c_void_p] + [P(moe_rows)] * 4 + [
         C.c_void_p, C.c_size_t, C.c_void_p]
     lib.moe_ffn_backward.restype = C.c_int
+    lib.moe_fp8_quantize.argtypes = [P(moe_fp8_quantize_problem), P(moe_rows), C.c_void_p, C.c_void_p, C.c_void_p]
+    lib.moe_fp8_quantize.restype = C.c_int
+    lib.moe_fp8_matmul.argtypes = [P(moe_fp8_matmul_problem), P(moe_rows), C.c_void_p, P(moe_mat), C.c_void_p,
+                                   C.c_void_p, P(moe_rows), C.c_void_p]
+    lib.moe_fp8_matmul.restype = C.c_int
     if path is None:
         _lib = lib
     return lib
@@ -340,6 +358,17 @@ def moe_ffn_backward(p, grad_out, x, gate, up, down, saved, grad_x, grad_gate, g
     return load().moe_ffn_backward(C.byref(p), _ref(grad_out), _ref(x), _ref(gate), _ref(up), _ref(down), saved,
                                    _ref(grad_x), _ref(grad_gate), _ref(grad_up), _ref(grad_down), workspace,
                                    workspace_bytes, stream)
+
+
+def moe_fp8_quantize(p, x, codes, scales, stream) -> int:
+    """Raw call: x is a moe_rows (or None), the rest integer device addresses; returns the status."""
+    return load().moe_fp8_quantize(C.byref(p), _ref(x), codes, scales, stream)
+
+
+def moe_fp8_matmul(p, a, a_scales, b, b_scales, offsets, out, stream) -> int:
+    """Raw call: a and out are moe_rows and b a moe_mat (or None), the rest integer device
+    addresses; returns the status."""
+    return load().moe_fp8_matmul(C.byref(p), _ref(a), a_scales, _ref(b), b_scales, offsets, _ref(out), stream)
 
 
 def moe_kernel_timer_enable(on: bool) -> None:
@@ -824,3 +853,87 @@ class FeedForward(_Fixed):
         _call(where, dev, load().moe_ffn_backward, p, ms[0], rx, *ms[1:], _ptr(saved) or None, gx, gg, gu, gd,
               self.workspace.data_ptr(), self.ws_bytes)
         return grad_x
+
+
+class Fp8Quantizer(_Fixed):
+    """BF16 or FP32 matrices to E4M3 codes with one FP32 scale for each 128 values of a row (kind
+    "rows") or each 128 x 128 values ("tiles"); transpose: of the transposed matrix.  Holds
+    options only; every buffer is the caller's."""
+
+    def __init__(self, kind="rows", transpose=False, dtype=None):
+        import torch
+        self.dtype = dtype or torch.bfloat16
+        code = {"rows": MOE_FP8_ROWS, "tiles": MOE_FP8_TILES}.get(kind, 0)
+        self._p = moe_fp8_quantize_problem(0, 1, code, _moe_dtype(self.dtype, "Fp8Quantizer"),
+                                           MOE_FP8_TRANSPOSE if transpose else 0)
+        st = moe_fp8_quantize(self._p, None, None, None, None)    # no rows: checks the options
+        if st != MOE_OK:
+            raise MoeError(st, "Fp8Quantizer")
+        self.kind, self.transpose, q = kind, bool(transpose), self._p
+        self._problems = _Problems(lambda R, N: moe_fp8_quantize_problem(R, N, q.kind, q.dtype, q.flags))
+
+    def shapes(self, rows, cols):
+        """Shapes of codes and scales for x [rows, cols]."""
+        P, Q = (cols, rows) if self.transpose else (rows, cols)
+        blocks = (Q + 127) // 128
+        return (P, (Q + 15) // 16 * 16), (blocks, P) if self.kind == "rows" else ((P + 127) // 128, blocks)
+
+    def forward(self, x, codes, scales):
+        """Writes codes (torch.float8_e4m3fn) and scales (float32) of x, of the shapes that shapes() gives."""
+        import torch
+        where = "moe_fp8_quantize"
+        dev, (R, N) = _device(where, x), x.shape
+        if N == 0:
+            raise MoeError(MOE_ERR_SHAPE, where)
+        rows = moe_rows(x.data_ptr(), _check_rows(where, dev, x, self.dtype, (R, N)))
+        qs, ss = self.shapes(R, N)
+        _check(where, dev, codes, torch.float8_e4m3fn, qs)
+        _check(where, dev, scales, torch.float32, ss)
+        _call(where, dev, load().moe_fp8_quantize, self._problems[R, N], rows, codes.data_ptr(), scales.data_ptr())
+        return codes, scales
+
+
+class Fp8Matmul(_Fixed):
+    """out = a b^T of E4M3 codes with scales of 128 (as Fp8Quantizer gives them), rows in groups
+    with a weight each or all in one.  scales: of b, "tiles" or "rows" (one group); accumulate: add
+    to out.  Holds options only; every buffer is the caller's."""
+
+    def __init__(self, scales="tiles", out_dtype=None, accumulate=False, device="cuda"):
+        import torch
+        self.out_dtype = out_dtype or torch.bfloat16
+        code = {"rows": MOE_FP8_ROWS, "tiles": MOE_FP8_TILES}.get(scales, 0)
+        self._p = moe_fp8_matmul_problem(0, 1, 16, 1, code, _moe_dtype(self.out_dtype, "Fp8Matmul"),
+                                         MOE_FP8_ACCUMULATE if accumulate else 0)
+        st = moe_fp8_matmul(self._p, None, None, None, None, None, None, None)    # no rows: checks the options
+        if st != MOE_OK:
+            raise MoeError(st, "Fp8Matmul")
+        self.scales, q = scales, self._p
+        self._problems = _Problems(lambda M, N, K, G: moe_fp8_matmul_problem(M, N, K, G, q.scales, q.out_dtype, q.flags))
+
+    def forward(self, a, a_scales, b, b_scales, out, offsets=None):
+        """a [M, K], b [N, K] or [G, N, K] (contiguous groups), out [M, N]; scales as
+        moe_fp8_matmul describes them ([N / 128, K / 128] may stand for [1, ...]).  offsets: int32 [G + 1]."""
+        import torch
+        where, f8, f32 = "moe_fp8_matmul", torch.float8_e4m3fn, torch.float32
+        dev, (M, K) = _device(where, a), a.shape
+        if b is None:
+            raise MoeError(MOE_ERR_NULL, where)
+        if b.dim() not in (2, 3) or b.shape[-1] != K:
+            raise MoeError(MOE_ERR_SHAPE, where)
+        G, N = b.shape[0] if b.dim() == 3 else 1, b.shape[-2]
+        ra = moe_rows(a.data_ptr(), _check_rows(where, dev, a, f8, (M, K)))
+        kb, nb = (K + 127) // 128, (N + 127) // 128
+        _check(where, dev, a_scales, f32, (kb, M))
+        _check(where, dev, b, f8, b.shape)
+        if b_scales is None:
+            raise MoeError(MOE_ERR_NULL, where)
+        if self.scales == "rows":
+            _check(where, dev, b_scales, f32, (kb, N))
+        else:
+            _check(where, dev, b_scales, f32, (nb, kb) if G == 1 and b_scales.dim() == 2 else (G, nb, kb))
+        if offsets is not None:
+            _check(where, dev, offsets, torch.int32, (G + 1,))
+        ro = moe_rows(out.data_ptr() if out is not None else 0, _check_rows(where, dev, out, self.out_dtype, (M, N)))
+        _call(where, dev, load().moe_fp8_matmul, self._problems[M, N, K, G], ra, a_scales.data_ptr(),
+              moe_mat(b.data_ptr(), N * K, None, K), b_scales.data_ptr(), _ptr(offsets) or None, ro)
+        return out

@@ -1,0 +1,375 @@
+// 8-bit matrix products with a scale for each block of 128, for rows in groups:
+//   out[m][n] = sum over blocks b of 128 k:  sa[b][m] sb[..n..][b]  sum_{k in b} A[m][k] B[g(m)][n][k]
+//
+// One v_mfma_f32_16x16x128 covers a block of k.  Weights are its 16-row operand and tokens its 16
+// columns, so a lane's four results belong to one token: with a scale a 128 x 128 weight tile a
+// lane multiplies its four results by one number, 16 cycles of vector work next to the 32 of the
+// product, which the other accumulators' products cover.  The sums over a block start from zero, are scaled
+// and added in FP32.
+//
+// The 8-bit matrix instructions keep a sum to about 2^-16 of its largest product (measured on
+// normal values, 128 products: 1.3e-5 of the result; the K = 32 form and sums of parts the same).  Under
+// the 2^-9 of a BF16 result that is nothing, in an FP32 one it would be the largest error by far.  So products
+// with an FP32 result decode the codes to BF16 (exact) and take the BF16 instruction (4e-9 on the
+// same values), at half its rate.
+#include <hip/hip_runtime.h>
+
+#include "../../include/moe.h"
+#include "fp8.hpp"
+#include "gemm.hpp"
+#include "host.hpp"
+
+namespace moe {
+namespace fp8 {
+
+using gemm::dma16;
+using gemm::dma4;
+using gemm::g_zero_page;
+using gemm::lds_off;
+using gemm::swz_kc;
+using gemm::u32x4_t;
+using gemm::wait_vm;
+
+namespace {
+
+constexpr int kKB = 128;                   // k of a stage, and of a scale
+
+template <int TN_, int TM_, int NWN_, int NWM_, int MINB_>
+struct Shape {
+  static constexpr int TN = TN_, TM = TM_, NWN = NWN_, NWM = NWM_, MINB = MINB_;
+  static constexpr int NW = NWN * NWM, NTH = 64 * NW;
+  static constexpr int NB = TN / NWN / 16, MB = TM / NWM / 16;   // 16 x 16 blocks of a wave
+  static constexpr int W_DMA = TN * kKB / 1024 / NW, A_DMA = TM * kKB / 1024 / NW;
+  static constexpr int STAGE = (TN + TM) * kKB, SCALES = 4 * (TN + TM);
+  static constexpr int LDS = 2 * (STAGE + SCALES);
+  static_assert(TN * kKB % (1024 * NW) == 0 && TM * kKB % (1024 * NW) == 0, "copies a wave");
+  static_assert(TN % 64 == 0 && TM % 64 == 0, "scale copies");
+};
+
+struct Tile {
+  int g, m0, rows, n0;
+  bool ok;
+};
+
+// Tile of a block.  Groups' tile counts come from the offsets, one thread a group; entries outside
+// [0, M] are taken as the nearest end, so every row index stays inside.
+template <class S>
+__device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int* prefix) {
+  const int nt = (p.N + S::TN - 1) / S::TN;
+  Tile t{0, 0, 0, 0, false};
+  int mt = (p.M + S::TM - 1) / S::TM, begin = 0, count = p.M, lo = 0;
+  const int x = blockIdx.x & 7, j = blockIdx.x >> 3;
+  if (p.offsets) {
+    if (threadIdx.x < 64) {                // an inclusive scan by one wave, 64 groups at a time
+      const int lane = threadIdx.x;
+      int carry = 0;
+      for (int g0 = 0; g0 < p.G; g0 += 64) {
+        int n = 0;
+        if (g0 + lane < p.G) {
+          const int o0 = min(max(p.offsets[g0 + lane], 0), p.M), o1 = min(max(p.offsets[g0 + lane + 1], 0), p.M);
+          n = max(o1 - o0, 0);
+          n = (n + S::TM - 1) / S::TM;
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+          const int v = __shfl_up(n, o);
+          n += lane >= o ? v : 0;
+        }
+        if (g0 + lane < p.G) prefix[g0 + lane + 1] = carry + n;
+        carry += __shfl(n, 63);
+      }
+      if (lane == 0) prefix[0] = 0;
+    }
+    __syncthreads();
+    mt = prefix[p.G];
+  }
+  const int64_t total = (int64_t)mt * nt;
+  const int64_t t0 = total * x / 8, t1 = total * (x + 1) / 8;
+  if (j >= t1 - t0) return t;
+  const int64_t L = t0 + j;
+  int first = 0, tiles = mt;
+  if (p.offsets) {
+    const int at = (int)(L / nt);
+    int hi = p.G - 1;
+    while (lo < hi) {                      // the last group that starts at or before the tile
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= at) lo = mid;
+      else hi = mid - 1;
+    }
+    first = prefix[lo];
+    tiles = prefix[lo + 1] - first;
+    begin = min(max(p.offsets[lo], 0), p.M);
+    count = min(max(p.offsets[lo + 1], 0), p.M) - begin;
+  }
+  // bands of m tiles, m fastest, as in the layer's products
+  const int64_t in = L - (int64_t)first * nt;
+  const int band = (int)(in / (gemm::kBandM * nt));
+  const int r = (int)(in - (int64_t)band * gemm::kBandM * nt), h = min(gemm::kBandM, tiles - band * gemm::kBandM);
+  const int m = (band * gemm::kBandM + r % h) * S::TM;
+  t.g = lo;
+  t.m0 = begin + m;
+  t.rows = min(S::TM, count - m);
+  t.n0 = r / h * S::TN;
+  t.ok = true;
+  return t;
+}
+
+// a lane's 32 codes in BF16 (exact), 8 for each of four products of 32 k
+struct Wide {
+  bf16x8_t v[4];
+};
+__device__ __forceinline__ Wide widen(const i32x8_t& c) {
+  Wide w;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    u32x4_t r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t q = (uint32_t)c[2 * u + h];
+      r[2 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, false));
+      r[2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, true));
+    }
+    w.v[u] = __builtin_bit_cast(bf16x8_t, r);
+  }
+  return w;
+}
+
+template <class S, bool ROWS_B, bool F32, bool ADD>
+__global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
+  __shared__ __align__(16) uint8_t lds[S::LDS];
+  const Tile t = find_tile<S>(p, reinterpret_cast<int*>(lds));
+  if (!t.ok) return;
+  __syncthreads();                         // the groups' table is read before the stages take its place
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q4 = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = w % S::NWN, wm = w / S::NWN;
+  const int cols = min(S::TN, p.N - t.n0), rows = t.rows;
+  const uint32_t lds0 = lds_off(lds);
+  const uint8_t* zp = reinterpret_cast<const uint8_t*>(g_zero_page) + 16 * lane;
+  const int nk = (p.K + kKB - 1) / kKB;
+
+  // stage: weights [TN][128], tokens [TM][128] (16-byte chunks swizzled by row), then the scales:
+  // tokens' [TM], and weights' [TN] (ROWS_B) or of the tile's 128-column parts
+  const uint8_t *pw[S::W_DMA], *pa[S::A_DMA];
+  int kw[S::W_DMA], kx[S::A_DMA];          // the chunk's first k, or past any K for rows that do not exist
+#pragma unroll
+  for (int i = 0; i < S::W_DMA; ++i) {
+    const int off = (w * S::W_DMA + i) * 1024 + 16 * lane, r = off / kKB, c = ((off % kKB) >> 4) ^ swz_kc<128>(r);
+    pw[i] = p.b + (int64_t)t.g * p.stride_b + (int64_t)(t.n0 + r) * p.ldb + 16 * c;
+    kw[i] = r < cols ? 16 * c : 1 << 30;
+  }
+#pragma unroll
+  for (int i = 0; i < S::A_DMA; ++i) {
+    const int off = (w * S::A_DMA + i) * 1024 + 16 * lane, r = off / kKB, c = ((off % kKB) >> 4) ^ swz_kc<128>(r);
+    pa[i] = p.a + (int64_t)(t.m0 + r) * p.lda + 16 * c;
+    kx[i] = r < rows ? 16 * c : 1 << 30;
+  }
+  const int sb_rows = (p.N + 127) / 128, sb_cols = nk;
+  auto issue = [&](int kt) __attribute__((always_inline)) {
+    const uint32_t base = lds0 + (kt & 1) * (S::STAGE + S::SCALES);
+    const int k0 = kt * kKB;
+#pragma unroll
+    for (int i = 0; i < S::W_DMA; ++i) {
+      dma16(k0 + kw[i] < p.K ? pw[i] : zp, base + (w * S::W_DMA + i) * 1024);
+      pw[i] += kKB;
+    }
+#pragma unroll
+    for (int i = 0; i < S::A_DMA; ++i) {
+      dma16(k0 + kx[i] < p.K ? pa[i] : zp, base + S::TN * kKB + (w * S::A_DMA + i) * 1024);
+      pa[i] += kKB;
+    }
+    for (int i = w; i < S::TM / 64 + (ROWS_B ? S::TN / 64 : 1); i += S::NW) {
+      const void* src = reinterpret_cast<const uint8_t*>(g_zero_page) + 4 * lane;
+      if (i < S::TM / 64) {
+        if (64 * i + lane < rows) src = p.sa + (int64_t)kt * p.M + t.m0 + 64 * i + lane;
+      } else if (ROWS_B) {
+        const int n = 64 * (i - S::TM / 64) + lane;
+        if (n < cols) src = p.sb + (int64_t)kt * p.N + t.n0 + n;
+      } else {
+        const int n = t.n0 / 128 + lane;
+        if (lane < (S::TN + 127) / 128 && n < sb_rows) src = p.sb + ((int64_t)t.g * sb_rows + n) * sb_cols + kt;
+      }
+      dma4(src, base + S::STAGE + 256 * i);
+    }
+  };
+
+  f32x4_t acc[S::NB][S::MB];
+#pragma unroll
+  for (int i = 0; i < S::NB; ++i)
+#pragma unroll
+    for (int j = 0; j < S::MB; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  // a lane's 32 codes of row r16 of a 16-row block: chunks q4 and q4 + 4 (which 32 is free, as long as
+  // both operands agree)
+  auto frag = [&](const uint8_t* tile, int r0) __attribute__((always_inline)) {
+    const int r = r0 + r16;
+    const uint8_t* q = tile + r * kKB;
+    const u32x4_t u0 = *reinterpret_cast<const u32x4_t*>(q + ((q4 ^ swz_kc<128>(r)) << 4));
+    const u32x4_t u1 = *reinterpret_cast<const u32x4_t*>(q + (((q4 + 4) ^ swz_kc<128>(r)) << 4));
+    return i32x8_t{(int)u0[0], (int)u0[1], (int)u0[2], (int)u0[3], (int)u1[0], (int)u1[1], (int)u1[2], (int)u1[3]};
+  };
+  constexpr int kOne = 0x7f7f7f7f;         // E8M0 1.0: the hardware's own scales stay out
+  issue(0);
+  for (int kt = 0; kt < nk; ++kt) {
+    wait_vm<0>();
+    __syncthreads();
+    if (kt + 1 < nk) issue(kt + 1);
+    const uint8_t* W = lds + (kt & 1) * (S::STAGE + S::SCALES);
+    const uint8_t* A = W + S::TN * kKB;
+    const float* sc = reinterpret_cast<const float*>(W + S::STAGE);
+    i32x8_t x[S::MB];
+    [[maybe_unused]] Wide xw[F32 ? S::MB : 1];
+    float s[S::MB];
+#pragma unroll
+    for (int j = 0; j < S::MB; ++j) {
+      const int m = (wm * S::MB + j) * 16;
+      x[j] = frag(A, m);
+      if constexpr (F32) xw[j] = widen(x[j]);
+      s[j] = sc[m + r16];
+    }
+    if constexpr (!ROWS_B) {
+      static_assert(S::NB * 16 <= 128 && 128 % (S::NB * 16) == 0, "one weight scale a wave");
+      const float sb = sc[S::TM + wn * S::NB * 16 / 128];
+#pragma unroll
+      for (int j = 0; j < S::MB; ++j) s[j] *= sb;
+    }
+#pragma unroll
+    for (int i = 0; i < S::NB; ++i) {
+      const int n = (wn * S::NB + i) * 16;
+      const i32x8_t wf = frag(W, n);
+      [[maybe_unused]] Wide ww;
+      if constexpr (F32) ww = widen(wf);
+      f32x4_t sb{1.0f, 1.0f, 1.0f, 1.0f};
+      if constexpr (ROWS_B) sb = *reinterpret_cast<const f32x4_t*>(sc + S::TM + n + 4 * q4);
+#pragma unroll
+      for (int j = 0; j < S::MB; ++j) {
+        f32x4_t d{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (F32) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww.v[u], xw[j].v[u], d, 0, 0, 0);
+        } else {
+          d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, x[j], d, 0, 0, 0, kOne, 0, kOne);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] += (ROWS_B ? s[j] * sb[e] : s[j]) * d[e];
+      }
+    }
+  }
+
+  // lane: token r16 of a block, columns 4 q4 .. 4 q4 + 3
+  const bool vec = p.ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & (F32 ? 15u : 7u)) == 0;
+#pragma unroll
+  for (int j = 0; j < S::MB; ++j) {
+    const int m = (wm * S::MB + j) * 16 + r16;
+    if (m >= rows) continue;
+#pragma unroll
+    for (int i = 0; i < S::NB; ++i) {
+      const int n = (wn * S::NB + i) * 16 + 4 * q4;
+      if (n >= cols) continue;
+      uint8_t* to = p.out + ((int64_t)(t.m0 + m) * p.ldo + t.n0 + n) * (F32 ? 4 : 2);
+      const f32x4_t v = acc[i][j];
+      if (vec && n + 4 <= cols) {
+        if constexpr (F32) {
+          f32x4_t* o = reinterpret_cast<f32x4_t*>(to);
+          *o = ADD ? *o + v : v;
+        } else {
+          uint2* o = reinterpret_cast<uint2*>(to);
+          uint2 z = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
+          if constexpr (ADD) {
+            const uint2 y = *o;
+            z = make_uint2(pack_bf2(lo_bf(y.x) + lo_bf(z.x), hi_bf(y.x) + hi_bf(z.x)),
+                           pack_bf2(lo_bf(y.y) + lo_bf(z.y), hi_bf(y.y) + hi_bf(z.y)));
+          }
+          *o = z;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (n + e >= cols) break;
+          if constexpr (F32) {
+            float* o = reinterpret_cast<float*>(to) + e;
+            *o = ADD ? *o + v[e] : v[e];
+          } else {
+            uint16_t* o = reinterpret_cast<uint16_t*>(to) + e;
+            const uint32_t z = f2bf(v[e]);
+            *o = (uint16_t)(ADD ? f2bf(bf2f(*o) + bf2f(z)) : z);
+          }
+        }
+      }
+    }
+  }
+}
+
+using Large = Shape<256, 192, 2, 2, 1>;
+using Small = Shape<128, 128, 2, 2, 2>;
+
+template <class S>
+int64_t tiles(const MatmulArgs& a) {
+  const int64_t m = (a.M + S::TM - 1) / S::TM + (a.offsets ? a.G : 0);
+  return m * ((a.N + S::TN - 1) / S::TN);
+}
+
+template <class S, bool ROWS_B, bool F32>
+void launch_as(hipStream_t st, const MatmulArgs& a) {
+  const dim3 grid((unsigned)((tiles<S>(a) + 7) / 8 * 8 + 8)), block(S::NTH);
+  if (a.accumulate) hipLaunchKernelGGL((k_fp8_matmul<S, ROWS_B, F32, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_fp8_matmul<S, ROWS_B, F32, false>), grid, block, 0, st, a);
+}
+template <class S, bool F32>
+void launch_shape(hipStream_t st, const MatmulArgs& a) {
+  if (a.rows_b) launch_as<S, true, F32>(st, a);
+  else launch_as<S, false, F32>(st, a);
+}
+
+moe_status check(const moe_fp8_matmul_problem* p) {
+  if (!p) return MOE_ERR_NULL;
+  const int64_t M = p->rows, N = p->cols, K = p->depth;
+  if (M < 0 || M > (1 << 24) || N < 1 || N > (1 << 20) || K < 16 || K > (1 << 24) || K % 16) return MOE_ERR_SHAPE;
+  if (p->groups < 1 || p->groups > kMaxGroups) return MOE_ERR_SHAPE;
+  if ((M / 64 + 1 + p->groups) * (N / 128 + 1) > (1 << 22)) return MOE_ERR_SHAPE;   // a launch holds 2^32 threads
+  if (p->scales != MOE_FP8_ROWS && p->scales != MOE_FP8_TILES) return MOE_ERR_UNSUPPORTED;
+  if (p->scales == MOE_FP8_ROWS && p->groups != 1) return MOE_ERR_UNSUPPORTED;
+  if (p->out_dtype != MOE_BF16 && p->out_dtype != MOE_FP32) return MOE_ERR_DTYPE;
+  if (p->flags & ~MOE_FP8_ACCUMULATE) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+void launch_matmul(hipStream_t st, const MatmulArgs& a) {
+  if (a.out_fp32) launch_shape<Small, true>(st, a);
+  else launch_shape<Large, false>(st, a);
+}
+
+}  // namespace fp8
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_fp8_matmul(const moe_fp8_matmul_problem* p, const moe_rows* a, const float* a_scales,
+                                     const moe_mat* b, const float* b_scales, const int32_t* offsets,
+                                     const moe_rows* out, void* stream) {
+  MOE_TRY(fp8::check(p));
+  if (p->rows == 0) return MOE_OK;
+  if (!a || !a->base || !a_scales || !b || !b->base || !b_scales || !out || !out->base) return MOE_ERR_NULL;
+  if (p->groups > 1 && !offsets) return MOE_ERR_NULL;
+  if (b->table) return MOE_ERR_LAYOUT;
+  if (a->ld < p->depth || a->ld % 16 || !aligned16(a->base)) return MOE_ERR_LAYOUT;
+  if (b->ld < p->depth || b->ld % 16 || !aligned16(b->base)) return MOE_ERR_LAYOUT;
+  if (p->groups > 1 && (b->expert_stride < 0 || b->expert_stride % 16)) return MOE_ERR_LAYOUT;
+  if (out->ld < p->cols || !elem_aligned(out->base, p->out_dtype)) return MOE_ERR_LAYOUT;
+  if (!aligned4(a_scales) || !aligned4(b_scales) || !aligned4(offsets)) return MOE_ERR_LAYOUT;
+  fp8::MatmulArgs m{};
+  m.a = static_cast<const uint8_t*>(a->base);
+  m.sa = a_scales;
+  m.b = static_cast<const uint8_t*>(b->base);
+  m.sb = b_scales;
+  m.out = static_cast<uint8_t*>(out->base);
+  m.offsets = offsets;
+  m.lda = a->ld; m.ldb = b->ld; m.stride_b = b->expert_stride; m.ldo = out->ld;
+  m.M = (int)p->rows; m.N = (int)p->cols; m.K = (int)p->depth; m.G = p->groups;
+  m.out_fp32 = p->out_dtype == MOE_FP32;
+  m.accumulate = (p->flags & MOE_FP8_ACCUMULATE) != 0;
+  m.rows_b = p->scales == MOE_FP8_ROWS;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return launch("fp8_matmul", st, [&] { fp8::launch_matmul(st, m); });
+}
