@@ -29,7 +29,9 @@ SOURCES = [
     ("checkpoint.hip", []),                  # activation checkpoints in 8 bits
     ("ffn_api.hip", []),                     # the gated feed-forward block: checks and launches
     ("ffn.hip", []),                         # its products over many tokens
+    ("ffn_few.hip", []),                     # and over a few
     ("fp8.hip", []),                         # 8-bit products with scales of 128
+    ("fp8_few.hip", []),                     # over a few rows
     ("fp8_quantize.hip", []),                # their operands
 ]
 

@@ -12,6 +12,7 @@
 
 #include "dense.hpp"
 #include "ffn.hpp"
+#include "ffn_act.hpp"
 #include "mxint8.hpp"
 
 namespace moe {
@@ -22,21 +23,6 @@ using namespace dense;
 namespace {
 
 using Large = Tile<256, 256, 2, 2, 2, 1>;
-
-// act(a) = a s(z(a)) with the logistic function s: SiLU z = a, GELU (tanh form)
-// z = 2 sqrt(2 / pi) (a + 0.044715 a^3).
-constexpr float kZ1 = 1.5957691216057308f, kZ3 = 1.5957691216057308f * 0.044715f;
-template <int ACT>
-__device__ __forceinline__ float act(float a) {
-  return a * sigmoidf_(ACT == kSilu ? a : a * (kZ1 + kZ3 * a * a));
-}
-// act(a) and act'(a) = s (1 + a (1 - s) z'(a))
-template <int ACT>
-__device__ __forceinline__ void act_grad(float a, float& f, float& d) {
-  const float s = sigmoidf_(ACT == kSilu ? a : a * (kZ1 + kZ3 * a * a));
-  f = a * s;
-  d = s + f * (1.0f - s) * (ACT == kSilu ? 1.0f : kZ1 + 3.0f * kZ3 * a * a);
-}
 
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));

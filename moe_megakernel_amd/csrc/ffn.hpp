@@ -55,5 +55,10 @@ void launch_dh(hipStream_t st, const DhArgs& a);
 void launch_dx(hipStream_t st, const RowsArgs& a);
 void launch_wgrad(hipStream_t st, const WgradArgs& a);
 
+// up to kFewTokens tokens, nothing kept
+constexpr int kFewTokens = 64;
+void launch_up_few(hipStream_t st, const UpArgs& a);
+void launch_down_few(hipStream_t st, const RowsArgs& a);
+
 }  // namespace ffn
 }  // namespace moe

@@ -1,0 +1,24 @@
+// The activations of the gated feed-forward block: act(a) = a s(z(a)) with the logistic function s.
+#pragma once
+#include "common.hpp"
+#include "ffn.hpp"
+
+namespace moe {
+namespace ffn {
+
+// SiLU z = a; GELU (tanh form) z = 2 sqrt(2 / pi) (a + 0.044715 a^3)
+constexpr float kZ1 = 1.5957691216057308f, kZ3 = 1.5957691216057308f * 0.044715f;
+template <int ACT>
+__device__ __forceinline__ float act(float a) {
+  return a * sigmoidf_(ACT == kSilu ? a : a * (kZ1 + kZ3 * a * a));
+}
+// act(a) and act'(a) = s + a s (1 - s) z'(a)
+template <int ACT>
+__device__ __forceinline__ void act_grad(float a, float& f, float& d) {
+  const float s = sigmoidf_(ACT == kSilu ? a : a * (kZ1 + kZ3 * a * a));
+  f = a * s;
+  d = s + f * (1.0f - s) * (ACT == kSilu ? 1.0f : kZ1 + 3.0f * kZ3 * a * a);
+}
+
+}  // namespace ffn
+}  // namespace moe

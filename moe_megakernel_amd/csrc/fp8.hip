@@ -6,16 +6,11 @@
 // lane multiplies its four results by one number, 16 cycles of vector work next to the 32 of the
 // product, which the other accumulators' products cover.  The sums over a block start from zero, are scaled
 // and added in FP32.
-//
-// The 8-bit matrix instructions keep a sum to about 2^-16 of its largest product (measured on
-// normal values, 128 products: 1.3e-5 of the result; the K = 32 form and sums of parts the same).  Under
-// the 2^-9 of a BF16 result that is nothing, in an FP32 one it would be the largest error by far.  So products
-// with an FP32 result decode the codes to BF16 (exact) and take the BF16 instruction (4e-9 on the
-// same values), at half its rate.
 #include <hip/hip_runtime.h>
 
 #include "../../include/moe.h"
 #include "fp8.hpp"
+#include "fp8_wide.hpp"
 #include "gemm.hpp"
 #include "host.hpp"
 
@@ -114,26 +109,6 @@ __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int* prefix) {
   return t;
 }
 
-// a lane's 32 codes in BF16 (exact), 8 for each of four products of 32 k
-struct Wide {
-  bf16x8_t v[4];
-};
-__device__ __forceinline__ Wide widen(const i32x8_t& c) {
-  Wide w;
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    u32x4_t r;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t q = (uint32_t)c[2 * u + h];
-      r[2 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, false));
-      r[2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, true));
-    }
-    w.v[u] = __builtin_bit_cast(bf16x8_t, r);
-  }
-  return w;
-}
-
 template <class S, bool ROWS_B, bool F32, bool ADD>
 __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
   __shared__ __align__(16) uint8_t lds[S::LDS];
@@ -207,7 +182,6 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
     const u32x4_t u1 = *reinterpret_cast<const u32x4_t*>(q + (((q4 + 4) ^ swz_kc<128>(r)) << 4));
     return i32x8_t{(int)u0[0], (int)u0[1], (int)u0[2], (int)u0[3], (int)u1[0], (int)u1[1], (int)u1[2], (int)u1[3]};
   };
-  constexpr int kOne = 0x7f7f7f7f;         // E8M0 1.0: the hardware's own scales stay out
   issue(0);
   for (int kt = 0; kt < nk; ++kt) {
     wait_vm<0>();
@@ -242,13 +216,9 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
       if constexpr (ROWS_B) sb = *reinterpret_cast<const f32x4_t*>(sc + S::TM + n + 4 * q4);
 #pragma unroll
       for (int j = 0; j < S::MB; ++j) {
-        f32x4_t d{0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (F32) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ww.v[u], xw[j].v[u], d, 0, 0, 0);
-        } else {
-          d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, x[j], d, 0, 0, 0, kOne, 0, kOne);
-        }
+        f32x4_t d;
+        if constexpr (F32) d = wide_product(ww, xw[j]);
+        else d = code_product(wf, x[j]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][j][e] += (ROWS_B ? s[j] * sb[e] : s[j]) * d[e];
       }
@@ -336,7 +306,8 @@ moe_status check(const moe_fp8_matmul_problem* p) {
 }  // namespace
 
 void launch_matmul(hipStream_t st, const MatmulArgs& a) {
-  if (a.out_fp32) launch_shape<Small, true>(st, a);
+  if (a.M <= kFewRows) launch_few(st, a);
+  else if (a.out_fp32) launch_shape<Small, true>(st, a);
   else launch_shape<Large, false>(st, a);
 }
 

@@ -30,6 +30,8 @@ struct MatmulArgs {
   int out_fp32, accumulate, rows_b;
 };
 void launch_matmul(hipStream_t st, const MatmulArgs& a);
+constexpr int kFewRows = 64;               // in all groups together
+void launch_few(hipStream_t st, const MatmulArgs& a);
 
 }  // namespace fp8
 }  // namespace moe

@@ -1,0 +1,51 @@
+// The product of a block of 128 k for 16 rows of codes and 16 tokens' codes.
+//
+// The 8-bit matrix instructions keep a sum to about 2^-16 of its largest product (measured on
+// normal values, 128 products: 1.3e-5 of the result; the K = 32 form and sums of parts the same).  Under
+// the 2^-9 of a BF16 result that is nothing, in an FP32 one it would be the largest error by far.  So products
+// with an FP32 result decode the codes to BF16 (exact) and take the BF16 instruction (4e-9 on the
+// same values), at half its rate.
+#pragma once
+#include "common.hpp"
+
+namespace moe {
+namespace fp8 {
+
+// a lane's 32 codes in BF16 (exact), 8 for each of four products of 32 k
+struct Wide {
+  bf16x8_t v[4];
+};
+__device__ __forceinline__ Wide widen(const i32x8_t& c) {
+  Wide w;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    uint32_t r[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t q = (uint32_t)c[2 * u + h];
+      r[2 * h] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, false));
+      r[2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, 1.0f, true));
+    }
+    w.v[u] = __builtin_bit_cast(bf16x8_t, make_uint4(r[0], r[1], r[2], r[3]));
+  }
+  return w;
+}
+
+__device__ __forceinline__ f32x4_t wide_product(const Wide& a, const Wide& b) {
+  f32x4_t d{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int u = 0; u < 4; ++u) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[u], b.v[u], d, 0, 0, 0);
+  return d;
+}
+__device__ __forceinline__ f32x4_t code_product(const i32x8_t& a, const i32x8_t& b) {
+  constexpr int kOne = 0x7f7f7f7f;         // E8M0 1.0: the instruction's own scales stay out
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, kOne, 0, kOne);
+}
+template <bool F32>
+__device__ __forceinline__ f32x4_t block_product(const i32x8_t& a, const i32x8_t& b) {
+  if constexpr (F32) return wide_product(widen(a), widen(b));
+  else return code_product(a, b);
+}
+
+}  // namespace fp8
+}  // namespace moe
