@@ -527,14 +527,14 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
  * scale NaN and codes 0. */
 typedef enum { MOE_FP8_ROWS = 1, MOE_FP8_TILES = 2 } moe_fp8_blocks;
 #define MOE_FP8_TRANSPOSE 1u   /* write the transposed matrix's codes and scales              */
-#define MOE_FP8_ACCUMULATE 2u  /* moe_fp8_matmul: add to out                                  */
+#define MOE_FP8_ACCUMULATE 2u  /* moe_block_matmul: add to out                                  */
 typedef struct {
   int64_t rows;          /* R in [0, 2^31]                                                */
   int64_t cols;          /* C in [1, 2^24]                                                */
   int32_t kind;          /* moe_fp8_blocks: 128 values of a row, or 128 x 128              */
   int32_t dtype;         /* MOE_BF16 or MOE_FP32, of x                                    */
   uint32_t flags;        /* MOE_FP8_TRANSPOSE or 0                                        */
-} moe_fp8_quantize_problem;
+} moe_block_quantize_problem;
 
 /*  x       [R][C], any element-aligned base and any ld >= C (rows of whole 16-byte pieces at 16-byte
  *          alignment move in those)
@@ -544,7 +544,7 @@ typedef struct {
  *          all rows lie side by side), MOE_FP8_TILES [ceil(P / 128)][ceil(Q / 128)]
  * A weight gradient's operands are the transposed MOE_FP8_ROWS of the tokens' rows, a data
  * gradient's weight the transposed MOE_FP8_TILES. */
-moe_status moe_fp8_quantize(const moe_fp8_quantize_problem* p, const moe_rows* x, void* codes, float* scales,
+moe_status moe_block_quantize(const moe_block_quantize_problem* p, const moe_rows* x, void* codes, float* scales,
                             void* stream);
 
 /* Product of rows in groups, each group with a weight of its own (the tokens of each expert, sorted
@@ -559,7 +559,7 @@ typedef struct {
   int32_t scales;        /* moe_fp8_blocks of b: MOE_FP8_TILES, or MOE_FP8_ROWS with one group */
   int32_t out_dtype;     /* MOE_BF16 or MOE_FP32                                          */
   uint32_t flags;        /* MOE_FP8_ACCUMULATE or 0                                       */
-} moe_fp8_matmul_problem;
+} moe_block_matmul_problem;
 #define MOE_FP8_MAX_GROUPS 256
 /* (M / 64 + 1 + G) (N / 128 + 1) is at most 2^22 as well (MOE_ERR_SHAPE above). */
 
@@ -573,7 +573,7 @@ typedef struct {
  *            as the nearest end; descending ones leave rows of out unspecified
  *  out       [M][N], any element-aligned base and any ld >= N; must not overlap an input.
  *            Accumulation into BF16 rounds the product first, as a BF16 main_grad does */
-moe_status moe_fp8_matmul(const moe_fp8_matmul_problem* p, const moe_rows* a, const float* a_scales, const moe_mat* b,
+moe_status moe_block_matmul(const moe_block_matmul_problem* p, const moe_rows* a, const float* a_scales, const moe_mat* b,
                           const float* b_scales, const int32_t* offsets, const moe_rows* out, void* stream);
 
 /* A static description of a status code. */

@@ -42,7 +42,7 @@ EXPORTED = ("moe_saved_bytes", "moe_workspace_bytes", "moe_saved_view", "moe_for
             "moe_decode_workspace_bytes", "moe_forward_decode", "moe_router_forward", "moe_router_backward",
             "moe_norm_forward", "moe_norm_backward", "moe_norm_workspace_bytes", "moe_checkpoint_store",
             "moe_checkpoint_load", "moe_ffn_saved_bytes", "moe_ffn_workspace_bytes", "moe_ffn_saved_view",
-            "moe_ffn_forward", "moe_ffn_backward", "moe_fp8_quantize", "moe_fp8_matmul")
+            "moe_ffn_forward", "moe_ffn_backward", "moe_block_quantize", "moe_block_matmul")
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 MOE_DECODE_MAX_TOKENS = 64
 MOE_DECODE_MAX_INTERMEDIATE = 65536
@@ -115,12 +115,12 @@ class moe_ffn_saved_layout(C.Structure):
     _fields_ = [(n, C.c_size_t) for n in ("ab", "ab_scales", "x", "x_scales")]
 
 
-class moe_fp8_quantize_problem(C.Structure):
+class moe_block_quantize_problem(C.Structure):
     _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("kind", C.c_int32), ("dtype", C.c_int32),
                 ("flags", C.c_uint32)]
 
 
-class moe_fp8_matmul_problem(C.Structure):
+class moe_block_matmul_problem(C.Structure):
     _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("depth", C.c_int64), ("groups", C.c_int32),
                 ("scales", C.c_int32), ("out_dtype", C.c_int32), ("flags", C.c_uint32)]
 
@@ -202,11 +202,11 @@ def load(path: str | None = None):
     lib.moe_ffn_backward.argtypes = [P(moe_ffn_problem)] + [P(moe_rows)] * 5 + [C.c_void_p] + [P(moe_rows)] * 4 + [
         C.c_void_p, C.c_size_t, C.c_void_p]
     lib.moe_ffn_backward.restype = C.c_int
-    lib.moe_fp8_quantize.argtypes = [P(moe_fp8_quantize_problem), P(moe_rows), C.c_void_p, C.c_void_p, C.c_void_p]
-    lib.moe_fp8_quantize.restype = C.c_int
-    lib.moe_fp8_matmul.argtypes = [P(moe_fp8_matmul_problem), P(moe_rows), C.c_void_p, P(moe_mat), C.c_void_p,
+    lib.moe_block_quantize.argtypes = [P(moe_block_quantize_problem), P(moe_rows), C.c_void_p, C.c_void_p, C.c_void_p]
+    lib.moe_block_quantize.restype = C.c_int
+    lib.moe_block_matmul.argtypes = [P(moe_block_matmul_problem), P(moe_rows), C.c_void_p, P(moe_mat), C.c_void_p,
                                    C.c_void_p, P(moe_rows), C.c_void_p]
-    lib.moe_fp8_matmul.restype = C.c_int
+    lib.moe_block_matmul.restype = C.c_int
     if path is None:
         _lib = lib
     return lib
@@ -360,15 +360,15 @@ def moe_ffn_backward(p, grad_out, x, gate, up, down, saved, grad_x, grad_gate, g
                                    workspace_bytes, stream)
 
 
-def moe_fp8_quantize(p, x, codes, scales, stream) -> int:
+def moe_block_quantize(p, x, codes, scales, stream) -> int:
     """Raw call: x is a moe_rows (or None), the rest integer device addresses; returns the status."""
-    return load().moe_fp8_quantize(C.byref(p), _ref(x), codes, scales, stream)
+    return load().moe_block_quantize(C.byref(p), _ref(x), codes, scales, stream)
 
 
-def moe_fp8_matmul(p, a, a_scales, b, b_scales, offsets, out, stream) -> int:
+def moe_block_matmul(p, a, a_scales, b, b_scales, offsets, out, stream) -> int:
     """Raw call: a and out are moe_rows and b a moe_mat (or None), the rest integer device
     addresses; returns the status."""
-    return load().moe_fp8_matmul(C.byref(p), _ref(a), a_scales, _ref(b), b_scales, offsets, _ref(out), stream)
+    return load().moe_block_matmul(C.byref(p), _ref(a), a_scales, _ref(b), b_scales, offsets, _ref(out), stream)
 
 
 def moe_kernel_timer_enable(on: bool) -> None:
@@ -864,13 +864,13 @@ class Fp8Quantizer(_Fixed):
         import torch
         self.dtype = dtype or torch.bfloat16
         code = {"rows": MOE_FP8_ROWS, "tiles": MOE_FP8_TILES}.get(kind, 0)
-        self._p = moe_fp8_quantize_problem(0, 1, code, _moe_dtype(self.dtype, "Fp8Quantizer"),
+        self._p = moe_block_quantize_problem(0, 1, code, _moe_dtype(self.dtype, "Fp8Quantizer"),
                                            MOE_FP8_TRANSPOSE if transpose else 0)
-        st = moe_fp8_quantize(self._p, None, None, None, None)    # no rows: checks the options
+        st = moe_block_quantize(self._p, None, None, None, None)    # no rows: checks the options
         if st != MOE_OK:
             raise MoeError(st, "Fp8Quantizer")
         self.kind, self.transpose, q = kind, bool(transpose), self._p
-        self._problems = _Problems(lambda R, N: moe_fp8_quantize_problem(R, N, q.kind, q.dtype, q.flags))
+        self._problems = _Problems(lambda R, N: moe_block_quantize_problem(R, N, q.kind, q.dtype, q.flags))
 
     def shapes(self, rows, cols):
         """Shapes of codes and scales for x [rows, cols]."""
@@ -881,7 +881,7 @@ class Fp8Quantizer(_Fixed):
     def forward(self, x, codes, scales):
         """Writes codes (torch.float8_e4m3fn) and scales (float32) of x, of the shapes that shapes() gives."""
         import torch
-        where = "moe_fp8_quantize"
+        where = "moe_block_quantize"
         dev, (R, N) = _device(where, x), x.shape
         if N == 0:
             raise MoeError(MOE_ERR_SHAPE, where)
@@ -889,7 +889,7 @@ class Fp8Quantizer(_Fixed):
         qs, ss = self.shapes(R, N)
         _check(where, dev, codes, torch.float8_e4m3fn, qs)
         _check(where, dev, scales, torch.float32, ss)
-        _call(where, dev, load().moe_fp8_quantize, self._problems[R, N], rows, codes.data_ptr(), scales.data_ptr())
+        _call(where, dev, load().moe_block_quantize, self._problems[R, N], rows, codes.data_ptr(), scales.data_ptr())
         return codes, scales
 
 
@@ -902,19 +902,19 @@ class Fp8Matmul(_Fixed):
         import torch
         self.out_dtype = out_dtype or torch.bfloat16
         code = {"rows": MOE_FP8_ROWS, "tiles": MOE_FP8_TILES}.get(scales, 0)
-        self._p = moe_fp8_matmul_problem(0, 1, 16, 1, code, _moe_dtype(self.out_dtype, "Fp8Matmul"),
+        self._p = moe_block_matmul_problem(0, 1, 16, 1, code, _moe_dtype(self.out_dtype, "Fp8Matmul"),
                                          MOE_FP8_ACCUMULATE if accumulate else 0)
-        st = moe_fp8_matmul(self._p, None, None, None, None, None, None, None)    # no rows: checks the options
+        st = moe_block_matmul(self._p, None, None, None, None, None, None, None)    # no rows: checks the options
         if st != MOE_OK:
             raise MoeError(st, "Fp8Matmul")
         self.scales, q = scales, self._p
-        self._problems = _Problems(lambda M, N, K, G: moe_fp8_matmul_problem(M, N, K, G, q.scales, q.out_dtype, q.flags))
+        self._problems = _Problems(lambda M, N, K, G: moe_block_matmul_problem(M, N, K, G, q.scales, q.out_dtype, q.flags))
 
     def forward(self, a, a_scales, b, b_scales, out, offsets=None):
         """a [M, K], b [N, K] or [G, N, K] (contiguous groups), out [M, N]; scales as
-        moe_fp8_matmul describes them ([N / 128, K / 128] may stand for [1, ...]).  offsets: int32 [G + 1]."""
+        moe_block_matmul describes them ([N / 128, K / 128] may stand for [1, ...]).  offsets: int32 [G + 1]."""
         import torch
-        where, f8, f32 = "moe_fp8_matmul", torch.float8_e4m3fn, torch.float32
+        where, f8, f32 = "moe_block_matmul", torch.float8_e4m3fn, torch.float32
         dev, (M, K) = _device(where, a), a.shape
         if b is None:
             raise MoeError(MOE_ERR_NULL, where)
@@ -934,6 +934,6 @@ class Fp8Matmul(_Fixed):
         if offsets is not None:
             _check(where, dev, offsets, torch.int32, (G + 1,))
         ro = moe_rows(out.data_ptr() if out is not None else 0, _check_rows(where, dev, out, self.out_dtype, (M, N)))
-        _call(where, dev, load().moe_fp8_matmul, self._problems[M, N, K, G], ra, a_scales.data_ptr(),
+        _call(where, dev, load().moe_block_matmul, self._problems[M, N, K, G], ra, a_scales.data_ptr(),
               moe_mat(b.data_ptr(), N * K, None, K), b_scales.data_ptr(), _ptr(offsets) or None, ro)
         return out

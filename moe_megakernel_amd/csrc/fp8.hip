@@ -290,7 +290,7 @@ void launch_shape(hipStream_t st, const MatmulArgs& a) {
   else launch_as<S, false, F32>(st, a);
 }
 
-moe_status check(const moe_fp8_matmul_problem* p) {
+moe_status check(const moe_block_matmul_problem* p) {
   if (!p) return MOE_ERR_NULL;
   const int64_t M = p->rows, N = p->cols, K = p->depth;
   if (M < 0 || M > (1 << 24) || N < 1 || N > (1 << 20) || K < 16 || K > (1 << 24) || K % 16) return MOE_ERR_SHAPE;
@@ -316,7 +316,7 @@ void launch_matmul(hipStream_t st, const MatmulArgs& a) {
 
 using namespace moe;
 
-extern "C" moe_status moe_fp8_matmul(const moe_fp8_matmul_problem* p, const moe_rows* a, const float* a_scales,
+extern "C" moe_status moe_block_matmul(const moe_block_matmul_problem* p, const moe_rows* a, const float* a_scales,
                                      const moe_mat* b, const float* b_scales, const int32_t* offsets,
                                      const moe_rows* out, void* stream) {
   MOE_TRY(fp8::check(p));
@@ -342,5 +342,5 @@ extern "C" moe_status moe_fp8_matmul(const moe_fp8_matmul_problem* p, const moe_
   m.accumulate = (p->flags & MOE_FP8_ACCUMULATE) != 0;
   m.rows_b = p->scales == MOE_FP8_ROWS;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return launch("fp8_matmul", st, [&] { fp8::launch_matmul(st, m); });
+  return launch("block_matmul", st, [&] { fp8::launch_matmul(st, m); });
 }

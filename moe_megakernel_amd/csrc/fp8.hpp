@@ -13,7 +13,7 @@ struct QuantArgs {
   int64_t R, C;
   uint8_t* codes;         // [R][Cp], or transposed [C][Rp]; padded to multiples of 16
   int64_t ldq;
-  float* scales;          // see moe_fp8_quantize
+  float* scales;          // see moe_block_quantize
   int64_t lds;            // floats between rows of the scales
 };
 void launch_quantize(hipStream_t st, const QuantArgs& a, bool fp32, bool tiles, bool transpose);

@@ -218,7 +218,7 @@ void launch_quantize(hipStream_t st, const QuantArgs& a, bool fp32, bool tiles, 
 
 using namespace moe;
 
-extern "C" moe_status moe_fp8_quantize(const moe_fp8_quantize_problem* p, const moe_rows* x, void* codes,
+extern "C" moe_status moe_block_quantize(const moe_block_quantize_problem* p, const moe_rows* x, void* codes,
                                        float* scales, void* stream) {
   if (!p) return MOE_ERR_NULL;
   if (p->rows < 0 || p->rows > (1ll << 31) || p->cols < 1 || p->cols > (1 << 24)) return MOE_ERR_SHAPE;
@@ -234,5 +234,5 @@ extern "C" moe_status moe_fp8_quantize(const moe_fp8_quantize_problem* p, const 
   const int64_t lds = tiles ? ((turn ? R : C) + 127) / 128 : (turn ? C : R);
   const fp8::QuantArgs a{static_cast<const uint8_t*>(x->base), x->ld, R, C, static_cast<uint8_t*>(codes), up16, scales, lds};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return launch("fp8_quantize", st, [&] { fp8::launch_quantize(st, a, p->dtype == MOE_FP32, tiles, turn); });
+  return launch("block_quantize", st, [&] { fp8::launch_quantize(st, a, p->dtype == MOE_FP32, tiles, turn); });
 }
