@@ -477,7 +477,9 @@ typedef struct {
   int32_t grad_dtype;    /* MOE_FP32 or MOE_BF16: the weight gradients                    */
   uint32_t flags;        /* MOE_FFN_OVERWRITE_GRADS or 0                                  */
 } moe_ffn_problem;
-/* T (H + 2 I) is at most 2^38 as well (a launch holds 2^32 threads; MOE_ERR_SHAPE above). */
+/* T (H + 2 I) is at most 2^38 as well (a launch holds 2^32 threads; MOE_ERR_SHAPE above), and rows of every
+ * matrix at most MOE_FFN_MAX_LD elements apart (MOE_ERR_LAYOUT above). */
+#define MOE_FFN_MAX_LD (1 << 22)
 
 /* Byte offsets inside `saved`: ab [T][2I] (a at column j, b at I + j) in BF16, or int8 codes with
  * their scale bytes ab_scales [T][2I / 32], and x codes [T][H] with x_scales [T][H / 32] (the last

@@ -30,7 +30,10 @@ SOURCES = [
     ("ffn_api.hip", []),                     # the gated feed-forward block: checks and launches
     ("ffn.hip", []),                         # its products over many tokens
     ("ffn_few.hip", []),                     # and over a few
-    ("fp8.hip", []),                         # 8-bit products with scales of 128
+    # 8-bit products with scales of 128: a block's products are scaled by vector instructions, so
+    # they belong in vector registers (by default the compiler puts results of kernels this large into the
+    # accumulation registers and moves each value back)
+    ("fp8.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]),
     ("fp8_few.hip", []),                     # over a few rows
     ("fp8_quantize.hip", []),                # their operands
 ]

@@ -18,14 +18,30 @@ namespace dense {
 
 using namespace gemm;
 
-// acc += A[TM x K] B[TN x K]^T.
-//  KC operand: f(r) -> bytes of tile row r at K = 0, called for r < rows (the others are zero);
-//              K is then a multiple of the stage.
-//  RC operand: f(k) -> bytes of element (k, tile row 0), called for k < kdim; tile rows at or past
-//              rows (a multiple of 8) are zero.
-template <class TL, int AM, int BM, class FA, class FB>
-__device__ __forceinline__ void tile_product(Acc<TL>& acc, int kdim, const FA& fa, int arows, const FB& fb, int brows,
-                                             uint8_t* lds) {
+// LDS copy with a uniform base and a 32-bit offset a lane: no vector instruction moves the address on.
+__device__ __forceinline__ void dma16s(const uint8_t* base, uint32_t off, uint32_t m0v) {
+  const uint32_t m = __builtin_amdgcn_readfirstlane(m0v);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(m)
+               : "memory", "m0");
+}
+
+// An operand of tile_product: `p` its element (tile row 0, K = 0), rows `ld` bytes apart (64 rows, and a KC
+// tile's rows, span less than 2^32 bytes), `rows` > 0 tile rows exist (RC: a multiple of 8).
+//  KC: consecutive K, rows of the tile `ld` apart; RC: consecutive tile rows, K `ld` apart;
+//  KC2: as KC, 32 rows of one matrix and 32 of a second one (p2, ld2) in turn; rows counts both.
+struct Operand {
+  const uint16_t* p;
+  int64_t ld;
+  int rows;
+  const uint16_t* p2 = nullptr;
+  int64_t ld2 = 0;
+};
+constexpr int KC2 = 2;
+
+// acc += A[TM x K] B[TN x K]^T.  Tile rows past the last repeat it (their results are not used).  With a KC operand
+// K is a multiple of the stage; with two RC ones the last stage's k past K are zeros.
+template <class TL, int AM, int BM>
+__device__ __forceinline__ void tile_product(Acc<TL>& acc, int kdim, const Operand& A, const Operand& B, uint8_t* lds) {
   constexpr int KB = TL::KB, KST = KB / 2, NKS = KST / 16, NS = TL::NS;
   constexpr int RBA = TL::TM * 2, RBB = TL::TN * 2;       // bytes of a row-contiguous stage row
   constexpr int LPS = TL::A_DMA + TL::B_DMA;              // copies a stage and wave
@@ -34,59 +50,62 @@ __device__ __forceinline__ void tile_product(Acc<TL>& acc, int kdim, const FA& f
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w / TL::NWN, wn = w % TL::NWN;
   const uint32_t lds0 = lds_off(lds);
-  const uint8_t* zp = reinterpret_cast<const uint8_t*>(g_zero_page) + 16 * lane;
   const int nk = (kdim + KST - 1) / KST;
   if (nk == 0) return;
 
-  // the lane's source of each copy: KC: a pointer that moves KB a stage (or stays, on zeros); RC:
-  // the row within the stage and the byte inside it
-  const uint8_t *pa[TL::A_DMA], *pb[TL::B_DMA];
-  int ka[TL::A_DMA], kb[TL::B_DMA], ca[TL::A_DMA], cb[TL::B_DMA];
-  auto setup = [&](auto mode, int dma, int rb, const auto& f, int rows, const uint8_t** p, int* kr, int* cr)
-                   __attribute__((always_inline)) {
+  // the lane's offset of each copy from the stage's first byte, and (RC) its k within the stage
+  uint32_t oa[TL::A_DMA], ob[TL::B_DMA];
+  auto rc_k = [&](int copy, int rb) { return (copy * 1024 + 16 * lane) / rb; };
+  auto setup = [&](auto mode, int dma, int rb, const Operand& X, uint32_t* o) __attribute__((always_inline)) {
     for (int i = 0; i < dma; ++i) {
       const int off = (w * dma + i) * 1024 + 16 * lane;
       if constexpr (decltype(mode)::value == KC) {
         const int r = off / KB, c = ((off % KB) >> 4) ^ swz_kc<KB>(r);
-        p[i] = r < rows ? reinterpret_cast<const uint8_t*>(f(r)) + 16 * c : zp;
-        kr[i] = r < rows ? KB : 0;
-        cr[i] = 0;
+        o[i] = (uint32_t)(min(r, X.rows - 1) * X.ld) + 16 * c;
+      } else if constexpr (decltype(mode)::value == KC2) {
+        const int r = off / KB, c = ((off % KB) >> 4) ^ swz_kc<KB>(r);
+        o[i] = (uint32_t)(min((r >> 6) * 32 + (r & 31), X.rows / 2 - 1) * ((r >> 5) & 1 ? X.ld2 : X.ld)) + 16 * c;
       } else {
         const int k = off / rb, c = ((off % rb) >> 4) ^ swz_rc16(k);
-        p[i] = nullptr;
-        kr[i] = 8 * c < rows ? k : (1 << 30);
-        cr[i] = 16 * c;
+        o[i] = (uint32_t)(k * X.ld) + 16 * min(c, X.rows / 8 - 1);
       }
     }
   };
-  setup(std::integral_constant<int, AM>{}, TL::A_DMA, RBA, fa, arows, pa, ka, ca);
-  setup(std::integral_constant<int, BM>{}, TL::B_DMA, RBB, fb, brows, pb, kb, cb);
-
-  auto issue = [&](int kt) __attribute__((always_inline)) {
-    const uint32_t sa = lds0 + (kt % NS) * TL::A_BYTES;
-    const uint32_t sb = lds0 + NS * TL::A_BYTES + (kt % NS) * TL::B_BYTES;
+  using MA = std::integral_constant<int, AM>;
+  using MB = std::integral_constant<int, BM>;
+  setup(MA{}, TL::A_DMA, RBA, A, oa);
+  setup(MB{}, TL::B_DMA, RBB, B, ob);
+  const uint8_t *ga = reinterpret_cast<const uint8_t*>(A.p), *gb = reinterpret_cast<const uint8_t*>(B.p);   // the next stage's
+  const uint8_t* gb2 = reinterpret_cast<const uint8_t*>(B.p2);
+  const int64_t sa = AM == RC ? KST * A.ld : KB, sb = BM == RC ? KST * B.ld : KB;
+  static_assert(AM != KC2, "the second operand may come from two matrices");
+  int put = 0;                                              // its slot in the ring
+  auto issue = [&]() __attribute__((always_inline)) {
+    const uint32_t la = lds0 + put * TL::A_BYTES, lb = lds0 + NS * TL::A_BYTES + put * TL::B_BYTES;
 #pragma unroll
-    for (int i = 0; i < TL::A_DMA; ++i) {
-      const uint32_t m0v = sa + (w * TL::A_DMA + i) * 1024;
-      if constexpr (AM == KC) {
-        dma16(pa[i], m0v);
-        pa[i] += ka[i];
-      } else {
-        const int k = kt * KST + ka[i];
-        dma16(k < kdim ? reinterpret_cast<const uint8_t*>(fa(k)) + ca[i] : zp, m0v);
-      }
-    }
+    for (int i = 0; i < TL::A_DMA; ++i) dma16s(ga, oa[i], la + (w * TL::A_DMA + i) * 1024);
 #pragma unroll
     for (int i = 0; i < TL::B_DMA; ++i) {
-      const uint32_t m0v = sb + (w * TL::B_DMA + i) * 1024;
-      if constexpr (BM == KC) {
-        dma16(pb[i], m0v);
-        pb[i] += kb[i];
-      } else {
-        const int k = kt * KST + kb[i];
-        dma16(k < kdim ? reinterpret_cast<const uint8_t*>(fb(k)) + cb[i] : zp, m0v);
-      }
+      constexpr int kCopies = 32 * KB / 1024;   // of 32 rows
+      const bool second = BM == KC2 && (((w * TL::B_DMA + i) / kCopies) & 1);
+      dma16s(second ? gb2 : gb, ob[i], lb + (w * TL::B_DMA + i) * 1024);
     }
+    ga += sa;
+    gb += sb;
+    if constexpr (BM == KC2) gb2 += sb;
+    put = put + 1 == NS ? 0 : put + 1;
+  };
+  // the last stage, which may end early
+  auto issue_last = [&]() __attribute__((always_inline)) {
+    const int left = kdim - (nk - 1) * KST;
+    if (AM != RC || BM != RC || left == KST) {
+      issue();
+      return;
+    }
+    const uint32_t la = lds0 + put * TL::A_BYTES, lb = lds0 + NS * TL::A_BYTES + put * TL::B_BYTES;
+    const uint8_t* zp = reinterpret_cast<const uint8_t*>(g_zero_page) + 16 * lane;
+    for (int i = 0; i < TL::A_DMA; ++i) dma16(rc_k(w * TL::A_DMA + i, RBA) < left ? ga + oa[i] : zp, la + (w * TL::A_DMA + i) * 1024);
+    for (int i = 0; i < TL::B_DMA; ++i) dma16(rc_k(w * TL::B_DMA + i, RBB) < left ? gb + ob[i] : zp, lb + (w * TL::B_DMA + i) * 1024);
   };
 
   const int g = lane >> 5, grp = lane >> 4, j16 = lane & 15;
@@ -95,7 +114,7 @@ __device__ __forceinline__ void tile_product(Acc<TL>& acc, int kdim, const FA& f
   };
   // one 32-row fragment of K step ks from a stage's operand tile, tile rows from r0
   auto frag = [&](auto mode, const uint8_t* tile, int rb, int r0, int ks) __attribute__((always_inline)) {
-    if constexpr (decltype(mode)::value == KC) {
+    if constexpr (decltype(mode)::value != RC) {
       const int r = r0 + (lane & 31);
       return *reinterpret_cast<const bf16x8_t*>(tile + r * KB + (((2 * ks + g) ^ swz_kc<KB>(r)) << 4));
     } else {
@@ -111,13 +130,13 @@ __device__ __forceinline__ void tile_product(Acc<TL>& acc, int kdim, const FA& f
       return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
     }
   };
-  auto load = [&](int kt, int ks, Frags& f) __attribute__((always_inline)) {
-    const uint8_t* At = lds + (kt % NS) * TL::A_BYTES;
-    const uint8_t* Bt = lds + NS * TL::A_BYTES + (kt % NS) * TL::B_BYTES;
+  auto load = [&](int slot, int ks, Frags& f) __attribute__((always_inline)) {
+    const uint8_t* At = lds + slot * TL::A_BYTES;
+    const uint8_t* Bt = lds + NS * TL::A_BYTES + slot * TL::B_BYTES;
 #pragma unroll
-    for (int j = 0; j < TL::NJ; ++j) f.b[j] = frag(std::integral_constant<int, BM>{}, Bt, RBB, wn * TL::WNC + j * 32, ks);
+    for (int j = 0; j < TL::NJ; ++j) f.b[j] = frag(MB{}, Bt, RBB, wn * TL::WNC + j * 32, ks);
 #pragma unroll
-    for (int i = 0; i < TL::MI; ++i) f.a[i] = frag(std::integral_constant<int, AM>{}, At, RBA, wm * TL::WMR + i * 32, ks);
+    for (int i = 0; i < TL::MI; ++i) f.a[i] = frag(MA{}, At, RBA, wm * TL::WMR + i * 32, ks);
   };
   auto mma = [&](const Frags& f) __attribute__((always_inline)) {
 #pragma unroll
@@ -126,40 +145,46 @@ __device__ __forceinline__ void tile_product(Acc<TL>& acc, int kdim, const FA& f
       for (int j = 0; j < TL::NJ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
   };
-  // waits until stage kt of the wave's copies is in LDS (those of `later` stages may fly)
-  auto landed = [&](int later) __attribute__((always_inline)) {
-    if (NS >= 4 && later >= 2) wait_vm<NS >= 4 ? 2 * LPS : 0>();
-    else if (NS >= 3 && later >= 1) wait_vm<NS >= 3 ? LPS : 0>();
-    else wait_vm<0>();
-  };
 
-  for (int s = 0; s < NS - 1; ++s)
-    if (s < nk) issue(s);
-  landed(min(NS - 2, nk - 1));
+  for (int s = 0; s < min(NS - 1, nk - 1); ++s) issue();
+  if (nk < NS) {
+    issue_last();
+    wait_vm<0>();
+  } else {
+    wait_vm<(NS - 2) * LPS>();
+  }
   __syncthreads();
   Frags f[2];
+  int slot = 0;
   load(0, 0, f[0]);
-  // Stage kt: its first fragments are on their way.  Its copies' ring slot for stage kt + NS - 1 is
-  // that of stage kt - 1, which every wave has read by the barrier that opened stage kt.
-  for (int kt = 0; kt < nk - 1; ++kt) {
-    if (kt + NS - 1 < nk) issue(kt + NS - 1);
+  // A stage: its first fragments are on their way.  Its copies go to the slot of the stage before, which every
+  // wave has read by the barrier that opened this one; that of the next stage waits for its copies, those of
+  // FLY stages after it may fly.  The steady loop has no branch: products touch no memory, so the compiler would
+  // move them past branches and barriers to where their results are used.
+  auto stage = [&](auto what, auto fly) __attribute__((always_inline)) {
+    const int next = slot + 1 == NS ? 0 : slot + 1;
+    if constexpr (decltype(what)::value == 0) issue();
+    if constexpr (decltype(what)::value == 1) issue_last();
 #pragma unroll
     for (int ks = 0; ks < NKS; ++ks) {
+      __builtin_amdgcn_sched_barrier(0);
       if (ks + 1 < NKS) {
-        load(kt, ks + 1, f[(ks + 1) & 1]);
-      } else {
-        landed(min(NS - 2, nk - 2 - kt));
+        load(slot, ks + 1, f[(ks + 1) & 1]);
+      } else if constexpr (decltype(what)::value != 3) {
+        wait_vm<decltype(fly)::value * LPS>();
         __syncthreads();
-        load(kt + 1, 0, f[0]);
+        __builtin_amdgcn_sched_barrier(0);
+        load(next, 0, f[0]);
       }
       mma(f[ks & 1]);
     }
-  }
-#pragma unroll
-  for (int ks = 0; ks < NKS; ++ks) {
-    if (ks + 1 < NKS) load(nk - 1, ks + 1, f[(ks + 1) & 1]);
-    mma(f[ks & 1]);
-  }
+    slot = next;
+  };
+  using std::integral_constant;
+  for (int kt = 0; kt < nk - NS; ++kt) stage(integral_constant<int, 0>{}, integral_constant<int, NS - 2>{});
+  if (nk >= NS) stage(integral_constant<int, 1>{}, integral_constant<int, NS - 2>{});
+  for (int kt = max(nk - NS + 1, 0); kt < nk - 1; ++kt) stage(integral_constant<int, 2>{}, integral_constant<int, 0>{});
+  stage(integral_constant<int, 3>{}, integral_constant<int, 0>{});
 }
 
 // Tile of a block: the blocks that one XCD receives (blockIdx % 8) walk a contiguous eighth of the

@@ -38,16 +38,12 @@ __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_up(UpArgs p) {
   const int m0 = at.m * TL::TM, i0 = at.n * TI, rows = min(TL::TM, p.T - m0), cols = min(TI, p.I - i0);
   Acc<TL> acc;
   zero_acc<TL>(acc);
-  const uint16_t* x = p.x.p + (int64_t)m0 * p.x.ld;
-  const uint16_t *wg = p.gate.p + (int64_t)i0 * p.gate.ld, *wu = p.up.p + (int64_t)i0 * p.up.ld;
-  auto fa = [&](int r) { return x + (int64_t)r * p.x.ld; };
   // 32 gate rows, 32 up rows in turn: a lane's accumulators of blocks 2j and 2j + 1 are a and b of the
   // same elements; cols is a multiple of 64, so the rows that exist come first
-  auto fb = [&](int r) {
-    const int64_t i = (r >> 6) * 32 + (r & 31);
-    return (r >> 5) & 1 ? wu + i * p.up.ld : wg + i * p.gate.ld;
-  };
-  tile_product<TL, KC, KC>(acc, p.H, fa, rows, fb, 2 * cols, lds);
+  const Operand x{p.x.p + (int64_t)m0 * p.x.ld, 2 * p.x.ld, rows};
+  const Operand w{p.gate.p + (int64_t)i0 * p.gate.ld, 2 * p.gate.ld, 2 * cols,
+                  p.up.p + (int64_t)i0 * p.up.ld, 2 * p.up.ld};
+  tile_product<TL, KC, KC2>(acc, p.H, x, w, lds);
   each_piece<TL, true>(acc, lds, rows, cols, [&](int row, int col, const float* a, const float* b) {
     const int64_t R = m0 + row;
     const int i = i0 + col;
@@ -76,7 +72,8 @@ __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_up(UpArgs p) {
   });
 }
 
-// BM = KC: b0 rows are the result's columns; RC: b0 rows run along K, those from ksplit on in b1
+// BM = KC: b0 rows are the result's columns (ksplit = K); RC: b0 rows run along K, those of its second half in
+// b1 (K = 2 ksplit)
 template <class TL, int BM>
 __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_rows(RowsArgs p) {
   __shared__ __align__(16) uint8_t lds[TL::LDS];
@@ -85,13 +82,17 @@ __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_rows(RowsArgs p) {
   const int m0 = at.m * TL::TM, n0 = at.n * TL::TN, rows = min(TL::TM, p.T - m0), cols = min(TL::TN, p.N - n0);
   Acc<TL> acc;
   zero_acc<TL>(acc);
-  const uint16_t* a = p.a.p + (int64_t)m0 * p.a.ld;
-  auto fa = [&](int r) { return a + (int64_t)r * p.a.ld; };
-  auto fb = [&](int r) {
-    if constexpr (BM == KC) return p.b0.p + (int64_t)(n0 + r) * p.b0.ld;
-    else return (r < p.ksplit ? p.b0.p + (int64_t)r * p.b0.ld : p.b1.p + (int64_t)(r - p.ksplit) * p.b1.ld) + n0;
-  };
-  tile_product<TL, KC, BM>(acc, p.K, fa, rows, fb, cols, lds);
+  Operand a{p.a.p + (int64_t)m0 * p.a.ld, 2 * p.a.ld, rows};
+  Operand b{BM == KC ? p.b0.p + (int64_t)n0 * p.b0.ld : p.b0.p + n0, 2 * p.b0.ld, cols};
+  for (int k = 0; k < p.K; k += p.ksplit) {
+    if (k > 0) {
+      __syncthreads();                       // the first part's stages have been read
+      a.p += k;
+      b.p = p.b1.p + n0;
+      b.ld = 2 * p.b1.ld;
+    }
+    tile_product<TL, KC, BM>(acc, p.ksplit, a, b, lds);
+  }
   each_piece<TL, false>(acc, lds, rows, cols, [&](int row, int col, const float* v) {
     *reinterpret_cast<uint4*>(p.c.p + (int64_t)(m0 + row) * p.c.ld + n0 + col) = pack8(v);
   });
@@ -105,10 +106,8 @@ __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_dh(DhArgs p) {
   const int m0 = at.m * TL::TM, n0 = at.n * TL::TN, rows = min(TL::TM, p.T - m0), cols = min(TL::TN, p.I - n0);
   Acc<TL> acc;
   zero_acc<TL>(acc);
-  const uint16_t *dy = p.dy.p + (int64_t)m0 * p.dy.ld, *wd = p.down.p + n0;
-  auto fa = [&](int r) { return dy + (int64_t)r * p.dy.ld; };
-  auto fb = [&](int k) { return wd + (int64_t)k * p.down.ld; };
-  tile_product<TL, KC, RC>(acc, p.H, fa, rows, fb, cols, lds);
+  tile_product<TL, KC, RC>(acc, p.H, {p.dy.p + (int64_t)m0 * p.dy.ld, 2 * p.dy.ld, rows},
+                           {p.down.p + n0, 2 * p.down.ld, cols}, lds);
   each_piece<TL, false>(acc, lds, rows, cols, [&](int row, int col, const float* dh) {
     const int64_t R = m0 + row;
     const int i = n0 + col;
@@ -147,9 +146,7 @@ __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_wgrad(WgradArgs p) {
   const int m0 = at.m * TL::TM, n0 = at.n * TL::TN, rows = min(TL::TM, p.M - m0), cols = min(TL::TN, p.N - n0);
   Acc<TL> acc;
   zero_acc<TL>(acc);
-  auto fa = [&](int k) { return p.a.p + (int64_t)k * p.a.ld + m0; };
-  auto fb = [&](int k) { return p.b.p + (int64_t)k * p.b.ld + n0; };
-  tile_product<TL, RC, RC>(acc, p.T, fa, rows, fb, cols, lds);
+  tile_product<TL, RC, RC>(acc, p.T, {p.a.p + m0, 2 * p.a.ld, rows}, {p.b.p + n0, 2 * p.b.ld, cols}, lds);
   each_piece<TL, false>(acc, lds, rows, cols, [&](int row, int col, const float* v) {
     const int m = m0 + row;
     const int64_t at0 = m < p.msplit ? (int64_t)m * p.ldc0 : (int64_t)(m - p.msplit) * p.ldc1;

@@ -74,7 +74,7 @@ Bwd bwd_layout(const moe_ffn_problem* p) {
 // A matrix of `cols` columns that moves in 16-byte pieces.
 moe_status check_rows(const moe_rows* m, int64_t cols, int per16) {
   if (!m || !m->base) return MOE_ERR_NULL;
-  if (m->ld < cols || m->ld % per16 || m->ld > (int64_t)1 << 40 || !aligned16(m->base)) return MOE_ERR_LAYOUT;
+  if (m->ld < cols || m->ld % per16 || m->ld > MOE_FFN_MAX_LD || !aligned16(m->base)) return MOE_ERR_LAYOUT;
   return MOE_OK;
 }
 moe_status check_bf16(const moe_rows* m, int64_t cols) { return check_rows(m, cols, 8); }

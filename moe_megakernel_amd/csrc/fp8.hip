@@ -29,16 +29,23 @@ namespace {
 
 constexpr int kKB = 128;                   // k of a stage, and of a scale
 
-template <int TN_, int TM_, int NWN_, int NWM_, int MINB_>
+// Tile of TN weight rows and TM tokens; NSW stages of weights in LDS, two of tokens.
+template <int TN_, int TM_, int NWN_, int NWM_, int MINB_, int NSW_>
 struct Shape {
-  static constexpr int TN = TN_, TM = TM_, NWN = NWN_, NWM = NWM_, MINB = MINB_;
+  static constexpr int TN = TN_, TM = TM_, NWN = NWN_, NWM = NWM_, MINB = MINB_, NSW = NSW_;
   static constexpr int NW = NWN * NWM, NTH = 64 * NW;
   static constexpr int NB = TN / NWN / 16, MB = TM / NWM / 16;   // 16 x 16 blocks of a wave
-  static constexpr int W_DMA = TN * kKB / 1024 / NW, A_DMA = TM * kKB / 1024 / NW;
-  static constexpr int STAGE = (TN + TM) * kKB, SCALES = 4 * (TN + TM);
-  static constexpr int LDS = 2 * (STAGE + SCALES);
-  static_assert(TN * kKB % (1024 * NW) == 0 && TM * kKB % (1024 * NW) == 0, "copies a wave");
-  static_assert(TN % 64 == 0 && TM % 64 == 0, "scale copies");
+  static constexpr int W_BYTES = TN * kKB, A_BYTES = TM * kKB;
+  static constexpr int W_DMA = W_BYTES / 1024 / NW, A_DMA = A_BYTES / 1024 / NW;   // copies a wave and stage
+  static_assert(W_BYTES % (1024 * NW) == 0 && A_BYTES % (1024 * NW) == 0, "copies a wave");
+  static_assert(TN % 64 == 0 && TM % 64 == 0 && (NSW == 2 || NSW == 3), "scale copies, ring");
+  static_assert(NB * 16 <= 128 && 128 % (NB * 16) == 0 && NB >= 4 && NB % 2 == 0 && NB * MB % 2 == 0, "one weight scale a wave");
+  // copies of 64 scales: the tokens', then the weights' rows' or those of the tile's 128-row parts; the same
+  // number a wave, so that its copies can be counted
+  template <bool ROWS_B>
+  static constexpr int scale_copies() { return (TM / 64 + (ROWS_B ? TN / 64 : 1) + NW - 1) / NW * NW; }
+  template <bool ROWS_B>
+  static constexpr int lds() { return NSW * (W_BYTES + 256 * scale_copies<ROWS_B>()) + 2 * A_BYTES; }
 };
 
 struct Tile {
@@ -111,7 +118,7 @@ __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int* prefix) {
 
 template <class S, bool ROWS_B, bool F32, bool ADD>
 __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
-  __shared__ __align__(16) uint8_t lds[S::LDS];
+  __shared__ __align__(16) uint8_t lds[S::template lds<ROWS_B>()];
   const Tile t = find_tile<S>(p, reinterpret_cast<int*>(lds));
   if (!t.ok) return;
   __syncthreads();                         // the groups' table is read before the stages take its place
@@ -122,49 +129,52 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
   const uint8_t* zp = reinterpret_cast<const uint8_t*>(g_zero_page) + 16 * lane;
   const int nk = (p.K + kKB - 1) / kKB;
 
-  // stage: weights [TN][128], tokens [TM][128] (16-byte chunks swizzled by row), then the scales:
-  // tokens' [TM], and weights' [TN] (ROWS_B) or of the tile's 128-column parts
+  // LDS: the weights' stages [NSW][TN][128], the tokens' [2][TM][128] (16-byte chunks swizzled by row), the
+  // scales' [NSW].  Rows past the last repeat it, their results go nowhere; chunks past the last k are zeros.
+  constexpr int SC = S::template scale_copies<ROWS_B>(), SC_DMA = SC / S::NW;
+  constexpr int A0 = S::NSW * S::W_BYTES, SC0 = A0 + 2 * S::A_BYTES;
   const uint8_t *pw[S::W_DMA], *pa[S::A_DMA];
-  int kw[S::W_DMA], kx[S::A_DMA];          // the chunk's first k, or past any K for rows that do not exist
 #pragma unroll
   for (int i = 0; i < S::W_DMA; ++i) {
     const int off = (w * S::W_DMA + i) * 1024 + 16 * lane, r = off / kKB, c = ((off % kKB) >> 4) ^ swz_kc<128>(r);
-    pw[i] = p.b + (int64_t)t.g * p.stride_b + (int64_t)(t.n0 + r) * p.ldb + 16 * c;
-    kw[i] = r < cols ? 16 * c : 1 << 30;
+    pw[i] = p.b + (int64_t)t.g * p.stride_b + (int64_t)(t.n0 + min(r, cols - 1)) * p.ldb + 16 * c;
   }
 #pragma unroll
   for (int i = 0; i < S::A_DMA; ++i) {
     const int off = (w * S::A_DMA + i) * 1024 + 16 * lane, r = off / kKB, c = ((off % kKB) >> 4) ^ swz_kc<128>(r);
-    pa[i] = p.a + (int64_t)(t.m0 + r) * p.lda + 16 * c;
-    kx[i] = r < rows ? 16 * c : 1 << 30;
+    pa[i] = p.a + (int64_t)(t.m0 + min(r, rows - 1)) * p.lda + 16 * c;
   }
-  const int sb_rows = (p.N + 127) / 128, sb_cols = nk;
-  auto issue = [&](int kt) __attribute__((always_inline)) {
-    const uint32_t base = lds0 + (kt & 1) * (S::STAGE + S::SCALES);
-    const int k0 = kt * kKB;
-#pragma unroll
-    for (int i = 0; i < S::W_DMA; ++i) {
-      dma16(k0 + kw[i] < p.K ? pw[i] : zp, base + (w * S::W_DMA + i) * 1024);
-      pw[i] += kKB;
-    }
-#pragma unroll
-    for (int i = 0; i < S::A_DMA; ++i) {
-      dma16(k0 + kx[i] < p.K ? pa[i] : zp, base + S::TN * kKB + (w * S::A_DMA + i) * 1024);
-      pa[i] += kKB;
-    }
-    for (int i = w; i < S::TM / 64 + (ROWS_B ? S::TN / 64 : 1); i += S::NW) {
-      const void* src = reinterpret_cast<const uint8_t*>(g_zero_page) + 4 * lane;
-      if (i < S::TM / 64) {
-        if (64 * i + lane < rows) src = p.sa + (int64_t)kt * p.M + t.m0 + 64 * i + lane;
-      } else if (ROWS_B) {
-        const int n = 64 * (i - S::TM / 64) + lane;
-        if (n < cols) src = p.sb + (int64_t)kt * p.N + t.n0 + n;
-      } else {
-        const int n = t.n0 / 128 + lane;
-        if (lane < (S::TN + 127) / 128 && n < sb_rows) src = p.sb + ((int64_t)t.g * sb_rows + n) * sb_cols + kt;
+  // copies of a stage; `copy` holds rows 8 copy .. 8 copy + 7, and swz_kc has period 16
+  auto copies = [&](int kt, const uint8_t** q, int n, int first, uint32_t to) __attribute__((always_inline)) {
+    if (kt * kKB + kKB <= p.K) {
+      for (int i = 0; i < n; ++i) {
+        dma16(q[i], to + (first + i) * 1024);
+        q[i] += kKB;
       }
-      dma4(src, base + S::STAGE + 256 * i);
+    } else {
+      for (int i = 0; i < n; ++i) {
+        const int k = kt * kKB + 16 * ((lane & 7) ^ swz_kc<128>(8 * (first + i) + (lane >> 3)));
+        dma16(k < p.K ? q[i] : zp, to + (first + i) * 1024);
+      }
     }
+  };
+  const int sb_rows = (p.N + 127) / 128;
+  const float* sb0 = ROWS_B ? p.sb + t.n0
+                            : p.sb + ((int64_t)t.g * sb_rows + min(t.n0 / 128 + min(lane, S::TN / 128 - 1), sb_rows - 1)) * nk;
+  auto issue_w = [&](int kt, int slot) __attribute__((always_inline)) {
+    copies(kt, pw, S::W_DMA, w * S::W_DMA, lds0 + slot * S::W_BYTES);
+#pragma unroll
+    for (int u = 0; u < SC_DMA; ++u) {
+      const int i = u * S::NW + w;
+      const float* src;
+      if (i < S::TM / 64) src = p.sa + (int64_t)kt * p.M + t.m0 + min(64 * i + lane, rows - 1);
+      else if (ROWS_B) src = sb0 + (int64_t)kt * p.N + min(64 * (i - S::TM / 64) + lane, cols - 1);
+      else src = sb0 + kt;
+      dma4(src, lds0 + SC0 + (slot * SC + i) * 256);
+    }
+  };
+  auto issue_a = [&](int kt) __attribute__((always_inline)) {
+    copies(kt, pa, S::A_DMA, w * S::A_DMA, lds0 + A0 + (kt & 1) * S::A_BYTES);
   };
 
   f32x4_t acc[S::NB][S::MB];
@@ -173,57 +183,111 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
 #pragma unroll
     for (int j = 0; j < S::MB; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // a lane's 32 codes of row r16 of a 16-row block: chunks q4 and q4 + 4 (which 32 is free, as long as
-  // both operands agree)
-  auto frag = [&](const uint8_t* tile, int r0) __attribute__((always_inline)) {
-    const int r = r0 + r16;
-    const uint8_t* q = tile + r * kKB;
-    const u32x4_t u0 = *reinterpret_cast<const u32x4_t*>(q + ((q4 ^ swz_kc<128>(r)) << 4));
-    const u32x4_t u1 = *reinterpret_cast<const u32x4_t*>(q + (((q4 + 4) ^ swz_kc<128>(r)) << 4));
+  // A lane's 32 codes of row r16 of a 16-row block: chunks q4 and q4 + 4 (which 32 is free, as long as
+  // both operands agree).  The swizzle is the same for every block, so the blocks lie at constant distances.
+  const int f0 = r16 * kKB + ((q4 ^ swz_kc<128>(r16)) << 4), f1 = f0 ^ 64;
+  auto frag = [&](const uint8_t* block) __attribute__((always_inline)) {
+    const u32x4_t u0 = *reinterpret_cast<const u32x4_t*>(block + f0), u1 = *reinterpret_cast<const u32x4_t*>(block + f1);
     return i32x8_t{(int)u0[0], (int)u0[1], (int)u0[2], (int)u0[3], (int)u1[0], (int)u1[1], (int)u1[2], (int)u1[3]};
   };
-  issue(0);
-  for (int kt = 0; kt < nk; ++kt) {
-    wait_vm<0>();
-    __syncthreads();
-    if (kt + 1 < nk) issue(kt + 1);
-    const uint8_t* W = lds + (kt & 1) * (S::STAGE + S::SCALES);
-    const uint8_t* A = W + S::TN * kKB;
-    const float* sc = reinterpret_cast<const float*>(W + S::STAGE);
+  struct Tokens {                          // a stage's token fragments and scales
     i32x8_t x[S::MB];
-    [[maybe_unused]] Wide xw[F32 ? S::MB : 1];
     float s[S::MB];
+  };
+  struct Weights {                         // 16 weight rows and their scales
+    i32x8_t w;
+    f32x4_t s;
+  };
+  const uint8_t *lw = lds + wn * S::NB * 16 * kKB, *la = lds + A0 + wm * S::MB * 16 * kKB;
+  const float* ls = reinterpret_cast<const float*>(lds + SC0);
+  auto load_tokens = [&](int kt, int slot, int j, Tokens& o) __attribute__((always_inline)) {
+    const float* sc = ls + slot * SC * 64;
+    o.x[j] = frag(la + (kt & 1) * S::A_BYTES + j * 16 * kKB);
+    o.s[j] = sc[(wm * S::MB + j) * 16 + r16];
+    if constexpr (!ROWS_B) o.s[j] *= sc[S::TM + wn * S::NB * 16 / 128];
+  };
+  auto load_weights = [&](int slot, int i, Weights& o) __attribute__((always_inline)) {
+    o.w = frag(lw + slot * S::W_BYTES + i * 16 * kKB);
+    if constexpr (ROWS_B)
+      o.s = *reinterpret_cast<const f32x4_t*>(ls + slot * SC * 64 + S::TM + (wn * S::NB + i) * 16 + 4 * q4);
+  };
+
+  // Barrier B(kt) opens stage kt: its copies have landed.  The weights' fragment of block i + 1 is read while
+  // block i multiplies, and the last block of a stage multiplies behind the barrier that opens the next, each
+  // token fragment replaced by the next stage's as soon as it has been used.  So the weights' slot of stage
+  // kt - 1 is free at B(kt), and the tokens' of stage kt once every wave has started it: a second barrier behind
+  // the first block, which gives their copies two stages of lead with two slots.  A product's result is scaled
+  // and added two products later, when it is there.
+  constexpr int FLY = S::A_DMA + (S::NSW == 3 ? S::W_DMA + SC_DMA : 0);   // copies younger than stage kt + 1's at B(kt + 1)
+  issue_w(0, 0);
+  issue_a(0);
+  if (nk > 1) {
+    if constexpr (S::NSW == 3) issue_w(1, 1);
+    issue_a(1);
+    wait_vm<FLY>();
+  } else {
+    wait_vm<0>();
+  }
+  __syncthreads();
+  Tokens tk;
+  Weights wt[2];
 #pragma unroll
-    for (int j = 0; j < S::MB; ++j) {
-      const int m = (wm * S::MB + j) * 16;
-      x[j] = frag(A, m);
-      if constexpr (F32) xw[j] = widen(x[j]);
-      s[j] = sc[m + r16];
-    }
-    if constexpr (!ROWS_B) {
-      static_assert(S::NB * 16 <= 128 && 128 % (S::NB * 16) == 0, "one weight scale a wave");
-      const float sb = sc[S::TM + wn * S::NB * 16 / 128];
+  for (int j = 0; j < S::MB; ++j) load_tokens(0, 0, j, tk);
+  load_weights(0, 0, wt[0]);
+  constexpr int LAST = S::NB * S::MB;
+  struct Pending {
+    f32x4_t d, s;
+  };
+  Pending pend[2];
 #pragma unroll
-      for (int j = 0; j < S::MB; ++j) s[j] *= sb;
-    }
+  for (int u = 0; u < 2; ++u) pend[u].d = pend[u].s = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  auto settle = [&](f32x4_t& a, const Pending& q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] += q.s[ROWS_B ? e : 0] * q.d[e];
+  };
+  int slot = 0;                            // the stage's weights
+  auto run_stage = [&](int kt, auto more) __attribute__((always_inline)) {
+    constexpr bool MORE = decltype(more)::value;
+    const int next = slot + 1 == S::NSW ? 0 : slot + 1, last = slot == 0 ? S::NSW - 1 : slot - 1;
+    if (MORE && kt + S::NSW - 1 < nk) issue_w(kt + S::NSW - 1, last);
 #pragma unroll
     for (int i = 0; i < S::NB; ++i) {
-      const int n = (wn * S::NB + i) * 16;
-      const i32x8_t wf = frag(W, n);
-      [[maybe_unused]] Wide ww;
-      if constexpr (F32) ww = widen(wf);
-      f32x4_t sb{1.0f, 1.0f, 1.0f, 1.0f};
-      if constexpr (ROWS_B) sb = *reinterpret_cast<const f32x4_t*>(sc + S::TM + n + 4 * q4);
+      // products stay on their side of the barriers (they touch no memory, so the compiler would move all of
+      // them behind the last one, and every copy would be waited for where it is issued)
+      __builtin_amdgcn_sched_barrier(0);
+      if (i == 1 && MORE) {
+        __syncthreads();
+        if (kt + 2 < nk) issue_a(kt + 2);
+      }
+      if (i + 1 < S::NB) {
+        load_weights(slot, i + 1, wt[(i + 1) & 1]);
+      } else if constexpr (MORE) {
+        if (kt + 2 < nk) wait_vm<FLY>();
+        else wait_vm<0>();
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+        load_weights(next, 0, wt[0]);
+      }
 #pragma unroll
       for (int j = 0; j < S::MB; ++j) {
-        f32x4_t d;
-        if constexpr (F32) d = wide_product(ww, xw[j]);
-        else d = code_product(wf, x[j]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] += (ROWS_B ? s[j] * sb[e] : s[j]) * d[e];
+        const int k = i * S::MB + j;
+        Pending q;
+        if constexpr (F32) q.d = wide_product(widen(wt[i & 1].w), widen(tk.x[j]));
+        else q.d = code_product(wt[i & 1].w, tk.x[j]);
+        if constexpr (ROWS_B) q.s = wt[i & 1].s * tk.s[j];
+        else q.s[0] = tk.s[j];
+        const int o = (k + LAST - 2) % LAST;
+        settle(acc[o / S::MB][o % S::MB], pend[k & 1]);
+        pend[k & 1] = q;
+        if (MORE && i + 1 == S::NB) load_tokens(kt + 1, next, j, tk);
       }
     }
-  }
+    slot = next;
+  };
+  for (int kt = 0; kt + 1 < nk; ++kt) run_stage(kt, std::true_type{});
+  run_stage(nk - 1, std::false_type{});
+#pragma unroll
+  for (int u = 0; u < 2; ++u) settle(acc[(LAST - 2 + u) / S::MB][(LAST - 2 + u) % S::MB], pend[(LAST - 2 + u) & 1]);
 
   // lane: token r16 of a block, columns 4 q4 .. 4 q4 + 3
   const bool vec = p.ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & (F32 ? 15u : 7u)) == 0;
@@ -269,8 +333,8 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
   }
 }
 
-using Large = Shape<256, 192, 2, 2, 1>;
-using Small = Shape<128, 128, 2, 2, 2>;
+using Large = Shape<256, 192, 2, 2, 1, 3>;
+using Wide32 = Shape<128, 128, 2, 2, 1, 3>;
 
 template <class S>
 int64_t tiles(const MatmulArgs& a) {
@@ -307,7 +371,7 @@ moe_status check(const moe_block_matmul_problem* p) {
 
 void launch_matmul(hipStream_t st, const MatmulArgs& a) {
   if (a.M <= kFewRows) launch_few(st, a);
-  else if (a.out_fp32) launch_shape<Small, true>(st, a);
+  else if (a.out_fp32) launch_shape<Wide32, true>(st, a);
   else launch_shape<Large, false>(st, a);
 }
 
