@@ -22,7 +22,9 @@ using namespace dense;
 
 namespace {
 
-using Large = Tile<256, 256, 2, 2, 2, 1>;
+using Large = Tile<256, 256, 2, 2, 4, 1, 0, 64>;
+
+constexpr auto no_more = [](int, int) { return Nothing{}; };   // an epilogue without operands from memory
 
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));
@@ -36,15 +38,15 @@ __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_up(UpArgs p) {
   const TileAt at = tile_at((p.T + TL::TM - 1) / TL::TM, (p.I + TI - 1) / TI);
   if (!at.ok) return;
   const int m0 = at.m * TL::TM, i0 = at.n * TI, rows = min(TL::TM, p.T - m0), cols = min(TI, p.I - i0);
-  Acc<TL> acc;
-  zero_acc<TL>(acc);
+  Sums<TL> acc;
+  zero<TL>(acc);
   // 32 gate rows, 32 up rows in turn: a lane's accumulators of blocks 2j and 2j + 1 are a and b of the
   // same elements; cols is a multiple of 64, so the rows that exist come first
   const Operand x{p.x.p + (int64_t)m0 * p.x.ld, 2 * p.x.ld, rows};
   const Operand w{p.gate.p + (int64_t)i0 * p.gate.ld, 2 * p.gate.ld, 2 * cols,
                   p.up.p + (int64_t)i0 * p.up.ld, 2 * p.up.ld};
   tile_product<TL, KC, KC2>(acc, p.H, x, w, lds);
-  each_piece<TL, true>(acc, lds, rows, cols, [&](int row, int col, const float* a, const float* b) {
+  each_piece<TL, true>(acc, lds, rows, cols, no_more, [&](int row, int col, const float* a, const float* b, Nothing) {
     const int64_t R = m0 + row;
     const int i = i0 + col;
     float h[8];
@@ -80,8 +82,8 @@ __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_rows(RowsArgs p) {
   const TileAt at = tile_at((p.T + TL::TM - 1) / TL::TM, (p.N + TL::TN - 1) / TL::TN);
   if (!at.ok) return;
   const int m0 = at.m * TL::TM, n0 = at.n * TL::TN, rows = min(TL::TM, p.T - m0), cols = min(TL::TN, p.N - n0);
-  Acc<TL> acc;
-  zero_acc<TL>(acc);
+  Sums<TL> acc;
+  zero<TL>(acc);
   Operand a{p.a.p + (int64_t)m0 * p.a.ld, 2 * p.a.ld, rows};
   Operand b{BM == KC ? p.b0.p + (int64_t)n0 * p.b0.ld : p.b0.p + n0, 2 * p.b0.ld, cols};
   for (int k = 0; k < p.K; k += p.ksplit) {
@@ -93,7 +95,7 @@ __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_rows(RowsArgs p) {
     }
     tile_product<TL, KC, BM>(acc, p.ksplit, a, b, lds);
   }
-  each_piece<TL, false>(acc, lds, rows, cols, [&](int row, int col, const float* v) {
+  each_piece<TL, false>(acc, lds, rows, cols, no_more, [&](int row, int col, const float* v, Nothing) {
     *reinterpret_cast<uint4*>(p.c.p + (int64_t)(m0 + row) * p.c.ld + n0 + col) = pack8(v);
   });
 }
@@ -104,22 +106,41 @@ __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_dh(DhArgs p) {
   const TileAt at = tile_at((p.T + TL::TM - 1) / TL::TM, (p.I + TL::TN - 1) / TL::TN);
   if (!at.ok) return;
   const int m0 = at.m * TL::TM, n0 = at.n * TL::TN, rows = min(TL::TM, p.T - m0), cols = min(TL::TN, p.I - n0);
-  Acc<TL> acc;
-  zero_acc<TL>(acc);
+  Sums<TL> acc;
+  zero<TL>(acc);
   tile_product<TL, KC, RC>(acc, p.H, {p.dy.p + (int64_t)m0 * p.dy.ld, 2 * p.dy.ld, rows},
                            {p.down.p + n0, 2 * p.down.ld, cols}, lds);
-  each_piece<TL, false>(acc, lds, rows, cols, [&](int row, int col, const float* dh) {
+  // a and b of a piece: 8 BF16 values each, or 8 codes and a scale byte
+  struct Saved8 {
+    uint4 a, b;
+    int sa, sb;
+  };
+  auto pre = [&](int row, int col) {
+    const int64_t R = m0 + row;
+    const int i = n0 + col;
+    Saved8 q{};
+    if constexpr (SAVED == kBf16) {
+      const uint16_t* ab = reinterpret_cast<const uint16_t*>(p.kept.ab) + R * 2 * p.I + i;
+      q.a = *reinterpret_cast<const uint4*>(ab);
+      q.b = *reinterpret_cast<const uint4*>(ab + p.I);
+    } else {
+      const uint8_t *ab = p.kept.ab + R * 2 * p.I + i, *sc = p.kept.scales + R * (p.I / 16) + i / 32;
+      const uint2 a = *reinterpret_cast<const uint2*>(ab), b = *reinterpret_cast<const uint2*>(ab + p.I);
+      q.a.x = a.x, q.a.y = a.y, q.b.x = b.x, q.b.y = b.y;
+      q.sa = sc[0], q.sb = sc[p.I / 32];
+    }
+    return q;
+  };
+  each_piece<TL, false>(acc, lds, rows, cols, pre, [&](int row, int col, const float* dh, const Saved8& q) {
     const int64_t R = m0 + row;
     const int i = n0 + col;
     float a[8], b[8], da[8], db[8], h[8];
     if constexpr (SAVED == kBf16) {
-      const uint16_t* ab = reinterpret_cast<const uint16_t*>(p.kept.ab) + R * 2 * p.I + i;
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(ab), a);
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(ab + p.I), b);
+      unpack_bf16x8(q.a, a);
+      unpack_bf16x8(q.b, b);
     } else {
-      const uint8_t *ab = p.kept.ab + R * 2 * p.I + i, *sc = p.kept.scales + R * (p.I / 16) + i / 32;
-      int8_values8(*reinterpret_cast<const uint2*>(ab), int8_step(sc[0]), a);
-      int8_values8(*reinterpret_cast<const uint2*>(ab + p.I), int8_step(sc[p.I / 32]), b);
+      int8_values8(make_uint2(q.a.x, q.a.y), int8_step(q.sa), a);
+      int8_values8(make_uint2(q.b.x, q.b.y), int8_step(q.sb), b);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -144,30 +165,44 @@ __global__ __launch_bounds__(TL::NTH, TL::MINB) void k_ffn_wgrad(WgradArgs p) {
   const TileAt at = tile_at((p.M + TL::TM - 1) / TL::TM, (p.N + TL::TN - 1) / TL::TN);
   if (!at.ok) return;
   const int m0 = at.m * TL::TM, n0 = at.n * TL::TN, rows = min(TL::TM, p.M - m0), cols = min(TL::TN, p.N - n0);
-  Acc<TL> acc;
-  zero_acc<TL>(acc);
+  Sums<TL> acc;
+  zero<TL>(acc);
   tile_product<TL, RC, RC>(acc, p.T, {p.a.p + m0, 2 * p.a.ld, rows}, {p.b.p + n0, 2 * p.b.ld, cols}, lds);
-  each_piece<TL, false>(acc, lds, rows, cols, [&](int row, int col, const float* v) {
+  auto place = [&](int row, int col) {
     const int m = m0 + row;
-    const int64_t at0 = m < p.msplit ? (int64_t)m * p.ldc0 : (int64_t)(m - p.msplit) * p.ldc1;
-    void* c = m < p.msplit ? p.c0 : p.c1;
+    const int64_t at = m < p.msplit ? (int64_t)m * p.ldc0 : (int64_t)(m - p.msplit) * p.ldc1;
+    return static_cast<uint8_t*>(m < p.msplit ? p.c0 : p.c1) + (at + n0 + col) * (F32 ? 4 : 2);
+  };
+  struct Old {
+    uint4 v[OVER ? 1 : (F32 ? 2 : 1)];
+  };
+  auto pre = [&](int row, int col) {
+    Old q{};
+    if constexpr (!OVER) {
+      const uint4* from = reinterpret_cast<const uint4*>(place(row, col));
+      q.v[0] = from[0];
+      if constexpr (F32) q.v[1] = from[1];
+    }
+    return q;
+  };
+  each_piece<TL, false>(acc, lds, rows, cols, pre, [&](int row, int col, const float* v, const Old& q) {
+    uint8_t* c = place(row, col);
     if constexpr (F32) {
-      f32x4_t* to = reinterpret_cast<f32x4_t*>(static_cast<float*>(c) + at0 + n0 + col);
+      f32x4_t* to = reinterpret_cast<f32x4_t*>(c);
       f32x4_t r[2] = {f32x4_t{v[0], v[1], v[2], v[3]}, f32x4_t{v[4], v[5], v[6], v[7]}};
 #pragma unroll
-      for (int u = 0; u < 2; ++u) to[u] = OVER ? r[u] : to[u] + r[u];
+      for (int u = 0; u < 2; ++u) to[u] = OVER ? r[u] : __builtin_bit_cast(f32x4_t, q.v[OVER ? 0 : u]) + r[u];
     } else {
-      uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(c) + at0 + n0 + col);
       uint4 r = pack8(v);
       if constexpr (!OVER) {
         float old[8], add[8];
-        unpack_bf16x8(*to, old);
+        unpack_bf16x8(q.v[0], old);
         unpack_bf16x8(r, add);
 #pragma unroll
         for (int k = 0; k < 8; ++k) old[k] += add[k];
         r = pack8(old);
       }
-      *to = r;
+      *reinterpret_cast<uint4*>(c) = r;
     }
   });
 }
