@@ -5,8 +5,7 @@
 // rows of the tile's width read with the transposing reads; 16-byte chunks swizzled so that neither copies nor
 // reads collide on banks).  A stage's fragments are read while the one before multiplies, so one wave a SIMD with a
 // 128 x 128 block is enough.  That block is what the LDS rate asks for: per stage and
-// 256 x 256 tile, the four waves read 64 KB and the copies write 32 KB, 768 cycles at 128 bytes a clock,
-// against 1024 cycles of multiplying (eight waves of 128 x 64 read 96 KB, 1024 cycles).
+// 256 x 256 tile, the four waves read 64 KB, which leaves them most of the time to multiply.
 //
 // The instruction is the 16 x 16 x 32 one.  On random values the card is held by its power, and registers alone
 // multiply at 1885 TFLOP/s with it, at 1617 with 32 x 32 x 16 (one wave a SIMD; on zeros 2327 and 2117).
@@ -26,6 +25,11 @@ struct Blocks {
 };
 template <class TL>
 using Sums = f32x4_t[Blocks<TL>::MI][Blocks<TL>::NJ];
+
+// K-contiguous stages, rows of 64 bytes.  A 16-byte read of 64 lanes takes four clocks of 256 bytes, and a clock serves
+// lanes 0-3, 12-15, 20-23 and 24-27 (or 4-7, 8-11, 16-19 and 28-31; the same 32 on): of 16 rows' chunk 0 and 1 some
+// each, which this puts in different places (290 B/ns a CU with (r >> 2) & 3, 570 without collisions).
+__device__ __forceinline__ int swz_rows(int r) { return ((r >> 1) & 2) ^ ((r >> 3) & 1 ? 3 : 0); }
 
 // Row-contiguous stages: a transposing read takes 32 bytes of 4 k rows for each of two groups 8 rows apart at once,
 // which this moves to eight different places of 256 bytes.
@@ -74,10 +78,10 @@ __device__ __forceinline__ void tile_product(Sums<TL>& acc, int kdim, const Oper
     for (int i = 0; i < dma; ++i) {
       const int off = (w * dma + i) * 1024 + 16 * lane;
       if constexpr (decltype(mode)::value == KC) {
-        const int r = off / KB, c = ((off % KB) >> 4) ^ swz_kc<KB>(r);
+        const int r = off / KB, c = ((off % KB) >> 4) ^ swz_rows(r);
         o[i] = (uint32_t)(min(r, X.rows - 1) * X.ld) + 16 * c;
       } else if constexpr (decltype(mode)::value == KC2) {
-        const int r = off / KB, c = ((off % KB) >> 4) ^ swz_kc<KB>(r);
+        const int r = off / KB, c = ((off % KB) >> 4) ^ swz_rows(r);
         o[i] = (uint32_t)(min((r >> 6) * 32 + (r & 31), X.rows / 2 - 1) * ((r >> 5) & 1 ? X.ld2 : X.ld)) + 16 * c;
       } else {
         const int k = off / rb, c = ((off % rb) >> 4) ^ swz_rc(k);
@@ -131,7 +135,7 @@ __device__ __forceinline__ void tile_product(Sums<TL>& acc, int kdim, const Oper
   auto frag = [&](auto mode, const uint8_t* tile, int rb, int r0) __attribute__((always_inline)) {
     if constexpr (decltype(mode)::value != RC) {
       const int r = r0 + r16;
-      return *reinterpret_cast<const bf16x8_t*>(tile + r * KB + ((q4 ^ swz_kc<KB>(r16)) << 4));
+      return *reinterpret_cast<const bf16x8_t*>(tile + r * KB + ((q4 ^ swz_rows(r16)) << 4));
     } else {
       i16x4_t h[2];
 #pragma unroll
