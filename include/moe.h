@@ -556,18 +556,20 @@ moe_status moe_block_quantize(const moe_block_quantize_problem* p, const moe_row
 typedef struct {
   int64_t rows;          /* M in [0, 2^24]                                                */
   int64_t cols;          /* N in [1, 2^20]                                                */
-  int64_t depth;         /* K in [16, 2^24], a multiple of 16; the last block may be short */
+  int64_t depth;         /* K in [16, 2^22], a multiple of 16; the last block may be short */
   int32_t groups;        /* G in [1, MOE_FP8_MAX_GROUPS]                                  */
   int32_t scales;        /* moe_fp8_blocks of b: MOE_FP8_TILES, or MOE_FP8_ROWS with one group */
   int32_t out_dtype;     /* MOE_BF16 or MOE_FP32                                          */
   uint32_t flags;        /* MOE_FP8_ACCUMULATE or 0                                       */
 } moe_block_matmul_problem;
 #define MOE_FP8_MAX_GROUPS 256
+#define MOE_FP8_MAX_LD (1 << 23)
 /* (M / 64 + 1 + G) (N / 128 + 1) is at most 2^22 as well (MOE_ERR_SHAPE above). */
 
 /*  a         E4M3 [M][K], 16-byte aligned, ld a multiple of 16
  *  a_scales  float [ceil(K / 128)][M]
- *  b         E4M3 [G][N][K]: base (16-byte aligned), ld and expert_stride multiples of 16; no table
+ *  b         E4M3 [G][N][K]: base (16-byte aligned), ld (up to MOE_FP8_MAX_LD) and expert_stride
+ *            multiples of 16; no table
  *  b_scales  float: MOE_FP8_TILES [G][ceil(N / 128)][ceil(K / 128)], MOE_FP8_ROWS [ceil(K / 128)][N]
  *  offsets   int32 [G + 1] on the device, ascending: group g is rows offsets[g] .. offsets[g + 1] - 1
  *            (the layer's routing state holds such a table); NULL with one group: all rows.  Rows

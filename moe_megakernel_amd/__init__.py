@@ -36,6 +36,7 @@ MOE_FFN_MAX_LD = 1 << 22
 MOE_FP8_ROWS, MOE_FP8_TILES = 1, 2
 MOE_FP8_TRANSPOSE, MOE_FP8_ACCUMULATE = 1, 2
 MOE_FP8_MAX_GROUPS = 256
+MOE_FP8_MAX_LD = 1 << 23
 
 EXPORTED = ("moe_saved_bytes", "moe_workspace_bytes", "moe_saved_view", "moe_forward",
             "moe_forward_topk", "moe_forward_noalloc", "moe_backward", "moe_status_str",

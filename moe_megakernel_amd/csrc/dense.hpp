@@ -35,13 +35,6 @@ __device__ __forceinline__ int swz_rows(int r) { return ((r >> 1) & 2) ^ ((r >> 
 // which this moves to eight different places of 256 bytes.
 __device__ __forceinline__ int swz_rc(int k) { return ((k & 3) << 2) | ((k >> 2) & 2); }
 
-// LDS copy with a uniform base and a 32-bit offset a lane: no vector instruction moves the address on.
-__device__ __forceinline__ void dma16s(const uint8_t* base, uint32_t off, uint32_t m0v) {
-  const uint32_t m = __builtin_amdgcn_readfirstlane(m0v);
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(m)
-               : "memory", "m0");
-}
-
 // An operand of tile_product: `p` its element (tile row 0, K = 0), rows `ld` bytes apart (64 rows, and a KC
 // tile's rows, span less than 2^32 bytes), `rows` > 0 tile rows exist (RC: a multiple of 8).
 //  KC: consecutive K, rows of the tile `ld` apart; RC: consecutive tile rows, K `ld` apart;
@@ -283,7 +276,7 @@ struct Nothing {};
 template <class TL, bool PAIR, class PRE, class F>
 __device__ __forceinline__ void each_piece(const Sums<TL>& acc, uint8_t* lds, int rows, int cols, const PRE& pre, const F& f) {
   constexpr int PPR = PAIR ? TL::TN / 16 : TL::TN / 8, PPT = TL::WMR * PPR / TL::NTH;
-  constexpr int kAhead = PPT % 4 == 0 ? 4 : 2, RPP = TL::NTH / PPR;   // rows a pass of the workgroup
+  constexpr int kAhead = PPT >= 8 ? 4 : PPT / 2, RPP = TL::NTH / PPR;   // rows a pass of the workgroup
   static_assert(TL::WMR * TL::TN * 4 <= TL::LDS && TL::NTH % PPR == 0 && PPT % (2 * kAhead) == 0, "epilogue round");
   float* ct = reinterpret_cast<float*>(lds);
   const int t = threadIdx.x, lane = t & 63, wm = wave_m<TL>(), wn = wave_n<TL>();

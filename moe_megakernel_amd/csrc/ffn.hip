@@ -23,6 +23,7 @@ using namespace dense;
 namespace {
 
 using Large = Tile<256, 256, 2, 2, 4, 1, 0, 64>;
+using Medium = Tile<128, 128, 2, 2, 4, 2, 0, 64>;
 
 constexpr auto no_more = [](int, int) { return Nothing{}; };   // an epilogue without operands from memory
 
@@ -236,23 +237,44 @@ void wgrad_as(hipStream_t st, const WgradArgs& a) {
 
 }  // namespace
 
+// Large or Medium tiles for an m x n result over k, whichever is expected to end first.  A round of 256 Large
+// tiles (one a CU) takes 0.60 us a stage of 32 k and 14 us for its start and end; one of 512 Medium tiles (two
+// a CU, half the work) 0.57 and 10, of up to 256 of them (one a CU) 0.21 and 8.  Measured, Large against
+// Medium: 777 x 24576 over 4096 200 us and 263, 777 x 4096 over 12288 231 and 131, 4096 x 4096 over 4096 118 and
+// 173, 2048 x 2048 over 8192 161 and 75, 256 x 4096 over 4096 81 and 33.
+bool large(int64_t m, int64_t n, int64_t k) {
+  const double stages = (double)ceil_div(k, 32);
+  const int64_t l = ceil_div(m, Large::TM) * ceil_div(n, Large::TN), s = ceil_div(m, Medium::TM) * ceil_div(n, Medium::TN);
+  const int64_t rest = s % 512;
+  const double tl = (double)ceil_div(l, 256) * (0.60 * stages + 14.0);
+  const double ts = (double)(s / 512 + (rest > 256)) * (0.57 * stages + 10.0) +
+                    (rest > 0 && rest <= 256 ? 0.21 * stages + 8.0 : 0.0);
+  return tl <= ts;
+}
+
 void launch_up(hipStream_t st, const UpArgs& a) {
-  if (a.act == kSilu) up_as<Large, kSilu>(st, a);
-  else up_as<Large, kGelu>(st, a);
+  const bool l = large(a.T, 2 * a.I, a.H);
+  if (a.act == kSilu) l ? up_as<Large, kSilu>(st, a) : up_as<Medium, kSilu>(st, a);
+  else l ? up_as<Large, kGelu>(st, a) : up_as<Medium, kGelu>(st, a);
 }
-void launch_down(hipStream_t st, const RowsArgs& a) {
-  hipLaunchKernelGGL((k_ffn_rows<Large, KC>), grid_of<Large>(a, a.T, a.N, Large::TN), dim3(Large::NTH), 0, st, a);
+template <int BM>
+void rows_as(hipStream_t st, const RowsArgs& a) {
+  if (large(a.T, a.N, a.K))
+    hipLaunchKernelGGL((k_ffn_rows<Large, BM>), grid_of<Large>(a, a.T, a.N, Large::TN), dim3(Large::NTH), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_ffn_rows<Medium, BM>), grid_of<Medium>(a, a.T, a.N, Medium::TN), dim3(Medium::NTH), 0, st, a);
 }
-void launch_dx(hipStream_t st, const RowsArgs& a) {
-  hipLaunchKernelGGL((k_ffn_rows<Large, RC>), grid_of<Large>(a, a.T, a.N, Large::TN), dim3(Large::NTH), 0, st, a);
-}
+void launch_down(hipStream_t st, const RowsArgs& a) { rows_as<KC>(st, a); }
+void launch_dx(hipStream_t st, const RowsArgs& a) { rows_as<RC>(st, a); }
 void launch_dh(hipStream_t st, const DhArgs& a) {
-  if (a.act == kSilu) dh_as<Large, kSilu>(st, a);
-  else dh_as<Large, kGelu>(st, a);
+  const bool l = large(a.T, a.I, a.H);
+  if (a.act == kSilu) l ? dh_as<Large, kSilu>(st, a) : dh_as<Medium, kSilu>(st, a);
+  else l ? dh_as<Large, kGelu>(st, a) : dh_as<Medium, kGelu>(st, a);
 }
 void launch_wgrad(hipStream_t st, const WgradArgs& a) {
-  if (a.fp32) wgrad_as<Large, true>(st, a);
-  else wgrad_as<Large, false>(st, a);
+  const bool l = large(a.M, a.N, a.T);
+  if (a.fp32) l ? wgrad_as<Large, true>(st, a) : wgrad_as<Medium, true>(st, a);
+  else l ? wgrad_as<Large, false>(st, a) : wgrad_as<Medium, false>(st, a);
 }
 
 }  // namespace ffn

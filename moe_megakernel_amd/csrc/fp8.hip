@@ -18,6 +18,7 @@ namespace moe {
 namespace fp8 {
 
 using gemm::dma16;
+using gemm::dma16s;
 using gemm::dma4;
 using gemm::g_zero_page;
 using gemm::lds_off;
@@ -116,6 +117,9 @@ __device__ __forceinline__ Tile find_tile(const MatmulArgs& p, int* prefix) {
   return t;
 }
 
+// The steady loop has no branch, and products stay on their side of the barriers: they touch no memory, so the compiler
+// would move them to where their results are used, behind the last barrier.  Code that runs once a tile is kept
+// short: a workgroup fetches it anew, at about 60 ns for each 64 bytes.
 template <class S, bool ROWS_B, bool F32, bool ADD>
 __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
   __shared__ __align__(16) uint8_t lds[S::template lds<ROWS_B>()];
@@ -126,62 +130,84 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = w % S::NWN, wm = w / S::NWN;
   const int cols = min(S::TN, p.N - t.n0), rows = t.rows;
   const uint32_t lds0 = lds_off(lds);
-  const uint8_t* zp = reinterpret_cast<const uint8_t*>(g_zero_page) + 16 * lane;
   const int nk = (p.K + kKB - 1) / kKB;
 
   // LDS: the weights' stages [NSW][TN][128], the tokens' [2][TM][128] (16-byte chunks swizzled by row), the
   // scales' [NSW].  Rows past the last repeat it, their results go nowhere; chunks past the last k are zeros.
   constexpr int SC = S::template scale_copies<ROWS_B>(), SC_DMA = SC / S::NW;
   constexpr int A0 = S::NSW * S::W_BYTES, SC0 = A0 + 2 * S::A_BYTES;
-  const uint8_t *pw[S::W_DMA], *pa[S::A_DMA];
+  // The lane's offset of each copy from the stage's first byte (host checks keep them below 2^32).
+  const uint8_t* gw = p.b + (int64_t)t.g * p.stride_b + (int64_t)t.n0 * p.ldb;
+  const uint8_t* ga = p.a + (int64_t)t.m0 * p.lda;
+  uint32_t ow[S::W_DMA], oa[S::A_DMA];
 #pragma unroll
   for (int i = 0; i < S::W_DMA; ++i) {
     const int off = (w * S::W_DMA + i) * 1024 + 16 * lane, r = off / kKB, c = ((off % kKB) >> 4) ^ swz_kc<128>(r);
-    pw[i] = p.b + (int64_t)t.g * p.stride_b + (int64_t)(t.n0 + min(r, cols - 1)) * p.ldb + 16 * c;
+    ow[i] = (uint32_t)(min(r, cols - 1) * p.ldb) + 16 * c;
   }
 #pragma unroll
   for (int i = 0; i < S::A_DMA; ++i) {
     const int off = (w * S::A_DMA + i) * 1024 + 16 * lane, r = off / kKB, c = ((off % kKB) >> 4) ^ swz_kc<128>(r);
-    pa[i] = p.a + (int64_t)(t.m0 + min(r, rows - 1)) * p.lda + 16 * c;
+    oa[i] = (uint32_t)(min(r, rows - 1) * p.lda) + 16 * c;
   }
-  // copies of a stage; `copy` holds rows 8 copy .. 8 copy + 7, and swz_kc has period 16
-  auto copies = [&](int kt, const uint8_t** q, int n, int first, uint32_t to) __attribute__((always_inline)) {
-    if (kt * kKB + kKB <= p.K) {
-      for (int i = 0; i < n; ++i) {
-        dma16(q[i], to + (first + i) * 1024);
-        q[i] += kKB;
-      }
-    } else {
-      for (int i = 0; i < n; ++i) {
-        const int k = kt * kKB + 16 * ((lane & 7) ^ swz_kc<128>(8 * (first + i) + (lane >> 3)));
-        dma16(k < p.K ? q[i] : zp, to + (first + i) * 1024);
-      }
-    }
-  };
-  const int sb_rows = (p.N + 127) / 128;
-  const float* sb0 = ROWS_B ? p.sb + t.n0
-                            : p.sb + ((int64_t)t.g * sb_rows + min(t.n0 / 128 + min(lane, S::TN / 128 - 1), sb_rows - 1)) * nk;
-  auto issue_w = [&](int kt, int slot) __attribute__((always_inline)) {
-    copies(kt, pw, S::W_DMA, w * S::W_DMA, lds0 + slot * S::W_BYTES);
+  // scales, 64 a copy: the tokens', then the weights' rows' or those of the tile's 128-row parts
+  const float* ps[SC_DMA];
+  int64_t step[SC_DMA];                    // floats from a stage's to the next one's
 #pragma unroll
-    for (int u = 0; u < SC_DMA; ++u) {
-      const int i = u * S::NW + w;
-      const float* src;
-      if (i < S::TM / 64) src = p.sa + (int64_t)kt * p.M + t.m0 + min(64 * i + lane, rows - 1);
-      else if (ROWS_B) src = sb0 + (int64_t)kt * p.N + min(64 * (i - S::TM / 64) + lane, cols - 1);
-      else src = sb0 + kt;
-      dma4(src, lds0 + SC0 + (slot * SC + i) * 256);
-    }
+  for (int u = 0; u < SC_DMA; ++u) {
+    const int i = u * S::NW + w;
+    const int nb = (p.N + 127) / 128;
+    const bool tok = i < S::TM / 64;
+    const int64_t tiles = ((int64_t)t.g * nb + min(t.n0 / 128 + min(lane, S::TN / 128 - 1), nb - 1)) * nk;
+    ps[u] = tok ? p.sa + t.m0 + min(64 * i + lane, rows - 1)
+                : p.sb + (ROWS_B ? t.n0 + min(64 * (i - S::TM / 64) + lane, cols - 1) : tiles);
+    step[u] = tok ? p.M : (ROWS_B ? p.N : 1);
+  }
+  int put = 0, pet = 0;                    // ring slots of the next weights and tokens
+  auto copy_scales = [&](int u) __attribute__((always_inline)) {
+    dma4(ps[u], lds0 + SC0 + (put * SC + u * S::NW + w) * 256);
+    ps[u] += step[u];
+  };
+  auto copy_w = [&](int i) __attribute__((always_inline)) {
+    if (i < S::W_DMA) dma16s(gw, ow[i], lds0 + put * S::W_BYTES + (w * S::W_DMA + i) * 1024);
+    else copy_scales(i - S::W_DMA);
+  };
+  auto copy_a = [&](int i) __attribute__((always_inline)) {
+    dma16s(ga, oa[i], lds0 + A0 + pet * S::A_BYTES + (w * S::A_DMA + i) * 1024);
+  };
+  auto turn = [&](int& slot, int n) __attribute__((always_inline)) { slot = slot + 1 == n ? 0 : slot + 1; };
+  // Whole stages at once; of the last, chunks past K come from the zero page.  (Copy c holds rows 8 c .. 8 c + 7, and
+  // swz_kc has period 16.)
+  auto chunk = [&](int kt, const uint8_t* q, int c) __attribute__((always_inline)) {
+    return kt * kKB + 16 * ((lane & 7) ^ swz_kc<128>(8 * c + (lane >> 3))) < p.K
+               ? q : reinterpret_cast<const uint8_t*>(g_zero_page) + 16 * lane;
+  };
+  auto issue_w = [&](int kt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < S::W_DMA; ++i)
+      dma16(chunk(kt, gw + ow[i], w * S::W_DMA + i), lds0 + put * S::W_BYTES + (w * S::W_DMA + i) * 1024);
+#pragma unroll
+    for (int u = 0; u < SC_DMA; ++u) copy_scales(u);
+    gw += kKB;
+    turn(put, S::NSW);
   };
   auto issue_a = [&](int kt) __attribute__((always_inline)) {
-    copies(kt, pa, S::A_DMA, w * S::A_DMA, lds0 + A0 + (kt & 1) * S::A_BYTES);
+#pragma unroll
+    for (int i = 0; i < S::A_DMA; ++i)
+      dma16(chunk(kt, ga + oa[i], w * S::A_DMA + i), lds0 + A0 + pet * S::A_BYTES + (w * S::A_DMA + i) * 1024);
+    ga += kKB;
+    turn(pet, 2);
   };
 
   f32x4_t acc[S::NB][S::MB];
+  {
+    float z = 0.0f;                        // not known to be zero: see the dense products
+    asm volatile("" : "+v"(z));
 #pragma unroll
-  for (int i = 0; i < S::NB; ++i)
+    for (int i = 0; i < S::NB; ++i)
 #pragma unroll
-    for (int j = 0; j < S::MB; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < S::MB; ++j) acc[i][j] = f32x4_t{z, z, z, z};
+  }
 
   // A lane's 32 codes of row r16 of a 16-row block: chunks q4 and q4 + 4 (which 32 is free, as long as
   // both operands agree).  The swizzle is the same for every block, so the blocks lie at constant distances.
@@ -190,26 +216,21 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
     const u32x4_t u0 = *reinterpret_cast<const u32x4_t*>(block + f0), u1 = *reinterpret_cast<const u32x4_t*>(block + f1);
     return i32x8_t{(int)u0[0], (int)u0[1], (int)u0[2], (int)u0[3], (int)u1[0], (int)u1[1], (int)u1[2], (int)u1[3]};
   };
-  struct Tokens {                          // a stage's token fragments and scales
-    i32x8_t x[S::MB];
-    float s[S::MB];
-  };
-  struct Weights {                         // 16 weight rows and their scales
-    i32x8_t w;
-    f32x4_t s;
-  };
+  i32x8_t x[S::MB], wf[2];                 // token fragments of a stage, weight fragments of a block and the next
+  float s[S::MB];                          // the tokens' scales (times the weight tile's)
+  f32x4_t sw[2];                           // ROWS_B: the weight rows' scales
   const uint8_t *lw = lds + wn * S::NB * 16 * kKB, *la = lds + A0 + wm * S::MB * 16 * kKB;
   const float* ls = reinterpret_cast<const float*>(lds + SC0);
-  auto load_tokens = [&](int kt, int slot, int j, Tokens& o) __attribute__((always_inline)) {
+  auto load_tokens = [&](int aslot, int slot, int j) __attribute__((always_inline)) {
     const float* sc = ls + slot * SC * 64;
-    o.x[j] = frag(la + (kt & 1) * S::A_BYTES + j * 16 * kKB);
-    o.s[j] = sc[(wm * S::MB + j) * 16 + r16];
-    if constexpr (!ROWS_B) o.s[j] *= sc[S::TM + wn * S::NB * 16 / 128];
+    x[j] = frag(la + aslot * S::A_BYTES + j * 16 * kKB);
+    s[j] = sc[(wm * S::MB + j) * 16 + r16];
+    if constexpr (!ROWS_B) s[j] *= sc[S::TM + wn * S::NB * 16 / 128];
   };
-  auto load_weights = [&](int slot, int i, Weights& o) __attribute__((always_inline)) {
-    o.w = frag(lw + slot * S::W_BYTES + i * 16 * kKB);
+  auto load_weights = [&](int slot, int i) __attribute__((always_inline)) {
+    wf[i & 1] = frag(lw + slot * S::W_BYTES + (i % S::NB) * 16 * kKB);
     if constexpr (ROWS_B)
-      o.s = *reinterpret_cast<const f32x4_t*>(ls + slot * SC * 64 + S::TM + (wn * S::NB + i) * 16 + 4 * q4);
+      sw[i & 1] = *reinterpret_cast<const f32x4_t*>(ls + slot * SC * 64 + S::TM + (wn * S::NB + i % S::NB) * 16 + 4 * q4);
   };
 
   // Barrier B(kt) opens stage kt: its copies have landed.  The weights' fragment of block i + 1 is read while
@@ -219,113 +240,164 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
   // the first block, which gives their copies two stages of lead with two slots.  A product's result is scaled
   // and added two products later, when it is there.
   constexpr int FLY = S::A_DMA + (S::NSW == 3 ? S::W_DMA + SC_DMA : 0);   // copies younger than stage kt + 1's at B(kt + 1)
-  issue_w(0, 0);
+  constexpr int LAST = S::NB * S::MB;
+  f32x4_t pd[2], pq[2];                    // results on their way and their scales
+#pragma unroll
+  for (int u = 0; u < 2; ++u) pd[u] = pq[u] = acc[0][0];
+  auto settle = [&](f32x4_t& a, int u) __attribute__((always_inline)) {
+    if constexpr (ROWS_B) a = __builtin_elementwise_fma(pq[u], pd[u], a);
+    else a = __builtin_elementwise_fma(f32x4_t{pq[u][0], pq[u][0], pq[u][0], pq[u][0]}, pd[u], a);
+  };
+  auto products = [&](int i, bool more, int aslot, int next) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < S::MB; ++j) {
+      const int k = i * S::MB + j, o = (k + LAST - 2) % LAST;
+      f32x4_t d;
+      if constexpr (F32) d = wide_product(widen(wf[i & 1]), widen(x[j]));
+      else d = code_product(wf[i & 1], x[j]);
+      settle(acc[o / S::MB][o % S::MB], k & 1);
+      pd[k & 1] = d;
+      if constexpr (ROWS_B) pq[k & 1] = sw[i & 1] * s[j];
+      else pq[k & 1][0] = s[j];
+      if (more && i + 1 == S::NB) load_tokens(aslot, next, j);
+    }
+  };
+  int slot = 0, aslot = 0;                 // the stage's
+  auto steady = [&]() __attribute__((always_inline)) {
+    const int next = slot + 1 == S::NSW ? 0 : slot + 1;
+#pragma unroll
+    for (int i = 0; i < S::NB; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int NWC = S::W_DMA + SC_DMA, B = S::NB - 1;
+      if (i == 1) __syncthreads();
+      if (i + 1 == S::NB) {
+        wait_vm<FLY>();
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
+#pragma unroll
+        for (int c = i * NWC / B; c < (i + 1) * NWC / B; ++c) copy_w(c);
+        if (i > 0)
+#pragma unroll
+          for (int c = (i - 1) * S::A_DMA / (B - 1); c < i * S::A_DMA / (B - 1); ++c) copy_a(c);
+      }
+      load_weights(i + 1 == S::NB ? next : slot, i + 1);
+      products(i, true, aslot ^ 1, next);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    gw += kKB;
+    ga += kKB;
+    turn(put, S::NSW);
+    turn(pet, 2);
+    slot = next;
+    aslot ^= 1;
+  };
+  auto any = [&](int kt) __attribute__((always_inline)) {   // the last stages
+    const int next = slot + 1 == S::NSW ? 0 : slot + 1;
+    if (kt + S::NSW - 1 < nk) issue_w(kt + S::NSW - 1);
+#pragma unroll
+    for (int i = 0; i < S::NB; ++i) {
+      if (i == 1) {
+        __syncthreads();
+        if (kt + 2 < nk) issue_a(kt + 2);
+      }
+      if (i + 1 == S::NB) {
+        if (kt + 2 < nk) wait_vm<FLY>();
+        else wait_vm<0>();
+        __syncthreads();
+      }
+      load_weights(i + 1 == S::NB ? next : slot, i + 1);   // (behind the last stage: read and not used)
+      products(i, true, aslot ^ 1, next);
+    }
+    slot = next;
+    aslot ^= 1;
+  };
+
+  issue_w(0);
   issue_a(0);
   if (nk > 1) {
-    if constexpr (S::NSW == 3) issue_w(1, 1);
+    if constexpr (S::NSW == 3) issue_w(1);
     issue_a(1);
     wait_vm<FLY>();
   } else {
     wait_vm<0>();
   }
   __syncthreads();
-  Tokens tk;
-  Weights wt[2];
 #pragma unroll
-  for (int j = 0; j < S::MB; ++j) load_tokens(0, 0, j, tk);
-  load_weights(0, 0, wt[0]);
-  constexpr int LAST = S::NB * S::MB;
-  struct Pending {
-    f32x4_t d, s;
-  };
-  Pending pend[2];
+  for (int j = 0; j < S::MB; ++j) load_tokens(0, 0, j);
+  load_weights(0, 0);
+  int kt = 0;
+  if (kt + 3 < nk) {
+    do steady();                           // its copies are whole stages
+    while (++kt + 3 < nk);
+    asm volatile("; steady done" ::: "memory");   // a block of its own, for what the register allocator moves on the way out
+  }
+#pragma unroll 1
+  for (; kt < nk; ++kt) any(kt);
 #pragma unroll
-  for (int u = 0; u < 2; ++u) pend[u].d = pend[u].s = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  auto settle = [&](f32x4_t& a, const Pending& q) __attribute__((always_inline)) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] += q.s[ROWS_B ? e : 0] * q.d[e];
-  };
-  int slot = 0;                            // the stage's weights
-  auto run_stage = [&](int kt, auto more) __attribute__((always_inline)) {
-    constexpr bool MORE = decltype(more)::value;
-    const int next = slot + 1 == S::NSW ? 0 : slot + 1, last = slot == 0 ? S::NSW - 1 : slot - 1;
-    if (MORE && kt + S::NSW - 1 < nk) issue_w(kt + S::NSW - 1, last);
-#pragma unroll
-    for (int i = 0; i < S::NB; ++i) {
-      // products stay on their side of the barriers (they touch no memory, so the compiler would move all of
-      // them behind the last one, and every copy would be waited for where it is issued)
-      __builtin_amdgcn_sched_barrier(0);
-      if (i == 1 && MORE) {
-        __syncthreads();
-        if (kt + 2 < nk) issue_a(kt + 2);
-      }
-      if (i + 1 < S::NB) {
-        load_weights(slot, i + 1, wt[(i + 1) & 1]);
-      } else if constexpr (MORE) {
-        if (kt + 2 < nk) wait_vm<FLY>();
-        else wait_vm<0>();
-        __syncthreads();
-        __builtin_amdgcn_sched_barrier(0);
-        load_weights(next, 0, wt[0]);
-      }
-#pragma unroll
-      for (int j = 0; j < S::MB; ++j) {
-        const int k = i * S::MB + j;
-        Pending q;
-        if constexpr (F32) q.d = wide_product(widen(wt[i & 1].w), widen(tk.x[j]));
-        else q.d = code_product(wt[i & 1].w, tk.x[j]);
-        if constexpr (ROWS_B) q.s = wt[i & 1].s * tk.s[j];
-        else q.s[0] = tk.s[j];
-        const int o = (k + LAST - 2) % LAST;
-        settle(acc[o / S::MB][o % S::MB], pend[k & 1]);
-        pend[k & 1] = q;
-        if (MORE && i + 1 == S::NB) load_tokens(kt + 1, next, j, tk);
-      }
-    }
-    slot = next;
-  };
-  for (int kt = 0; kt + 1 < nk; ++kt) run_stage(kt, std::true_type{});
-  run_stage(nk - 1, std::false_type{});
-#pragma unroll
-  for (int u = 0; u < 2; ++u) settle(acc[(LAST - 2 + u) / S::MB][(LAST - 2 + u) % S::MB], pend[(LAST - 2 + u) & 1]);
+  for (int u = 0; u < 2; ++u) settle(acc[(LAST - 2 + u) / S::MB][(LAST - 2 + u) % S::MB], (LAST - 2 + u) & 1);
 
-  // lane: token r16 of a block, columns 4 q4 .. 4 q4 + 3
-  const bool vec = p.ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & (F32 ? 15u : 7u)) == 0;
+  // Results through LDS, a wave row's tokens at a time, so that a lane has 8 neighbouring columns.  Row r holds
+  // 16-byte chunk c at c ^ (r % 16): the 16 rows a wave writes at once fall in disjoint banks.
+  constexpr int WT = S::TM / S::NWM, PPR = S::TN / 8;
+  static_assert(WT * S::TN * 4 <= S::template lds<ROWS_B>(), "epilogue round");
+  float* ct = reinterpret_cast<float*>(lds);
+  const int es = F32 ? 4 : 2;
+  const bool vec = (p.ldo * es) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15u) == 0;
+#pragma unroll 1
+  for (int k = 0; k < S::NWM; ++k) {
+    __syncthreads();
+    if (wm == k) {
 #pragma unroll
-  for (int j = 0; j < S::MB; ++j) {
-    const int m = (wm * S::MB + j) * 16 + r16;
-    if (m >= rows) continue;
+      for (int i = 0; i < S::NB; ++i)
 #pragma unroll
-    for (int i = 0; i < S::NB; ++i) {
-      const int n = (wn * S::NB + i) * 16 + 4 * q4;
-      if (n >= cols) continue;
-      uint8_t* to = p.out + ((int64_t)(t.m0 + m) * p.ldo + t.n0 + n) * (F32 ? 4 : 2);
-      const f32x4_t v = acc[i][j];
-      if (vec && n + 4 <= cols) {
+        for (int j = 0; j < S::MB; ++j) {
+          const int r = j * 16 + r16, c = (wn * S::NB + i) * 4 + q4;
+          *reinterpret_cast<f32x4_t*>(ct + r * S::TN + ((c ^ r16) << 2)) = acc[i][j];
+        }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int o = threadIdx.x; o < WT * PPR; o += S::NTH) {
+      const int r = o / PPR, n = 8 * (o % PPR), m = k * WT + r;
+      if (m >= rows || n >= cols) continue;
+      float v[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4_t q = *reinterpret_cast<const f32x4_t*>(ct + r * S::TN + (((n / 4 + h) ^ (r & 15)) << 2));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * h + e] = q[e];
+      }
+      uint8_t* to = p.out + ((int64_t)(t.m0 + m) * p.ldo + t.n0 + n) * es;
+      if (vec && n + 8 <= cols) {
         if constexpr (F32) {
-          f32x4_t* o = reinterpret_cast<f32x4_t*>(to);
-          *o = ADD ? *o + v : v;
-        } else {
-          uint2* o = reinterpret_cast<uint2*>(to);
-          uint2 z = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
-          if constexpr (ADD) {
-            const uint2 y = *o;
-            z = make_uint2(pack_bf2(lo_bf(y.x) + lo_bf(z.x), hi_bf(y.x) + hi_bf(z.x)),
-                           pack_bf2(lo_bf(y.y) + lo_bf(z.y), hi_bf(y.y) + hi_bf(z.y)));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            f32x4_t* q = reinterpret_cast<f32x4_t*>(to) + h;
+            const f32x4_t z{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+            *q = ADD ? *q + z : z;
           }
-          *o = z;
+        } else {
+          if constexpr (ADD) {
+            float old[8];
+            unpack_bf16x8(*reinterpret_cast<const uint4*>(to), old);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = old[e] + bf2f(f2bf(v[e]));
+          }
+          *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]),
+                                                     pack_bf2(v[6], v[7]));
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 8; ++e) {
           if (n + e >= cols) break;
           if constexpr (F32) {
-            float* o = reinterpret_cast<float*>(to) + e;
-            *o = ADD ? *o + v[e] : v[e];
+            float* q = reinterpret_cast<float*>(to) + e;
+            *q = ADD ? *q + v[e] : v[e];
           } else {
-            uint16_t* o = reinterpret_cast<uint16_t*>(to) + e;
+            uint16_t* q = reinterpret_cast<uint16_t*>(to) + e;
             const uint32_t z = f2bf(v[e]);
-            *o = (uint16_t)(ADD ? f2bf(bf2f(*o) + bf2f(z)) : z);
+            *q = (uint16_t)(ADD ? f2bf(bf2f(*q) + bf2f(z)) : z);
           }
         }
       }
@@ -357,7 +429,7 @@ void launch_shape(hipStream_t st, const MatmulArgs& a) {
 moe_status check(const moe_block_matmul_problem* p) {
   if (!p) return MOE_ERR_NULL;
   const int64_t M = p->rows, N = p->cols, K = p->depth;
-  if (M < 0 || M > (1 << 24) || N < 1 || N > (1 << 20) || K < 16 || K > (1 << 24) || K % 16) return MOE_ERR_SHAPE;
+  if (M < 0 || M > (1 << 24) || N < 1 || N > (1 << 20) || K < 16 || K > (1 << 22) || K % 16) return MOE_ERR_SHAPE;
   if (p->groups < 1 || p->groups > kMaxGroups) return MOE_ERR_SHAPE;
   if ((M / 64 + 1 + p->groups) * (N / 128 + 1) > (1 << 22)) return MOE_ERR_SHAPE;   // a launch holds 2^32 threads
   if (p->scales != MOE_FP8_ROWS && p->scales != MOE_FP8_TILES) return MOE_ERR_UNSUPPORTED;
@@ -388,8 +460,8 @@ extern "C" moe_status moe_block_matmul(const moe_block_matmul_problem* p, const 
   if (!a || !a->base || !a_scales || !b || !b->base || !b_scales || !out || !out->base) return MOE_ERR_NULL;
   if (p->groups > 1 && !offsets) return MOE_ERR_NULL;
   if (b->table) return MOE_ERR_LAYOUT;
-  if (a->ld < p->depth || a->ld % 16 || !aligned16(a->base)) return MOE_ERR_LAYOUT;
-  if (b->ld < p->depth || b->ld % 16 || !aligned16(b->base)) return MOE_ERR_LAYOUT;
+  if (a->ld < p->depth || a->ld % 16 || a->ld > MOE_FP8_MAX_LD || !aligned16(a->base)) return MOE_ERR_LAYOUT;
+  if (b->ld < p->depth || b->ld % 16 || b->ld > MOE_FP8_MAX_LD || !aligned16(b->base)) return MOE_ERR_LAYOUT;
   if (p->groups > 1 && (b->expert_stride < 0 || b->expert_stride % 16)) return MOE_ERR_LAYOUT;
   if (out->ld < p->cols || !elem_aligned(out->base, p->out_dtype)) return MOE_ERR_LAYOUT;
   if (!aligned4(a_scales) || !aligned4(b_scales) || !aligned4(offsets)) return MOE_ERR_LAYOUT;

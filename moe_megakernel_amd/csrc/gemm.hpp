@@ -106,6 +106,13 @@ __device__ __forceinline__ void dma4(const void* gptr, uint32_t m0v) {
                : "memory", "m0");
 }
 
+// LDS copy with a uniform base and a 32-bit offset a lane: no vector instruction moves the address on.
+__device__ __forceinline__ void dma16s(const uint8_t* base, uint32_t off, uint32_t m0v) {
+  const uint32_t m = __builtin_amdgcn_readfirstlane(m0v);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "s"(m)
+               : "memory", "m0");
+}
+
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
