@@ -405,13 +405,34 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
   }
 }
 
-using Large = Shape<256, 192, 2, 2, 1, 3>;
+// Large is the fastest where there are tiles for every CU (8192 x 4096 x 7168: 226 us; 256 x 192 is 7 % faster where one round
+// of it covers what takes Large two, and up to 7 % slower elsewhere; 256 x 256 does not fit the registers).  FP32 results have
+// more vector work a product, and a smaller tile for the registers of it.
+using Large = Shape<256, 128, 2, 2, 1, 3>;
+using Medium = Shape<128, 64, 2, 2, 2, 3>;
 using Wide32 = Shape<128, 128, 2, 2, 1, 3>;
 
 template <class S>
 int64_t tiles(const MatmulArgs& a) {
   const int64_t m = (a.M + S::TM - 1) / S::TM + (a.offsets ? a.G : 0);
   return m * ((a.N + S::TN - 1) / S::TN);
+}
+
+// Whether Medium tiles are the faster ones, from the rounds each needs: 0.8 us a stage of k and 7 us for 256 Large tiles (one a
+// CU), 0.62 and 8 for 512 Medium ones (two), 0.42 and 6 for a last round of at most 256 of them.  Measured, Large and
+// Medium, in us at N 4096, K 7168: M 128 51.8 and 28.7, 512 53.1 and 31.7, 1024 55.3 and 43.3, 2048 64.3 and 93.1; at
+// N 2048, K 4096: M 2000 35.8 and 26.7, 4000 40.5 and 49.6.  Groups are taken to end in the middle of a tile.
+bool medium(const MatmulArgs& a) {
+  const int stages = (a.K + kKB - 1) / kKB;
+  auto count = [&](int tm, int tn) {
+    const int64_t m = a.offsets ? a.M / tm + (a.G + 1) / 2 : (a.M + tm - 1) / tm;
+    return m * ((a.N + tn - 1) / tn);
+  };
+  const int64_t l = (count(Large::TM, Large::TN) + 255) / 256, m = count(Medium::TM, Medium::TN), rest = m % 512;
+  const float large = l * (0.8f * stages + 7.0f);
+  const float small = (m / 512) * (0.62f * stages + 8.0f) +
+                      (rest == 0 ? 0.0f : rest > 256 ? 0.62f * stages + 8.0f : 0.42f * stages + 6.0f);
+  return small < large;
 }
 
 template <class S, bool ROWS_B, bool F32>
@@ -444,6 +465,7 @@ moe_status check(const moe_block_matmul_problem* p) {
 void launch_matmul(hipStream_t st, const MatmulArgs& a) {
   if (a.M <= kFewRows) launch_few(st, a);
   else if (a.out_fp32) launch_shape<Wide32, true>(st, a);
+  else if (medium(a)) launch_shape<Medium, false>(st, a);
   else launch_shape<Large, false>(st, a);
 }
 

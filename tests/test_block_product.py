@@ -403,3 +403,25 @@ def test_captured_and_on_another_stream(gpu_lib, M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want), i
+
+
+def test_products_past_the_limits_are_refused():
+    far = mk.MOE_FP8_MAX_LD + 16
+    assert _call(_mm(), a=(PTR, far)) == mk.MOE_ERR_LAYOUT
+    assert _call(_mm(), b=(PTR, 0, 0, far)) == mk.MOE_ERR_LAYOUT
+    assert _call(_mm(depth=(1 << 22) + 16), a=(PTR, 1 << 23), b=(PTR, 0, 0, 1 << 23)) == mk.MOE_ERR_SHAPE
+
+
+# Enough tiles for every CU: the sizes where the product goes in large tiles, of two and of nine blocks of k.
+@pytest.mark.gpu
+@pytest.mark.parametrize("scales", ["tiles", "rows"])
+@pytest.mark.parametrize("K", [144, 1040])
+@pytest.mark.parametrize("accumulate,pad", [(False, 1), (True, 6)])
+def test_wide_product_matches_formula(gpu_lib, scales, K, accumulate, pad):
+    check_product(1050, 5130, K, scales=scales, accumulate=accumulate, pad=pad, seed=K)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ends", [[0, 0, 129, 1200], [5, 500, 1100, 1150]])
+def test_wide_product_in_groups_matches_formula(gpu_lib, ends):
+    check_product(1200, 5130, 1040, G=3, ends=ends, seed=ends[1])

@@ -504,3 +504,30 @@ def test_shared_expert_run_by_the_caller(gpu_lib):
     torch.cuda.synchronize()
     got, ref = routed.out.double() + out.double(), both.out.double()
     assert float((got - ref).abs().max() / ref.abs().max()) <= 2e-2
+
+
+def test_strides_past_the_limit_are_refused():
+    far = mk.MOE_FFN_MAX_LD + 64
+    for name in ("x", "gate", "up", "down", "out"):
+        assert fwd(problem(), **{name: (PTR, far)}) == mk.MOE_ERR_LAYOUT, name
+    for name in ("dy", "x", "gate", "up", "down", "gx", "gg", "gu", "gd"):
+        assert bwd(problem(), **{name: (PTR, far)}) == mk.MOE_ERR_LAYOUT, name
+
+
+# Enough tiles for every CU, few k: the sizes where the products go in large tiles (up and dh; down and dx; the weights' gradients).
+WIDE = [(1101, 64, 8256), (1101, 8256, 64), (70, 3200, 3264)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("saved", ["bf16", "int8"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("T,H,I", WIDE)
+def test_wide_forward_matches_formula(gpu_lib, T, H, I, kind, saved):
+    test_forward_matches_formula(gpu_lib, T, H, I, kind, saved)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gdt", [BF, torch.float32])
+@pytest.mark.parametrize("T,H,I", WIDE)
+def test_wide_backward_matches_formula(gpu_lib, T, H, I, gdt):
+    test_backward_matches_formula(gpu_lib, T, H, I, "gelu" if gdt == BF else "silu", "bf16", gdt)
