@@ -252,20 +252,50 @@ __device__ __forceinline__ void zero(Sums<TL>& acc) {
 // tiles, in bands of kBandM m-tiles, m fastest: an XCD's 32 CUs then share about 8 row panels and
 // 4 column panels in its L2.
 struct TileAt {
-  int m, n;
+  int m, n, part;
   bool ok;
 };
-__device__ __forceinline__ TileAt tile_at(int mt, int nt) {
-  const int total = mt * nt, x = blockIdx.x & 7, j = blockIdx.x >> 3;
+// With a split contraction the parts are walked one after the other.
+__device__ __forceinline__ TileAt tile_at(int mt, int nt, int split = 1) {
+  const int total = mt * nt * split, x = blockIdx.x & 7, j = blockIdx.x >> 3;
   const int t0 = (int)((int64_t)total * x / 8), t1 = (int)((int64_t)total * (x + 1) / 8);
-  TileAt t{0, 0, j < t1 - t0};
+  TileAt t{0, 0, 0, j < t1 - t0};
   if (!t.ok) return t;
-  const int L = t0 + j, band = L / (kBandM * nt), r = L - band * kBandM * nt, h = min(kBandM, mt - band * kBandM);
+  t.part = (t0 + j) / (mt * nt);
+  const int L = t0 + j - t.part * mt * nt;
+  const int band = L / (kBandM * nt), r = L - band * kBandM * nt, h = min(kBandM, mt - band * kBandM);
   t.n = r / h;
   t.m = band * kBandM + r % h;
   return t;
 }
 inline unsigned tile_grid(int64_t tiles) { return (unsigned)((tiles + 7) / 8 * 8 + 8); }
+
+// A contraction split over `n` workgroups a tile: their sums, [n][rows][cols] of the whole result, which a second kernel
+// adds up.  (The last workgroup of a tile to do that itself, as the layer's kernels for a few tokens have it, keeps the
+// registers of these tiles from fitting.)
+struct Split {
+  float* sums;
+  int n;
+};
+// First stage of a part.
+__device__ __forceinline__ int part_begin(int stages, int part, int n) { return (int)((int64_t)stages * part / n); }
+
+// The tile's sums to their part's, from `to` (row 0, column 0 of the tile), rows ld apart.  PAIR: gate and up columns
+// alternate in 32s; the up ones' sums lie `up` on.
+template <class TL, bool PAIR>
+__device__ __forceinline__ void leave(const Sums<TL>& acc, float* to, int64_t ld, int rows, int cols, int up) {
+  const int lane = threadIdx.x & 63, r0 = wave_m<TL>() * TL::WMR + (lane & 15), c0 = wave_n<TL>() * TL::WNC + 4 * (lane >> 4);
+#pragma unroll
+  for (int i = 0; i < Blocks<TL>::MI; ++i) {
+    if (r0 + 16 * i >= rows) continue;
+    float* line = to + (int64_t)(r0 + 16 * i) * ld;
+#pragma unroll
+    for (int j = 0; j < Blocks<TL>::NJ; ++j) {
+      const int c = c0 + 16 * j, col = PAIR ? (c >> 6) * 32 + (c & 31) : c;
+      if (col < cols) *reinterpret_cast<f32x4_t*>(line + col + (PAIR && ((c >> 5) & 1) ? up : 0)) = acc[i][j];
+    }
+  }
+}
 
 // Hands the accumulators out through LDS, a wave row at a time, so that a lane has 8
 // neighbouring columns: f(row, col, v, q) for row < rows, col < cols.  PAIR: gate and up columns
@@ -276,7 +306,7 @@ struct Nothing {};
 template <class TL, bool PAIR, class PRE, class F>
 __device__ __forceinline__ void each_piece(const Sums<TL>& acc, uint8_t* lds, int rows, int cols, const PRE& pre, const F& f) {
   constexpr int PPR = PAIR ? TL::TN / 16 : TL::TN / 8, PPT = TL::WMR * PPR / TL::NTH;
-  constexpr int kAhead = PPT >= 8 ? 4 : PPT / 2, RPP = TL::NTH / PPR;   // rows a pass of the workgroup
+  constexpr int kAhead = PPT % 8 == 0 ? 4 : PPT % 6 == 0 ? 3 : PPT / 2, RPP = TL::NTH / PPR;   // rows a pass of the workgroup
   static_assert(TL::WMR * TL::TN * 4 <= TL::LDS && TL::NTH % PPR == 0 && PPT % (2 * kAhead) == 0, "epilogue round");
   float* ct = reinterpret_cast<float*>(lds);
   const int t = threadIdx.x, lane = t & 63, wm = wave_m<TL>(), wn = wave_n<TL>();

@@ -2,6 +2,8 @@
 // the launches.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "../../include/moe.h"
 #include "checkpoint.hpp"
 #include "ffn.hpp"
@@ -47,18 +49,61 @@ size_t saved_layout(const moe_ffn_problem* p, moe_ffn_saved_layout* L) {
   return o.total > kAlign ? o.total : kAlign;
 }
 
+// What a round of `w` workgroups at once takes, in us, for `stages` stages of 32 k each: a start and an end, and a time a stage
+// that grows with the CUs at work (up to 256 tiles one a CU; Medium ones up to 512, two a CU).
+double round_us(int shape, int64_t w, double stages) {
+  const double a = (double)w / 256;
+  if (shape == ffn::kLarge) return (0.57 + 0.28 * a) * stages + 14.0;
+  if (shape == ffn::kMid) return (0.50 + 0.10 * a) * stages + 14.0;
+  return w > 256 ? 0.62 * stages + 10.0 : (0.20 + 0.12 * a * a) * stages + 8.0;
+}
+
+// How an m x n product over k is cut: the tiles and the parts of the contraction that are expected to end first.  Adding up
+// parts costs a launch and their way to memory and back.  Measured, in us, Medium / Mid / Large tiles, the parts in brackets:
+// 777 x 24576 over 4096 260 / 176 / 199, 777 x 4096 over 12288 133 / 140 [2] / 116 [4] (one part: 133 / 204 / 230), 777 x 4096 over 24576
+// 241 / 263 [2] / 199 [4], 300 x 1024 over 5632 22 [8] / 32 [8] / 37 [8] (45 / 96 / 113), 200 x 1024 over 4096 19 [8] / 29 [8] / 34 [8]
+// (37 / 85 / 96), 512 x 1024 over 4096 21 [8] / - / 33 [8] (35 / - / 90), 4096 x 4096 over 4096 173 / - / 118.
+constexpr int kMaxSplit = 16;
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+ffn::Plan cut(int64_t m, int64_t n, int64_t k, bool mid, float* sums) {
+  ffn::Plan best{ffn::kMedium, {sums, 1}};
+  double least = 1e30;
+  for (int s = ffn::kMedium; s <= ffn::kLarge; ++s) {
+    if (s == ffn::kMid && !mid) continue;
+    const int64_t tiles = ceil_div(m, ffn::kShapeRows[s]) * ceil_div(n, ffn::kShapeCols[s]), most = s == ffn::kMedium ? 512 : 256;
+    for (int parts = 1; parts <= kMaxSplit; ++parts) {
+      const int64_t w = tiles * parts;
+      const double stages = (double)ceil_div(k, 32) / parts;
+      if (parts > 1 && (w > most || stages < 8)) break;
+      double us = (double)(w / most) * round_us(s, most, stages) + (w % most ? round_us(s, w % most, stages) : 0.0);
+      if (parts > 1) us += 4.0 + (double)(parts * m * n) * 4 * 2 / 6e6;
+      if (us < least) least = us, best.shape = s, best.split.n = parts;
+    }
+  }
+  return best;
+}
+// Bytes of a split product's sums, no less than what fewer rows or a shorter contraction take: all workgroups of a round
+// at most, and all parts of the result.
+size_t split_bytes(int64_t m, int64_t n, int64_t k) {
+  const int64_t parts = std::min<int64_t>(ceil_div(k, 32) / 8, kMaxSplit), round = (int64_t)256 * 256 * 256 * 4;
+  return parts < 2 ? 0 : (size_t)std::min(m * n * 4 * parts, round);
+}
+
 struct Fwd {
-  size_t h, total;
+  size_t h, sums, total;
 };
 Fwd fwd_layout(const moe_ffn_problem* p) {
+  const size_t T = p->tokens, H = p->hidden, I = p->intermediate;
   Offsets o;
   Fwd f;
   f.h = o.take((size_t)2 * p->tokens * p->intermediate);
+  f.sums = o.take(std::max(split_bytes(T, 2 * I, H), split_bytes(T, H, I)));
   f.total = o.total > kAlign ? o.total : kAlign;
   return f;
 }
 struct Bwd {
-  size_t dab, h, x, total;
+  size_t dab, h, x, sums, total;
 };
 Bwd bwd_layout(const moe_ffn_problem* p) {
   const size_t T = p->tokens, H = p->hidden, I = p->intermediate;
@@ -67,6 +112,7 @@ Bwd bwd_layout(const moe_ffn_problem* p) {
   b.dab = o.take(4 * T * I);
   b.h = o.take(2 * T * I);
   b.x = o.take(p->saved_dtype == MOE_MXINT8 ? 2 * T * H : 0);
+  b.sums = o.take(std::max(std::max(split_bytes(T, I, H), split_bytes(T, H, 2 * I)), split_bytes(2 * I, H, T)));
   b.total = o.total > kAlign ? o.total : kAlign;
   return b;
 }
@@ -133,14 +179,20 @@ moe_status moe_ffn_forward(const moe_ffn_problem* p, const moe_rows* x, const mo
     const checkpoint::Args c{static_cast<uint8_t*>(x->base), x->ld, T, H, s + L.x, s + L.x_scales};
     MOE_TRY(launch("checkpoint_store", st, [&] { checkpoint::launch_store(st, c, false); }));
   }
-  const ffn::UpArgs u{mat(x), mat(gate), mat(up), h, kept(saved, L), T, H, I, p->activation, p->saved_dtype};
-  const ffn::RowsArgs d{h, mat(down), mat(down), mat(out), T, H, I, I};
+  ffn::UpArgs u{mat(x), mat(gate), mat(up), h, kept(saved, L), T, H, I, p->activation, p->saved_dtype};
+  ffn::RowsArgs d{h, mat(down), mat(down), mat(out), T, H, I, I};
   if (T <= ffn::kFewTokens && !p->saved_dtype) {
     MOE_TRY(launch("ffn_up_few", st, [&] { ffn::launch_up_few(st, u); }));
     return launch("ffn_down_few", st, [&] { ffn::launch_down_few(st, d); });
   }
+  float* sums = reinterpret_cast<float*>(ws + F.sums);
+  u.plan = cut(T, 2 * (int64_t)I, H, true, sums);
+  d.plan = cut(T, H, I, true, sums);
   MOE_TRY(launch("ffn_up", st, [&] { ffn::launch_up(st, u); }));
-  return launch("ffn_down", st, [&] { ffn::launch_down(st, d); });
+  if (u.plan.split.n > 1) MOE_TRY(launch("ffn_up_sum", st, [&] { ffn::launch_up_sum(st, u); }));
+  MOE_TRY(launch("ffn_down", st, [&] { ffn::launch_down(st, d); }));
+  if (d.plan.split.n > 1) MOE_TRY(launch("ffn_down_sum", st, [&] { ffn::launch_rows_sum(st, d); }));
+  return MOE_OK;
 }
 
 moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, const moe_rows* x,
@@ -177,12 +229,16 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
   moe_ffn_saved_layout L;
   saved_layout(p, &L);
   const ffn::Mat dab{reinterpret_cast<uint16_t*>(ws + B.dab), 2 * I}, h{reinterpret_cast<uint16_t*>(ws + B.h), I};
+  float* sums = reinterpret_cast<float*>(ws + B.sums);
   if (T > 0) {
-    const ffn::DhArgs d{mat(grad_out), mat(down), kept(saved, L), dab.p, h.p, T, H, I, p->activation, p->saved_dtype};
+    const ffn::DhArgs d{mat(grad_out), mat(down), kept(saved, L), dab.p, h.p, T, H, I, p->activation, p->saved_dtype,
+                        cut(T, I, H, true, sums)};
     MOE_TRY(launch("ffn_dh", st, [&] { ffn::launch_dh(st, d); }));
+    if (d.plan.split.n > 1) MOE_TRY(launch("ffn_dh_sum", st, [&] { ffn::launch_dh_sum(st, d); }));
     if (grad_x) {
-      const ffn::RowsArgs r{dab, mat(gate), mat(up), mat(grad_x), T, H, 2 * I, I};
+      const ffn::RowsArgs r{dab, mat(gate), mat(up), mat(grad_x), T, H, 2 * I, I, cut(T, H, 2 * (int64_t)I, true, sums)};
       MOE_TRY(launch("ffn_dx", st, [&] { ffn::launch_dx(st, r); }));
+      if (r.plan.split.n > 1) MOE_TRY(launch("ffn_dx_sum", st, [&] { ffn::launch_rows_sum(st, r); }));
     }
   } else if (!(p->flags & MOE_FFN_OVERWRITE_GRADS)) {
     return MOE_OK;
@@ -190,8 +246,9 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
   const int over = (p->flags & MOE_FFN_OVERWRITE_GRADS) ? 1 : 0;
   if (grad_down) {
     const ffn::Mat dy = T > 0 ? mat(grad_out) : ffn::Mat{nullptr, H};
-    const ffn::WgradArgs w{dy, h, grad_down->base, nullptr, grad_down->ld, 0, H, I, T, H, f32, over};
+    const ffn::WgradArgs w{dy, h, grad_down->base, nullptr, grad_down->ld, 0, H, I, T, H, f32, over, cut(H, I, T, false, sums)};
     MOE_TRY(launch("ffn_wgrad_down", st, [&] { ffn::launch_wgrad(st, w); }));
+    if (w.plan.split.n > 1) MOE_TRY(launch("ffn_wgrad_down_sum", st, [&] { ffn::launch_wgrad_sum(st, w); }));
   }
   if (grad_gate) {
     ffn::Mat xs{reinterpret_cast<uint16_t*>(ws + B.x), H};
@@ -205,8 +262,9 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
       }
     }
     const ffn::WgradArgs w{dab, xs, grad_gate->base, grad_up->base, grad_gate->ld, grad_up->ld, 2 * I, H, T, I, f32,
-                           over};
+                           over, cut(2 * (int64_t)I, H, T, false, sums)};
     MOE_TRY(launch("ffn_wgrad_up", st, [&] { ffn::launch_wgrad(st, w); }));
+    if (w.plan.split.n > 1) MOE_TRY(launch("ffn_wgrad_up_sum", st, [&] { ffn::launch_wgrad_sum(st, w); }));
   }
   return MOE_OK;
 }

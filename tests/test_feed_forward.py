@@ -514,8 +514,8 @@ def test_strides_past_the_limit_are_refused():
         assert bwd(problem(), **{name: (PTR, far)}) == mk.MOE_ERR_LAYOUT, name
 
 
-# Enough tiles for every CU, few k: the sizes where the products go in large tiles (up and dh; down and dx; the weights' gradients).
-WIDE = [(1101, 64, 8256), (1101, 8256, 64), (70, 3200, 3264)]
+# Enough tiles for every CU, few k: the sizes where the products go in larger tiles (up and dh; down and dx; the weights' gradients).
+WIDE = [(1101, 64, 8256), (1101, 8256, 64), (70, 3200, 3264), (967, 64, 5440)]
 
 
 @pytest.mark.gpu
@@ -531,3 +531,80 @@ def test_wide_forward_matches_formula(gpu_lib, T, H, I, kind, saved):
 @pytest.mark.parametrize("T,H,I", WIDE)
 def test_wide_backward_matches_formula(gpu_lib, T, H, I, gdt):
     test_backward_matches_formula(gpu_lib, T, H, I, "gelu" if gdt == BF else "silu", "bf16", gdt)
+
+
+# Few tiles, long contractions: split ones, in tiles of 128 columns (up, dh; down, dx; the weights' gradients) ...
+SPLIT = [(67, 1152, 64), (76, 64, 1088), (965, 64, 64), (300, 1024, 704)]
+# ... and in larger ones (up; down and dx; dx; dh; up)
+SPLIT_WIDE = [(257, 1536, 5568), (1043, 3648, 1856), (129, 3392, 6144), (663, 1536, 5504), (387, 2880, 5504)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("saved", ["bf16", "int8"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+@pytest.mark.parametrize("T,H,I", SPLIT)
+def test_split_forward_matches_formula(gpu_lib, T, H, I, kind, saved):
+    test_forward_matches_formula(gpu_lib, T, H, I, kind, saved)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("saved", ["bf16", "int8"])
+@pytest.mark.parametrize("gdt", [BF, torch.float32])
+@pytest.mark.parametrize("T,H,I", SPLIT)
+def test_split_backward_matches_formula(gpu_lib, T, H, I, saved, gdt):
+    test_backward_matches_formula(gpu_lib, T, H, I, "silu" if gdt == BF else "gelu", saved, gdt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I", SPLIT_WIDE)
+def test_split_wide_block_matches_formula(gpu_lib, T, H, I):
+    test_forward_matches_formula(gpu_lib, T, H, I, "gelu", "int8")
+    test_backward_matches_formula(gpu_lib, T, H, I, "silu", "bf16", torch.float32)
+
+
+@pytest.mark.gpu
+def test_split_gradients_accumulate_repeat_and_capture(gpu_lib):
+    """Gradients added to what is there, the same bits in every run, and a captured forward and backward whose
+    replays share a workspace with eager calls."""
+    T, H, I = 1500, 128, 192
+    x, wg, wu, wd, dy = inputs(T, H, I)
+    op = mk.FeedForward(H, I, T, "silu", "bf16", grad_dtype=torch.float32)
+    sv = torch.zeros(op.saved_bytes(T), dtype=torch.uint8, device="cuda")
+    out, dx = torch.empty(T, H, dtype=BF, device="cuda"), torch.empty(T, H, dtype=BF, device="cuda")
+    g = [torch.zeros(*s, device="cuda") for s in ((I, H), (I, H), (H, I))]
+
+    def step():
+        op.forward(x, wg, wu, wd, out, sv)
+        op.backward(dy, x, wg, wu, wd, sv, dx, *g)
+
+    step()
+    torch.cuda.synchronize()
+    first = [t.clone() for t in [out, dx] + g]
+    step()
+    torch.cuda.synchronize()
+    for t, f in zip([out, dx], first):
+        assert torch.equal(t, f)
+    for t, f in zip(g, first[2:]):
+        assert torch.equal(t, f + f)
+    for t in g:
+        t.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n in range(1, 4):
+        out.zero_(), dx.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, f in zip([out, dx], first):
+            assert torch.equal(t, f)
+        other = torch.empty_like(out)
+        op.forward(x, wg, wu, wd, other, sv)             # eager work between the replays, in the same workspace
+        torch.cuda.synchronize()
+        assert torch.equal(other, first[0])
+        want = first[2:]
+        total = [f.clone() for f in want]
+        for _ in range(n - 1):
+            total = [t + f for t, f in zip(total, want)]
+        for t, f in zip(g, total):
+            assert torch.equal(t, f)
