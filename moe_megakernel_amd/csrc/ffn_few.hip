@@ -119,17 +119,37 @@ void down_as(hipStream_t st, const RowsArgs& a) {
   hipLaunchKernelGGL((k_few_down<R, NF, W, D>), grid, block, 0, st, a);
 }
 
+// f(fragments a workgroup, token tiles, waves, stages in flight).  Two fragments share the tokens' copies, which pays where
+// one would leave more workgroups than CUs anyway (T > 32: first kernel of 48 tokens, H 4096, I 12288 45 us against 67, second
+// one of 37, H 7168, I 2048 10 against 12.5; but its first one, 256 workgroups, 16 against 15.4) or, with two token
+// tiles, many more (first kernel of 24 tokens, H 4096, I 12288 39 us against 47).  Four waves and two stages in flight leave
+// room for two workgroups a CU; one token tile is so small that eight waves do (13 tokens, H 4096, I 12288: 57 us,
+// 64 with four stages).
+template <class F>
+void by_tokens(int T, int64_t frags, const F& f) {
+  using std::integral_constant;
+  constexpr integral_constant<int, 1> c1{};
+  constexpr integral_constant<int, 2> c2{};
+  constexpr integral_constant<int, 3> c3{};
+  constexpr integral_constant<int, 4> c4{};
+  constexpr integral_constant<int, 8> c8{};
+  if (T <= 16) f(c1, c1, c8, c2);
+  else if (T <= 32) frags > 512 ? f(c2, c2, c4, c2) : f(c1, c2, c4, c3);
+  else if (T <= 48) frags > 256 ? f(c2, c3, c4, c2) : f(c1, c3, c8, c2);
+  else frags > 256 ? f(c2, c4, c4, c2) : f(c1, c4, c4, c2);
+}
+
 }  // namespace
 
 void launch_up_few(hipStream_t st, const UpArgs& a) {
-  if (a.T <= 16) up_as<1, 1, 8, 4>(st, a);
-  else if (a.T <= 32) up_as<1, 2, 8, 3>(st, a);
-  else up_as<1, 4, 4, 3>(st, a);
+  by_tokens(a.T, a.I / 8, [&](auto r, auto nf, auto w, auto d) {
+    up_as<decltype(r)::value, decltype(nf)::value, decltype(w)::value, decltype(d)::value>(st, a);
+  });
 }
 void launch_down_few(hipStream_t st, const RowsArgs& a) {
-  if (a.T <= 16) down_as<1, 1, 8, 4>(st, a);
-  else if (a.T <= 32) down_as<1, 2, 8, 3>(st, a);
-  else down_as<1, 4, 4, 3>(st, a);
+  by_tokens(a.T, a.N / 16, [&](auto r, auto nf, auto w, auto d) {
+    down_as<decltype(r)::value, decltype(nf)::value, decltype(w)::value, decltype(d)::value>(st, a);
+  });
 }
 
 }  // namespace ffn

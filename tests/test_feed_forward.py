@@ -608,3 +608,11 @@ def test_split_gradients_accumulate_repeat_and_capture(gpu_lib):
             total = [t + f for t, f in zip(total, want)]
         for t, f in zip(g, total):
             assert torch.equal(t, f)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I", [(16, 192, 4160), (32, 192, 4160), (24, 8256, 64), (48, 192, 2112), (33, 4160, 64), (64, 4160, 2112),
+                                   (49, 64, 64), (40, 320, 192)])
+def test_few_tokens_of_wide_blocks_match_formula(gpu_lib, T, H, I):
+    test_forward_matches_formula(gpu_lib, T, H, I, "silu", "none")
+    test_forward_matches_formula(gpu_lib, T, H, I, "gelu", "none")
