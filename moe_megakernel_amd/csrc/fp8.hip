@@ -30,23 +30,26 @@ namespace {
 
 constexpr int kKB = 128;                   // k of a stage, and of a scale
 
-// Tile of TN weight rows and TM tokens; NSW stages of weights in LDS, two of tokens.
-template <int TN_, int TM_, int NWN_, int NWM_, int MINB_, int NSW_>
+constexpr int kStages = 3;                 // in LDS
+
+// Tile of TN weight rows and TM tokens.
+template <int TN_, int TM_, int NWN_, int NWM_, int MINB_>
 struct Shape {
-  static constexpr int TN = TN_, TM = TM_, NWN = NWN_, NWM = NWM_, MINB = MINB_, NSW = NSW_;
+  static constexpr int TN = TN_, TM = TM_, NWN = NWN_, NWM = NWM_, MINB = MINB_;
   static constexpr int NW = NWN * NWM, NTH = 64 * NW;
   static constexpr int NB = TN / NWN / 16, MB = TM / NWM / 16;   // 16 x 16 blocks of a wave
   static constexpr int W_BYTES = TN * kKB, A_BYTES = TM * kKB;
   static constexpr int W_DMA = W_BYTES / 1024 / NW, A_DMA = A_BYTES / 1024 / NW;   // copies a wave and stage
   static_assert(W_BYTES % (1024 * NW) == 0 && A_BYTES % (1024 * NW) == 0, "copies a wave");
-  static_assert(TN % 64 == 0 && TM % 64 == 0 && (NSW == 2 || NSW == 3), "scale copies, ring");
-  static_assert(NB * 16 <= 128 && 128 % (NB * 16) == 0 && NB >= 4 && NB % 2 == 0 && NB * MB % 2 == 0, "one weight scale a wave");
+  static_assert(TN % 64 == 0 && TM % 64 == 0, "scale copies");
+  static_assert(NB * 16 <= 128 && 128 % (NB * 16) == 0, "one weight scale a wave");
+  static_assert(NB % 4 == 0, "fragment buffers");
   // copies of 64 scales: the tokens', then the weights' rows' or those of the tile's 128-row parts; the same
   // number a wave, so that its copies can be counted
   template <bool ROWS_B>
   static constexpr int scale_copies() { return (TM / 64 + (ROWS_B ? TN / 64 : 1) + NW - 1) / NW * NW; }
   template <bool ROWS_B>
-  static constexpr int lds() { return NSW * (W_BYTES + 256 * scale_copies<ROWS_B>()) + 2 * A_BYTES; }
+  static constexpr int lds() { return kStages * (W_BYTES + A_BYTES + 256 * scale_copies<ROWS_B>()); }
 };
 
 struct Tile {
@@ -132,10 +135,10 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
   const uint32_t lds0 = lds_off(lds);
   const int nk = (p.K + kKB - 1) / kKB;
 
-  // LDS: the weights' stages [NSW][TN][128], the tokens' [2][TM][128] (16-byte chunks swizzled by row), the
-  // scales' [NSW].  Rows past the last repeat it, their results go nowhere; chunks past the last k are zeros.
+  // LDS: the weights' stages [3][TN][128], the tokens' [3][TM][128] (16-byte chunks swizzled by row), the
+  // scales' [3].  Rows past the last repeat it, their results go nowhere; chunks past the last k are zeros.
   constexpr int SC = S::template scale_copies<ROWS_B>(), SC_DMA = SC / S::NW;
-  constexpr int A0 = S::NSW * S::W_BYTES, SC0 = A0 + 2 * S::A_BYTES;
+  constexpr int A0 = kStages * S::W_BYTES, SC0 = A0 + kStages * S::A_BYTES;
   // The lane's offset of each copy from the stage's first byte (host checks keep them below 2^32).
   const uint8_t* gw = p.b + (int64_t)t.g * p.stride_b + (int64_t)t.n0 * p.ldb;
   const uint8_t* ga = p.a + (int64_t)t.m0 * p.lda;
@@ -163,40 +166,39 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
                 : p.sb + (ROWS_B ? t.n0 + min(64 * (i - S::TM / 64) + lane, cols - 1) : tiles);
     step[u] = tok ? p.M : (ROWS_B ? p.N : 1);
   }
-  int put = 0, pet = 0;                    // ring slots of the next weights and tokens
+  int put = 0;                             // ring slot of the next stage
+  auto after = [](int slot) __attribute__((always_inline)) { return slot + 1 == kStages ? 0 : slot + 1; };
   auto copy_scales = [&](int u) __attribute__((always_inline)) {
     dma4(ps[u], lds0 + SC0 + (put * SC + u * S::NW + w) * 256);
     ps[u] += step[u];
   };
-  auto copy_w = [&](int i) __attribute__((always_inline)) {
-    if (i < S::W_DMA) dma16s(gw, ow[i], lds0 + put * S::W_BYTES + (w * S::W_DMA + i) * 1024);
-    else copy_scales(i - S::W_DMA);
+  auto to_w = [&](int i) __attribute__((always_inline)) { return lds0 + put * S::W_BYTES + (w * S::W_DMA + i) * 1024; };
+  auto to_a = [&](int i) __attribute__((always_inline)) { return lds0 + A0 + put * S::A_BYTES + (w * S::A_DMA + i) * 1024; };
+  constexpr int COPIES = S::W_DMA + S::A_DMA + SC_DMA;       // a wave and stage
+  auto copy = [&](int i) __attribute__((always_inline)) {
+    if (i < S::W_DMA) dma16s(gw, ow[i], to_w(i));
+    else if (i < S::W_DMA + S::A_DMA) dma16s(ga, oa[i - S::W_DMA], to_a(i - S::W_DMA));
+    else copy_scales(i - S::W_DMA - S::A_DMA);
   };
-  auto copy_a = [&](int i) __attribute__((always_inline)) {
-    dma16s(ga, oa[i], lds0 + A0 + pet * S::A_BYTES + (w * S::A_DMA + i) * 1024);
+  auto advance = [&]() __attribute__((always_inline)) {
+    gw += kKB;
+    ga += kKB;
+    put = after(put);
   };
-  auto turn = [&](int& slot, int n) __attribute__((always_inline)) { slot = slot + 1 == n ? 0 : slot + 1; };
-  // Whole stages at once; of the last, chunks past K come from the zero page.  (Copy c holds rows 8 c .. 8 c + 7, and
+  // Any stage: of the last, chunks past K come from the zero page.  (Copy c holds rows 8 c .. 8 c + 7, and
   // swz_kc has period 16.)
   auto chunk = [&](int kt, const uint8_t* q, int c) __attribute__((always_inline)) {
     return kt * kKB + 16 * ((lane & 7) ^ swz_kc<128>(8 * c + (lane >> 3))) < p.K
                ? q : reinterpret_cast<const uint8_t*>(g_zero_page) + 16 * lane;
   };
-  auto issue_w = [&](int kt) __attribute__((always_inline)) {
+  auto issue = [&](int kt) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < S::W_DMA; ++i)
-      dma16(chunk(kt, gw + ow[i], w * S::W_DMA + i), lds0 + put * S::W_BYTES + (w * S::W_DMA + i) * 1024);
+    for (int i = 0; i < S::W_DMA; ++i) dma16(chunk(kt, gw + ow[i], w * S::W_DMA + i), to_w(i));
+#pragma unroll
+    for (int i = 0; i < S::A_DMA; ++i) dma16(chunk(kt, ga + oa[i], w * S::A_DMA + i), to_a(i));
 #pragma unroll
     for (int u = 0; u < SC_DMA; ++u) copy_scales(u);
-    gw += kKB;
-    turn(put, S::NSW);
-  };
-  auto issue_a = [&](int kt) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < S::A_DMA; ++i)
-      dma16(chunk(kt, ga + oa[i], w * S::A_DMA + i), lds0 + A0 + pet * S::A_BYTES + (w * S::A_DMA + i) * 1024);
-    ga += kKB;
-    turn(pet, 2);
+    advance();
   };
 
   f32x4_t acc[S::NB][S::MB];
@@ -216,31 +218,31 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
     const u32x4_t u0 = *reinterpret_cast<const u32x4_t*>(block + f0), u1 = *reinterpret_cast<const u32x4_t*>(block + f1);
     return i32x8_t{(int)u0[0], (int)u0[1], (int)u0[2], (int)u0[3], (int)u1[0], (int)u1[1], (int)u1[2], (int)u1[3]};
   };
-  i32x8_t x[S::MB], wf[2];                 // token fragments of a stage, weight fragments of a block and the next
+  i32x8_t x[S::MB], wf[4];                 // token fragments of a stage, weight fragments of a block and the next two
   float s[S::MB];                          // the tokens' scales (times the weight tile's)
-  f32x4_t sw[2];                           // ROWS_B: the weight rows' scales
+  f32x4_t sw[4];                           // ROWS_B: the weight rows' scales
   const uint8_t *lw = lds + wn * S::NB * 16 * kKB, *la = lds + A0 + wm * S::MB * 16 * kKB;
   const float* ls = reinterpret_cast<const float*>(lds + SC0);
-  auto load_tokens = [&](int aslot, int slot, int j) __attribute__((always_inline)) {
+  auto load_tokens = [&](int slot, int j) __attribute__((always_inline)) {
     const float* sc = ls + slot * SC * 64;
-    x[j] = frag(la + aslot * S::A_BYTES + j * 16 * kKB);
+    x[j] = frag(la + slot * S::A_BYTES + j * 16 * kKB);
     s[j] = sc[(wm * S::MB + j) * 16 + r16];
     if constexpr (!ROWS_B) s[j] *= sc[S::TM + wn * S::NB * 16 / 128];
   };
   auto load_weights = [&](int slot, int i) __attribute__((always_inline)) {
-    wf[i & 1] = frag(lw + slot * S::W_BYTES + (i % S::NB) * 16 * kKB);
+    wf[i % 4] = frag(lw + slot * S::W_BYTES + i * 16 * kKB);
     if constexpr (ROWS_B)
-      sw[i & 1] = *reinterpret_cast<const f32x4_t*>(ls + slot * SC * 64 + S::TM + (wn * S::NB + i % S::NB) * 16 + 4 * q4);
+      sw[i % 4] = *reinterpret_cast<const f32x4_t*>(ls + slot * SC * 64 + S::TM + (wn * S::NB + i) * 16 + 4 * q4);
   };
 
-  // Barrier B(kt) opens stage kt: its copies have landed.  The weights' fragment of block i + 1 is read while
-  // block i multiplies, and the last block of a stage multiplies behind the barrier that opens the next, each
-  // token fragment replaced by the next stage's as soon as it has been used.  So the weights' slot of stage
-  // kt - 1 is free at B(kt), and the tokens' of stage kt once every wave has started it: a second barrier behind
-  // the first block, which gives their copies two stages of lead with two slots.  A product's result is scaled
-  // and added two products later, when it is there.
-  constexpr int FLY = S::A_DMA + (S::NSW == 3 ? S::W_DMA + SC_DMA : 0);   // copies younger than stage kt + 1's at B(kt + 1)
-  constexpr int LAST = S::NB * S::MB;
+  // Stage kt multiplies NB blocks of 16 weight rows, each with the MB token fragments.  A block's weights are read two blocks
+  // ahead, and each token fragment is replaced by the next stage's as soon as the last block has used it.  So the
+  // barrier that opens stage kt + 1 (its copies have landed) stands two blocks before the end of stage kt, whose
+  // slot has then been read for good; the copies of stage kt + 2 take the slot of stage kt - 1, freed a barrier ago.  A
+  // product's result is scaled and added two products later, when it is there.
+  constexpr int LAST = S::NB * S::MB, OPEN = (S::NB - 2) * S::MB;   // products a stage, those before the barrier
+  auto copies_before = [](int product) constexpr { return product * COPIES / LAST; };
+  constexpr int FLY = copies_before(OPEN);                 // copies of stage kt + 2 at the barrier
   f32x4_t pd[2], pq[2];                    // results on their way and their scales
 #pragma unroll
   for (int u = 0; u < 2; ++u) pd[u] = pq[u] = acc[0][0];
@@ -248,84 +250,72 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
     if constexpr (ROWS_B) a = __builtin_elementwise_fma(pq[u], pd[u], a);
     else a = __builtin_elementwise_fma(f32x4_t{pq[u][0], pq[u][0], pq[u][0], pq[u][0]}, pd[u], a);
   };
-  auto products = [&](int i, bool more, int aslot, int next) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < S::MB; ++j) {
-      const int k = i * S::MB + j, o = (k + LAST - 2) % LAST;
-      f32x4_t d;
-      if constexpr (F32) d = wide_product(widen(wf[i & 1]), widen(x[j]));
-      else d = code_product(wf[i & 1], x[j]);
-      settle(acc[o / S::MB][o % S::MB], k & 1);
-      pd[k & 1] = d;
-      if constexpr (ROWS_B) pq[k & 1] = sw[i & 1] * s[j];
-      else pq[k & 1][0] = s[j];
-      if (more && i + 1 == S::NB) load_tokens(aslot, next, j);
-    }
+  auto product = [&](int i, int j) __attribute__((always_inline)) {
+    const int k = i * S::MB + j, o = (k + LAST - 2) % LAST;
+    f32x4_t d;
+    if constexpr (F32) d = wide_product(widen(wf[i % 4]), widen(x[j]));
+    else d = code_product(wf[i % 4], x[j]);
+    settle(acc[o / S::MB][o % S::MB], k & 1);
+    pd[k & 1] = d;
+    if constexpr (ROWS_B) pq[k & 1] = sw[i % 4] * s[j];
+    else pq[k & 1][0] = s[j];
   };
-  int slot = 0, aslot = 0;                 // the stage's
+  static_assert(LAST % 2 == 0, "results on their way");
+  int slot = 0;                            // the stage's
   auto steady = [&]() __attribute__((always_inline)) {
-    const int next = slot + 1 == S::NSW ? 0 : slot + 1;
+    const int next = after(slot);
 #pragma unroll
     for (int i = 0; i < S::NB; ++i) {
-      __builtin_amdgcn_sched_barrier(0);
-      constexpr int NWC = S::W_DMA + SC_DMA, B = S::NB - 1;
-      if (i == 1) __syncthreads();
-      if (i + 1 == S::NB) {
+      if (i + 2 == S::NB) {
         wait_vm<FLY>();
         __syncthreads();
-        __builtin_amdgcn_sched_barrier(0);
-      } else {
-#pragma unroll
-        for (int c = i * NWC / B; c < (i + 1) * NWC / B; ++c) copy_w(c);
-        if (i > 0)
-#pragma unroll
-          for (int c = (i - 1) * S::A_DMA / (B - 1); c < i * S::A_DMA / (B - 1); ++c) copy_a(c);
       }
-      load_weights(i + 1 == S::NB ? next : slot, i + 1);
-      products(i, true, aslot ^ 1, next);
+#pragma unroll
+      for (int j = 0; j < S::MB; ++j) {
+        __builtin_amdgcn_sched_barrier(0);
+        product(i, j);
+        if (j == 0) load_weights(i + 2 < S::NB ? slot : next, (i + 2) % S::NB);
+        if (i + 1 == S::NB) load_tokens(next, j);
+#pragma unroll
+        for (int c = copies_before(i * S::MB + j); c < copies_before(i * S::MB + j + 1); ++c) copy(c);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
-    gw += kKB;
-    ga += kKB;
-    turn(put, S::NSW);
-    turn(pet, 2);
+    advance();
     slot = next;
-    aslot ^= 1;
   };
-  auto any = [&](int kt) __attribute__((always_inline)) {   // the last stages
-    const int next = slot + 1 == S::NSW ? 0 : slot + 1;
-    if (kt + S::NSW - 1 < nk) issue_w(kt + S::NSW - 1);
+  auto any = [&](int kt) __attribute__((always_inline)) {   // the last stages; behind the last one nothing is used that is read
+    const int next = after(slot);
+    if (kt + 2 < nk) issue(kt + 2);
 #pragma unroll
     for (int i = 0; i < S::NB; ++i) {
-      if (i == 1) {
-        __syncthreads();
-        if (kt + 2 < nk) issue_a(kt + 2);
-      }
-      if (i + 1 == S::NB) {
-        if (kt + 2 < nk) wait_vm<FLY>();
+      if (i + 2 == S::NB) {
+        if (kt + 2 < nk) wait_vm<COPIES>();
         else wait_vm<0>();
         __syncthreads();
       }
-      load_weights(i + 1 == S::NB ? next : slot, i + 1);   // (behind the last stage: read and not used)
-      products(i, true, aslot ^ 1, next);
+#pragma unroll
+      for (int j = 0; j < S::MB; ++j) {
+        product(i, j);
+        if (j == 0) load_weights(i + 2 < S::NB ? slot : next, (i + 2) % S::NB);
+        if (i + 1 == S::NB) load_tokens(next, j);
+      }
     }
     slot = next;
-    aslot ^= 1;
   };
 
-  issue_w(0);
-  issue_a(0);
+  issue(0);
   if (nk > 1) {
-    if constexpr (S::NSW == 3) issue_w(1);
-    issue_a(1);
-    wait_vm<FLY>();
+    issue(1);
+    wait_vm<COPIES>();
   } else {
     wait_vm<0>();
   }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < S::MB; ++j) load_tokens(0, 0, j);
+  for (int j = 0; j < S::MB; ++j) load_tokens(0, j);
   load_weights(0, 0);
+  load_weights(0, 1);
   int kt = 0;
   if (kt + 3 < nk) {
     do steady();                           // its copies are whole stages
@@ -408,9 +398,9 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
 // Large is the fastest where there are tiles for every CU (8192 x 4096 x 7168: 226 us; 256 x 192 is 7 % faster where one round
 // of it covers what takes Large two, and up to 7 % slower elsewhere; 256 x 256 does not fit the registers).  FP32 results have
 // more vector work a product, and a smaller tile for the registers of it.
-using Large = Shape<256, 128, 2, 2, 1, 3>;
-using Medium = Shape<128, 64, 2, 2, 2, 3>;
-using Wide32 = Shape<128, 128, 2, 2, 1, 3>;
+using Large = Shape<256, 128, 2, 2, 1>;
+using Medium = Shape<128, 64, 2, 2, 2>;
+using Wide32 = Shape<128, 128, 2, 2, 1>;
 
 template <class S>
 int64_t tiles(const MatmulArgs& a) {
