@@ -347,6 +347,33 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
         }
     }
     __syncthreads();
+    if (!vec) {                            // rows that no 16 bytes fit: a column a lane, eight rows at once
+      constexpr int RPP = S::NTH / S::TN;  // rows a pass of the workgroup
+      static_assert(S::NTH % S::TN == 0 && WT % (8 * RPP) == 0, "rows at once");
+      const int n = threadIdx.x % S::TN, r0 = threadIdx.x / S::TN;
+      if (n >= cols) continue;
+#pragma unroll 1
+      for (int e = 0; e < WT; e += 8 * RPP) {
+        if (k * WT + e >= rows) break;
+        float v[8], old[8];
+        uint8_t* to[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int r = e + r0 + u * RPP, m = k * WT + r;
+          v[u] = ct[r * S::TN + (((n / 4) ^ (r & 15)) << 2) + n % 4];
+          to[u] = p.out + ((int64_t)(t.m0 + m) * p.ldo + t.n0 + n) * es;
+          if constexpr (ADD)
+            if (m < rows) old[u] = F32 ? *reinterpret_cast<const float*>(to[u]) : bf2f(*reinterpret_cast<const uint16_t*>(to[u]));
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (k * WT + e + r0 + u * RPP >= rows) continue;
+          if constexpr (F32) *reinterpret_cast<float*>(to[u]) = ADD ? old[u] + v[u] : v[u];
+          else *reinterpret_cast<uint16_t*>(to[u]) = (uint16_t)f2bf(ADD ? old[u] + bf2f(f2bf(v[u])) : v[u]);
+        }
+      }
+      continue;
+    }
 #pragma unroll 1
     for (int o = threadIdx.x; o < WT * PPR; o += S::NTH) {
       const int r = o / PPR, n = 8 * (o % PPR), m = k * WT + r;
@@ -359,7 +386,7 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
         for (int e = 0; e < 4; ++e) v[4 * h + e] = q[e];
       }
       uint8_t* to = p.out + ((int64_t)(t.m0 + m) * p.ldo + t.n0 + n) * es;
-      if (vec && n + 8 <= cols) {
+      if (n + 8 <= cols) {
         if constexpr (F32) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -377,7 +404,7 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
           *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]),
                                                      pack_bf2(v[6], v[7]));
         }
-      } else {
+      } else {                             // the last columns
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if (n + e >= cols) break;
@@ -395,7 +422,7 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
   }
 }
 
-// Large is the fastest where there are tiles for every CU (8192 x 4096 x 7168: 226 us; 256 x 192 is 7 % faster where one round
+// Large is the fastest where there are tiles for every CU (8192 x 4096 x 7168: 241 us; 256 x 192 is 7 % faster where one round
 // of it covers what takes Large two, and up to 7 % slower elsewhere; 256 x 256 does not fit the registers).  FP32 results have
 // more vector work a product, and a smaller tile for the registers of it.
 using Large = Shape<256, 128, 2, 2, 1>;
@@ -408,21 +435,21 @@ int64_t tiles(const MatmulArgs& a) {
   return m * ((a.N + S::TN - 1) / S::TN);
 }
 
-// Whether Medium tiles are the faster ones, from the rounds each needs: 0.8 us a stage of k and 7 us for 256 Large tiles (one a
-// CU), 0.62 and 8 for 512 Medium ones (two), 0.42 and 6 for a last round of at most 256 of them.  Measured, Large and
-// Medium, in us at N 4096, K 7168: M 128 51.8 and 28.7, 512 53.1 and 31.7, 1024 55.3 and 43.3, 2048 64.3 and 93.1; at
-// N 2048, K 4096: M 2000 35.8 and 26.7, 4000 40.5 and 49.6.  Groups are taken to end in the middle of a tile.
+// Whether Medium tiles are the faster ones, from the rounds each needs: a Large round of w tiles (up to 256, one a CU) takes
+// 0.78 + 0.12 w / 256 us a stage of k and 7 us; 512 Medium ones (two a CU) 0.58 and 6, up to 256 of them 0.42 and 6.  Measured,
+// Large and Medium, in us at N 4096, K 7168: M 128 51.4 and 29.6, 1024 55.6 and 38.7, 1500 58.4 and 65.5, 4096 115 and 149; at
+// N 2048, K 4096: M 2000 33.8 and 24.9, 3000 35.8 and 41.1; at N 1024, K 1024: M 4096 14.5 and 10.4, 16384 28.9 and 32.4.  Groups
+// are taken to end in the middle of a tile.
 bool medium(const MatmulArgs& a) {
   const int stages = (a.K + kKB - 1) / kKB;
   auto count = [&](int tm, int tn) {
     const int64_t m = a.offsets ? a.M / tm + (a.G + 1) / 2 : (a.M + tm - 1) / tm;
     return m * ((a.N + tn - 1) / tn);
   };
-  const int64_t l = (count(Large::TM, Large::TN) + 255) / 256, m = count(Medium::TM, Medium::TN), rest = m % 512;
-  const float large = l * (0.8f * stages + 7.0f);
-  const float small = (m / 512) * (0.62f * stages + 8.0f) +
-                      (rest == 0 ? 0.0f : rest > 256 ? 0.62f * stages + 8.0f : 0.42f * stages + 6.0f);
-  return small < large;
+  auto large_us = [&](int64_t w) { return w ? (0.78f + 0.12f * w / 256) * stages + 7.0f : 0.0f; };
+  auto medium_us = [&](int64_t w) { return w ? (w > 256 ? 0.58f : 0.42f) * stages + 6.0f : 0.0f; };
+  const int64_t l = count(Large::TM, Large::TN), m = count(Medium::TM, Medium::TN);
+  return m / 512 * medium_us(512) + medium_us(m % 512) < l / 256 * large_us(256) + large_us(l % 256);
 }
 
 template <class S, bool ROWS_B, bool F32>
