@@ -423,11 +423,10 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
 }
 
 // Large is the fastest where there are tiles for every CU (8192 x 4096 x 7168: 241 us; 256 x 192 is 7 % faster where one round
-// of it covers what takes Large two, and up to 7 % slower elsewhere; 256 x 256 does not fit the registers).  FP32 results have
-// more vector work a product, and a smaller tile for the registers of it.
+// of it covers what takes Large two, and up to 7 % slower elsewhere; 256 x 256 does not fit the registers).  FP32 results go in
+// Medium tiles: 473 us, which 128 x 128 take too, and 88 against 94 for 8245 x 7334 over 224.
 using Large = Shape<256, 128, 2, 2, 1>;
 using Medium = Shape<128, 64, 2, 2, 2>;
-using Wide32 = Shape<128, 128, 2, 2, 1>;
 
 template <class S>
 int64_t tiles(const MatmulArgs& a) {
@@ -481,7 +480,7 @@ moe_status check(const moe_block_matmul_problem* p) {
 
 void launch_matmul(hipStream_t st, const MatmulArgs& a) {
   if (a.M <= kFewRows) launch_few(st, a);
-  else if (a.out_fp32) launch_shape<Wide32, true>(st, a);
+  else if (a.out_fp32) launch_shape<Medium, true>(st, a);
   else if (medium(a)) launch_shape<Medium, false>(st, a);
   else launch_shape<Large, false>(st, a);
 }
