@@ -219,15 +219,15 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
     return i32x8_t{(int)u0[0], (int)u0[1], (int)u0[2], (int)u0[3], (int)u1[0], (int)u1[1], (int)u1[2], (int)u1[3]};
   };
   i32x8_t x[S::MB], wf[4];                 // token fragments of a stage, weight fragments of a block and the next two
-  float s[S::MB];                          // the tokens' scales (times the weight tile's)
+  float s[S::MB], st[S::MB], swt;          // the tokens' scales (times the weight tile's), the next stage's as read
   f32x4_t sw[4];                           // ROWS_B: the weight rows' scales
   const uint8_t *lw = lds + wn * S::NB * 16 * kKB, *la = lds + A0 + wm * S::MB * 16 * kKB;
   const float* ls = reinterpret_cast<const float*>(lds + SC0);
   auto load_tokens = [&](int slot, int j) __attribute__((always_inline)) {
     const float* sc = ls + slot * SC * 64;
     x[j] = frag(la + slot * S::A_BYTES + j * 16 * kKB);
-    s[j] = sc[(wm * S::MB + j) * 16 + r16];
-    if constexpr (!ROWS_B) s[j] *= sc[S::TM + wn * S::NB * 16 / 128];
+    st[j] = sc[(wm * S::MB + j) * 16 + r16];
+    if (!ROWS_B && j == 0) swt = sc[S::TM + wn * S::NB * 16 / 128];
   };
   auto load_weights = [&](int slot, int i) __attribute__((always_inline)) {
     wf[i % 4] = frag(lw + slot * S::W_BYTES + i * 16 * kKB);
@@ -235,8 +235,9 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
       sw[i % 4] = *reinterpret_cast<const f32x4_t*>(ls + slot * SC * 64 + S::TM + (wn * S::NB + i) * 16 + 4 * q4);
   };
 
-  // Stage kt multiplies NB blocks of 16 weight rows, each with the MB token fragments.  A block's weights are read two blocks
-  // ahead, and each token fragment is replaced by the next stage's as soon as the last block has used it.  So the
+  // Stage kt multiplies NB blocks of 16 weight rows, each with the MB token fragments; the last two blocks in turn, a token
+  // fragment at a time, which is replaced by the next stage's as soon as both have used it (in the last block
+  // alone, those reads would crowd the LDS: 3 % of the whole).  A block's weights are read two blocks ahead.  So the
   // barrier that opens stage kt + 1 (its copies have landed) stands two blocks before the end of stage kt, whose
   // slot has then been read for good; the copies of stage kt + 2 take the slot of stage kt - 1, freed a barrier ago.  A
   // product's result is scaled and added two products later, when it is there.
@@ -250,35 +251,38 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
     if constexpr (ROWS_B) a = __builtin_elementwise_fma(pq[u], pd[u], a);
     else a = __builtin_elementwise_fma(f32x4_t{pq[u][0], pq[u][0], pq[u][0], pq[u][0]}, pd[u], a);
   };
-  auto product = [&](int i, int j) __attribute__((always_inline)) {
-    const int k = i * S::MB + j, o = (k + LAST - 2) % LAST;
+  auto block_of = [](int k) constexpr { return k < OPEN ? k / S::MB : S::NB - 2 + (k - OPEN) % 2; };
+  auto token_of = [](int k) constexpr { return k < OPEN ? k % S::MB : (k - OPEN) / 2; };
+  // product k of a stage and what is read behind it
+  auto product = [&](int k, int slot, int next) __attribute__((always_inline)) {
+    const int i = block_of(k), j = token_of(k), o = (k + LAST - 2) % LAST;
+    if (i == 0) s[j] = ROWS_B ? st[j] : st[j] * swt;   // not where they are read: that would wait for them
     f32x4_t d;
     if constexpr (F32) d = wide_product(widen(wf[i % 4]), widen(x[j]));
     else d = code_product(wf[i % 4], x[j]);
-    settle(acc[o / S::MB][o % S::MB], k & 1);
+    settle(acc[block_of(o)][token_of(o)], k & 1);
     pd[k & 1] = d;
     if constexpr (ROWS_B) pq[k & 1] = sw[i % 4] * s[j];
     else pq[k & 1][0] = s[j];
+    if (k < OPEN && j == 0) load_weights(slot, i + 2);
+    if (k == OPEN) load_weights(next, 0);
+    if (k == OPEN + S::MB) load_weights(next, 1);
+    if (k >= OPEN && (k - OPEN) % 2) load_tokens(next, j);
   };
   static_assert(LAST % 2 == 0, "results on their way");
   int slot = 0;                            // the stage's
   auto steady = [&]() __attribute__((always_inline)) {
     const int next = after(slot);
 #pragma unroll
-    for (int i = 0; i < S::NB; ++i) {
-      if (i + 2 == S::NB) {
+    for (int k = 0; k < LAST; ++k) {
+      if (k == OPEN) {
         wait_vm<FLY>();
         __syncthreads();
       }
+      __builtin_amdgcn_sched_barrier(0);
+      product(k, slot, next);
 #pragma unroll
-      for (int j = 0; j < S::MB; ++j) {
-        __builtin_amdgcn_sched_barrier(0);
-        product(i, j);
-        if (j == 0) load_weights(i + 2 < S::NB ? slot : next, (i + 2) % S::NB);
-        if (i + 1 == S::NB) load_tokens(next, j);
-#pragma unroll
-        for (int c = copies_before(i * S::MB + j); c < copies_before(i * S::MB + j + 1); ++c) copy(c);
-      }
+      for (int c = copies_before(k); c < copies_before(k + 1); ++c) copy(c);
     }
     __builtin_amdgcn_sched_barrier(0);
     advance();
@@ -288,18 +292,13 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
     const int next = after(slot);
     if (kt + 2 < nk) issue(kt + 2);
 #pragma unroll
-    for (int i = 0; i < S::NB; ++i) {
-      if (i + 2 == S::NB) {
+    for (int k = 0; k < LAST; ++k) {
+      if (k == OPEN) {
         if (kt + 2 < nk) wait_vm<COPIES>();
         else wait_vm<0>();
         __syncthreads();
       }
-#pragma unroll
-      for (int j = 0; j < S::MB; ++j) {
-        product(i, j);
-        if (j == 0) load_weights(i + 2 < S::NB ? slot : next, (i + 2) % S::NB);
-        if (i + 1 == S::NB) load_tokens(next, j);
-      }
+      product(k, slot, next);
     }
     slot = next;
   };
@@ -325,7 +324,7 @@ __global__ __launch_bounds__(S::NTH, S::MINB) void k_fp8_matmul(MatmulArgs p) {
 #pragma unroll 1
   for (; kt < nk; ++kt) any(kt);
 #pragma unroll
-  for (int u = 0; u < 2; ++u) settle(acc[(LAST - 2 + u) / S::MB][(LAST - 2 + u) % S::MB], (LAST - 2 + u) & 1);
+  for (int u = 0; u < 2; ++u) settle(acc[block_of(LAST - 2 + u)][token_of(LAST - 2 + u)], (LAST - 2 + u) & 1);
 
   // Results through LDS, a wave row's tokens at a time, so that a lane has 8 neighbouring columns.  Row r holds
   // 16-byte chunk c at c ^ (r % 16): the 16 rows a wave writes at once fall in disjoint banks.
