@@ -50,23 +50,26 @@ size_t saved_layout(const moe_ffn_problem* p, moe_ffn_saved_layout* L) {
 }
 
 // What a round of `w` workgroups at once takes, in us, for `stages` stages of 32 k each: a start and an end, and a time a stage
-// that grows with the CUs at work (up to 256 tiles one a CU; Medium ones up to 512, two a CU).
-double round_us(int shape, int64_t w, double stages) {
-  const double a = (double)w / 256;
-  if (shape == ffn::kLarge) return (0.57 + 0.28 * a) * stages + 14.0;
-  if (shape == ffn::kMid) return (0.50 + 0.10 * a) * stages + 14.0;
-  return w > 256 ? 0.62 * stages + 10.0 : (0.20 + 0.12 * a * a) * stages + 8.0;
+// that grows with the CUs at work.  Larger tiles have a CU to themselves (up to 256), so what their ends read
+// and write (`bytes` a result element, 2 in the figures) is time in which nothing multiplies; Medium ones (up to 512, two a
+// CU) hide most of that behind each other.
+double round_us(int shape, int64_t w, double stages, double bytes) {
+  const double a = (double)w / 256, end = (bytes - 2.0) * ffn::kShapeRows[shape] * ffn::kShapeCols[shape] * w / 4.9e6;
+  if (shape == ffn::kLarge) return (0.57 + 0.20 * a) * stages + 14.0 + end;
+  if (shape == ffn::kMid) return (0.50 + 0.19 * a) * stages + 14.0 + end;
+  return (w > 256 ? 0.62 * stages + 10.0 : (0.20 + 0.08 * a * a) * stages + 8.0) + 0.1 * end;
 }
 
 // How an m x n product over k is cut: the tiles and the parts of the contraction that are expected to end first.  Adding up
 // parts costs a launch and their way to memory and back.  Measured, in us, Medium / Mid / Large tiles, the parts in brackets:
-// 777 x 24576 over 4096 260 / 176 / 199, 777 x 4096 over 12288 133 / 140 [2] / 116 [4] (one part: 133 / 204 / 230), 777 x 4096 over 24576
-// 241 / 263 [2] / 199 [4], 300 x 1024 over 5632 22 [8] / 32 [8] / 37 [8] (45 / 96 / 113), 200 x 1024 over 4096 19 [8] / 29 [8] / 34 [8]
-// (37 / 85 / 96), 512 x 1024 over 4096 21 [8] / - / 33 [8] (35 / - / 90), 4096 x 4096 over 4096 173 / - / 118.
+// 777 x 24576 over 4096 260 / 176 / 198, 777 x 4096 over 12288 124 [4] / 110 [3] / 100 [4] (one part: 133 / 204 / 230), 777 x 4096 over
+// 24576 224 [4] / 202 [3] / 168 [4], 300 x 1024 over 5632 22 [8] / 32 [8] / 37 [8] (45 / 96 / 113), 200 x 1024 over 4096 19 [8] / 29 [8] /
+// 34 [8] (37 / 85 / 96), 512 x 1024 over 4096 21 [8] / - / 33 [8] (35 / - / 90), 4096 x 4096 over 4096 173 / - / 118; dh, which ends with
+// 10 bytes an element, 4096 x 12288 over 4096 540 / - / 445, 4690 x 5504 over 1024 107 / - / 142.
 constexpr int kMaxSplit = 16;
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-ffn::Plan cut(int64_t m, int64_t n, int64_t k, bool mid, float* sums) {
+ffn::Plan cut(int64_t m, int64_t n, int64_t k, double bytes, bool mid, float* sums) {
   ffn::Plan best{ffn::kMedium, {sums, 1}};
   double least = 1e30;
   for (int s = ffn::kMedium; s <= ffn::kLarge; ++s) {
@@ -74,10 +77,10 @@ ffn::Plan cut(int64_t m, int64_t n, int64_t k, bool mid, float* sums) {
     const int64_t tiles = ceil_div(m, ffn::kShapeRows[s]) * ceil_div(n, ffn::kShapeCols[s]), most = s == ffn::kMedium ? 512 : 256;
     for (int parts = 1; parts <= kMaxSplit; ++parts) {
       const int64_t w = tiles * parts;
-      const double stages = (double)ceil_div(k, 32) / parts;
+      const double stages = (double)ceil_div(k, 32) / parts, out = parts > 1 ? 4.0 : bytes;
       if (parts > 1 && (w > most || stages < 8)) break;
-      double us = (double)(w / most) * round_us(s, most, stages) + (w % most ? round_us(s, w % most, stages) : 0.0);
-      if (parts > 1) us += 4.0 + (double)(parts * m * n) * 4 * 2 / 6e6;
+      double us = (double)(w / most) * round_us(s, most, stages, out) + (w % most ? round_us(s, w % most, stages, out) : 0.0);
+      if (parts > 1) us += 4.0 + ((double)parts * 4 + bytes) * (double)(m * n) / 6e6;
       if (us < least) least = us, best.shape = s, best.split.n = parts;
     }
   }
@@ -186,8 +189,9 @@ moe_status moe_ffn_forward(const moe_ffn_problem* p, const moe_rows* x, const mo
     return launch("ffn_down_few", st, [&] { ffn::launch_down_few(st, d); });
   }
   float* sums = reinterpret_cast<float*>(ws + F.sums);
-  u.plan = cut(T, 2 * (int64_t)I, H, true, sums);
-  d.plan = cut(T, H, I, true, sums);
+  const double ab = p->saved_dtype == 0 ? 0.0 : p->saved_dtype == MOE_BF16 ? 2.0 : 1.0;   // kept of each of a and b
+  u.plan = cut(T, 2 * (int64_t)I, H, 1.0 + ab, true, sums);
+  d.plan = cut(T, H, I, 2.0, true, sums);
   MOE_TRY(launch("ffn_up", st, [&] { ffn::launch_up(st, u); }));
   if (u.plan.split.n > 1) MOE_TRY(launch("ffn_up_sum", st, [&] { ffn::launch_up_sum(st, u); }));
   MOE_TRY(launch("ffn_down", st, [&] { ffn::launch_down(st, d); }));
@@ -232,11 +236,11 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
   float* sums = reinterpret_cast<float*>(ws + B.sums);
   if (T > 0) {
     const ffn::DhArgs d{mat(grad_out), mat(down), kept(saved, L), dab.p, h.p, T, H, I, p->activation, p->saved_dtype,
-                        cut(T, I, H, true, sums)};
+                        cut(T, I, H, i8 ? 8.0 : 10.0, true, sums)};
     MOE_TRY(launch("ffn_dh", st, [&] { ffn::launch_dh(st, d); }));
     if (d.plan.split.n > 1) MOE_TRY(launch("ffn_dh_sum", st, [&] { ffn::launch_dh_sum(st, d); }));
     if (grad_x) {
-      const ffn::RowsArgs r{dab, mat(gate), mat(up), mat(grad_x), T, H, 2 * I, I, cut(T, H, 2 * (int64_t)I, true, sums)};
+      const ffn::RowsArgs r{dab, mat(gate), mat(up), mat(grad_x), T, H, 2 * I, I, cut(T, H, 2 * (int64_t)I, 2.0, true, sums)};
       MOE_TRY(launch("ffn_dx", st, [&] { ffn::launch_dx(st, r); }));
       if (r.plan.split.n > 1) MOE_TRY(launch("ffn_dx_sum", st, [&] { ffn::launch_rows_sum(st, r); }));
     }
@@ -244,9 +248,10 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
     return MOE_OK;
   }
   const int over = (p->flags & MOE_FFN_OVERWRITE_GRADS) ? 1 : 0;
+  const double grad = (f32 ? 4.0 : 2.0) * (over ? 1 : 2);
   if (grad_down) {
     const ffn::Mat dy = T > 0 ? mat(grad_out) : ffn::Mat{nullptr, H};
-    const ffn::WgradArgs w{dy, h, grad_down->base, nullptr, grad_down->ld, 0, H, I, T, H, f32, over, cut(H, I, T, false, sums)};
+    const ffn::WgradArgs w{dy, h, grad_down->base, nullptr, grad_down->ld, 0, H, I, T, H, f32, over, cut(H, I, T, grad, false, sums)};
     MOE_TRY(launch("ffn_wgrad_down", st, [&] { ffn::launch_wgrad(st, w); }));
     if (w.plan.split.n > 1) MOE_TRY(launch("ffn_wgrad_down_sum", st, [&] { ffn::launch_wgrad_sum(st, w); }));
   }
@@ -262,7 +267,7 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
       }
     }
     const ffn::WgradArgs w{dab, xs, grad_gate->base, grad_up->base, grad_gate->ld, grad_up->ld, 2 * I, H, T, I, f32,
-                           over, cut(2 * (int64_t)I, H, T, false, sums)};
+                           over, cut(2 * (int64_t)I, H, T, grad, false, sums)};
     MOE_TRY(launch("ffn_wgrad_up", st, [&] { ffn::launch_wgrad(st, w); }));
     if (w.plan.split.n > 1) MOE_TRY(launch("ffn_wgrad_up_sum", st, [&] { ffn::launch_wgrad_sum(st, w); }));
   }

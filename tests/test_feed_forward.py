@@ -616,3 +616,17 @@ def test_split_gradients_accumulate_repeat_and_capture(gpu_lib):
 def test_few_tokens_of_wide_blocks_match_formula(gpu_lib, T, H, I):
     test_forward_matches_formula(gpu_lib, T, H, I, "silu", "none")
     test_forward_matches_formula(gpu_lib, T, H, I, "gelu", "none")
+
+
+# Every product in every tile, whole and split: 192 x 256 tiles (down, dx; up; dh), 256 x 256 (down, dx; dh), split 192 x 256 (dh;
+# down; up), split 256 x 256 (dh; down; dx; up; the weights' gradients).
+TILES = [(1031, 7296, 64), (527, 64, 6592), (1706, 768, 6976), (1729, 6528, 64), (1959, 832, 6272), (527, 2112, 6784),
+         (536, 6656, 1984), (259, 1792, 5632), (771, 2432, 4800), (680, 5440, 1920), (673, 5440, 960), (391, 1984, 4224),
+         (1965, 448, 4224), (2059, 4160, 960)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I", TILES)
+def test_tiles_match_formula(gpu_lib, T, H, I):
+    test_forward_matches_formula(gpu_lib, T, H, I, "silu", "bf16")
+    test_backward_matches_formula(gpu_lib, T, H, I, "gelu", "int8" if T % 2 else "bf16", BF)
