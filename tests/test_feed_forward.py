@@ -630,3 +630,31 @@ TILES = [(1031, 7296, 64), (527, 64, 6592), (1706, 768, 6976), (1729, 6528, 64),
 def test_tiles_match_formula(gpu_lib, T, H, I):
     test_forward_matches_formula(gpu_lib, T, H, I, "silu", "bf16")
     test_backward_matches_formula(gpu_lib, T, H, I, "gelu", "int8" if T % 2 else "bf16", BF)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("saved", ["bf16", "int8"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_saturated_activations_have_finite_gradients(gpu_lib, kind, saved):
+    """Pre-activations of +-2^76, whose square is past FP32: act' is 1 or 0.  Every value is a power of two, so
+    the results are exact."""
+    T, H, I = 70, 64, 64
+    sign = torch.tensor([1.0, -1.0]).repeat(I // 2)[:, None]
+    x = torch.full((T, H), 2.0 ** 40).to(BF).cuda()
+    wg = (sign * torch.full((I, H), 2.0 ** 30)).to(BF).cuda()
+    wu = torch.full((I, H), 2.0 ** -46).to(BF).cuda()
+    wd = torch.full((H, I), 2.0 ** -6).to(BF).cuda()
+    dy = torch.ones(T, H).to(BF).cuda()
+    op = mk.FeedForward(H, I, T, kind, saved, grad_dtype=torch.float32)
+    sv = torch.zeros(op.saved_bytes(T), dtype=torch.uint8, device="cuda")
+    out, dx = torch.empty(T, H, dtype=BF, device="cuda"), torch.empty(T, H, dtype=BF, device="cuda")
+    gg, gu, gd = torch.empty(I, H, device="cuda"), torch.empty(I, H, device="cuda"), torch.empty(H, I, device="cuda")
+    op.forward(x, wg, wu, wd, out, sv)
+    op.backward(dy, x if saved == "bf16" else None, wg, wu, wd, sv, dx, gg, gu, gd, overwrite=True)
+    torch.cuda.synchronize()
+    on = (sign > 0).float()                                   # a = 2^76 or -2^76, b = 1, dh = 1
+    assert torch.equal(out.cpu(), torch.full((T, H), 2.0 ** 75).to(BF))          # 32 times 2^76 2^-6
+    assert torch.equal(dx.cpu(), torch.full((T, H), 2.0 ** 36).to(BF))           # 32 times (2^30 + 2^76 2^-46)
+    assert torch.equal(gg.cpu(), (on * (T * 2.0 ** 40)).expand(I, H))            # da = 1 or 0
+    assert torch.equal(gu.cpu(), (on * (T * 2.0 ** 116)).expand(I, H))           # db = 2^76 or 0
+    assert torch.equal(gd.cpu(), (on * (T * 2.0 ** 76)).t().expand(H, I))
