@@ -1,6 +1,7 @@
 // Values to E4M3 codes with one FP32 scale a block of 128 (along a row, or 128 x 128 tiles):
 //   scale = m / 448, code = E4M3(448 v / m) to nearest even, m the block's largest magnitude
-// One pass bound by memory: 2 (4) bytes read and 1 written a value.
+// One pass bound by memory: 2 (4) bytes read and 1 written a value (8192 x 7168 BF16 along rows: 38 us, 4.7 TB/s, a large
+// copy's 4.9; the transposed form turns codes, not values, through LDS).
 //
 // The quotient is formed as the formula says, not as v times a rounded 448 / m: products of that
 // kind land on either side of a tie by chance, and with BF16 values exact ties are common.
@@ -119,7 +120,7 @@ __global__ __launch_bounds__(kThreads) void k_fp8_rows(QuantArgs a) {
 template <bool F32, bool WHOLE, bool TILES, bool TRANSPOSE>
 __global__ __launch_bounds__(kThreads) void k_fp8_tile(QuantArgs a) {
   static_assert(TILES || TRANSPOSE, "blocks along a row have a kernel of their own");
-  constexpr int kPitch = 128 + 16;       // bytes of a column of codes in LDS
+  constexpr int kPitch = 128 + 16;       // bytes of a column of codes in LDS, its 16-byte pieces p at p ^ (column / 16)
   __shared__ __align__(16) uint8_t turned[TRANSPOSE ? 128 * kPitch : 16];
   __shared__ uint32_t part[16][TILES ? 1 : 128];
   const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
@@ -174,7 +175,8 @@ __global__ __launch_bounds__(kThreads) void k_fp8_tile(QuantArgs a) {
       float t[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[i] = v[i][j];
-      *reinterpret_cast<uint2*>(turned + (8 * c + j) * kPitch + 8 * g) = codes8(t, d[TILES ? 0 : j]);
+      *reinterpret_cast<uint2*>(turned + (8 * c + j) * kPitch + (((g >> 1) ^ (c >> 1)) << 4) + 8 * (g & 1)) =
+          codes8(t, d[TILES ? 0 : j]);
     }
     __syncthreads();
 #pragma unroll
@@ -182,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void k_fp8_tile(QuantArgs a) {
       const int piece = u * kThreads + threadIdx.x, j = piece >> 3, k = 16 * (piece & 7);
       if (tc * 128 + j < a.C && tr * 128 + k < a.ldq)
         *reinterpret_cast<uint4*>(a.codes + (tc * 128 + j) * a.ldq + tr * 128 + k) =
-            *reinterpret_cast<const uint4*>(turned + j * kPitch + k);
+            *reinterpret_cast<const uint4*>(turned + j * kPitch + (((piece & 7) ^ (j >> 4)) << 4));
     }
   }
 }
