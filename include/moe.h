@@ -436,8 +436,8 @@ moe_status moe_norm_backward(const moe_norm_problem* p, const moe_rows* grad_y, 
  *   value = code 2^(s - 133), s the smallest byte in [0, 254] for which the block's largest
  *   magnitude is at most 127 steps; code = value / step to nearest, ties to even
  * so a value is off by at most half a step, 2^-7 of the block's largest.  Values above 127.5
- * 2^121 are stored as 127 2^121, parts of values below 2^-133 are dropped.  A block that holds an infinity or NaN has s = 255 and
- * loads as NaN throughout.  Loading into BF16 is exact. */
+ * 2^121 are stored as 127 2^121, parts of values below 2^-133 are dropped.  A block that holds
+ * an infinity or NaN has s = 255 and loads as NaN throughout.  Loading into BF16 is exact. */
 typedef struct {
   int64_t rows;          /* in [0, 2^31]                                                  */
   int64_t cols;          /* in [1, MOE_CHECKPOINT_MAX_COLS]                               */

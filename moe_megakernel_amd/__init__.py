@@ -898,7 +898,7 @@ class Fp8Quantizer(_Fixed):
 class Fp8Matmul(_Fixed):
     """out = a b^T of E4M3 codes with scales of 128 (as Fp8Quantizer gives them), rows in groups
     with a weight each or all in one.  scales: of b, "tiles" or "rows" (one group); accumulate: add
-    to out.  Holds options only; every buffer is the caller's."""
+    to out.  Holds options only; every buffer is the caller's (and nothing on `device`)."""
 
     def __init__(self, scales="tiles", out_dtype=None, accumulate=False, device="cuda"):
         import torch

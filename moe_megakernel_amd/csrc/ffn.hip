@@ -22,6 +22,11 @@ using namespace dense;
 
 namespace {
 
+// Bound by the matrix units and their power: at 4096 tokens, H 4096, I 12288 grad_x runs at 1340 to 1370 TFLOP/s with
+// the matrix units busy 69 % of the time at 1.75 GHz, the weight gradients at 1230, and dh at 930, since its end reads a and b and
+// writes da, db and h, 10 bytes an element (500 MB, 100 us at a copy's rate), which a tile with a CU to itself hides
+// behind nothing.  256 x 128 with two a CU is slower there (480 us against 445) and 10 % faster only where the contraction is
+// short (up of 4690 tokens, H 1024, I 5504: 122 us against 135).
 using Large = Tile<256, 256, 2, 2, 4, 1, 0, 64>;
 using Mid = Tile<192, 256, 2, 2, 4, 1, 0, 64>;
 using Medium = Tile<128, 128, 2, 2, 4, 2, 0, 64>;
