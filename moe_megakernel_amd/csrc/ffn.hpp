@@ -73,7 +73,7 @@ void launch_rows_sum(hipStream_t st, const RowsArgs& a);
 void launch_dh_sum(hipStream_t st, const DhArgs& a);
 void launch_wgrad_sum(hipStream_t st, const WgradArgs& a);
 
-// up to kFewTokens tokens, nothing kept
+// up to kFewTokens tokens, nothing kept or a and b in BF16 (a block of 32 columns does not end in one workgroup there)
 constexpr int kFewTokens = 64;
 void launch_up_few(hipStream_t st, const UpArgs& a);
 void launch_down_few(hipStream_t st, const RowsArgs& a);

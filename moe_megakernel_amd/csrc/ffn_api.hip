@@ -184,7 +184,7 @@ moe_status moe_ffn_forward(const moe_ffn_problem* p, const moe_rows* x, const mo
   }
   ffn::UpArgs u{mat(x), mat(gate), mat(up), h, kept(saved, L), T, H, I, p->activation, p->saved_dtype};
   ffn::RowsArgs d{h, mat(down), mat(down), mat(out), T, H, I, I};
-  if (T <= ffn::kFewTokens && !p->saved_dtype) {
+  if (T <= ffn::kFewTokens && p->saved_dtype != MOE_MXINT8) {
     MOE_TRY(launch("ffn_up_few", st, [&] { ffn::launch_up_few(st, u); }));
     return launch("ffn_down_few", st, [&] { ffn::launch_down_few(st, d); });
   }

@@ -1,10 +1,11 @@
 // The gated feed-forward block for a few tokens (serving): two kernels built around one read of the
 // weights (stream.hpp).
 //
-//   k_few_up    h = act(a) b: a fragment of 16 rows is 8 gate and 8 up rows in turn, so a pair ends
-//               in neighbouring results of a lane
+//   k_few_up    h = act(a) b, a and b kept in BF16 where asked for: a fragment of 16 rows is 8 gate and
+//               8 up rows in turn, so a pair ends in neighbouring results of a lane
 //   k_few_down  out = h down^T
-// h is rounded to BF16 between them, as over many tokens.
+// h is rounded to BF16 between them, as over many tokens.  (34 tokens, H 2112, I 9024, a and b kept: 32 us, 44 in the
+// tiles of many tokens; 21, H 1216, I 1664: 11 and 18.)
 #include <hip/hip_runtime.h>
 
 #include "ffn.hpp"
@@ -86,7 +87,13 @@ __global__ __launch_bounds__(64 * W) void k_few_up(UpArgs p) {
                            [&](const uint8_t* wt, const uint8_t* xt, const float*) { stage<R, NF>(wt, xt, acc); });
   join<R, NF, W>(acc, lds, p.T, [&](int t, int row, float2 v) {
     const int i = i0 + row / 2;
-    if (i < p.I) p.h.p[(int64_t)t * p.h.ld + i] = (uint16_t)f2bf(act<ACT>(v.x) * v.y);
+    if (i >= p.I) return;
+    p.h.p[(int64_t)t * p.h.ld + i] = (uint16_t)f2bf(act<ACT>(v.x) * v.y);
+    if (p.saved == kBf16) {
+      uint16_t* ab = reinterpret_cast<uint16_t*>(p.kept.ab) + (int64_t)t * 2 * p.I + i;
+      ab[0] = (uint16_t)f2bf(v.x);
+      ab[p.I] = (uint16_t)f2bf(v.y);
+    }
   });
 }
 

@@ -658,3 +658,10 @@ def test_saturated_activations_have_finite_gradients(gpu_lib, kind, saved):
     assert torch.equal(gg.cpu(), (on * (T * 2.0 ** 40)).expand(I, H))            # da = 1 or 0
     assert torch.equal(gu.cpu(), (on * (T * 2.0 ** 116)).expand(I, H))           # db = 2^76 or 0
     assert torch.equal(gd.cpu(), (on * (T * 2.0 ** 76)).t().expand(H, I))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I", [(16, 192, 4160), (24, 8256, 64), (33, 4160, 64), (48, 192, 2112), (64, 4160, 2112)])
+def test_few_tokens_keep_their_pre_activations(gpu_lib, T, H, I):
+    test_forward_matches_formula(gpu_lib, T, H, I, "gelu", "bf16")
+    test_backward_matches_formula(gpu_lib, T, H, I, "silu", "bf16", torch.float32)
