@@ -461,7 +461,8 @@ moe_status moe_checkpoint_load(const moe_checkpoint_problem* p, const void* code
  *   act(a) = a / (1 + e^-a) (MOE_FFN_SILU) or a / (1 + e^-z), z = 2 sqrt(2 / pi) (a + 0.044715 a^3)
  *   (MOE_FFN_GELU, the tanh form)
  * x, out and the weights are BF16; sums are FP32; h, and in the backward da, db and h again,
- * are rounded to BF16 once each as operands of the next product, outputs once.
+ * are rounded to BF16 once each as operands of the next product, outputs once.  The forward of up to
+ * MOE_FFN_FEW_TOKENS tokens that keeps nothing or BF16 holds h to 2^-16 of itself (in two BF16 parts).
  * What a training forward keeps (`saved`) is a and b in BF16, or a, b and x in 8 bits
  * (MOE_MXINT8, as moe_checkpoint_store writes them; a and b from their FP32 sums); the backward takes
  * the gradient at the values kept. */
@@ -480,6 +481,7 @@ typedef struct {
 /* T (H + 2 I) is at most 2^38 as well (a launch holds 2^32 threads; MOE_ERR_SHAPE above), and rows of every
  * matrix at most MOE_FFN_MAX_LD elements apart (MOE_ERR_LAYOUT above). */
 #define MOE_FFN_MAX_LD (1 << 22)
+#define MOE_FFN_FEW_TOKENS 64
 
 /* Byte offsets inside `saved`: ab [T][2I] (a at column j, b at I + j) in BF16, or int8 codes with
  * their scale bytes ab_scales [T][2I / 32], and x codes [T][H] with x_scales [T][H / 32] (the last

@@ -33,6 +33,7 @@ MOE_CHECKPOINT_MAX_COLS = 1 << 24
 MOE_FFN_SILU, MOE_FFN_GELU = 1, 2
 MOE_FFN_OVERWRITE_GRADS = 1
 MOE_FFN_MAX_LD = 1 << 22
+MOE_FFN_FEW_TOKENS = 64
 MOE_FP8_ROWS, MOE_FP8_TILES = 1, 2
 MOE_FP8_TRANSPOSE, MOE_FP8_ACCUMULATE = 1, 2
 MOE_FP8_MAX_GROUPS = 256

@@ -75,7 +75,8 @@ void launch_wgrad_sum(hipStream_t st, const WgradArgs& a);
 
 // up to kFewTokens tokens, nothing kept or a and b in BF16 (a block of 32 columns does not end in one workgroup there)
 constexpr int kFewTokens = 64;
-void launch_up_few(hipStream_t st, const UpArgs& a);
+void launch_up_few(hipStream_t st, const UpArgs& a);   // h in two parts: rows T .. 2T - 1 are the second's
+int few_parts(int T, int N, int K);                    // of the contraction of launch_down_few
 void launch_down_few(hipStream_t st, const RowsArgs& a);
 
 }  // namespace ffn

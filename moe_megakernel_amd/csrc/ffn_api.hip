@@ -11,6 +11,8 @@
 
 using namespace moe;
 
+static_assert(ffn::kFewTokens == MOE_FFN_FEW_TOKENS, "as the header says");
+
 namespace {
 
 moe_status check_problem(const moe_ffn_problem* p) {
@@ -100,7 +102,7 @@ Fwd fwd_layout(const moe_ffn_problem* p) {
   const size_t T = p->tokens, H = p->hidden, I = p->intermediate;
   Offsets o;
   Fwd f;
-  f.h = o.take((size_t)2 * p->tokens * p->intermediate);
+  f.h = o.take(2 * I * std::max<size_t>(T, 2 * std::min<size_t>(T, ffn::kFewTokens)));   // of few tokens in two parts
   f.sums = o.take(std::max(split_bytes(T, 2 * I, H), split_bytes(T, H, I)));
   f.total = o.total > kAlign ? o.total : kAlign;
   return f;
@@ -184,11 +186,14 @@ moe_status moe_ffn_forward(const moe_ffn_problem* p, const moe_rows* x, const mo
   }
   ffn::UpArgs u{mat(x), mat(gate), mat(up), h, kept(saved, L), T, H, I, p->activation, p->saved_dtype};
   ffn::RowsArgs d{h, mat(down), mat(down), mat(out), T, H, I, I};
-  if (T <= ffn::kFewTokens && p->saved_dtype != MOE_MXINT8) {
-    MOE_TRY(launch("ffn_up_few", st, [&] { ffn::launch_up_few(st, u); }));
-    return launch("ffn_down_few", st, [&] { ffn::launch_down_few(st, d); });
-  }
   float* sums = reinterpret_cast<float*>(ws + F.sums);
+  if (T <= ffn::kFewTokens && p->saved_dtype != MOE_MXINT8) {
+    d.plan.split = {sums, ffn::few_parts(T, H, I)};   // within kMaxSplit and eight stages a part, which split_bytes counts
+    MOE_TRY(launch("ffn_up_few", st, [&] { ffn::launch_up_few(st, u); }));
+    MOE_TRY(launch("ffn_down_few", st, [&] { ffn::launch_down_few(st, d); }));
+    if (d.plan.split.n > 1) MOE_TRY(launch("ffn_down_few_sum", st, [&] { ffn::launch_rows_sum(st, d); }));
+    return MOE_OK;
+  }
   const double ab = p->saved_dtype == 0 ? 0.0 : p->saved_dtype == MOE_BF16 ? 2.0 : 1.0;   // kept of each of a and b
   u.plan = cut(T, 2 * (int64_t)I, H, 1.0 + ab, true, sums);
   d.plan = cut(T, H, I, 2.0, true, sums);
