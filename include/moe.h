@@ -515,7 +515,8 @@ moe_status moe_ffn_forward(const moe_ffn_problem* p, const moe_rows* x, const mo
  *              BF16 main_grad (the call's contribution is rounded before it is added).  NULL: not
  *              computed (grad_gate and grad_up both or neither).  At least one output is needed
  *  workspace   moe_ffn_workspace_bytes(p, 1), 16-byte aligned
- * Sums run in a fixed order: the same call gives the same bits. */
+ * grad_x may take the place of grad_out or x (it is written last); no other output may overlap an input or
+ * another output.  Sums run in a fixed order: the same call gives the same bits. */
 moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, const moe_rows* x,
                             const moe_rows* gate, const moe_rows* up, const moe_rows* down, const void* saved,
                             const moe_rows* grad_x, const moe_rows* grad_gate, const moe_rows* grad_up,

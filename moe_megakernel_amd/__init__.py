@@ -843,7 +843,8 @@ class FeedForward(_Fixed):
     def backward(self, grad_out, x, gate, up, down, saved, grad_x=None, grad_gate=None, grad_up=None, grad_down=None,
                  overwrite=False):
         """x: the forward's (None with saved="int8").  The gradients given are computed: grad_x is
-        overwritten, those of the weights (grad_dtype) are accumulated, or overwritten."""
+        overwritten (it may be grad_out or x), those of the weights (grad_dtype) are accumulated, or
+        overwritten."""
         import torch
         where = "moe_ffn_backward"
         H, I, bf = self.hidden, self.intermediate, torch.bfloat16

@@ -244,11 +244,6 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
                         cut(T, I, H, i8 ? 8.0 : 10.0, true, sums)};
     MOE_TRY(launch("ffn_dh", st, [&] { ffn::launch_dh(st, d); }));
     if (d.plan.split.n > 1) MOE_TRY(launch("ffn_dh_sum", st, [&] { ffn::launch_dh_sum(st, d); }));
-    if (grad_x) {
-      const ffn::RowsArgs r{dab, mat(gate), mat(up), mat(grad_x), T, H, 2 * I, I, cut(T, H, 2 * (int64_t)I, 2.0, true, sums)};
-      MOE_TRY(launch("ffn_dx", st, [&] { ffn::launch_dx(st, r); }));
-      if (r.plan.split.n > 1) MOE_TRY(launch("ffn_dx_sum", st, [&] { ffn::launch_rows_sum(st, r); }));
-    }
   } else if (!(p->flags & MOE_FFN_OVERWRITE_GRADS)) {
     return MOE_OK;
   }
@@ -275,6 +270,11 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
                            over, cut(2 * (int64_t)I, H, T, grad, false, sums)};
     MOE_TRY(launch("ffn_wgrad_up", st, [&] { ffn::launch_wgrad(st, w); }));
     if (w.plan.split.n > 1) MOE_TRY(launch("ffn_wgrad_up_sum", st, [&] { ffn::launch_wgrad_sum(st, w); }));
+  }
+  if (grad_x && T > 0) {                     // last: it may take the place of grad_out or x
+    const ffn::RowsArgs r{dab, mat(gate), mat(up), mat(grad_x), T, H, 2 * I, I, cut(T, H, 2 * (int64_t)I, 2.0, true, sums)};
+    MOE_TRY(launch("ffn_dx", st, [&] { ffn::launch_dx(st, r); }));
+    if (r.plan.split.n > 1) MOE_TRY(launch("ffn_dx_sum", st, [&] { ffn::launch_rows_sum(st, r); }));
   }
   return MOE_OK;
 }
