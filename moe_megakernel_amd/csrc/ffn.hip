@@ -111,7 +111,7 @@ __device__ __forceinline__ void dh_end(const DhArgs& p, int row, int i, const fl
   for (int k = 0; k < 8; ++k) {
     float f, d;
     act_grad<ACT>(a[k], f, d);
-    da[k] = dh[k] * b[k] * d;
+    da[k] = dh[k] * (b[k] * d);              // d may be 0 where dh b overflows
     db[k] = dh[k] * f;
     h[k] = f * b[k];
   }
