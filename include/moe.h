@@ -555,7 +555,11 @@ moe_status moe_block_quantize(const moe_block_quantize_problem* p, const moe_row
 /* Product of rows in groups, each group with a weight of its own (the tokens of each expert, sorted
  * by expert), or of one group:
  *   out[m][n] = sum_b a_scales[b][m] S(g, n, b) sum_{k in block b} a[m][k] b[g][n][k],  m in group g
- * FP32 sums, rounded once. */
+ * The scales' product is formed first, in FP32.  Sums over blocks are FP32, and the result is rounded once.  A block's own
+ * sum is FP32 with MOE_FP32 results and with up to MOE_FP8_FEW_ROWS rows; with MOE_BF16 results of more rows it
+ * comes from the 8-bit matrix instruction, which keeps it to about 2^-16 of the block's largest product: next
+ * to the result's rounding only where large products of a block cancel. */
+#define MOE_FP8_FEW_ROWS 64
 typedef struct {
   int64_t rows;          /* M in [0, 2^24]                                                */
   int64_t cols;          /* N in [1, 2^20]                                                */

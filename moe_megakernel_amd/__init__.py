@@ -38,6 +38,7 @@ MOE_FP8_ROWS, MOE_FP8_TILES = 1, 2
 MOE_FP8_TRANSPOSE, MOE_FP8_ACCUMULATE = 1, 2
 MOE_FP8_MAX_GROUPS = 256
 MOE_FP8_MAX_LD = 1 << 23
+MOE_FP8_FEW_ROWS = 64
 
 EXPORTED = ("moe_saved_bytes", "moe_workspace_bytes", "moe_saved_view", "moe_forward",
             "moe_forward_topk", "moe_forward_noalloc", "moe_backward", "moe_status_str",
@@ -900,7 +901,9 @@ class Fp8Quantizer(_Fixed):
 class Fp8Matmul(_Fixed):
     """out = a b^T of E4M3 codes with scales of 128 (as Fp8Quantizer gives them), rows in groups
     with a weight each or all in one.  scales: of b, "tiles" or "rows" (one group); accumulate: add
-    to out.  Holds options only; every buffer is the caller's (and nothing on `device`)."""
+    to out.  FP32 results, and any of up to MOE_FP8_FEW_ROWS rows, have FP32 sums; BF16 results of
+    more rows keep a block of 128 to 2^-16 of its largest product.  Holds options only; every buffer is
+    the caller's (and nothing on `device`)."""
 
     def __init__(self, scales="tiles", out_dtype=None, accumulate=False, device="cuda"):
         import torch

@@ -21,6 +21,8 @@
 namespace moe {
 namespace fp8 {
 
+static_assert(kFewRows == MOE_FP8_FEW_ROWS, "as the header says");
+
 using gemm::dma16;
 using gemm::dma16s;
 using gemm::dma4;

@@ -1,10 +1,10 @@
 // The product of a block of 128 k for 16 rows of codes and 16 tokens' codes.
 //
 // The 8-bit matrix instructions keep a sum to about 2^-16 of its largest product (measured on
-// normal values, 128 products: 1.3e-5 of the result; the K = 32 form and sums of parts the same).  Under
-// the 2^-9 of a BF16 result that is nothing, in an FP32 one it would be the largest error by far.  So products
-// with an FP32 result decode the codes to BF16 (exact) and take the BF16 instruction (4e-9 on the
-// same values), at half its rate.
+// normal values, 128 products: 1.3e-5 of the result; the K = 32 form and sums of parts the same).  Unless a block's
+// largest products cancel, that is nothing under the 2^-8 of a BF16 result's rounding; in an FP32 one it would be the largest
+// error by far.  So products with an FP32 result, and those of a few rows, which the weights' bytes bound, decode the
+// codes to BF16 (exact) and take the BF16 instruction (4e-9 on the same values), at half its rate.
 #pragma once
 #include "common.hpp"
 
@@ -40,11 +40,6 @@ __device__ __forceinline__ f32x4_t wide_product(const Wide& a, const Wide& b) {
 __device__ __forceinline__ f32x4_t code_product(const i32x8_t& a, const i32x8_t& b) {
   constexpr int kOne = 0x7f7f7f7f;         // E8M0 1.0: the instruction's own scales stay out
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, kOne, 0, kOne);
-}
-template <bool F32>
-__device__ __forceinline__ f32x4_t block_product(const i32x8_t& a, const i32x8_t& b) {
-  if constexpr (F32) return wide_product(widen(a), widen(b));
-  else return code_product(a, b);
 }
 
 }  // namespace fp8
