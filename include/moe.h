@@ -498,10 +498,12 @@ size_t moe_ffn_workspace_bytes(const moe_ffn_problem* p, int for_backward);
 moe_status moe_ffn_saved_view(const moe_ffn_problem* p, moe_ffn_saved_layout* layout);
 
 /*  x [T][H], gate and up [I][H], down [H][I], out [T][H]: BF16, 16-byte aligned, ld a multiple of 8
- *    (gate and up may be row views of one tensor).  With MOE_MXINT8 x may not be out.
+ *    (gate and up may be row views of one tensor)
  *  saved       moe_ffn_saved_bytes(p), 16-byte aligned, written; NULL with saved_dtype 0
  *  workspace   moe_ffn_workspace_bytes(p, 0), 16-byte aligned
- * No output may overlap an input.  With no tokens nothing is enqueued. */
+ * out may take the place of x, which is read for the last time before out is written (but with MOE_BF16 the
+ * backward needs x as it was); no other output may overlap an input or another output.  With no tokens
+ * nothing is enqueued. */
 moe_status moe_ffn_forward(const moe_ffn_problem* p, const moe_rows* x, const moe_rows* gate, const moe_rows* up,
                            const moe_rows* down, const moe_rows* out, void* saved, void* workspace,
                            size_t workspace_bytes, void* stream);

@@ -831,7 +831,7 @@ class FeedForward(_Fixed):
         return dev, T, p, ms
 
     def forward(self, x, gate, up, down, out, saved=None):
-        """Writes out, and with saved="bf16" or "int8" the tensor `saved` (saved_bytes(tokens) bytes)."""
+        """Writes out (which may be x), and with saved="bf16" or "int8" the tensor `saved` (saved_bytes(tokens) bytes)."""
         import torch
         where = "moe_ffn_forward"
         dev, T, p, ms = self._common(where, x, gate, up, down, saved)

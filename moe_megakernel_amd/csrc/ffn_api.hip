@@ -179,6 +179,7 @@ moe_status moe_ffn_forward(const moe_ffn_problem* p, const moe_rows* x, const mo
   moe_ffn_saved_layout L;
   saved_layout(p, &L);
   const ffn::Mat h{reinterpret_cast<uint16_t*>(ws + F.h), I};
+  // x is read by the checkpoint and the first product alone: out, which the second writes, may take its place
   if (p->saved_dtype == MOE_MXINT8) {
     uint8_t* s = static_cast<uint8_t*>(saved);
     const checkpoint::Args c{static_cast<uint8_t*>(x->base), x->ld, T, H, s + L.x, s + L.x_scales};

@@ -29,3 +29,18 @@ def test_input_gradient_in_the_place_of_an_input(gpu_lib, T, H, I, saved, where)
     assert torch.equal(place, dx)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("saved", ["none", "bf16", "int8"])
+@pytest.mark.parametrize("T,H,I", SIZES + [(20, 128, 2048), (300, 1024, 704)])
+def test_output_in_the_place_of_the_input(gpu_lib, T, H, I, saved):
+    x, wg, wu, wd, _ = inputs(T, H, I)
+    op = mk.FeedForward(H, I, T, saved=saved)
+    kept = [None if saved == "none" else torch.zeros(op.saved_bytes(T), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    out = torch.empty_like(x)
+    op.forward(x, wg, wu, wd, out, kept[0])
+    op.forward(x, wg, wu, wd, x, kept[1])
+    torch.cuda.synchronize()
+    assert torch.equal(out, x)
+    assert saved == "none" or torch.equal(*kept)
