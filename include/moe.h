@@ -497,6 +497,19 @@ size_t moe_ffn_saved_bytes(const moe_ffn_problem* p);
 size_t moe_ffn_workspace_bytes(const moe_ffn_problem* p, int for_backward);
 moe_status moe_ffn_saved_view(const moe_ffn_problem* p, moe_ffn_saved_layout* layout);
 
+/* How the products of a call of these sizes and options are cut, for measurement and tests: tiles of
+ * rows x cols of the result (of up, gate and up columns together) and the parts of the contraction.
+ * rows and cols are 0 in the kernels for few tokens, everything is where a product is not run (no tokens;
+ * the backward's with saved_dtype 0). */
+typedef struct {
+  int32_t rows, cols, parts;
+} moe_ffn_cut;
+typedef struct {
+  moe_ffn_cut up, down;                        /* forward                                    */
+  moe_ffn_cut dh, dx, wgrad_down, wgrad_up;    /* backward                                   */
+} moe_ffn_plan;
+moe_status moe_ffn_plan_view(const moe_ffn_problem* p, moe_ffn_plan* plan);
+
 /*  x [T][H], gate and up [I][H], down [H][I], out [T][H]: BF16, 16-byte aligned, ld a multiple of 8
  *    (gate and up may be row views of one tensor)
  *  saved       moe_ffn_saved_bytes(p), 16-byte aligned, written; NULL with saved_dtype 0

@@ -46,7 +46,7 @@ EXPORTED = ("moe_saved_bytes", "moe_workspace_bytes", "moe_saved_view", "moe_for
             "moe_decode_workspace_bytes", "moe_forward_decode", "moe_router_forward", "moe_router_backward",
             "moe_norm_forward", "moe_norm_backward", "moe_norm_workspace_bytes", "moe_checkpoint_store",
             "moe_checkpoint_load", "moe_ffn_saved_bytes", "moe_ffn_workspace_bytes", "moe_ffn_saved_view",
-            "moe_ffn_forward", "moe_ffn_backward", "moe_block_quantize", "moe_block_matmul")
+            "moe_ffn_plan_view", "moe_ffn_forward", "moe_ffn_backward", "moe_block_quantize", "moe_block_matmul")
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 MOE_DECODE_MAX_TOKENS = 64
 MOE_DECODE_MAX_INTERMEDIATE = 65536
@@ -117,6 +117,14 @@ class moe_ffn_problem(C.Structure):
 
 class moe_ffn_saved_layout(C.Structure):
     _fields_ = [(n, C.c_size_t) for n in ("ab", "ab_scales", "x", "x_scales")]
+
+
+class moe_ffn_cut(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("rows", "cols", "parts")]
+
+
+class moe_ffn_plan(C.Structure):
+    _fields_ = [(n, moe_ffn_cut) for n in ("up", "down", "dh", "dx", "wgrad_down", "wgrad_up")]
 
 
 class moe_block_quantize_problem(C.Structure):
@@ -200,6 +208,8 @@ def load(path: str | None = None):
     lib.moe_ffn_workspace_bytes.restype = C.c_size_t
     lib.moe_ffn_saved_view.argtypes = [P(moe_ffn_problem), P(moe_ffn_saved_layout)]
     lib.moe_ffn_saved_view.restype = C.c_int
+    lib.moe_ffn_plan_view.argtypes = [P(moe_ffn_problem), P(moe_ffn_plan)]
+    lib.moe_ffn_plan_view.restype = C.c_int
     lib.moe_ffn_forward.argtypes = [P(moe_ffn_problem)] + [P(moe_rows)] * 5 + [C.c_void_p, C.c_void_p, C.c_size_t,
                                                                              C.c_void_p]
     lib.moe_ffn_forward.restype = C.c_int
@@ -345,6 +355,14 @@ def moe_ffn_saved_view(p: moe_ffn_problem) -> moe_ffn_saved_layout:
     st = load().moe_ffn_saved_view(C.byref(p), C.byref(out))
     if st != MOE_OK:
         raise MoeError(st, "moe_ffn_saved_view")
+    return out
+
+
+def moe_ffn_plan_view(p: moe_ffn_problem) -> moe_ffn_plan:
+    out = moe_ffn_plan()
+    st = load().moe_ffn_plan_view(C.byref(p), C.byref(out))
+    if st != MOE_OK:
+        raise MoeError(st, "moe_ffn_plan_view")
     return out
 
 

@@ -122,6 +122,36 @@ Bwd bwd_layout(const moe_ffn_problem* p) {
   return b;
 }
 
+// How each product is cut: bytes a result element at its end, and whether 192 x 256 tiles are built.
+bool few(const moe_ffn_problem* p) { return p->tokens <= ffn::kFewTokens && p->saved_dtype != MOE_MXINT8; }
+ffn::Plan plan_up(const moe_ffn_problem* p, float* sums) {
+  const double ab = p->saved_dtype == 0 ? 0.0 : p->saved_dtype == MOE_BF16 ? 2.0 : 1.0;   // kept of each of a and b
+  return cut(p->tokens, 2 * p->intermediate, p->hidden, 1.0 + ab, true, sums);
+}
+ffn::Plan plan_down(const moe_ffn_problem* p, float* sums) {
+  // few: within kMaxSplit and eight stages a part, which split_bytes counts
+  if (few(p)) return {0, {sums, ffn::few_parts((int)p->tokens, (int)p->hidden, (int)p->intermediate)}};
+  return cut(p->tokens, p->hidden, p->intermediate, 2.0, true, sums);
+}
+ffn::Plan plan_dh(const moe_ffn_problem* p, float* sums) {
+  return cut(p->tokens, p->intermediate, p->hidden, p->saved_dtype == MOE_MXINT8 ? 8.0 : 10.0, true, sums);
+}
+ffn::Plan plan_dx(const moe_ffn_problem* p, float* sums) {
+  return cut(p->tokens, p->hidden, 2 * p->intermediate, 2.0, true, sums);
+}
+double grad_bytes(const moe_ffn_problem* p) {
+  return (p->grad_dtype == MOE_FP32 ? 4.0 : 2.0) * (p->flags & MOE_FFN_OVERWRITE_GRADS ? 1 : 2);
+}
+ffn::Plan plan_wgrad_down(const moe_ffn_problem* p, float* sums) {
+  return cut(p->hidden, p->intermediate, p->tokens, grad_bytes(p), false, sums);
+}
+ffn::Plan plan_wgrad_up(const moe_ffn_problem* p, float* sums) {
+  return cut(2 * p->intermediate, p->hidden, p->tokens, grad_bytes(p), false, sums);
+}
+moe_ffn_cut shown(const ffn::Plan& c) {
+  return {(int32_t)ffn::kShapeRows[c.shape], (int32_t)ffn::kShapeCols[c.shape], c.split.n};
+}
+
 // A matrix of `cols` columns that moves in 16-byte pieces.
 moe_status check_rows(const moe_rows* m, int64_t cols, int per16) {
   if (!m || !m->base) return MOE_ERR_NULL;
@@ -159,6 +189,26 @@ moe_status moe_ffn_saved_view(const moe_ffn_problem* p, moe_ffn_saved_layout* la
   return MOE_OK;
 }
 
+moe_status moe_ffn_plan_view(const moe_ffn_problem* p, moe_ffn_plan* plan) {
+  MOE_TRY(check_problem(p));
+  if (!plan) return MOE_ERR_NULL;
+  *plan = moe_ffn_plan{};
+  if (p->tokens == 0) return MOE_OK;
+  if (few(p)) {
+    plan->up.parts = 1;
+    plan->down.parts = plan_down(p, nullptr).split.n;
+  } else {
+    plan->up = shown(plan_up(p, nullptr));
+    plan->down = shown(plan_down(p, nullptr));
+  }
+  if (!p->saved_dtype) return MOE_OK;
+  plan->dh = shown(plan_dh(p, nullptr));
+  plan->dx = shown(plan_dx(p, nullptr));
+  plan->wgrad_down = shown(plan_wgrad_down(p, nullptr));
+  plan->wgrad_up = shown(plan_wgrad_up(p, nullptr));
+  return MOE_OK;
+}
+
 moe_status moe_ffn_forward(const moe_ffn_problem* p, const moe_rows* x, const moe_rows* gate, const moe_rows* up,
                            const moe_rows* down, const moe_rows* out, void* saved, void* workspace,
                            size_t workspace_bytes, void* stream) {
@@ -188,16 +238,14 @@ moe_status moe_ffn_forward(const moe_ffn_problem* p, const moe_rows* x, const mo
   ffn::UpArgs u{mat(x), mat(gate), mat(up), h, kept(saved, L), T, H, I, p->activation, p->saved_dtype};
   ffn::RowsArgs d{h, mat(down), mat(down), mat(out), T, H, I, I};
   float* sums = reinterpret_cast<float*>(ws + F.sums);
-  if (T <= ffn::kFewTokens && p->saved_dtype != MOE_MXINT8) {
-    d.plan.split = {sums, ffn::few_parts(T, H, I)};   // within kMaxSplit and eight stages a part, which split_bytes counts
+  d.plan = plan_down(p, sums);
+  if (few(p)) {
     MOE_TRY(launch("ffn_up_few", st, [&] { ffn::launch_up_few(st, u); }));
     MOE_TRY(launch("ffn_down_few", st, [&] { ffn::launch_down_few(st, d); }));
     if (d.plan.split.n > 1) MOE_TRY(launch("ffn_down_few_sum", st, [&] { ffn::launch_rows_sum(st, d); }));
     return MOE_OK;
   }
-  const double ab = p->saved_dtype == 0 ? 0.0 : p->saved_dtype == MOE_BF16 ? 2.0 : 1.0;   // kept of each of a and b
-  u.plan = cut(T, 2 * (int64_t)I, H, 1.0 + ab, true, sums);
-  d.plan = cut(T, H, I, 2.0, true, sums);
+  u.plan = plan_up(p, sums);
   MOE_TRY(launch("ffn_up", st, [&] { ffn::launch_up(st, u); }));
   if (u.plan.split.n > 1) MOE_TRY(launch("ffn_up_sum", st, [&] { ffn::launch_up_sum(st, u); }));
   MOE_TRY(launch("ffn_down", st, [&] { ffn::launch_down(st, d); }));
@@ -242,17 +290,16 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
   float* sums = reinterpret_cast<float*>(ws + B.sums);
   if (T > 0) {
     const ffn::DhArgs d{mat(grad_out), mat(down), kept(saved, L), dab.p, h.p, T, H, I, p->activation, p->saved_dtype,
-                        cut(T, I, H, i8 ? 8.0 : 10.0, true, sums)};
+                        plan_dh(p, sums)};
     MOE_TRY(launch("ffn_dh", st, [&] { ffn::launch_dh(st, d); }));
     if (d.plan.split.n > 1) MOE_TRY(launch("ffn_dh_sum", st, [&] { ffn::launch_dh_sum(st, d); }));
   } else if (!(p->flags & MOE_FFN_OVERWRITE_GRADS)) {
     return MOE_OK;
   }
   const int over = (p->flags & MOE_FFN_OVERWRITE_GRADS) ? 1 : 0;
-  const double grad = (f32 ? 4.0 : 2.0) * (over ? 1 : 2);
   if (grad_down) {
     const ffn::Mat dy = T > 0 ? mat(grad_out) : ffn::Mat{nullptr, H};
-    const ffn::WgradArgs w{dy, h, grad_down->base, nullptr, grad_down->ld, 0, H, I, T, H, f32, over, cut(H, I, T, grad, false, sums)};
+    const ffn::WgradArgs w{dy, h, grad_down->base, nullptr, grad_down->ld, 0, H, I, T, H, f32, over, plan_wgrad_down(p, sums)};
     MOE_TRY(launch("ffn_wgrad_down", st, [&] { ffn::launch_wgrad(st, w); }));
     if (w.plan.split.n > 1) MOE_TRY(launch("ffn_wgrad_down_sum", st, [&] { ffn::launch_wgrad_sum(st, w); }));
   }
@@ -268,12 +315,12 @@ moe_status moe_ffn_backward(const moe_ffn_problem* p, const moe_rows* grad_out, 
       }
     }
     const ffn::WgradArgs w{dab, xs, grad_gate->base, grad_up->base, grad_gate->ld, grad_up->ld, 2 * I, H, T, I, f32,
-                           over, cut(2 * (int64_t)I, H, T, grad, false, sums)};
+                           over, plan_wgrad_up(p, sums)};
     MOE_TRY(launch("ffn_wgrad_up", st, [&] { ffn::launch_wgrad(st, w); }));
     if (w.plan.split.n > 1) MOE_TRY(launch("ffn_wgrad_up_sum", st, [&] { ffn::launch_wgrad_sum(st, w); }));
   }
   if (grad_x && T > 0) {                     // last: it may take the place of grad_out or x
-    const ffn::RowsArgs r{dab, mat(gate), mat(up), mat(grad_x), T, H, 2 * I, I, cut(T, H, 2 * (int64_t)I, 2.0, true, sums)};
+    const ffn::RowsArgs r{dab, mat(gate), mat(up), mat(grad_x), T, H, 2 * I, I, plan_dx(p, sums)};
     MOE_TRY(launch("ffn_dx", st, [&] { ffn::launch_dx(st, r); }));
     if (r.plan.split.n > 1) MOE_TRY(launch("ffn_dx_sum", st, [&] { ffn::launch_rows_sum(st, r); }));
   }

@@ -27,7 +27,7 @@ def reference(x, wg, wu, wd, kind):
 @pytest.mark.parametrize("kind,saved", [("silu", "none"), ("gelu", "bf16")])
 @pytest.mark.parametrize("T,H,I", [(1, 64, 64), (1, 4096, 64), (5, 320, 192), (8, 192, 64), (9, 64, 128), (16, 128, 64), (17, 192, 192),
                                    (32, 64, 64), (33, 320, 64), (40, 4160, 64), (48, 64, 192), (49, 192, 64), (64, 64, 64),
-                                   (24, 8256, 64), (64, 4160, 128),
+                                   (24, 8256, 64), (64, 4160, 128), (12, 4160, 64),
                                    (20, 128, 2048), (40, 64, 4160), (64, 320, 2112), (33, 4096, 2048)])    # in parts
 def test_only_the_output_is_rounded(gpu_lib, T, H, I, kind, saved):
     x, wg, wu, wd, _ = inputs(T, H, I)
