@@ -920,8 +920,8 @@ class Fp8Matmul(_Fixed):
     """out = a b^T of E4M3 codes with scales of 128 (as Fp8Quantizer gives them), rows in groups
     with a weight each or all in one.  scales: of b, "tiles" or "rows" (one group); accumulate: add
     to out.  FP32 results, and any of up to MOE_FP8_FEW_ROWS rows, have FP32 sums; BF16 results of
-    more rows keep a block of 128 to 2^-16 of its largest product.  Holds options only; every buffer is
-    the caller's (and nothing on `device`)."""
+    more rows have the 8-bit instruction's (moe.h).  Holds options only; every buffer is the caller's (and
+    nothing on `device`)."""
 
     def __init__(self, scales="tiles", out_dtype=None, accumulate=False, device="cuda"):
         import torch

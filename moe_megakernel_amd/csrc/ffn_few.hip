@@ -153,7 +153,7 @@ void down_as(hipStream_t st, const RowsArgs& a) {
 // pays where one would leave more workgroups than CUs anyway (T > 32: 48 tokens, H 4096, I 12288 45 us against 67; but 37 of
 // I 2048, 256 workgroups, 16 against 15.4) or, with two token tiles, many more (24 tokens, H 4096, I 12288 39 us
 // against 47).  Four waves and two stages in flight leave room for two workgroups a CU; one token tile is so small that eight
-// waves do (13 tokens, H 4096, I 12288: the whole forward 57 us, 64 with four stages).
+// waves do (13 tokens, H 4096, I 12288, with both kernels so and h in one part: 57 us, 64 with four stages).
 template <class F>
 void by_tokens(int T, int64_t frags, const F& f) {
   using std::integral_constant;
